@@ -291,6 +291,135 @@ fc_status fc_stamped_call(fc_op op, const void* P, fc_order p_order, const void*
                           fc_out_dtype out_dtype, int64_t M, int64_t K, int64_t N, void* stamps,
                           int64_t stamp_bytes, int64_t* blocks, void* stream);
 
+/* ------------------------------------------------------ fused operators
+ *
+ * The FC layer's products with what a language model does around them:
+ * activations in the epilogue, the loss over a vocabulary projection, and
+ * expert layers. Matrices are laid out as above (tightly packed, bf16 unless
+ * stated), sums are held in fp32 and rounded once on output unless stated.
+ * Calls enqueue kernels on `stream` and return: they neither allocate nor
+ * synchronize, keep nothing between calls and may be captured into graphs.
+ * Their plans depend on the arguments alone (fc_tune does not apply), and the
+ * same call gives the same bits (no atomics).
+ *
+ * Workspace. A call takes its scratch memory from the caller: `ws`, device
+ * memory of at least the bytes that the matching *_ws_bytes query returns for
+ * the same arguments, 256-byte aligned; NULL where the query returns 0. It
+ * holds nothing that a later call needs. Calls that can run at the same time
+ * need workspaces of their own. `aligned` says whether both bf16 matrices of
+ * the product (X and W, dY and W, X and dY) start on 16-byte boundaries; if
+ * not, or if their rows are not a multiple of 8 values, they are copied into
+ * the workspace with padded rows first. The queries return -1 for arguments
+ * that the call would refuse.
+ *
+ * Sizes are 1 .. 2^22. No output may overlap an input, another output or the
+ * workspace. FC_E_INVALID for arguments outside this text, FC_E_UNSUPPORTED
+ * on another device than gfx950, FC_E_HIP if a launch fails.
+ */
+
+/*
+ * The activations, and their slopes in the backward calls: none; max(z, 0)
+ * (slope 0 at 0); z Phi(z) with the exact normal distribution function
+ * (FC_ACT_GELU) or with its tanh form (FC_ACT_GELU_TANH); z / (1 + exp(-z)).
+ */
+typedef FC_INT_ENUM { FC_ACT_NONE = 0, FC_ACT_RELU = 1, FC_ACT_GELU = 2, FC_ACT_GELU_TANH = 3, FC_ACT_SILU = 4 } fc_act;
+
+/*
+ * Z = X . W + bias (bias added to every row), Y = act(Z) + R.
+ * bias (bf16, N values), R (bf16, M x N) and Z (bf16, M x N, an output: what
+ * the backward pass needs) may each be NULL. Y: bf16 or fp32. Y is computed
+ * from the fp32 Z, not from the rounded one.
+ */
+fc_status fc_fwd_act(const void* X, fc_order x_order, const void* W, fc_order w_order, const void* bias,
+                     const void* R, fc_act act, void* Z, void* Y, fc_out_dtype y_dtype, int64_t M, int64_t K,
+                     int64_t N, void* ws, int64_t ws_bytes, void* stream);
+int64_t fc_fwd_act_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order x_order, fc_order w_order, int aligned);
+
+/*
+ * dX[M x K] = (dY[M x N] . W[K x N]^T) * act'(Z), elementwise with Z (bf16,
+ * M x K): the gradient through this layer and through the activation of the
+ * one below, whose fc_fwd_act left Z. dX: bf16 or fp32. db (fp32, K values, or
+ * NULL): the sums of dX's columns before rounding, the gradient of the bias
+ * below.
+ */
+fc_status fc_bwd_data_act(const void* dY, const void* W, fc_order w_order, const void* Z, fc_act act, void* dX,
+                          fc_out_dtype dx_dtype, float* db, int64_t M, int64_t K, int64_t N, void* ws,
+                          int64_t ws_bytes, void* stream);
+int64_t fc_bwd_data_act_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned);
+
+/*
+ * dZ[M x N] = dY * act'(Z) elementwise, and db (fp32, N values) the sums of
+ * its columns before rounding: the first step back through one fc_fwd_act
+ * (the gradient of R is dY itself). dZ or db may be NULL, not both; Z may be
+ * NULL with FC_ACT_NONE. No workspace is needed without db.
+ */
+fc_status fc_bwd_act(const void* dY, const void* Z, fc_act act, void* dZ, float* db, int64_t M, int64_t N, void* ws,
+                     int64_t ws_bytes, void* stream);
+int64_t fc_bwd_act_ws_bytes(int64_t M, int64_t N);
+
+/*
+ * Softmax cross entropy of the vocabulary projection z = X . W, X: M x K
+ * row-major, W: K x N, whose logits z are never stored. W is the vocabulary's
+ * columns vocab_start .. vocab_start + N - 1: all of it, or one GPU's shard.
+ * For each row i:
+ *   lse[i]    = log sum_j exp(z_ij) over the columns given here
+ *   tlogit[i] = z_ij at j = targets[i] - vocab_start; 0 if that column is not
+ *               here or targets[i] = ignore_index
+ *   loss[i]   = lse[i] - tlogit[i]; 0 if targets[i] = ignore_index
+ * (all fp32, M values; loss may be NULL). With a sharded vocabulary the loss
+ * is the logarithm of the summed exponentials of the shards' lse, less their
+ * summed tlogit.
+ */
+fc_status fc_xent_fwd(const void* X, const void* W, fc_order w_order, const int64_t* targets, int64_t vocab_start,
+                      int64_t ignore_index, float* lse, float* tlogit, float* loss, int64_t M, int64_t K, int64_t N,
+                      void* ws, int64_t ws_bytes, void* stream);
+int64_t fc_xent_fwd_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned);
+
+/*
+ * Its gradient. With the rows' weights grad[i] (fp32: the gradient of each
+ * row's loss) and lse[i] (over the whole vocabulary, if it is sharded),
+ *   D_ij = grad[i] (exp(z_ij - lse[i]) - [j = targets[i] - vocab_start]),
+ * rows of zeros where targets[i] = ignore_index;
+ *   dX = D . W^T (M x K, bf16 or fp32; a shard's share of the sum)
+ *   dW = X^T . D (K x N row-major, any output type)
+ * The logits are computed again, a piece of the vocabulary at a time; a
+ * piece's D is rounded to bf16 for the two products, as every gradient
+ * between this library's products is. The workspace holds one piece.
+ */
+fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int64_t* targets, int64_t vocab_start,
+                      int64_t ignore_index, const float* lse, const float* grad, void* dX, fc_out_dtype dx_dtype,
+                      void* dW, fc_out_dtype dw_dtype, int64_t M, int64_t K, int64_t N, void* ws, int64_t ws_bytes,
+                      void* stream);
+int64_t fc_xent_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned);
+
+/*
+ * The three products of an expert layer. X (T x K) and dY (T x N), row-major,
+ * hold rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 belong to
+ * expert e, e < E (at most 2^20). offsets: E + 1 non-decreasing values within
+ * 0 .. T on the device; the host never reads them, experts may be without
+ * rows. W and dW hold E matrices one after the other, each K x N in w_order
+ * (dW: row-major).
+ *   fc_grouped_fwd         Y  = X . W[e]      rows of Y (T x N)
+ *   fc_grouped_bwd_data    dX = dY . W[e]^T   rows of dX (T x K)
+ *   fc_grouped_bwd_weight  dW[e] = X^T . dY   over expert e's rows; zeros for
+ *                                             an expert without any
+ * Y and dX: bf16 or fp32; rows before offsets[0] and from offsets[E] on are
+ * left as they were. dW: any output type. Offsets outside 0 .. T or
+ * decreasing are clamped, so that nothing outside the operands is read or
+ * written, but the results of such a call are unspecified.
+ */
+fc_status fc_grouped_fwd(const void* X, const void* W, fc_order w_order, const int64_t* offsets, void* Y,
+                         fc_out_dtype y_dtype, int64_t T, int64_t E, int64_t K, int64_t N, void* ws,
+                         int64_t ws_bytes, void* stream);
+fc_status fc_grouped_bwd_data(const void* dY, const void* W, fc_order w_order, const int64_t* offsets, void* dX,
+                              fc_out_dtype dx_dtype, int64_t T, int64_t E, int64_t K, int64_t N, void* ws,
+                              int64_t ws_bytes, void* stream);
+fc_status fc_grouped_bwd_weight(const void* X, const void* dY, const int64_t* offsets, void* dW,
+                                fc_out_dtype dw_dtype, int64_t T, int64_t E, int64_t K, int64_t N, void* ws,
+                                int64_t ws_bytes, void* stream);
+/* op: FC_OP_FWD, FC_OP_BWD_DATA or FC_OP_BWD_WEIGHT (which does not read w_order) */
+int64_t fc_grouped_ws_bytes(fc_op op, int64_t T, int64_t E, int64_t K, int64_t N, fc_order w_order, int aligned);
+
 /* static text for a status; never NULL */
 const char* fc_status_str(fc_status status);
 

@@ -8,6 +8,11 @@ computed by hand-written gfx950 MFMA kernels behind a C ABI
 (csrc/), their build script and the thin ctypes binding.
 """
 from .fcshard import (  # noqa: F401
+    ACT_GELU,
+    ACT_GELU_TANH,
+    ACT_NONE,
+    ACT_RELU,
+    ACT_SILU,
     COL,
     OP_BWD_DATA,
     OP_BWD_WEIGHT,
@@ -16,9 +21,15 @@ from .fcshard import (  # noqa: F401
     OUT_F32,
     ROW,
     FcError,
+    fc_bwd_act,
     fc_bwd_data,
+    fc_bwd_data_act,
     fc_bwd_weight,
     fc_fwd,
+    fc_fwd_act,
+    fc_grouped_bwd_data,
+    fc_grouped_bwd_weight,
+    fc_grouped_fwd,
     fc_plan_count,
     fc_plan_describe,
     fc_plans_load,
@@ -26,5 +37,7 @@ from .fcshard import (  # noqa: F401
     fc_release,
     fc_set_plan,
     fc_tune,
+    fc_xent_bwd,
+    fc_xent_fwd,
     status_str,
 )

@@ -30,6 +30,7 @@
 
 #include "fcshard.h"
 #include "fcshard_internal.h"
+#include "fused_internal.h"
 
 namespace fcs {
 namespace {
@@ -800,6 +801,13 @@ float median_of(std::vector<float> v) {
 }
 
 }  // namespace
+
+fc_status current_device_status() {
+    std::lock_guard<std::mutex> lk(g_mu);
+    int dev;
+    return check_device(&dev);
+}
+
 }  // namespace fcs
 
 using namespace fcs;

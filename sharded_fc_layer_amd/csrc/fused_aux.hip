@@ -1,0 +1,242 @@
+// Bandwidth-bound kernels around the fused products (gfx950): padded copies
+// of operands whose rows do not start on 16-byte boundaries, the sums of
+// column-sum partials, the epilogue of a split reduction, the elementwise
+// activation gradient, and the reduction of the cross entropy's partials.
+#include <algorithm>
+
+#include "fused_common.h"
+
+namespace fcs {
+namespace {
+
+// dst row r = src row r, then zeros up to ld; 8 values per thread and step.
+// Source rows start anywhere: a thread's 8 values are read one by one (a
+// wave's reads still fall into the same lines).
+__global__ __launch_bounds__(256) void pad_any_kernel(const uint16_t* __restrict__ src, uint16_t* __restrict__ dst,
+                                                      int64_t rows, int64_t cols, int64_t ld) {
+    const int64_t per_row = ld / 8, total = rows * per_row;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t r = i / per_row, c = (i - r * per_row) * 8;
+        const uint16_t* p = src + r * cols + c;
+        u16x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? p[e] : (uint16_t)0;
+        *reinterpret_cast<u16x8*>(dst + r * ld + c) = v;
+    }
+}
+
+// Column sums of partials, 64 columns per block, 16 partial rows at a time:
+// thread (r, c) sums rows r, r + 16, ..., then row 0 sums the 16 in order.
+__global__ __launch_bounds__(1024) void colsum_parts_kernel(const float* __restrict__ part, float* __restrict__ out,
+                                                            int64_t N, int parts) {
+    __shared__ float s[16][64];
+    const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
+    const int64_t n = (int64_t)blockIdx.x * 64 + c;
+    float v = 0.0f;
+    if (n < N)
+        for (int p = r; p < parts; p += 16) v += part[(int64_t)p * N + n];
+    s[r][c] = v;
+    __syncthreads();
+    if (r == 0 && n < N) {
+        float sum = s[0][c];
+#pragma unroll
+        for (int q = 1; q < 16; ++q) sum += s[q][c];
+        out[n] = sum;
+    }
+}
+
+// Sum of a split reduction's planes in order, and the epilogue. A block takes
+// 256 columns (4 per lane) of kSplitRows rows, each wave every fourth row;
+// EPI_DACT's column sums leave one partial row per block of rows.
+constexpr int kSplitRows = 16;
+template <EpiMode MODE>
+__global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const float* __restrict__ planes, int splits) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t nb = (g.N + 255) / 256;
+    const int64_t bm = blockIdx.x / nb, n = (blockIdx.x % nb) * 256 + lane * 4;
+    const bool vec = g.vec_out != 0;
+    [[maybe_unused]] __shared__ float cs_all[4][256];
+    [[maybe_unused]] float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (MODE == EPI_ACT && g.bias && n < g.N) load4(g.bias + n, n, g.N, false, b);
+    const bool pvec = g.N % 4 == 0;
+    if (n < g.N)
+        for (int64_t m = bm * kSplitRows + wave; m < g.M && m < (bm + 1) * kSplitRows; m += 4) {
+            const int64_t at = m * g.ldc + n;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int s = 0; s < splits; ++s) {
+                const float* p = planes + ((int64_t)s * g.M + m) * g.N + n;
+                if (pvec) {
+                    const f32x4 w = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] += w[q];
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (n + q < g.N) v[q] += p[q];
+                }
+            }
+            if constexpr (MODE == EPI_ACT) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += b[q];
+                if (g.Z) store4_bf16(g.Z + at, n, g.N, vec, v);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = act_value(g.act, v[q]);
+                if (g.R) {
+                    float r[4];
+                    load4(g.R + at, n, g.N, vec, r);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] += r[q];
+                }
+            } else if constexpr (MODE == EPI_DACT) {
+                float z[4];
+                load4(g.Z + at, n, g.N, vec, z);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[q] *= act_slope(g.act, z[q]);
+                    cs[q] += v[q];
+                }
+            }
+            if (g.out_f32)
+                store4_f32(static_cast<float*>(g.C) + at, n, g.N, vec, v, MODE == EPI_STORE && g.accumulate);
+            else
+                store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, vec, v);
+        }
+    if constexpr (MODE == EPI_DACT) {
+        if (g.colpart) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) cs_all[wave][lane * 4 + q] = cs[q];
+            __syncthreads();
+            const int64_t col = (blockIdx.x % nb) * 256 + threadIdx.x;
+            if (col < g.N)
+                g.colpart[bm * g.N + col] = ((cs_all[0][threadIdx.x] + cs_all[1][threadIdx.x]) +
+                                             cs_all[2][threadIdx.x]) + cs_all[3][threadIdx.x];
+        }
+    }
+}
+
+// dZ = dY act'(Z) and its column sums: a block takes 256 columns (4 per
+// lane) of rows p, p + parts, ... (4 at a time, one per wave), and leaves
+// one partial row.
+__global__ __launch_bounds__(256) void act_bwd_kernel(const uint16_t* __restrict__ dY, const uint16_t* __restrict__ Z,
+                                                      int act, uint16_t* __restrict__ dZ, float* __restrict__ part,
+                                                      int64_t M, int64_t N, int parts, bool vec) {
+    __shared__ float cs_all[4][256];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = (int64_t)blockIdx.x * 256 + lane * 4;
+    const int64_t rows = (M + parts - 1) / parts, m0 = blockIdx.y * rows;
+    const int64_t m1 = m0 + rows < M ? m0 + rows : M;
+    float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n < N)
+        for (int64_t m = m0 + wave; m < m1; m += 4) {
+            const int64_t at = m * N + n;
+            float v[4];
+            load4(dY + at, n, N, vec, v);
+            if (Z) {
+                float z[4];
+                load4(Z + at, n, N, vec, z);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] *= act_slope(act, z[q]);
+            }
+            if (dZ) store4_bf16(dZ + at, n, N, vec, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) cs[q] += v[q];
+        }
+    if (!part) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) cs_all[wave][lane * 4 + q] = cs[q];
+    __syncthreads();
+    const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (col < N)
+        part[(int64_t)blockIdx.y * N + col] =
+            ((cs_all[0][threadIdx.x] + cs_all[1][threadIdx.x]) + cs_all[2][threadIdx.x]) + cs_all[3][threadIdx.x];
+}
+
+// Rows' maxima and sums joined over the blocks of columns: 16 rows per block,
+// 64 threads for each, every 64th partial to a thread, joined pairwise over
+// the wave (one wave per row). Infinite maxima count as 0 (see EPI_STATS).
+__global__ __launch_bounds__(1024) void xent_finish_kernel(const float* __restrict__ stat, int parts,
+                                                           const int64_t* __restrict__ targets, int64_t v0,
+                                                           int64_t ignore, int64_t M, int64_t N,
+                                                           float* __restrict__ lse, float* __restrict__ tlogit,
+                                                           float* __restrict__ loss) {
+    // a wave's 64 lanes read 16 neighbouring rows x 4 partials at a time
+    __shared__ float smx[64][17], ssum[64][17];
+    const int row = threadIdx.x & 15, sl = threadIdx.x >> 4;  // 64 slices of the partials
+    const int64_t m = (int64_t)blockIdx.x * 16 + row;
+    float mx = -INFINITY, sum = 0.0f;
+    if (m < M)
+        for (int p = sl; p < parts; p += 64) {
+            const float x = stat[(int64_t)p * M + m], s = stat[(int64_t)(parts + p) * M + m];
+            const float top = fmaxf(mx, x), ref = __builtin_isinf(top) ? 0.0f : top;
+            const float r0 = __builtin_isinf(mx) ? 0.0f : mx, r1 = __builtin_isinf(x) ? 0.0f : x;
+            // a partial of nothing (maximum -inf, sum 0) adds nothing
+            sum = (sum != 0.0f ? sum * exp_f32(r0 - ref) : 0.0f) + (s != 0.0f ? s * exp_f32(r1 - ref) : 0.0f);
+            mx = top;
+        }
+    smx[sl][row] = mx, ssum[sl][row] = sum;
+    __syncthreads();
+    if (threadIdx.x < 16 && m < M) {
+        for (int q = 1; q < 64; ++q) {
+            const float x = smx[q][row], s = ssum[q][row];
+            const float top = fmaxf(mx, x), ref = __builtin_isinf(top) ? 0.0f : top;
+            const float r0 = __builtin_isinf(mx) ? 0.0f : mx, r1 = __builtin_isinf(x) ? 0.0f : x;
+            sum = (sum != 0.0f ? sum * exp_f32(r0 - ref) : 0.0f) + (s != 0.0f ? s * exp_f32(r1 - ref) : 0.0f);
+            mx = top;
+        }
+        const float ref = __builtin_isinf(mx) ? 0.0f : mx;
+        const float l = ref + logf(sum);
+        const int64_t t = targets[m];
+        const uint64_t at = (uint64_t)t - (uint64_t)v0;
+        const bool counts = t != ignore;
+        const float hit = counts && at < (uint64_t)N ? tlogit[m] : 0.0f;
+        lse[m] = l;
+        tlogit[m] = hit;
+        if (loss) loss[m] = counts ? l - hit : 0.0f;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_pad_any(const uint16_t* src, uint16_t* dst, int64_t rows, int64_t cols, int64_t ld, hipStream_t s) {
+    if (rows <= 0 || ld <= 0) return hipSuccess;
+    if (ld % 8 != 0 || cols > ld || (uintptr_t)dst % 16 != 0) return hipErrorInvalidValue;
+    const int64_t blocks = std::min<int64_t>((rows * (ld / 8) + 255) / 256, 8192);
+    hipLaunchKernelGGL(pad_any_kernel, dim3((unsigned)blocks), dim3(256), 0, s, src, dst, rows, cols, ld);
+    return hipGetLastError();
+}
+
+hipError_t launch_colsum_parts(const float* part, float* out, int64_t N, int parts, hipStream_t s) {
+    hipLaunchKernelGGL(colsum_parts_kernel, dim3((unsigned)((N + 63) / 64)), dim3(1024), 0, s, part, out, N, parts);
+    return hipGetLastError();
+}
+
+int split_epilogue_parts(int64_t M) { return (int)((M + kSplitRows - 1) / kSplitRows); }
+
+hipError_t launch_split_epilogue(EpiMode mode, const FusedArgs& g, const float* planes, int splits, hipStream_t s) {
+    const int64_t blocks = ((g.N + 255) / 256) * split_epilogue_parts(g.M);
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const auto fn = mode == EPI_ACT    ? split_epilogue_kernel<EPI_ACT>
+                    : mode == EPI_DACT ? split_epilogue_kernel<EPI_DACT>
+                                       : split_epilogue_kernel<EPI_STORE>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(256), 0, s, g, planes, splits);
+    return hipGetLastError();
+}
+
+hipError_t launch_act_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16_t* dZ, float* part, int64_t M,
+                          int64_t N, int parts, hipStream_t s) {
+    if (parts < 1 || parts > 65535) return hipErrorInvalidValue;
+    const bool vec = N % 4 == 0 && (uintptr_t)dY % 8 == 0 && (uintptr_t)Z % 8 == 0 && (uintptr_t)dZ % 8 == 0;
+    hipLaunchKernelGGL(act_bwd_kernel, dim3((unsigned)((N + 255) / 256), (unsigned)parts), dim3(256), 0, s, dY, Z,
+                       act, dZ, part, M, N, parts, vec);
+    return hipGetLastError();
+}
+
+hipError_t launch_xent_finish(const float* stat, int parts, const int64_t* targets, int64_t v0, int64_t ignore,
+                              int64_t M, int64_t N, float* lse, float* tlogit, float* loss, hipStream_t s) {
+    hipLaunchKernelGGL(xent_finish_kernel, dim3((unsigned)((M + 15) / 16)), dim3(1024), 0, s, stat, parts, targets, v0,
+                       ignore, M, N, lse, tlogit, loss);
+    return hipGetLastError();
+}
+
+}  // namespace fcs

@@ -1,0 +1,85 @@
+// The general fused kernel's plain and activation instances, and its launch
+// (see fused_gemm_impl.h).
+#include <algorithm>
+
+#include "fused_gemm_impl.h"
+
+namespace fcs {
+
+const FusedTile kFusedTiles[kNumFusedTiles] = {{128, 128, 2, 2}, {32, 128, 1, 4}};
+
+// Explicit instantiations (the host pass emits a launch stub for each).
+#define FCF_I(MODE, GRP, AOC, BOC) \
+    template __global__ void fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC>(FusedArgs);
+#define FCF_I2(MODE, GRP, BOC)      \
+    FCF_I(MODE, GRP, false, BOC)    \
+    template __global__ void fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, false, BOC>(FusedArgs);
+namespace {
+FCF_I2(EPI_STORE, GRP_NONE, false) FCF_I2(EPI_STORE, GRP_NONE, true)
+FCF_I2(EPI_STORE, GRP_ROWS, false) FCF_I2(EPI_STORE, GRP_ROWS, true)
+FCF_I2(EPI_ACT, GRP_NONE, false) FCF_I2(EPI_ACT, GRP_NONE, true)
+FCF_I2(EPI_DACT, GRP_NONE, false) FCF_I2(EPI_DACT, GRP_NONE, true)
+FCF_I(EPI_STORE, GRP_NONE, true, false) FCF_I(EPI_STORE, GRP_NONE, true, true)
+FCF_I(EPI_STORE, GRP_RED, true, true)
+FCF_I(EPI_ACT, GRP_NONE, true, false) FCF_I(EPI_ACT, GRP_NONE, true, true)
+}  // namespace
+#undef FCF_I2
+#undef FCF_I
+
+#define FCF_K(MODE, GRP, T, AOC, BOC) \
+    (T == 0 ? (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC> : (FusedFn)fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, AOC, BOC>)
+
+template <>
+FusedFn fused_kernel<EPI_STORE>(GroupMode grp, int tile, bool a_oc, bool b_oc) {
+    if (grp == GRP_RED) return tile == 0 && a_oc && b_oc ? fused_gemm_kernel<EPI_STORE, GRP_RED, 128, 128, 2, 2, true, true> : nullptr;
+    if (grp == GRP_ROWS) {
+        if (a_oc) return nullptr;
+        return b_oc ? FCF_K(EPI_STORE, GRP_ROWS, tile, false, true) : FCF_K(EPI_STORE, GRP_ROWS, tile, false, false);
+    }
+    if (a_oc) {
+        if (tile != 0) return nullptr;
+        return b_oc ? fused_gemm_kernel<EPI_STORE, GRP_NONE, 128, 128, 2, 2, true, true>
+                    : fused_gemm_kernel<EPI_STORE, GRP_NONE, 128, 128, 2, 2, true, false>;
+    }
+    return b_oc ? FCF_K(EPI_STORE, GRP_NONE, tile, false, true) : FCF_K(EPI_STORE, GRP_NONE, tile, false, false);
+}
+
+template <>
+FusedFn fused_kernel<EPI_ACT>(GroupMode grp, int tile, bool a_oc, bool b_oc) {
+    if (grp != GRP_NONE) return nullptr;
+    if (a_oc) {
+        if (tile != 0) return nullptr;
+        return b_oc ? fused_gemm_kernel<EPI_ACT, GRP_NONE, 128, 128, 2, 2, true, true>
+                    : fused_gemm_kernel<EPI_ACT, GRP_NONE, 128, 128, 2, 2, true, false>;
+    }
+    return b_oc ? FCF_K(EPI_ACT, GRP_NONE, tile, false, true) : FCF_K(EPI_ACT, GRP_NONE, tile, false, false);
+}
+
+template <>
+FusedFn fused_kernel<EPI_DACT>(GroupMode grp, int tile, bool a_oc, bool b_oc) {
+    if (grp != GRP_NONE || a_oc) return nullptr;
+    return b_oc ? FCF_K(EPI_DACT, GRP_NONE, tile, false, true) : FCF_K(EPI_DACT, GRP_NONE, tile, false, false);
+}
+#undef FCF_K
+
+hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc, const FusedArgs& g,
+                        hipStream_t s) {
+    if (tile < 0 || tile >= kNumFusedTiles) return hipErrorInvalidValue;
+    const FusedTile& t = kFusedTiles[tile];
+    const int64_t nbn = (g.N + t.bn - 1) / t.bn;
+    // ragged rows: every group may end with one partly filled tile
+    const int64_t nbm = grp == GRP_ROWS ? g.T / t.bm + std::min<int64_t>(g.E, g.T) : (g.M + t.bm - 1) / t.bm;
+    const int64_t blocks = nbm * nbn * (grp == GRP_RED ? g.E : grp == GRP_NONE ? g.splits : 1);
+    if (blocks <= 0) return hipSuccess;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const FusedFn fn = mode == EPI_STORE  ? fused_kernel<EPI_STORE>(grp, tile, a_oc, b_oc)
+                       : mode == EPI_ACT  ? fused_kernel<EPI_ACT>(grp, tile, a_oc, b_oc)
+                       : mode == EPI_DACT ? fused_kernel<EPI_DACT>(grp, tile, a_oc, b_oc)
+                       : mode == EPI_STATS ? fused_kernel<EPI_STATS>(grp, tile, a_oc, b_oc)
+                                           : fused_kernel<EPI_DLOGIT>(grp, tile, a_oc, b_oc);
+    if (!fn) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, g);
+    return hipGetLastError();
+}
+
+}  // namespace fcs

@@ -1,0 +1,163 @@
+// The general kernel of the fused operators: one tile of a product and its
+// epilogue. Built per epilogue in fused_gemm.hip and fused_gemm_xent.hip.
+//
+// Structure (256 threads = 4 wave64s, block tile BM x BN, 32-value reduction
+// stages in a ring of 4 LDS slots): global data goes straight into LDS with
+// 16 bytes per lane, chunks past the tile's rows or the end of the reduction
+// read zeros through an out-of-range offset; stage t + 4 is requested as soon
+// as every wave has read stage t. Layouts, swizzles and operand reads are
+// those of gemm_common.h. Each stage's buffer descriptor starts at that
+// stage's first row or column, so operands may be of any size. A reduction
+// length may differ from block to block (ragged groups) and may be zero.
+#pragma once
+
+#include "fused_common.h"
+
+namespace fcs {
+namespace {
+
+// Loads of one operand tile of R rows (output index) x 32 reduction values,
+// shared by the 4 waves in instructions of 64 chunks of 16 bytes. A tile of
+// 32 rows has two of them, which waves 2 and 3 repeat (the same bytes into
+// the same place), so that every wave counts the same loads.
+template <int R, bool OC>
+struct StageLoads {
+    static constexpr int kAll = R / 16, kInstr = kAll >= 4 ? kAll / 4 : 1;
+    static_assert(!OC || R == 128, "output-contiguous tiles have 128 rows");
+    uint32_t base[kInstr];  // byte offset within a stage, or kOOB
+    int kk[kInstr];         // reduction index of the chunk within a stage
+    static constexpr __device__ int slot(int wave, int j) { return (wave * kInstr + j) % kAll; }
+
+    __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t rows) {
+#pragma unroll
+        for (int j = 0; j < kInstr; ++j) {
+            if (!OC) {
+                const int i = slot(wave, j) * 16 + (lane >> 2);
+                const int c = (lane & 3) ^ ((lane >> 4) & 3);
+                kk[j] = 8 * c;
+                base[j] = i < rows ? (uint32_t)((i * ld + 8 * c) * 2) : kOOB;
+            } else {
+                constexpr int CPR = R / 8, RPI = 64 / CPR;
+                const int k = slot(wave, j) * RPI + lane / CPR;
+                const int c = (lane % CPR) ^ oc_swizzle(k);
+                kk[j] = k;
+                base[j] = 8 * c < rows ? (uint32_t)((k * ld + 8 * c) * 2) : kOOB;
+            }
+        }
+    }
+
+    // `p`: the tile's first row at the stage's first reduction value; `left`:
+    // reduction values from there to the end (none: every chunk reads zeros,
+    // and nothing is read at p)
+    __device__ __forceinline__ void issue(const uint16_t* p, char* region, int left, int wave) const {
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7FFFFFFF, kRsrcWord3);
+#pragma unroll
+        for (int j = 0; j < kInstr; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(region + slot(wave, j) * 1024), 16,
+                                                     kk[j] < left ? base[j] : kOOB, 0, 0, 0);
+    }
+};
+
+template <EpiMode MODE, GroupMode GRP, int BM, int BN, int WR, int WC, bool A_OC, bool B_OC>
+__global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
+    static_assert(WR * WC == 4, "four waves");
+    constexpr int WTM = BM / WR, WTN = BN / WC, TM = WTM / 32, TN = WTN / 32;
+    constexpr int kABytes = BM * kBK * 2, kStageBytes = (BM + BN) * kBK * 2;
+    typedef StageLoads<BM, A_OC> LoadA;
+    typedef StageLoads<BN, B_OC> LoadB;
+    constexpr int L = LoadA::kInstr + LoadB::kInstr;
+    __shared__ __attribute__((aligned(1024))) char smem[kStages * kStageBytes];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave_m = wave / WC, wave_n = wave % WC;
+    const int wm0 = wave_m * WTM, wn0 = wave_n * WTN;
+
+    const TilePos t = tile_position<BM, BN, GRP>(g);
+    if (!t.any) return;  // the whole block: no wave waits for another yet
+    const int nkt = (int)((t.kend - t.kbeg + kBK - 1) / kBK);
+
+    // the tile's first row (column) of each operand at reduction value 0
+    const int64_t a0 = t.row0 + t.m0;
+    const uint16_t* pa = g.A + (A_OC ? a0 : a0 * g.lda);
+    const uint16_t* pb = g.B + (GRP == GRP_ROWS ? (int64_t)t.e * g.b_stride : 0) + (B_OC ? t.n0 : t.n0 * g.ldb);
+    const int64_t sa = A_OC ? g.lda : 1, sb = B_OC ? g.ldb : 1;
+    LoadA da;
+    LoadB db;
+    da.init(wave, lane, g.lda, t.M - t.m0);
+    db.init(wave, lane, g.ldb, g.N - t.n0);
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    if (nkt > 0) {
+        const int len = (int)(t.kend - t.kbeg);
+        pa += t.kbeg * sa, pb += t.kbeg * sb;
+        // stages past the end of the reduction read zeros everywhere, so every
+        // iteration issues and waits for the same number of loads
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) {
+            char* st = smem + s * kStageBytes;
+            da.issue(pa + s * kBK * sa, st, len - s * kBK, wave);
+            db.issue(pb + s * kBK * sb, st + kABytes, len - s * kBK, wave);
+        }
+        waitcnt<(kStages - 1) * L, 0>();
+        __builtin_amdgcn_s_barrier();
+
+        bf16x8 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa0[i] = fragment<BM, A_OC>(smem, wm0 + i * 32, 0, lane);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb0[j] = fragment<BN, B_OC>(smem + kABytes, wn0 + j * 32, 0, lane);
+
+        const uint16_t* na = pa + kStages * kBK * sa;
+        const uint16_t* nb = pb + kStages * kBK * sb;
+        for (int k = 0; k < nkt; ++k) {
+            char* st = smem + (k % kStages) * kStageBytes;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa1[i] = fragment<BM, A_OC>(st, wm0 + i * 32, 1, lane);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb1[j] = fragment<BN, B_OC>(st + kABytes, wn0 + j * 32, 1, lane);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb0[j], fa0[i], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            // this wave has read all of stage k; stage k + 1 must have landed
+            waitcnt<(kStages - 2) * L, 0>();
+            __builtin_amdgcn_s_barrier();
+            const char* nx = smem + ((k + 1) % kStages) * kStageBytes;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa0[i] = fragment<BM, A_OC>(nx, wm0 + i * 32, 0, lane);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb0[j] = fragment<BN, B_OC>(nx + kABytes, wn0 + j * 32, 0, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            // the loads of stage k + 4 go into stage k's slot
+            const int left = len - (k + kStages) * kBK;
+            da.issue(na, st, left, wave);
+            db.issue(nb, st + kABytes, left, wave);
+            na += kBK * sa, nb += kBK * sb;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb1[j], fa1[i], acc[i][j], 0, 0, 0);
+        }
+        waitcnt<0, 0>();  // drain the trailing loads
+    }
+    fused_store<MODE, GRP, 32, TM, TN, WR, WC>(g, t, wave_m, wave_n, lane, acc);
+}
+
+
+
+}  // namespace
+
+}  // namespace fcs

@@ -1,0 +1,101 @@
+// Internal interface between the fused operators' C ABI (fused_api.hip) and
+// their gfx950 kernels. Not installed, not part of the ABI.
+#pragma once
+
+#include "fcshard.h"
+#include "fcshard_internal.h"
+
+namespace fcs {
+
+// FC_OK when the current device is a gfx950 (defined in fcshard_api.hip).
+fc_status current_device_status();
+
+// What a product does with its fp32 results.
+enum EpiMode : int {
+    EPI_STORE = 0,  // C = v, or C += v (fp32), or a split slice's partial plane
+    EPI_ACT = 1,    // z = v + bias; Z = z; C = act(z) + R
+    EPI_DACT = 2,   // C = v * act'(Z); column sums of C per block of rows
+    EPI_STATS = 3,  // per row and block of columns: maximum and sum of exponentials; the target's value
+    EPI_DLOGIT = 4, // C = w (exp(v - lse) - [column = target])
+    kNumEpiModes = 5
+};
+
+// Which rows a product's tiles cover.
+enum GroupMode : int {
+    GRP_NONE = 0,  // one product
+    GRP_ROWS = 1,  // rows offsets[e] .. offsets[e + 1] - 1 of A and C take matrix e of B
+    GRP_RED = 2,   // C matrix e reduces over rows offsets[e] .. offsets[e + 1] - 1 of A and B
+};
+
+// One product with its epilogue, in kernel terms (see GemmArgs). Only the
+// fields of the launch's modes are read.
+struct FusedArgs : GemmArgs {
+    int out_f32 = 0;      // C is fp32 (else bf16)
+    int vec_out = 0;      // rows of C (and R, Z) start on 16-byte boundaries: 4-column vectors
+    int act = 0;          // fc_act
+    const uint16_t* bias = nullptr;  // N values, or none
+    const uint16_t* R = nullptr;     // M x N, or none
+    uint16_t* Z = nullptr;           // EPI_ACT: written, or none; EPI_DACT: read
+    float* colpart = nullptr;        // EPI_DACT: column sums, one row of N per block of rows, or none
+    const int64_t* targets = nullptr;
+    int64_t v0 = 0;       // vocabulary index of column 0
+    int64_t ignore = 0;   // target of a row that takes no part
+    const float* lse = nullptr;
+    const float* gw = nullptr;       // EPI_DLOGIT: the rows' weights
+    float* stat = nullptr;           // EPI_STATS: [block of columns][M] maxima, then as many sums
+    float* tlogit = nullptr;
+    const int64_t* offsets = nullptr;  // E + 1 values on the device
+    int E = 1;
+    int64_t T = 0;        // rows that offsets may reach
+    int64_t b_stride = 0, c_stride = 0;  // elements between the groups' matrices of B (GRP_ROWS), of C (GRP_RED)
+};
+
+// General kernel (fused_gemm.hip): block tiles kFusedTiles[tile], any M, N and
+// K >= 0 with rows of both operands on 16-byte boundaries (lda, ldb multiples
+// of 8, aligned bases); a reduction-contiguous operand has zeros from K to
+// the next multiple of 8.
+struct FusedTile {
+    int bm, bn, wave_rows, wave_cols;  // the 4 waves' grid within the tile
+};
+constexpr int kNumFusedTiles = 2;
+extern const FusedTile kFusedTiles[kNumFusedTiles];
+typedef void (*FusedFn)(FusedArgs);
+// The kernels of one epilogue (fused_gemm.hip, fused_gemm_xent.hip); nullptr
+// for a combination that no operator uses.
+template <EpiMode MODE>
+FusedFn fused_kernel(GroupMode grp, int tile, bool a_oc, bool b_oc);
+template <>
+FusedFn fused_kernel<EPI_STORE>(GroupMode grp, int tile, bool a_oc, bool b_oc);
+template <>
+FusedFn fused_kernel<EPI_ACT>(GroupMode grp, int tile, bool a_oc, bool b_oc);
+template <>
+FusedFn fused_kernel<EPI_DACT>(GroupMode grp, int tile, bool a_oc, bool b_oc);
+template <>
+FusedFn fused_kernel<EPI_STATS>(GroupMode grp, int tile, bool a_oc, bool b_oc);
+template <>
+FusedFn fused_kernel<EPI_DLOGIT>(GroupMode grp, int tile, bool a_oc, bool b_oc);
+hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc, const FusedArgs& g,
+                        hipStream_t s);
+
+// dst (rows x ld) = src (rows x cols) with zeros in columns cols .. ld - 1;
+// any cols and src alignment; ld a multiple of 8, dst 16-byte aligned.
+hipError_t launch_pad_any(const uint16_t* src, uint16_t* dst, int64_t rows, int64_t cols, int64_t ld, hipStream_t s);
+
+// out[j] = sum over p < parts of part[p * N + j], in that order
+hipError_t launch_colsum_parts(const float* part, float* out, int64_t N, int parts, hipStream_t s);
+
+// The epilogue of a split reduction: v = sum of the slices' planes in order,
+// then EPI_STORE, EPI_ACT or EPI_DACT as g says (g.C rows of g.ldc = g.N).
+hipError_t launch_split_epilogue(EpiMode mode, const FusedArgs& g, const float* planes, int splits, hipStream_t s);
+// rows of its column-sum partials (EPI_DACT)
+int split_epilogue_parts(int64_t M);
+
+// dZ = dY * act'(Z) (dZ and Z may be none) and the column sums of the products
+hipError_t launch_act_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16_t* dZ, float* part, int64_t M,
+                          int64_t N, int parts, hipStream_t s);
+
+// lse, target value and loss of every row from EPI_STATS' partials
+hipError_t launch_xent_finish(const float* stat, int parts, const int64_t* targets, int64_t v0, int64_t ignore,
+                              int64_t M, int64_t N, float* lse, float* tlogit, float* loss, hipStream_t s);
+
+}  // namespace fcs

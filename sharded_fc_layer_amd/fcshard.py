@@ -23,6 +23,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "fcshard.h")
 ROW, COL = 0, 1                # fc_order
 OUT_BF16, OUT_F32, OUT_F32_ACC = 0, 1, 2  # fc_out_dtype (OUT_F32_ACC: fp32 out += product)
 OP_FWD, OP_BWD_DATA, OP_BWD_WEIGHT = 0, 1, 2  # fc_op
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4  # fc_act
 FC_OK, FC_E_INVALID, FC_E_UNSUPPORTED, FC_E_HIP, FC_E_NOMEM, FC_E_TOO_LARGE = 0, 1, 2, 3, 4, 5
 
 _lib = None
@@ -78,6 +79,25 @@ def lib() -> ctypes.CDLL:
         L.fc_mfma_probe_launch.argtypes = [i64, ci, vp, vp]
         L.fc_stamped_call.argtypes = [ci, vp, ci, vp, ci, vp, ci, i64, i64, i64, vp, i64,
                                       ctypes.POINTER(i64), vp]
+        L.fc_fwd_act.argtypes = [vp, ci, vp, ci, vp, vp, ci, vp, vp, ci, i64, i64, i64, vp, i64, vp]
+        L.fc_bwd_data_act.argtypes = [vp, vp, ci, vp, ci, vp, ci, vp, i64, i64, i64, vp, i64, vp]
+        L.fc_bwd_act.argtypes = [vp, vp, ci, vp, vp, i64, i64, vp, i64, vp]
+        L.fc_xent_fwd.argtypes = [vp, vp, ci, vp, i64, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+        L.fc_xent_bwd.argtypes = [vp, vp, ci, vp, i64, i64, vp, vp, vp, ci, vp, ci, i64, i64, i64, vp, i64, vp]
+        L.fc_grouped_fwd.argtypes = [vp, vp, ci, vp, vp, ci, i64, i64, i64, i64, vp, i64, vp]
+        L.fc_grouped_bwd_data.argtypes = [vp, vp, ci, vp, vp, ci, i64, i64, i64, i64, vp, i64, vp]
+        L.fc_grouped_bwd_weight.argtypes = [vp, vp, vp, vp, ci, i64, i64, i64, i64, vp, i64, vp]
+        L.fc_fwd_act_ws_bytes.argtypes = [i64, i64, i64, ci, ci, ci]
+        L.fc_bwd_act_ws_bytes.argtypes = [i64, i64]
+        L.fc_grouped_ws_bytes.argtypes = [ci, i64, i64, i64, i64, ci, ci]
+        for f in (L.fc_bwd_data_act_ws_bytes, L.fc_xent_fwd_ws_bytes, L.fc_xent_bwd_ws_bytes):
+            f.argtypes = [i64, i64, i64, ci, ci]
+        for f in (L.fc_fwd_act_ws_bytes, L.fc_bwd_data_act_ws_bytes, L.fc_bwd_act_ws_bytes, L.fc_xent_fwd_ws_bytes,
+                  L.fc_xent_bwd_ws_bytes, L.fc_grouped_ws_bytes):
+            f.restype = i64
+        for f in (L.fc_fwd_act, L.fc_bwd_data_act, L.fc_bwd_act, L.fc_xent_fwd, L.fc_xent_bwd, L.fc_grouped_fwd,
+                  L.fc_grouped_bwd_data, L.fc_grouped_bwd_weight):
+            f.restype = ci
         for f in (L.fc_fwd, L.fc_bwd_data, L.fc_bwd_weight, L.fc_bwd_weight_noalloc, L.fc_tune, L.fc_set_plan, L.fc_plan_describe,
                   L.fc_plan_count, L.fc_release, L.fc_plans_save, L.fc_plans_load, L.fc_mfma_probe,
                   L.fc_mfma_probe_launch, L.fc_stamped_call):
@@ -205,6 +225,252 @@ def fc_bwd_weight_noalloc(X, dY, x_order: int = ROW, out=None, out_dtype: int = 
     _check(lib().fc_bwd_weight_noalloc(X.data_ptr(), x_order, dY.data_ptr(), dW.data_ptr(), out_dtype, M, K, N,
                                        _stream(stream)), "fc_bwd_weight_noalloc")
     return dW
+
+
+# ---- fused operators: activations in the epilogue, the vocabulary's loss, expert layers
+
+def _alloc(shape, dtype, like, stream):
+    """A new tensor, allocated on the stream that the kernels using it run on
+    (None or torch's current stream, or another one: see _out)."""
+    import torch
+    if stream is None or _stream(stream) == torch.cuda.current_stream().cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    ts = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(_stream(stream), device=like.device)
+    with torch.cuda.stream(ts):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _workspace(need: int, what: str, like, stream):
+    """The call's workspace (None if it needs none) and its address. It lives
+    as long as the caller holds it; torch's allocator hands its memory on in
+    the order of the stream that it was allocated on."""
+    import torch
+    if need < 0:
+        raise FcError(FC_E_INVALID, what)
+    if need == 0:
+        return None, None
+    ws = _alloc((need,), torch.uint8, like, stream)
+    return ws, ws.data_ptr()
+
+
+def _tensor(t, dtype, shape, name: str):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise TypeError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA/HIP tensor")
+    return t
+
+
+def _given(t, dtype, shape, name: str, like, stream):
+    """An output: the caller's tensor, checked, or a new one."""
+    return _alloc(shape, dtype, like, stream) if t is None else _tensor(t, dtype, shape, name)
+
+
+def _out_type(out_dtype: int, name: str):
+    import torch
+    if out_dtype not in (OUT_BF16, OUT_F32):
+        raise ValueError(f"{name} must be OUT_BF16 or OUT_F32")
+    return torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
+
+
+def _aligned(*ts) -> int:
+    return int(all(t.data_ptr() % 16 == 0 for t in ts))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _order(order: int, name: str) -> int:
+    if order not in (ROW, COL):
+        raise ValueError(f"{name} must be ROW or COL")
+    return order
+
+
+def fc_fwd_act(X, W, bias=None, act: int = ACT_NONE, residual=None, x_order: int = ROW, w_order: int = ROW,
+               keep_z: bool = False, out=None, out_dtype: int = OUT_BF16, z_out=None, stream=None):
+    """Y = act(X . W + bias) + residual on the GPU; returns Y (M x N), or (Y, Z)
+    with the pre-activation Z (bf16) if keep_z or z_out is given. bias: N bf16
+    values; residual: M x N bf16."""
+    import torch
+    _bf16_2d(X, "X"), _bf16_2d(W, "W"), _order(x_order, "x_order"), _order(w_order, "w_order")
+    M, K = _logical(X, x_order)
+    K2, N = _logical(W, w_order)
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: X is {M}x{K}, W is {K2}x{N}")
+    if bias is not None:
+        _tensor(bias, torch.bfloat16, (N,), "bias")
+    if residual is not None:
+        _tensor(residual, torch.bfloat16, (M, N), "residual")
+    Y = _given(out, _out_type(out_dtype, "out_dtype"), (M, N), "out", X, stream)
+    Z = _given(z_out, torch.bfloat16, (M, N), "z_out", X, stream) if keep_z or z_out is not None else None
+    _one_device(*(t for t in (X, W, bias, residual, Y, Z) if t is not None))
+    al = _aligned(X, W)
+    ws, wp = _workspace(lib().fc_fwd_act_ws_bytes(M, K, N, x_order, w_order, al), "fc_fwd_act", X, stream)
+    _check(lib().fc_fwd_act(X.data_ptr(), x_order, W.data_ptr(), w_order, _ptr(bias), _ptr(residual), act, _ptr(Z),
+                            Y.data_ptr(), out_dtype, M, K, N, wp, 0 if ws is None else ws.numel(), _stream(stream)),
+           "fc_fwd_act")
+    return Y if Z is None else (Y, Z)
+
+
+def fc_bwd_data_act(dY, W, Z, act: int, w_order: int = ROW, bias_grad: bool = False, out=None,
+                    out_dtype: int = OUT_BF16, db=None, stream=None):
+    """dX = (dY . W^T) * act'(Z) on the GPU, Z (M x K, bf16) the pre-activation
+    of the layer below; returns dX (M x K), or (dX, db) with the sums of its
+    columns (fp32, K values: that layer's bias gradient) if bias_grad or db."""
+    import torch
+    _bf16_2d(dY, "dY"), _bf16_2d(W, "W"), _order(w_order, "w_order")
+    M, N = dY.shape
+    K, N2 = _logical(W, w_order)
+    if N2 != N:
+        raise ValueError(f"dY is {M}x{N} but W is {K}x{N2}")
+    _tensor(Z, torch.bfloat16, (M, K), "Z")
+    dX = _given(out, _out_type(out_dtype, "out_dtype"), (M, K), "out", dY, stream)
+    if bias_grad or db is not None:
+        db = _given(db, torch.float32, (K,), "db", dY, stream)
+    _one_device(*(t for t in (dY, W, Z, dX, db) if t is not None))
+    al = _aligned(dY, W)
+    ws, wp = _workspace(lib().fc_bwd_data_act_ws_bytes(M, K, N, w_order, al), "fc_bwd_data_act", dY, stream)
+    _check(lib().fc_bwd_data_act(dY.data_ptr(), W.data_ptr(), w_order, Z.data_ptr(), act, dX.data_ptr(), out_dtype,
+                                 _ptr(db), M, K, N, wp, 0 if ws is None else ws.numel(), _stream(stream)),
+           "fc_bwd_data_act")
+    return dX if db is None else (dX, db)
+
+
+def fc_bwd_act(dY, Z=None, act: int = ACT_NONE, bias_grad: bool = True, keep_dz: bool = True, out=None, db=None,
+               stream=None):
+    """dZ = dY * act'(Z) and db = the sums of its columns (fp32) on the GPU: the
+    first step back through an fc_fwd_act. Returns (dZ, db), None for what was
+    not asked for (keep_dz, bias_grad)."""
+    import torch
+    _bf16_2d(dY, "dY")
+    M, N = dY.shape
+    if Z is not None:
+        _tensor(Z, torch.bfloat16, (M, N), "Z")
+    dZ = _given(out, torch.bfloat16, (M, N), "out", dY, stream) if keep_dz or out is not None else None
+    if bias_grad or db is not None:
+        db = _given(db, torch.float32, (N,), "db", dY, stream)
+    _one_device(*(t for t in (dY, Z, dZ, db) if t is not None))
+    need = lib().fc_bwd_act_ws_bytes(M, N) if db is not None else 0
+    ws, wp = _workspace(need, "fc_bwd_act", dY, stream)
+    _check(lib().fc_bwd_act(dY.data_ptr(), _ptr(Z), act, _ptr(dZ), _ptr(db), M, N, wp,
+                            0 if ws is None else ws.numel(), _stream(stream)), "fc_bwd_act")
+    return dZ, db
+
+
+def _xent_operands(X, W, targets, w_order: int):
+    import torch
+    _bf16_2d(X, "X"), _bf16_2d(W, "W"), _order(w_order, "w_order")
+    M, K = X.shape
+    K2, N = _logical(W, w_order)
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: X is {M}x{K}, W is {K2}x{N}")
+    _tensor(targets, torch.int64, (M,), "targets")
+    return M, K, N
+
+
+def fc_xent_fwd(X, W, targets, w_order: int = ROW, vocab_start: int = 0, ignore_index: int = -100, stream=None):
+    """Cross entropy of the vocabulary projection X . W, without its logits:
+    returns (loss, lse, tlogit), M fp32 values each (see fcshard.h; W may be
+    the shard of a vocabulary that starts at vocab_start)."""
+    import torch
+    M, K, N = _xent_operands(X, W, targets, w_order)
+    loss, lse, tlogit = (_alloc((M,), torch.float32, X, stream) for _ in range(3))
+    _one_device(X, W, targets, loss)
+    ws, wp = _workspace(lib().fc_xent_fwd_ws_bytes(M, K, N, w_order, _aligned(X, W)), "fc_xent_fwd", X, stream)
+    _check(lib().fc_xent_fwd(X.data_ptr(), W.data_ptr(), w_order, targets.data_ptr(), vocab_start, ignore_index,
+                             lse.data_ptr(), tlogit.data_ptr(), loss.data_ptr(), M, K, N, wp,
+                             0 if ws is None else ws.numel(), _stream(stream)), "fc_xent_fwd")
+    return loss, lse, tlogit
+
+
+def fc_xent_bwd(X, W, targets, lse, grad, w_order: int = ROW, vocab_start: int = 0, ignore_index: int = -100,
+                dX=None, dx_dtype: int = OUT_BF16, dW=None, dw_dtype: int = OUT_BF16, stream=None):
+    """Gradients of fc_xent_fwd's loss: grad (fp32, M) weighs the rows, lse is
+    over the whole vocabulary. Returns (dX, dW): M x K, and K x N row-major;
+    dw_dtype = OUT_F32_ACC adds to the given dW."""
+    import torch
+    M, K, N = _xent_operands(X, W, targets, w_order)
+    _tensor(lse, torch.float32, (M,), "lse"), _tensor(grad, torch.float32, (M,), "grad")
+    dX = _given(dX, _out_type(dx_dtype, "dx_dtype"), (M, K), "dX", X, stream)
+    dW = _out(dW, K, N, dw_dtype, X, "dW", stream)
+    _one_device(X, W, targets, lse, grad, dX, dW)
+    ws, wp = _workspace(lib().fc_xent_bwd_ws_bytes(M, K, N, w_order, _aligned(X, W)), "fc_xent_bwd", X, stream)
+    _check(lib().fc_xent_bwd(X.data_ptr(), W.data_ptr(), w_order, targets.data_ptr(), vocab_start, ignore_index,
+                             lse.data_ptr(), grad.data_ptr(), dX.data_ptr(), dx_dtype, dW.data_ptr(), dw_dtype,
+                             M, K, N, wp, 0 if ws is None else ws.numel(), _stream(stream)), "fc_xent_bwd")
+    return dX, dW
+
+
+def _experts(W, w_order: int):
+    import torch
+    if not isinstance(W, torch.Tensor) or W.dtype != torch.bfloat16 or W.dim() != 3:
+        raise TypeError("W must be a 3-D torch.bfloat16 tensor")
+    if not W.is_cuda or not W.is_contiguous():
+        raise ValueError("W must be a contiguous CUDA/HIP tensor")
+    _order(w_order, "w_order")
+    E, r, c = W.shape
+    return (E, r, c) if w_order == ROW else (E, c, r)
+
+
+def _grouped(op: int, fn, P, Q, offsets, out, out_dtype: int, T: int, E: int, K: int, N: int, w_order: int, stream,
+             what: str):
+    import torch
+    _tensor(offsets, torch.int64, (E + 1,), "offsets")
+    _one_device(P, Q, offsets, out)
+    need = lib().fc_grouped_ws_bytes(op, T, E, K, N, w_order, _aligned(P, Q))
+    ws, wp = _workspace(need, what, P, stream)
+    orders = () if op == OP_BWD_WEIGHT else (w_order,)
+    _check(fn(P.data_ptr(), Q.data_ptr(), *orders, offsets.data_ptr(), out.data_ptr(), out_dtype, T, E, K, N, wp,
+              0 if ws is None else ws.numel(), _stream(stream)), what)
+    return out
+
+
+def fc_grouped_fwd(X, W, offsets, w_order: int = ROW, out=None, out_dtype: int = OUT_BF16, stream=None):
+    """Y = X . W[e] for the rows offsets[e] .. offsets[e + 1] - 1 of each expert
+    e: X is T x K, W is E x K x N (COL: E x N x K), offsets E + 1 int64 values
+    on the GPU. Rows outside offsets[0] .. offsets[E] of `out` are left as they were."""
+    _bf16_2d(X, "X")
+    E, K, N = _experts(W, w_order)
+    T, K2 = X.shape
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: X is {T}x{K2}, W is {K}x{N}")
+    Y = _given(out, _out_type(out_dtype, "out_dtype"), (T, N), "out", X, stream)
+    return _grouped(OP_FWD, lib().fc_grouped_fwd, X, W, offsets, Y, out_dtype, T, E, K, N, w_order, stream,
+                    "fc_grouped_fwd")
+
+
+def fc_grouped_bwd_data(dY, W, offsets, w_order: int = ROW, out=None, out_dtype: int = OUT_BF16, stream=None):
+    """dX = dY . W[e]^T for each expert's rows (see fc_grouped_fwd)."""
+    _bf16_2d(dY, "dY")
+    E, K, N = _experts(W, w_order)
+    T, N2 = dY.shape
+    if N2 != N:
+        raise ValueError(f"dY is {T}x{N2} but W is {K}x{N}")
+    dX = _given(out, _out_type(out_dtype, "out_dtype"), (T, K), "out", dY, stream)
+    return _grouped(OP_BWD_DATA, lib().fc_grouped_bwd_data, dY, W, offsets, dX, out_dtype, T, E, K, N, w_order,
+                    stream, "fc_grouped_bwd_data")
+
+
+def fc_grouped_bwd_weight(X, dY, offsets, out=None, out_dtype: int = OUT_BF16, stream=None):
+    """dW[e] = X^T . dY over each expert's rows: E x K x N, zeros for an expert
+    without rows; out_dtype = OUT_F32_ACC adds to the given `out`."""
+    import torch
+    _bf16_2d(X, "X"), _bf16_2d(dY, "dY")
+    T, K = X.shape
+    T2, N = dY.shape
+    if T2 != T:
+        raise ValueError(f"X is {T}x{K} but dY is {T2}x{N}")
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise TypeError("offsets must be a torch.int64 tensor of E + 1 values")
+    E = offsets.shape[0] - 1
+    if out_dtype == OUT_F32_ACC and out is None:
+        raise ValueError("out: accumulating needs the existing output tensor (out=)")
+    dW = _given(out, torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32, (E, K, N), "out", X, stream)
+    return _grouped(OP_BWD_WEIGHT, lib().fc_grouped_bwd_weight, X, dY, offsets, dW, out_dtype, T, E, K, N, ROW,
+                    stream, "fc_grouped_bwd_weight")
 
 
 STAMP_SLOTS = 8  # values per block written by fc_stamped_call

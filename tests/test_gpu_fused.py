@@ -1,0 +1,622 @@
+"""The fused operators on the GPU against plain implementations in 64 bits.
+
+Tolerances are bounds, derived from the arithmetic: u = 2^-24 is the rounding
+of one fp32 operation, h = 2^-8 that of a store to bf16.
+
+* A product of K terms accumulated in fp32: (K + 16) u (|A| |B|)_ij, which
+  holds for every order of summation.
+* An activation: its slope is at most 1.13 in size, so it passes on 1.13
+  times its argument's error, and its own evaluation (an exponential or erf
+  of a few u, a division) errs by at most 2^-20 (1 + |z|).
+* A softmax probability p = exp(z - lse): relative error e_z + 2^-22 (1 +
+  |z - lse|), e_z being the logit's error.
+* Sums of n terms in fp32: (n + 16) u times the sum of the terms' sizes.
+
+Integer inputs, whose products and sums fit fp32, are compared bit for bit.
+"""
+from __future__ import annotations
+
+import sys
+
+import pytest
+
+from sharded_fc_layer_amd import fcshard as F
+
+torch = pytest.importorskip("torch")
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+U, H = 2.0 ** -24, 2.0 ** -8
+ROW, COL = F.ROW, F.COL
+ACT_NAMES = {F.ACT_NONE: "none", F.ACT_RELU: "relu", F.ACT_GELU: "gelu", F.ACT_GELU_TANH: "gelu_tanh",
+             F.ACT_SILU: "silu"}
+ACTS = list(ACT_NAMES)
+
+
+def log(msg):
+    print(msg, file=sys.stderr, flush=True)
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(g, *shape, scale=1.0):
+    return (torch.randn(shape, device="cuda", generator=g) * scale).to(torch.bfloat16)
+
+
+def integers(g, *shape, top=3):
+    return torch.randint(-top, top + 1, shape, device="cuda", generator=g).to(torch.bfloat16)
+
+
+def stored(w, order):
+    """The storage of matrix w (or of each matrix of a stack) in an order."""
+    return w if order == ROW else w.transpose(-1, -2).contiguous()
+
+
+def shifted(t):
+    """The same values at an address that is 2 bytes past a 16-byte boundary."""
+    buf = torch.empty(t.numel() + 8, dtype=t.dtype, device=t.device)
+    out = buf[1:1 + t.numel()].view(t.shape)
+    out.copy_(t)
+    assert out.data_ptr() % 16 == 2
+    return out
+
+
+def within(got, want, tol, what):
+    err = (got.double() - want).abs()
+    ok = err <= tol
+    same = torch.isnan(got) & torch.isnan(want) | (got.double() == want)
+    ratio = torch.where(same, 0.0, err / tol).max().item() if got.numel() else 0.0
+    log(f"  {what}: largest error / bound = {ratio:.3g}")
+    assert bool((ok | same).all()), f"{what}: {int((~(ok | same)).sum())} of {got.numel()} outside the bound"
+
+
+def act64(z, act):
+    f = torch.nn.functional
+    return {F.ACT_NONE: lambda: z, F.ACT_RELU: lambda: f.relu(z), F.ACT_GELU: lambda: f.gelu(z),
+            F.ACT_GELU_TANH: lambda: f.gelu(z, approximate="tanh"), F.ACT_SILU: lambda: f.silu(z)}[act]()
+
+
+def slope64(z, act):
+    z = z.clone().requires_grad_()
+    (s,) = torch.autograd.grad(act64(z, act).sum(), z)
+    return s
+
+
+# from one row to several tiles, odd and aligned, reductions from one value to
+# several slices of a split one
+SHAPES = [(1, 1, 1), (1, 2048, 520), (3, 31, 7), (16, 512, 384), (32, 264, 136), (33, 129, 130), (100, 1001, 77),
+          (128, 64, 128), (130, 72, 259), (257, 520, 300), (300, 40, 1032), (520, 776, 264)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("xo, wo", [(ROW, ROW), (ROW, COL), (COL, ROW), (COL, COL)])
+def test_fwd_act(shape, xo, wo):
+    M, K, N = shape
+    g = gen(M * 7 + K * 3 + N)
+    X, W = normal(g, M, K), normal(g, K, N, scale=K ** -0.5)
+    b, R = normal(g, N), normal(g, M, N)
+    z = X.double() @ W.double() + b.double()
+    ez = (K + 16) * U * (X.double().abs() @ W.double().abs() + b.double().abs())
+    xs, ws = stored(X, xo), stored(W, wo)
+    for act in ACTS:
+        for res, keep, f32 in ((None, False, False), (R, True, True), (R, False, False)):
+            out = F.fc_fwd_act(xs, ws, bias=b, act=act, residual=res, x_order=xo, w_order=wo, keep_z=keep,
+                               out_dtype=F.OUT_F32 if f32 else F.OUT_BF16)
+            Y, Z = out if keep else (out, None)
+            a = act64(z, act)
+            y = a if res is None else a + res.double()
+            tol = 1.13 * ez + 2.0 ** -20 * (1 + z.abs()) + U * y.abs()
+            what = f"{shape} {xo}{wo} {ACT_NAMES[act]}"
+            within(Y, y, tol if f32 else tol + H * (y.abs() + tol), what)
+            if keep:
+                within(Z, z, ez + H * (z.abs() + ez), what + " Z")
+
+
+@pytest.mark.parametrize("shape", SHAPES + [(700, 2050, 513)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_fwd_act_integers_are_exact(shape, wo):
+    M, K, N = shape
+    g = gen(5)
+    X, W, b, R = integers(g, M, K), integers(g, K, N), integers(g, N), integers(g, M, N)
+    want = X.double() @ W.double() + b.double()
+    for act in (F.ACT_NONE, F.ACT_RELU):
+        y = act64(want, act) + R.double()
+        for align in (lambda t: t, shifted):
+            Y, Z = F.fc_fwd_act(align(X), align(stored(W, wo)), bias=align(b), act=act, residual=align(R), w_order=wo,
+                                out_dtype=F.OUT_F32, keep_z=True)
+            assert torch.equal(Y.double(), y), f"{shape} {wo}"
+            assert torch.equal(Z, want.float().to(torch.bfloat16))
+    # neither bias nor residual: the plain product's bits
+    assert torch.equal(F.fc_fwd_act(X, stored(W, wo), w_order=wo), (X.double() @ W.double()).float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_bwd_data_act(shape, wo):
+    M, N, K = shape  # the reduction runs over the layer's outputs N
+    g = gen(M + K * 5 + N * 11)
+    dY, W, Z = normal(g, M, N, scale=1e-3), normal(g, K, N, scale=0.02), normal(g, M, K)
+    up = dY.double() @ W.double().t()
+    e_up = (N + 16) * U * (dY.double().abs() @ W.double().abs().t())
+    for act in ACTS:
+        s = slope64(Z.double(), act)
+        want = up * s
+        tol = 1.13 * e_up + 2.0 ** -20 * up.abs()
+        what = f"{shape} {wo} {ACT_NAMES[act]}"
+        for f32 in (False, True):
+            dX, db = F.fc_bwd_data_act(dY, stored(W, wo), Z, act, w_order=wo, bias_grad=True,
+                                       out_dtype=F.OUT_F32 if f32 else F.OUT_BF16)
+            within(dX, want, tol if f32 else tol + H * (want.abs() + tol), what)
+            within(db, want.sum(0), tol.sum(0) + (M + 16) * U * (want.abs() + tol).sum(0), what + " db")
+        only = F.fc_bwd_data_act(dY, stored(W, wo), Z, act, w_order=wo, out_dtype=F.OUT_F32)
+        assert torch.equal(only, dX)
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (1, 300), (5, 7), (33, 256), (700, 130), (4100, 264), (64, 5000)])
+def test_bwd_act(shape):
+    M, N = shape
+    g = gen(M + N)
+    dY, Z = normal(g, M, N), normal(g, M, N, scale=2.0)
+    for act in ACTS:
+        want = dY.double() * slope64(Z.double(), act)
+        tol = 2.0 ** -20 * dY.double().abs()
+        for align in (lambda t: t, shifted):
+            dZ, db = F.fc_bwd_act(align(dY), align(Z), act)
+            within(dZ, want, tol + H * (want.abs() + tol), f"{shape} {ACT_NAMES[act]}")
+            within(db, want.sum(0), tol.sum(0) + (M + 16) * U * (want.abs() + tol).sum(0), "db")
+    dZ, db = F.fc_bwd_act(dY, keep_dz=False)  # no activation: the bias gradient alone
+    assert dZ is None
+    within(db, dY.double().sum(0), (M + 16) * U * dY.double().abs().sum(0), "db alone")
+    dZ, db = F.fc_bwd_act(dY, Z, F.ACT_SILU, bias_grad=False)
+    assert db is None and dZ.shape == dY.shape
+
+
+def test_slopes_by_differences_and_at_the_ends():
+    """The slopes against central differences of the library's own forward
+    activation, and at values where a formula could overflow or lose itself."""
+    z = torch.linspace(-8, 8, 4097, device="cuda").to(torch.bfloat16)
+    one = torch.ones((1, 1), dtype=torch.bfloat16, device="cuda")
+    h = 2.0 ** -7  # z +- h is exact in the fp32 sum z + bias
+    for act in (F.ACT_GELU, F.ACT_GELU_TANH, F.ACT_SILU):
+        up, down = (F.fc_fwd_act(z[:, None].contiguous(), one, act=act, out_dtype=F.OUT_F32,
+                                 bias=torch.full((1,), d, dtype=torch.bfloat16, device="cuda"))[:, 0].double()
+                    for d in (h, -h))
+        diff = (up - down) / (2 * h)
+        s = F.fc_bwd_data_act(torch.ones((z.numel(), 1), dtype=torch.bfloat16, device="cuda"), one, z[:, None], act,
+                              out_dtype=F.OUT_F32)[:, 0].double()
+        # third derivatives are at most 3: h^2 / 6 of them; the values' errors over 2 h
+        tol = h * h / 2 + 2 * 2.0 ** -20 * (1 + z.double().abs()) / (2 * h) + 2.0 ** -20
+        within(s.float(), diff, tol, f"slope of {ACT_NAMES[act]}")
+    ends = torch.tensor([-float("inf"), -3e38, -1e20, -300.0, -50.0, 50.0, 300.0, 1e20, 3e38, float("inf")],
+                        device="cuda").to(torch.bfloat16)
+    g1 = torch.ones((1, ends.numel()), dtype=torch.bfloat16, device="cuda")
+    for act in (F.ACT_RELU, F.ACT_GELU, F.ACT_GELU_TANH, F.ACT_SILU):
+        dZ, _ = F.fc_bwd_act(g1, ends[None], act)
+        # 0 or 1 but for tails of (1 + |z|) e^-|z| at most, largest at |z| = 50: 51 e^-50 < 1e-20
+        assert bool(((dZ[0].float() - (ends.float() > 0).float()).abs() <= 1e-20).all()), (ACT_NAMES[act], dZ)
+    nan = torch.full((1, 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    for act in (F.ACT_GELU, F.ACT_GELU_TANH, F.ACT_SILU):
+        assert bool(torch.isnan(F.fc_bwd_act(g1[:, :8].contiguous(), nan, act)[0]).all())
+
+
+# ---- cross entropy
+
+XENT = [(1, 8, 1), (1, 64, 1000), (5, 33, 130), (32, 128, 129), (33, 100, 999), (64, 264, 4001), (130, 72, 520),
+        (257, 520, 1032), (300, 65, 2050)]
+
+
+def xent64(X, W, t, v0, ignore, lse=None):
+    """(z, its error bound, hits, counted rows) of the definition."""
+    z = X.double() @ W.double()
+    ez = (X.shape[1] + 16) * U * (X.double().abs() @ W.double().abs())
+    counts = t != ignore
+    at = t - v0
+    here = counts & (at >= 0) & (at < W.shape[1])
+    return z, ez, counts, here, torch.where(here, at, 0)
+
+
+@pytest.mark.parametrize("shape", XENT)
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_xent_fwd(shape, wo):
+    M, K, N = shape
+    g = gen(M + 3 * K + N)
+    X, W = normal(g, M, K), normal(g, K, N, scale=0.3)
+    for v0, whole in ((0, N), (N, 3 * N), (5, N + 5)):
+        t = torch.randint(0, whole, (M,), device="cuda", generator=g)
+        t[::4] = -100
+        if M > 2:
+            t[1] = t[2]  # the same index twice
+        z, ez, counts, here, at = xent64(X, W, t, v0, -100)
+        loss, lse, tl = F.fc_xent_fwd(X, stored(W, wo), t, w_order=wo, vocab_start=v0)
+        want = torch.logsumexp(z, 1)
+        hit = torch.where(here, z.gather(1, at[:, None])[:, 0], 0.0)
+        e_hit = torch.where(here, ez.gather(1, at[:, None])[:, 0], 0.0)
+        # the sum's relative error: its terms' (2^-22 (1 + |z - max|) with |z - max| e^(z - max) <= 1) and N + 16 u
+        e_lse = ez.max(1).values + 2.0 ** -20 + (N + 16) * U + 4 * U * want.abs()
+        within(lse, want, e_lse, f"{shape} {wo} {v0} lse")
+        within(tl, hit, e_hit, "tlogit")
+        within(loss, torch.where(counts, want - hit, 0.0), e_lse + e_hit + U * (want.abs() + hit.abs()), "loss")
+        assert bool((loss[~counts] == 0).all()) and bool((tl[~here] == 0).all())
+
+
+def test_xent_shards_join_to_the_whole():
+    M, K, N = 70, 136, 1000
+    g = gen(8)
+    X, W = normal(g, M, K), normal(g, K, N, scale=0.3)
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    loss, lse, tl = F.fc_xent_fwd(X, W, t)
+    cuts = [0, 8, 301, 640, 1000]
+    parts = [F.fc_xent_fwd(X, W[:, a:b].contiguous(), t, vocab_start=a) for a, b in zip(cuts, cuts[1:])]
+    joined = torch.logsumexp(torch.stack([p[1].double() for p in parts]), 0)
+    within(lse, joined, 2.0 ** -18 * (1 + joined.abs()), "lse")
+    assert torch.allclose(sum(p[2] for p in parts), tl, rtol=1e-6, atol=1e-6)
+
+
+def test_xent_extreme_logits():
+    """Logits at infinity and far apart: what the definition gives, and nothing else is disturbed."""
+    inf = float("inf")
+    K, N = 16, 300
+    X = torch.zeros((6, K), dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros((K, N), dtype=torch.bfloat16, device="cuda")
+    W[0], W[1, :], W[2, 7] = 1.0, -1.0, 1.0
+    W[3] = torch.linspace(-3e4, 3e4, N, device="cuda").to(torch.bfloat16)
+    X[0, 0] = inf      # every logit +inf
+    X[1, 1] = inf      # every logit -inf
+    X[2, 2] = 1000.0   # one far above the others
+    X[3, 3] = 1.0      # spread over 6e4
+    X[4, 0] = float("nan")
+    X[5, 2] = -3e38    # one at the type's lowest value
+    t = torch.full((6,), 7, dtype=torch.int64, device="cuda")
+    # rows with infinities have NaN products with W's zeros: keep those out
+    W[0, :], W[1, :] = 1.0, -1.0
+    X2 = X.clone()
+    z = X2.double() @ W.double()
+    z[0], z[1], z[4] = inf, -inf, float("nan")
+    one = torch.zeros((2, 1), dtype=torch.bfloat16, device="cuda")
+    one[0, 0], one[1, 0] = inf, -inf  # K = 1: no zero times infinity
+    _, lse1, _ = F.fc_xent_fwd(one, torch.ones((1, N), dtype=torch.bfloat16, device="cuda"), t[:2])
+    assert lse1[0].item() == inf and lse1[1].item() == -inf
+    loss, lse, tl = F.fc_xent_fwd(X[2:], W, t[2:])
+    want = torch.logsumexp(z[2:], 1)
+    within(lse, want, 2.0 ** -18 * (1 + want.abs()), "lse")
+    assert torch.isnan(lse[2]) and tl[0].item() == 1000.0
+    dX, dW = F.fc_xent_bwd(X[2:4], W, t[2:4], lse[:2].contiguous(), torch.ones(2, device="cuda"))
+    p = torch.softmax(z[2:4], 1)
+    p[:, 7] -= 1
+    within(dX, p @ W.double().t(), H * 4 * (p.abs() @ W.double().abs().t()) + 1e-30, "dX")
+    # a row that does not count is zero, whatever its logits are
+    t[4] = -100
+    dX, dW = F.fc_xent_bwd(X[2:], W, t[2:], torch.nan_to_num(lse), torch.ones(4, device="cuda"))
+    assert bool((dX[2] == 0).all())
+
+
+@pytest.mark.parametrize("shape", XENT)
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_xent_bwd(shape, wo):
+    M, K, N = shape
+    g = gen(M + 5 * K + N)
+    X, W = normal(g, M, K), normal(g, K, N, scale=0.3)
+    for v0, whole, ignore in ((0, N, -100), (N, 3 * N, -100), (0, N, 0)):
+        t = torch.randint(0, whole, (M,), device="cuda", generator=g)
+        t[::3] = ignore
+        z, ez, counts, here, at = xent64(X, W, t, v0, ignore)
+        lse = (torch.logsumexp(z, 1) + (1.0 if v0 else 0.0)).float()  # a shard's probabilities sum to less than 1
+        w = torch.rand(M, device="cuda", generator=g) - 0.3
+        p = torch.exp(z - lse.double()[:, None])
+        # the fp32 subtraction and exponential: 2^-22 (1 + |z| + |lse|) relative
+        ep = p * torch.expm1(ez + 2.0 ** -22 * (1 + z.abs() + lse.double().abs()[:, None]))
+        hot = torch.zeros_like(p)
+        hot[here, at[here]] = 1.0
+        wc = torch.where(counts, w.double(), 0.0)[:, None]
+        D = wc * (p - hot)
+        eD = wc.abs() * (ep + 2 * U * (p + hot))
+        eD = eD + H * (D.abs() + eD)
+        aX, aW, aD = X.double().abs(), W.double().abs(), D.abs() + eD
+        tx = eD @ aW.t() + (N + 16) * U * (aD @ aW.t()) + 2.0 ** -126
+        tw = aX.t() @ eD + (M + 16) * U * (aX.t() @ aD) + 2.0 ** -126
+        wx, ww = D @ W.double().t(), X.double().t() @ D
+        what = f"{shape} {wo} {v0} {ignore}"
+        dX, dW = F.fc_xent_bwd(X, stored(W, wo), t, lse, w, w_order=wo, vocab_start=v0, ignore_index=ignore)
+        within(dX, wx, tx + H * (wx.abs() + tx), what + " dX")
+        within(dW, ww, tw + H * (ww.abs() + tw), what + " dW")
+        assert bool((dX[~counts] == 0).all())
+        acc = torch.ones((K, N), device="cuda")
+        dX, dW = F.fc_xent_bwd(X, stored(W, wo), t, lse, w, w_order=wo, vocab_start=v0, ignore_index=ignore,
+                               dx_dtype=F.OUT_F32, dW=acc, dw_dtype=F.OUT_F32_ACC)
+        within(dX, wx, tx, what + " dX fp32")
+        within(dW, ww + 1, tw + U * (ww.abs() + tw + 1), what + " dW accumulated")
+
+
+def test_xent_bwd_in_several_pieces():
+    """A vocabulary of more columns than one piece holds (256 MB of the logits' gradient)."""
+    M, K, N = 16500, 40, 17001  # pieces of 7936 columns
+    g = gen(12)
+    X, W = normal(g, M, K), normal(g, K, N, scale=0.3)
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    t[:100] = torch.arange(100, device="cuda") * 170  # targets in every piece
+    for wo in (ROW, COL):
+        loss, lse, _ = F.fc_xent_fwd(X, stored(W, wo), t, w_order=wo)
+        w = torch.full((M,), 1.0 / M, device="cuda")
+        dX, dW = F.fc_xent_bwd(X, stored(W, wo), t, lse, w, w_order=wo)
+        wX = torch.empty((M, K), dtype=torch.float64, device="cuda")
+        wW, tW = (torch.zeros((K, N), dtype=torch.float64, device="cuda") for _ in range(2))
+        tX = torch.empty_like(wX)
+        for r in torch.split(torch.arange(M, device="cuda"), 4096):
+            D = torch.exp(X[r].double() @ W.double() - lse[r].double()[:, None])
+            D[torch.arange(len(r)), t[r]] -= 1
+            D /= M
+            # D errs by its rounding and by 2^-16 of the probability (|z| + |lse| below 40)
+            eD = (H + 2.0 ** -16) * D.abs() + 2.0 ** -16 / M * D.abs().clamp(max=1)
+            wX[r], tX[r] = D @ W.double().t(), eD @ W.double().abs().t()
+            wW += X[r].double().t() @ D
+            tW += X[r].double().abs().t() @ eD
+        tX += (N + 16) * U / H * tX
+        tW += (M + 16) * U / H * tW
+        within(dX, wX, tX + H * (wX.abs() + tX), f"{wo} dX")
+        within(dW, wW, tW + H * (wW.abs() + tW), f"{wo} dW")
+
+
+def test_xent_gradient_by_differences():
+    """Directional differences of the library's own loss."""
+    M, K, N = 40, 64, 500
+    g = gen(31)
+    X, W = normal(g, M, K), normal(g, K, N, scale=0.2)
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    _, lse, _ = F.fc_xent_fwd(X, W, t)
+    dX, dW = F.fc_xent_bwd(X, W, t, lse, torch.ones(M, device="cuda"), dx_dtype=F.OUT_F32, dw_dtype=F.OUT_F32)
+    vX = torch.where(torch.rand((M, K), device="cuda", generator=g) < 0.5, -1.0, 1.0)
+    h = 2.0 ** -3
+
+    def loss_at(x):
+        return F.fc_xent_fwd(x.to(torch.bfloat16), W, t)[0].double().sum().item()
+
+    Xa, Xb = (X.float() + h * vX).to(torch.bfloat16), (X.float() - h * vX).to(torch.bfloat16)
+    # what the rounded steps really were; the mean slope between two points differs from
+    # the middle's by h^2 / 6 of the third derivative, which is at most |v.W|^3 a row
+    step = (Xa.double() - Xb.double())
+    mid = (Xa.double() + Xb.double()) / 2
+    _, lse_m, _ = F.fc_xent_fwd(X, W, t)
+    diff = loss_at(Xa) - loss_at(Xb)
+    z = (mid @ W.double()).requires_grad_()
+    torch.nn.functional.cross_entropy(z, t, reduction="sum").backward()
+    slope = (step * (z.grad @ W.double().t())).sum().item()
+    swing = (step @ W.double()).abs().max(1).values
+    assert abs(diff - slope) <= (swing ** 3).sum().item() / 24 + M * 2.0 ** -18 * 20
+    # and the analytic gradient at X itself is the library's
+    ours = (step * dX.double()).sum().item()
+    z0 = (X.double() @ W.double()).requires_grad_()
+    torch.nn.functional.cross_entropy(z0, t, reduction="sum").backward()
+    ref = z0.grad @ W.double().t()
+    bound = (step.abs() * (2 * H * (z0.grad.abs() @ W.double().abs().t()))).sum().item()
+    assert abs(ours - (step * ref).sum().item()) <= bound
+
+
+# ---- experts
+
+def offsets_of(counts, first=0):
+    return torch.tensor([first] + counts, device="cuda").cumsum(0)
+
+
+GROUPED = [  # rows of each expert, first row, rows behind the last, K, N
+    ([1], 0, 0, 8, 8), ([0, 5, 0], 0, 3, 33, 7), ([3, 0, 130, 1], 2, 9, 64, 136), ([300, 17, 0, 64], 0, 0, 136, 264),
+    ([0, 0, 0], 4, 1, 16, 24), ([1] * 70 + [0] * 30 + [5] * 33, 0, 2, 40, 130), ([260, 255, 257], 1, 0, 520, 100),
+    ([33, 31, 32, 129], 0, 40, 72, 520), ([700], 0, 0, 264, 300), ([40] * 8, 0, 0, 1001, 129)]
+
+
+@pytest.mark.parametrize("case", GROUPED, ids=lambda c: f"{len(c[0])}x{c[3]}x{c[4]}")
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_grouped_integers_are_exact(case, wo):
+    counts, first, behind, K, N = case
+    E, T = len(counts), first + sum(counts) + behind
+    g = gen(T + K + N)
+    X, dY, W = integers(g, T, K), integers(g, T, N), integers(g, E, K, N)
+    off = offsets_of(counts, first)
+    lo = off.tolist()
+    for align in (lambda t: t, shifted):
+        x, d, w = align(X), align(dY), align(stored(W, wo))
+        for dt, od in ((torch.bfloat16, F.OUT_BF16), (torch.float32, F.OUT_F32)):
+            Y = torch.full((T, N), 77.0, dtype=dt, device="cuda")
+            dX = torch.full((T, K), 77.0, dtype=dt, device="cuda")
+            wantY, wantX = Y.double(), dX.double()
+            for e in range(E):
+                s = slice(lo[e], lo[e + 1])
+                wantY[s] = (X[s].double() @ W[e].double()).to(dt).double()
+                wantX[s] = (dY[s].double() @ W[e].double().t()).to(dt).double()
+            assert F.fc_grouped_fwd(x, w, off, w_order=wo, out=Y, out_dtype=od) is Y
+            F.fc_grouped_bwd_data(d, w, off, w_order=wo, out=dX, out_dtype=od)
+            assert torch.equal(Y.double(), wantY) and torch.equal(dX.double(), wantX)
+        wantW = torch.stack([X[a:b].double().t() @ dY[a:b].double() for a, b in zip(lo, lo[1:])])
+        assert torch.equal(F.fc_grouped_bwd_weight(x, d, off, out_dtype=F.OUT_F32).double(), wantW)
+        assert torch.equal(F.fc_grouped_bwd_weight(x, d, off), wantW.float().to(torch.bfloat16))
+        acc = torch.full((E, K, N), 2.0, device="cuda")
+        F.fc_grouped_bwd_weight(x, d, off, out=acc, out_dtype=F.OUT_F32_ACC)
+        assert torch.equal(acc.double(), wantW + 2)
+
+
+@pytest.mark.parametrize("case", [([200, 0, 57, 300], 0, 0, 520, 264), ([3, 1, 0, 9] * 4, 0, 0, 1024, 384)],
+                         ids=["rows", "few"])
+def test_grouped_normal_inputs(case):
+    counts, _, _, K, N = case
+    E, T = len(counts), sum(counts)
+    g = gen(77)
+    X, dY, W = normal(g, T, K), normal(g, T, N, scale=1e-3), normal(g, E, K, N, scale=0.02)
+    off = offsets_of(counts)
+    lo = off.tolist()
+    Y, dX = F.fc_grouped_fwd(X, W, off), F.fc_grouped_bwd_data(dY, W, off)
+    dW = F.fc_grouped_bwd_weight(X, dY, off)
+    for e in range(E):
+        s = slice(lo[e], lo[e + 1])
+        x, d, w = X[s].double(), dY[s].double(), W[e].double()
+        for got, a, b in ((Y[s], x, w), (dX[s], d, w.t()), (dW[e], x.t(), d)):
+            want, tol = a @ b, (a.shape[1] + 16) * U * (a.abs() @ b.abs())
+            within(got, want, tol + H * (want.abs() + tol), f"expert {e}")
+
+
+def test_grouped_bad_offsets_stay_inside():
+    """Offsets outside the rows, or decreasing, are clamped: rows that no
+    expert can name keep their values, and neighbouring memory too."""
+    T, E, K, N = 50, 3, 24, 40
+    g = gen(3)
+    X, W = integers(g, T, K), integers(g, E, K, N)
+    big = torch.full((T + 20, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    Y = big[10:10 + T]
+    for bad in ([-5, 10, 30, 1 << 40], [60, 70, 80, 90], [40, 20, 10, 5], [-(1 << 62), -3, -2, -1]):
+        big.fill_(9.0)
+        off = torch.tensor(bad, device="cuda")
+        F.fc_grouped_fwd(X, W, off, out=Y)
+        torch.cuda.synchronize()
+        assert bool((big[:10] == 9).all()) and bool((big[10 + T:] == 9).all()), bad
+        F.fc_grouped_bwd_weight(X, X, off)
+    torch.cuda.synchronize()
+
+
+# ---- streams, graphs, several calls at once
+
+def _all_calls(seed, M=96, K=200, N=328, E=3):
+    """One call of each operator on inputs of a seed: the calls, by name."""
+    g = gen(seed)
+    X, W, b, R = normal(g, M, K), normal(g, K, N, scale=0.1), normal(g, N), normal(g, M, N)
+    dY, Z = normal(g, M, N), normal(g, M, K)
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    lse, w = torch.full((M,), 6.0, device="cuda"), torch.rand(M, device="cuda", generator=g)
+    We, off = normal(g, E, K, N, scale=0.1), offsets_of([M // 2, 0, M - M // 2])
+    return {
+        "fwd_act": lambda **k: F.fc_fwd_act(X, W, bias=b, act=F.ACT_GELU, residual=R, keep_z=True, **k),
+        "bwd_data_act": lambda **k: F.fc_bwd_data_act(dY, W, Z, F.ACT_SILU, bias_grad=True, **k),
+        "bwd_act": lambda **k: F.fc_bwd_act(dY, R, F.ACT_GELU_TANH, **k),
+        "xent_fwd": lambda **k: F.fc_xent_fwd(X, W, t, **k),
+        "xent_bwd": lambda **k: F.fc_xent_bwd(X, W, t, lse, w, **k),
+        "grouped_fwd": lambda **k: (F.fc_grouped_fwd(X, We, off, **k),),
+        "grouped_bwd_data": lambda **k: (F.fc_grouped_bwd_data(dY, We, off, **k),),
+        "grouped_bwd_weight": lambda **k: (F.fc_grouped_bwd_weight(X, dY, off, **k),),
+    }
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# odd sizes (copies, element stores), few rows (split reductions), and plain ones
+SIZES = [(96, 200, 328), (33, 1001, 131), (3, 2048, 264), (520, 264, 520)]
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_calls_are_deterministic_on_other_streams_and_at_once(size):
+    calls, others = _all_calls(1, *size), _all_calls(2, *size)
+    want = {n: c() for n, c in calls.items()}
+    want2 = {n: c() for n, c in others.items()}
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for n in calls:
+        got = [calls[n](stream=a) if r % 2 == 0 else others[n](stream=b) for r in range(6)]
+        torch.cuda.synchronize()
+        for r, o in enumerate(got):
+            assert same(o, (want, want2)[r % 2][n]), f"{n} round {r}"
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_graph_replays_match_eager(size):
+    """All operators captured into two graphs whose workspaces live on at once,
+    replayed in turn with eager calls between."""
+    sets = [_all_calls(1, *size), _all_calls(2, *size)]
+    want = [{n: c() for n, c in s.items()} for s in sets]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for s in sets:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append({n: c() for n, c in s.items()})
+        graphs.append(gr)
+    for r in range(3):
+        for i in (0, 1):
+            for o in outs[i].values():
+                for t in o:
+                    t.zero_()
+            graphs[i].replay()
+            eager = {n: c() for n, c in sets[1 - i].items()}
+            torch.cuda.synchronize()
+            for n in sets[i]:
+                assert same(outs[i][n], want[i][n]), f"replay {r} of graph {i}: {n}"
+                assert same(eager[n], want[1 - i][n]), f"eager {n}"
+
+
+def test_binding_refusals():
+    g = gen(1)
+    X, W, b = normal(g, 8, 16), normal(g, 16, 24), normal(g, 24)
+    t = torch.zeros(8, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError, match="inner"):
+        F.fc_fwd_act(X, W.t().contiguous())
+    with pytest.raises(TypeError, match="bias"):
+        F.fc_fwd_act(X, W, bias=b[:23])
+    with pytest.raises(TypeError, match="residual"):
+        F.fc_fwd_act(X, W, residual=X)
+    with pytest.raises(ValueError, match="contiguous"):
+        F.fc_fwd_act(X, W[:, ::2])
+    with pytest.raises(ValueError, match="OUT_BF16"):
+        F.fc_fwd_act(X, W, out_dtype=F.OUT_F32_ACC)
+    with pytest.raises(F.FcError):
+        F.fc_fwd_act(X, W, act=9)
+    with pytest.raises(F.FcError):
+        F.fc_fwd_act(X, W, residual=(R := normal(g, 8, 24)), out=R)  # the output on an input
+    with pytest.raises(TypeError, match="targets"):
+        F.fc_xent_fwd(X, W, t.int())
+    with pytest.raises(TypeError, match="targets"):
+        F.fc_xent_fwd(X, W, t[:7])
+    with pytest.raises(F.FcError):
+        F.fc_xent_fwd(X, W, t, vocab_start=-1)
+    with pytest.raises(ValueError, match="accumulating"):
+        F.fc_xent_bwd(X, W, t, torch.zeros(8, device="cuda"), torch.zeros(8, device="cuda"),
+                      dw_dtype=F.OUT_F32_ACC)
+    with pytest.raises(TypeError, match="offsets"):
+        F.fc_grouped_fwd(X, W[None], torch.zeros(3, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="accumulating"):
+        F.fc_grouped_bwd_weight(X, X, torch.zeros(2, dtype=torch.int64, device="cuda"), out_dtype=F.OUT_F32_ACC)
+
+
+# ---- together
+
+def test_a_step_of_all_of_them():
+    """One training step of a small model: an MLP with bias, activation and
+    residual, an expert layer, and the vocabulary's loss; forward and backward
+    with these calls, against the same model in 64 bits.
+
+    The step rounds to bf16 after each operator: 7 roundings lie between the
+    inputs and any of its outputs. In the Frobenius norm a rounding changes a
+    tensor by at most h = 2^-8 relative, and every map in between passes a
+    relative change on by at most the bound below: 16 h."""
+    M, K, Hd, N, E = 192, 128, 320, 1000, 4
+    g = gen(55)
+    X = normal(g, M, K)
+    W1, b1 = normal(g, K, Hd, scale=K ** -0.5), normal(g, Hd, scale=0.1)
+    W2 = normal(g, Hd, K, scale=Hd ** -0.5)
+    We, V = normal(g, E, K, K, scale=K ** -0.5), normal(g, K, N, scale=K ** -0.5)
+    off = offsets_of([70, 0, 90, 32])
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    t[::5] = -100
+    w = (t != -100).float() / (t != -100).sum()
+
+    A, Z = F.fc_fwd_act(X, W1, bias=b1, act=F.ACT_GELU_TANH, keep_z=True)
+    B = F.fc_fwd_act(A, W2, residual=X)
+    C = F.fc_grouped_fwd(B, We, off)
+    loss, lse, _ = F.fc_xent_fwd(C, V, t)
+    dC, dV = F.fc_xent_bwd(C, V, t, lse, w)
+    dB, dWe = F.fc_grouped_bwd_data(dC, We, off), F.fc_grouped_bwd_weight(B, dC, off)
+    dZ, db1 = F.fc_bwd_data_act(dB, W2, Z, F.ACT_GELU_TANH, bias_grad=True)
+    dW2 = F.fc_bwd_weight(A, dB)
+    dW1 = F.fc_bwd_weight(X, dZ)
+
+    x, w1, bb, w2, we, v = (q.double().requires_grad_() for q in (X, W1, b1, W2, We, V))
+    a = torch.nn.functional.gelu(x @ w1 + bb, approximate="tanh")
+    bq = a @ w2 + x
+    lo = off.tolist()
+    c = torch.cat([bq[p:q] @ we[e] for e, (p, q) in enumerate(zip(lo, lo[1:]))])
+    each = torch.nn.functional.cross_entropy(c @ v, t, reduction="none")
+    (each * w).sum().backward()
+    for name, got, want in (("loss", loss, each), ("dV", dV, v.grad), ("dWe", dWe, we.grad), ("dW2", dW2, w2.grad),
+                            ("dW1", dW1, w1.grad), ("db1", db1, bb.grad)):
+        rel = ((got.double() - want).norm() / want.norm()).item()
+        log(f"  {name}: {rel:.3g}")
+        assert rel <= 16 * H, name
