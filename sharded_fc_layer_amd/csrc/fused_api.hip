@@ -69,17 +69,30 @@ hipError_t place(const Operand& o, const void* src, char* ws, const uint16_t** o
     return launch_pad_any(static_cast<const uint16_t*>(src), dst, o.rows, o.cols, o.ld, s);
 }
 
-// Tile and reduction slices of one product of the general kernel. A product
-// with fewer tiles than the chip holds blocks (two per CU) splits a long
-// reduction, 256 values to a slice at least.
+// Tile and reduction slices of one product. The ring kernel's round of 256
+// tiles of 256 x 256 takes about as long as 0.7 rounds of the general
+// kernel's 512 tiles of 128 x 128. A product of the general kernel with fewer
+// tiles than the chip holds blocks (two per CU) splits a long reduction, 256
+// values to a slice at least.
 struct Shape {
     int tile, splits;
     int64_t k_split;
 };
-Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool may_split) {
-    Shape sh{M <= 32 && !a_oc ? 1 : 0, 1, up(K, 32)};
-    const FusedTile& t = kFusedTiles[sh.tile];
-    const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+int64_t tiles_of(int tile, int64_t M, int64_t N) {
+    const FusedTile& t = kFusedTiles[tile];
+    return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+}
+bool ring_pays(int64_t ring_tiles, int64_t tiles) {
+    return ring_tiles >= 96 && (ring_tiles + 255) / 256 * 7 <= (tiles + 511) / 512 * 10;
+}
+Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t lda, int64_t ldb, bool may_split) {
+    Shape sh{M <= 32 && !a_oc ? 1 : 0, 1, up(K, 64)};
+    if (sh.tile == 0 && ring_takes(GRP_NONE, a_oc, b_oc, N, K, lda, ldb) &&
+        ring_pays(tiles_of(kRingTile, M, N), tiles_of(0, M, N))) {
+        sh.tile = kRingTile;
+        return sh;
+    }
+    const int64_t tiles = tiles_of(sh.tile, M, N);
     if (may_split && tiles < 256) {
         const int64_t want = std::min<int64_t>({512 / tiles, K / 256, 16});
         if (want > 1) {
@@ -90,8 +103,10 @@ Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool may_split) {
     return sh;
 }
 
-bool vec_rows(int64_t N, const void* C, bool f32, const void* R, const void* Z) {
-    return N % 4 == 0 && !off(C, f32 ? 16 : 8) && !off(R, 8) && !off(Z, 8);
+// FusedArgs::vec_out for rows of ld values
+int vec_rows(int64_t ld, const void* C, bool f32, const void* R, const void* Z) {
+    if (ld % 8 == 0 && !off(C, 16) && !off(R, 16) && !off(Z, 16)) return 2;
+    return ld % 4 == 0 && !off(C, f32 ? 16 : 8) && !off(R, 8) && !off(Z, 8);
 }
 
 bool bad_ws(const void* ws, int64_t have, int64_t need) { return need > 0 && (!ws || have < need || off(ws, 256)); }
@@ -132,7 +147,7 @@ ActPlan act_plan(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, bool ali
     int64_t ws = 0;
     p.A = a_oc ? operand(K, M, aligned, &ws) : operand(M, K, aligned, &ws);
     p.B = b_oc ? operand(K, N, aligned, &ws) : operand(N, K, aligned, &ws);
-    p.sh = shape_of(M, N, K, a_oc, true);
+    p.sh = shape_of(M, N, K, a_oc, b_oc, p.A.ld, p.B.ld, true);
     p.planes = ws;
     if (p.sh.splits > 1) ws += up((int64_t)p.sh.splits * M * N * 4, 256);
     p.parts_off = ws;
@@ -169,7 +184,7 @@ XentFwdPlan xent_fwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool align
     int64_t ws = 0;
     p.A = operand(M, K, aligned, &ws);
     p.B = b_oc ? operand(K, N, aligned, &ws) : operand(N, K, aligned, &ws);
-    p.sh = shape_of(M, N, K, false, false);
+    p.sh = shape_of(M, N, K, false, b_oc, p.A.ld, p.B.ld, false);
     const FusedTile& t = kFusedTiles[p.sh.tile];
     p.parts = (int)((N + t.bn - 1) / t.bn) * t.wave_cols;
     p.stat = ws;
@@ -198,9 +213,10 @@ XentBwdPlan xent_bwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool align
     p.d_ld = up(p.piece, 64);
     p.d_off = ws;
     ws += up(M * p.d_ld * 2, 256);
-    p.logits = shape_of(M, p.piece, K, false, false);
-    p.dx = shape_of(M, K, p.piece, false, p.pieces == 1);
-    p.dw = shape_of(K, p.piece, M, true, false);
+    p.logits = shape_of(M, p.piece, K, false, b_oc, p.A.ld, p.B.ld, false);
+    p.dx = shape_of(M, K, p.piece, false, !b_oc, p.d_ld, p.B.ld, p.pieces == 1);
+    p.dw = shape_of(K, p.piece, M, true, true, p.A.ld, p.d_ld, false);
+    if (512 * N >= (int64_t)1 << 31) p.dw.tile = 0;  // its rows are N wide in dW
     p.plane_off = ws;
     if (p.pieces > 1 || p.dx.splits > 1) ws += up((int64_t)p.dx.splits * M * K * 4, 256);
     p.total = ws;
@@ -220,11 +236,20 @@ GroupedPlan grouped_plan(int op, int64_t T, int64_t E, int64_t K, int64_t N, int
     if (op == FC_OP_BWD_WEIGHT) {
         p.A = operand(T, K, aligned, &ws);
         p.B = operand(T, N, aligned, &ws);
-        p.tile = 0;
+        p.tile = ring_takes(GRP_RED, true, true, N, T, p.A.ld, p.B.ld) &&
+                         ring_pays(E * tiles_of(kRingTile, K, N), E * tiles_of(0, K, N))
+                     ? kRingTile
+                     : 0;
     } else {
         p.A = operand(T, op == FC_OP_FWD ? K : N, aligned, &ws);
         p.B = w_order == FC_ROW_MAJOR ? operand(E * K, N, aligned, &ws) : operand(E * N, K, aligned, &ws);
+        const bool fwd = op == FC_OP_FWD, b_oc = fwd == (w_order == FC_ROW_MAJOR);
+        const int64_t n = fwd ? N : K, k = fwd ? K : N;
         p.tile = T <= 32 * E ? 1 : 0;
+        // a group ends with a partly filled tile: half a tile's rows are lost on average
+        if (p.tile == 0 && ring_takes(GRP_ROWS, false, b_oc, n, k, p.A.ld, p.B.ld) &&
+            ring_pays(tiles_of(kRingTile, T + 128 * E, n), tiles_of(0, T + 64 * E, n)))
+            p.tile = kRingTile;
     }
     p.total = ws;
     return p;
@@ -496,7 +521,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         h.lda = pl.A.ld, h.ldb = pl.d_ld, h.ldc = N;
         h.out_f32 = wf32;
         h.accumulate = dw_dtype == FC_OUT_F32_ACCUMULATE;
-        h.vec_out = N % 4 == 0 && vec_rows(4, h.C, wf32, nullptr, nullptr);
+        h.vec_out = vec_rows(N, h.C, wf32, nullptr, nullptr);
         if ((e = run_product(EPI_STORE, pl.dw, true, true, h, nullptr, s)) != hipSuccess) return done(e);
         // dX = D W^T: in one go, or summed over the pieces in 32 bits
         FusedArgs d;
@@ -509,7 +534,8 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         d.accumulate = p > 0;
         d.vec_out = vec_rows(K, d.C, d.out_f32, nullptr, nullptr);
         Shape sh = pl.dx;
-        if (sh.splits == 1) sh.k_split = up(c, 32);
+        if (sh.splits == 1) sh.k_split = up(c, 64);
+        if (sh.tile == kRingTile && c < 64) sh.tile = 0;  // a last piece of less than one stage
         if ((e = run_product(EPI_STORE, sh, false, !w_row, d, planes, s)) != hipSuccess) return done(e);
     }
     if (pl.pieces > 1) {

@@ -80,8 +80,7 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] += b[q];
                 if (g.Z) store4_bf16(g.Z + at, n, g.N, vec, v);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = act_value(g.act, v[q]);
+                act_values(g.act, v);
                 if (g.R) {
                     float r[4];
                     load4(g.R + at, n, g.N, vec, r);
@@ -91,9 +90,10 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
             } else if constexpr (MODE == EPI_DACT) {
                 float z[4];
                 load4(g.Z + at, n, g.N, vec, z);
+                act_slopes(g.act, z);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    v[q] *= act_slope(g.act, z[q]);
+                    v[q] *= z[q];
                     cs[q] += v[q];
                 }
             }
@@ -135,8 +135,9 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const uint16_t* __restrict
             if (Z) {
                 float z[4];
                 load4(Z + at, n, N, vec, z);
+                act_slopes(act, z);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] *= act_slope(act, z[q]);
+                for (int q = 0; q < 4; ++q) v[q] *= z[q];
             }
             if (dZ) store4_bf16(dZ + at, n, N, vec, v);
 #pragma unroll

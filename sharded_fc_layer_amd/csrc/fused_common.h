@@ -20,45 +20,98 @@ __device__ __forceinline__ float bf16_f32(uint16_t b) { return __builtin_bit_cas
 // with log2 e adds at most |x| 2^-24 relative
 __device__ __forceinline__ float exp_f32(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
-// gelu by tanh is z sigma(2u), u = sqrt(2/pi) (z + 0.044715 z^3): written
-// with the exponential it has no cancellation for negative z
-constexpr float kGeluC = 0.7978845608028654f, kGeluA = 0.044715f;
+// 1 / x by the hardware's reciprocal (one ulp)
+__device__ __forceinline__ float rcp_f32(float x) { return __builtin_amdgcn_rcpf(x); }
 
-__device__ __forceinline__ float act_value(int act, float z) {
-    switch (act) {
-        case FC_ACT_RELU: return z < 0.0f ? 0.0f : z;
-        case FC_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
-        case FC_ACT_GELU_TANH: {
-            const float u2 = 2.0f * kGeluC * (z + kGeluA * z * z * z);
-            return z / (1.0f + exp_f32(-u2));
-        }
-        case FC_ACT_SILU: return z / (1.0f + exp_f32(-z));
-        default: return z;
+// The activations are of two kinds, so that an epilogue's code holds one of
+// them without branches between its rows:
+//
+// * z sigma(z (c1 + c3 z^2)), not below lo: silu (c1 = 1, c3 = 0); gelu by
+//   tanh, since (1 + tanh u) / 2 = sigma(2 u) with u = sqrt(2 / pi) (z +
+//   0.044715 z^3), which written so has no cancellation for negative z; none
+//   and relu as sigma = 1 (c0 = inf), relu with lo = 0.
+// * z Phi(z), gelu with the exact normal distribution function: Phi(z) = 1 -
+//   q(|z|) for z > 0, else q(|z|), where q(x) = exp(-x^2 / 2) P(t) / 2, t =
+//   1 / (1 + 0.3275911 x / sqrt 2), P of degree 5: Abramowitz and Stegun,
+//   Handbook of Mathematical Functions, 7.1.26, off by at most 1.5e-7 in erf.
+//
+// Either takes one exponential and one reciprocal. In sigma's argument z is
+// clamped to +-64, where sigma is 0 or 1 in fp32 for every kind, so that
+// infinities meet no zeros there; NaNs pass through the final product.
+struct ActParams {
+    float c0, c1, c3, lo;
+};
+constexpr float kGeluC = 1.5957691216057308f /* 2 sqrt(2 / pi) */, kGeluA = 0.044715f;
+__device__ __forceinline__ ActParams act_params(int act) {
+    if (act == FC_ACT_SILU) return ActParams{0.0f, 1.0f, 0.0f, -INFINITY};
+    if (act == FC_ACT_GELU_TANH) return ActParams{0.0f, kGeluC, kGeluC * kGeluA, -INFINITY};
+    return ActParams{INFINITY, 0.0f, 0.0f, act == FC_ACT_RELU ? 0.0f : -INFINITY};
+}
+
+// Phi(z), and exp(-z^2 / 2) in e
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+    const float x = fabsf(z);
+    const float t = rcp_f32(1.0f + 0.23164189f * x);  // 0.3275911 / sqrt 2
+    e = __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
+    float p = 0.5f * 1.061405429f;
+    p = p * t - 0.5f * 1.453152027f;
+    p = p * t + 0.5f * 1.421413741f;
+    p = p * t - 0.5f * 0.284496736f;
+    p = p * t + 0.5f * 0.254829592f;
+    const float q = p * t * e;
+    return z > 0.0f ? 1.0f - q : q;
+}
+
+template <bool ERF>
+__device__ __forceinline__ float act_value(const ActParams& a, float z) {
+    if constexpr (ERF) {
+        float e;
+        return z * normal_cdf(z, e);
+    } else {
+        const float zc = __builtin_amdgcn_fmed3f(z, -64.0f, 64.0f);
+        const float v = z * rcp_f32(1.0f + exp_f32(-(a.c0 + zc * (a.c1 + a.c3 * (zc * zc)))));
+        return v < a.lo ? a.lo : v;
     }
 }
 
-// d act / dz. Beyond +-40 every slope is exactly 0 or 1 in fp32 (sigma(-40)
-// is 4e-18), and the clamp keeps infinities from meeting zeros; written so
-// that a NaN stays one.
-__device__ __forceinline__ float act_slope(int act, float z) {
-    switch (act) {
-        case FC_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-        case FC_ACT_GELU: {
-            z = z > 40.0f ? 40.0f : z < -40.0f ? -40.0f : z;
-            return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * 0.3989422804014327f * exp_f32(-0.5f * z * z);
-        }
-        case FC_ACT_GELU_TANH: {
-            z = z > 40.0f ? 40.0f : z < -40.0f ? -40.0f : z;
-            const float z2 = z * z;
-            const float s = 1.0f / (1.0f + exp_f32(-2.0f * kGeluC * z * (1.0f + kGeluA * z2)));
-            return s + z * s * (1.0f - s) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * z2);
-        }
-        case FC_ACT_SILU: {
-            z = z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z;
-            const float s = 1.0f / (1.0f + exp_f32(-z));
-            return s * (1.0f + z * (1.0f - s));
-        }
-        default: return 1.0f;
+// d act / dz: with s = sigma(u(z)), s + z s (1 - s) u'(z), 0 up to lo; Phi(z)
+// + z phi(z). Beyond +-64 every slope is 0 or 1.
+template <bool ERF>
+__device__ __forceinline__ float act_slope(const ActParams& a, float z) {
+    const float zc = z > 64.0f ? 64.0f : z < -64.0f ? -64.0f : z;  // a NaN stays one
+    if constexpr (ERF) {
+        float e;
+        const float c = normal_cdf(zc, e);
+        return c + zc * 0.3989422804014327f * e;
+    } else {
+        const float z2 = zc * zc;
+        const float s = rcp_f32(1.0f + exp_f32(-(a.c0 + zc * (a.c1 + a.c3 * z2))));
+        const float d = s + zc * s * (1.0f - s) * (a.c1 + 3.0f * a.c3 * z2);
+        return zc <= a.lo ? 0.0f : d;
+    }
+}
+
+// over several values, with one branch on the kind
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
+    const ActParams a = act_params(act);
+    if (act == FC_ACT_GELU) {
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] = act_value<true>(a, v[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] = act_value<false>(a, v[q]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void act_slopes(int act, float (&v)[N]) {
+    const ActParams a = act_params(act);
+    if (act == FC_ACT_GELU) {
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] = act_slope<true>(a, v[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] = act_slope<false>(a, v[q]);
     }
 }
 
@@ -240,8 +293,7 @@ __device__ __forceinline__ void fused_store(const FusedArgs& g, const TilePos& t
 #pragma unroll
                         for (int q = 0; q < 4; ++q) v[q] += b[q];
                         if (g.Z) store4_bf16(g.Z + at, n, g.N, vec, v);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = act_value(g.act, v[q]);
+                        act_values(g.act, v);
                         if (g.R) {
                             float r[4];
                             load4(g.R + at, n, g.N, vec, r);
@@ -269,9 +321,10 @@ __device__ __forceinline__ void fused_store(const FusedArgs& g, const TilePos& t
                     const int64_t at = m * g.ldc + n;
                     float z[4], v[4];
                     load4(g.Z + at, n, g.N, vec, z);
+                    act_slopes(g.act, z);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        v[q] = acc[i][j][gq * 4 + q] * act_slope(g.act, z[q]);
+                        v[q] = acc[i][j][gq * 4 + q] * z[q];
                         cs[q] += v[q];
                     }
                     if (g.out_f32)

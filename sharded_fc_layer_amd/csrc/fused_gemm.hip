@@ -6,7 +6,22 @@
 
 namespace fcs {
 
-const FusedTile kFusedTiles[kNumFusedTiles] = {{128, 128, 2, 2}, {32, 128, 1, 4}};
+const FusedTile kFusedTiles[kNumFusedTiles] = {{128, 128, 2, 2}, {32, 128, 1, 4}, {256, 256, 2, 2}};
+
+bool ring_takes(GroupMode grp, bool a_oc, bool b_oc, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
+    const int64_t lim = (int64_t)1 << 31;
+    return (a_oc ? K * lda * 2 : 512 * lda) < lim && (b_oc ? K * ldb * 2 : 512 * ldb) < lim &&
+           512 * N < lim &&
+           (grp == GRP_RED || K >= 64);
+}
+
+// The ring's head form: the stage count mod 6 when that is 2 or 4 and a whole
+// period follows, else -1 (padded at the front). Ragged reductions differ
+// from block to block: padded.
+static int head_of(GroupMode grp, int64_t K) {
+    const int64_t n = K / 64;
+    return grp != GRP_RED && K % 64 == 0 && (n % 6 == 2 || n % 6 == 4) && n > 6 ? (int)(n % 6) : -1;
+}
 
 // Explicit instantiations (the host pass emits a launch stub for each).
 #define FCF_I(MODE, GRP, AOC, BOC) \
@@ -72,6 +87,28 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
     const int64_t blocks = nbm * nbn * (grp == GRP_RED ? g.E : grp == GRP_NONE ? g.splits : 1);
     if (blocks <= 0) return hipSuccess;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (tile == kRingTile) {
+        if (!ring_takes(grp, a_oc, b_oc, g.ldc, g.K, g.lda, g.ldb) || g.splits != 1) return hipErrorInvalidValue;
+        const int head = head_of(grp, g.K);
+        const bool vec = g.vec_out == 2, f32 = g.out_f32 != 0, erf = g.act == FC_ACT_GELU;
+        FusedFn fn;
+        if (grp != GRP_NONE)
+            fn = f32 ? fused_ring_grouped<true>(grp, head, vec, b_oc) : fused_ring_grouped<false>(grp, head, vec, b_oc);
+        else if (mode == EPI_STORE)
+            fn = f32 ? fused_ring<EPI_STORE, true>(head, vec, a_oc, b_oc)
+                     : fused_ring<EPI_STORE, false>(head, vec, a_oc, b_oc);
+        else if (mode == EPI_ACT)
+            fn = erf ? fused_ring<EPI_ACT, true>(head, vec, a_oc, b_oc) : fused_ring<EPI_ACT, false>(head, vec, a_oc, b_oc);
+        else if (mode == EPI_DACT)
+            fn = erf ? fused_ring<EPI_DACT, true>(head, vec, a_oc, b_oc)
+                     : fused_ring<EPI_DACT, false>(head, vec, a_oc, b_oc);
+        else
+            fn = mode == EPI_STATS ? fused_ring<EPI_STATS, false>(head, true, a_oc, b_oc)
+                                   : fused_ring<EPI_DLOGIT, false>(head, true, a_oc, b_oc);
+        if (!fn) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, g);
+        return hipGetLastError();
+    }
     const FusedFn fn = mode == EPI_STORE  ? fused_kernel<EPI_STORE>(grp, tile, a_oc, b_oc)
                        : mode == EPI_ACT  ? fused_kernel<EPI_ACT>(grp, tile, a_oc, b_oc)
                        : mode == EPI_DACT ? fused_kernel<EPI_DACT>(grp, tile, a_oc, b_oc)

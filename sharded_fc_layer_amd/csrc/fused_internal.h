@@ -31,7 +31,9 @@ enum GroupMode : int {
 // fields of the launch's modes are read.
 struct FusedArgs : GemmArgs {
     int out_f32 = 0;      // C is fp32 (else bf16)
-    int vec_out = 0;      // rows of C (and R, Z) start on 16-byte boundaries: 4-column vectors
+    // how C's rows (and R's, Z's) start: 2: pieces of 8 columns on 16-byte
+    // boundaries, 1: of 4 columns (8 bytes in bf16, 16 in fp32), 0: anywhere
+    int vec_out = 0;
     int act = 0;          // fc_act
     const uint16_t* bias = nullptr;  // N values, or none
     const uint16_t* R = nullptr;     // M x N, or none
@@ -57,23 +59,50 @@ struct FusedArgs : GemmArgs {
 struct FusedTile {
     int bm, bn, wave_rows, wave_cols;  // the 4 waves' grid within the tile
 };
-constexpr int kNumFusedTiles = 2;
+constexpr int kNumFusedTiles = 3;
+constexpr int kRingTile = 2;  // the ring kernel's tile: see ring_takes
 extern const FusedTile kFusedTiles[kNumFusedTiles];
 typedef void (*FusedFn)(FusedArgs);
-// The kernels of one epilogue (fused_gemm.hip, fused_gemm_xent.hip); nullptr
-// for a combination that no operator uses.
+// The general kernel's instances of one epilogue (fused_gemm.hip,
+// fused_gemm_xent.hip); nullptr for a combination that no operator uses.
 template <EpiMode MODE>
 FusedFn fused_kernel(GroupMode grp, int tile, bool a_oc, bool b_oc);
+// The ring kernel's (fused_ring_*.hip), 256 x 256 block tiles: one product, or
+// an expert layer's (EPI_STORE).
+template <EpiMode MODE, bool KIND>
+FusedFn fused_ring(int head, bool vec, bool a_oc, bool b_oc);
+template <bool KIND>
+FusedFn fused_ring_grouped(GroupMode grp, int head, bool vec, bool b_oc);
+#define FCU_DECLARE(MODE) \
+    template <>           \
+    FusedFn fused_kernel<MODE>(GroupMode grp, int tile, bool a_oc, bool b_oc);
+#define FCU_DECLARE_RING(MODE, KIND) \
+    template <>                      \
+    FusedFn fused_ring<MODE, KIND>(int head, bool vec, bool a_oc, bool b_oc);
+FCU_DECLARE(EPI_STORE)
+FCU_DECLARE(EPI_ACT)
+FCU_DECLARE(EPI_DACT)
+FCU_DECLARE(EPI_STATS)
+FCU_DECLARE(EPI_DLOGIT)
+FCU_DECLARE_RING(EPI_STORE, false)
+FCU_DECLARE_RING(EPI_STORE, true)
+FCU_DECLARE_RING(EPI_ACT, false)
+FCU_DECLARE_RING(EPI_ACT, true)
+FCU_DECLARE_RING(EPI_DACT, false)
+FCU_DECLARE_RING(EPI_DACT, true)
+FCU_DECLARE_RING(EPI_STATS, false)
+FCU_DECLARE_RING(EPI_DLOGIT, false)
+#undef FCU_DECLARE
+#undef FCU_DECLARE_RING
 template <>
-FusedFn fused_kernel<EPI_STORE>(GroupMode grp, int tile, bool a_oc, bool b_oc);
+FusedFn fused_ring_grouped<false>(GroupMode grp, int head, bool vec, bool b_oc);
 template <>
-FusedFn fused_kernel<EPI_ACT>(GroupMode grp, int tile, bool a_oc, bool b_oc);
-template <>
-FusedFn fused_kernel<EPI_DACT>(GroupMode grp, int tile, bool a_oc, bool b_oc);
-template <>
-FusedFn fused_kernel<EPI_STATS>(GroupMode grp, int tile, bool a_oc, bool b_oc);
-template <>
-FusedFn fused_kernel<EPI_DLOGIT>(GroupMode grp, int tile, bool a_oc, bool b_oc);
+FusedFn fused_ring_grouped<true>(GroupMode grp, int head, bool vec, bool b_oc);
+
+// Whether the ring kernel can run a product: an output-contiguous operand has
+// to lie within 2 GiB, as do 256 rows of a reduction-contiguous one and 128 of
+// the output; without ragged reductions, at least one whole stage of 64 values.
+bool ring_takes(GroupMode grp, bool a_oc, bool b_oc, int64_t N, int64_t K, int64_t lda, int64_t ldb);
 hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc, const FusedArgs& g,
                         hipStream_t s);
 

@@ -13,6 +13,16 @@
 #define FCW4_RING_NA 3
 #endif
 
+#define FCR_SETUP const W4Setup w = w4_setup<A_OC, B_OC, BKP, BN>(g);
+#define FCR_ROWS g.M
+#define FCR_COLS g.N
+#define FCR_SHORT false
+#define FCR_EPILOGUE                                                              \
+    if constexpr (OUT_F32)                                                        \
+        store_tile_f32_staged(g, w.slice, w.m0, w.n0, wm0, wn0, lane, acc, stage); \
+    else                                                                          \
+        store_tile_bf16_staged(g, w.m0, w.n0, wm0, wn0, lane, acc, stage);
+
 namespace fcs {
 namespace {
 

@@ -40,7 +40,7 @@ MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
 WRITE_WINDOW = 6   # slots between an AGPR write and an MFMA reading it
 READ_WINDOW = 18   # slots between an MFMA and a non-MFMA access of its result
 VALU_WINDOW = 2    # slots between a VALU write of a VGPR and an MFMA reading it
-ASM_KERNELS = re.compile(r"gemm_w4k64r?(_stamped)?_kernel")
+ASM_KERNELS = re.compile(r"gemm_w4k64r?(_stamped)?_kernel|fused_ring_kernel")
 
 
 def tools_available() -> bool:

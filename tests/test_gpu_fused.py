@@ -87,11 +87,14 @@ def slope64(z, act):
 
 # from one row to several tiles, odd and aligned, reductions from one value to
 # several slices of a split one
+# ... and enough tiles for the 256 x 256 ones, with reductions of a partial
+# stage after a whole one, 2 and 4 stages past a period of 6, and whole periods
+WIDE = [(2600, 100, 2600), (2570, 512, 2700), (4100, 640, 1500), (2600, 384, 2560), (2309, 1001, 3001)]
 SHAPES = [(1, 1, 1), (1, 2048, 520), (3, 31, 7), (16, 512, 384), (32, 264, 136), (33, 129, 130), (100, 1001, 77),
           (128, 64, 128), (130, 72, 259), (257, 520, 300), (300, 40, 1032), (520, 776, 264)]
 
 
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", SHAPES + WIDE)
 @pytest.mark.parametrize("xo, wo", [(ROW, ROW), (ROW, COL), (COL, ROW), (COL, COL)])
 def test_fwd_act(shape, xo, wo):
     M, K, N = shape
@@ -115,7 +118,7 @@ def test_fwd_act(shape, xo, wo):
                 within(Z, z, ez + H * (z.abs() + ez), what + " Z")
 
 
-@pytest.mark.parametrize("shape", SHAPES + [(700, 2050, 513)])
+@pytest.mark.parametrize("shape", SHAPES + WIDE + [(700, 2050, 513)])
 @pytest.mark.parametrize("wo", [ROW, COL])
 def test_fwd_act_integers_are_exact(shape, wo):
     M, K, N = shape
@@ -133,7 +136,7 @@ def test_fwd_act_integers_are_exact(shape, wo):
     assert torch.equal(F.fc_fwd_act(X, stored(W, wo), w_order=wo), (X.double() @ W.double()).float().to(torch.bfloat16))
 
 
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", SHAPES + [(m, n, k) for m, k, n in WIDE])
 @pytest.mark.parametrize("wo", [ROW, COL])
 def test_bwd_data_act(shape, wo):
     M, N, K = shape  # the reduction runs over the layer's outputs N
@@ -205,7 +208,8 @@ def test_slopes_by_differences_and_at_the_ends():
 # ---- cross entropy
 
 XENT = [(1, 8, 1), (1, 64, 1000), (5, 33, 130), (32, 128, 129), (33, 100, 999), (64, 264, 4001), (130, 72, 520),
-        (257, 520, 1032), (300, 65, 2050)]
+        (257, 520, 1032), (300, 65, 2050),
+        (2600, 100, 2600), (2570, 512, 2700), (4100, 640, 1500), (2309, 131, 3001)]
 
 
 def xent64(X, W, t, v0, ignore, lse=None):
@@ -291,6 +295,16 @@ def test_xent_extreme_logits():
     t[4] = -100
     dX, dW = F.fc_xent_bwd(X[2:], W, t[2:], torch.nan_to_num(lse), torch.ones(4, device="cuda"))
     assert bool((dX[2] == 0).all())
+    # the same where the 256 x 256 tiles are taken
+    X, W = normal(gen(4), 2600, 72), normal(gen(5), 72, 2600, scale=0.1)
+    X[5], X[2599] = float("nan"), inf
+    t = torch.arange(2600, device="cuda")
+    t[5] = t[2599] = -100
+    for wo in (ROW, COL):
+        loss, lse, _ = F.fc_xent_fwd(X, stored(W, wo), t, w_order=wo)
+        assert loss[5].item() == 0 and loss[2599].item() == 0 and bool(torch.isfinite(loss).all())
+        dX, _ = F.fc_xent_bwd(X, stored(W, wo), t, lse, torch.ones(2600, device="cuda"), w_order=wo)
+        assert bool((dX[5] == 0).all()) and bool((dX[2599] == 0).all()) and bool(torch.isfinite(dX).all())
 
 
 @pytest.mark.parametrize("shape", XENT)
@@ -403,7 +417,8 @@ def offsets_of(counts, first=0):
 GROUPED = [  # rows of each expert, first row, rows behind the last, K, N
     ([1], 0, 0, 8, 8), ([0, 5, 0], 0, 3, 33, 7), ([3, 0, 130, 1], 2, 9, 64, 136), ([300, 17, 0, 64], 0, 0, 136, 264),
     ([0, 0, 0], 4, 1, 16, 24), ([1] * 70 + [0] * 30 + [5] * 33, 0, 2, 40, 130), ([260, 255, 257], 1, 0, 520, 100),
-    ([33, 31, 32, 129], 0, 40, 72, 520), ([700], 0, 0, 264, 300), ([40] * 8, 0, 0, 1001, 129)]
+    ([33, 31, 32, 129], 0, 40, 72, 520), ([700, 0, 30, 1500, 63, 64, 65, 257], 3, 5, 1200, 1300),
+    ([1100, 900, 0, 1], 0, 0, 1032, 2570), ([2600], 0, 1, 640, 2600), ([700], 0, 0, 264, 300), ([40] * 8, 0, 0, 1001, 129)]
 
 
 @pytest.mark.parametrize("case", GROUPED, ids=lambda c: f"{len(c[0])}x{c[3]}x{c[4]}")
