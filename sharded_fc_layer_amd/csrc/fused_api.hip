@@ -61,12 +61,16 @@ Operand operand(int64_t rows, int64_t cols, bool aligned, int64_t* ws) {
     }
     return o;
 }
-hipError_t place(const Operand& o, const void* src, char* ws, const uint16_t** out, hipStream_t s) {
-    *out = static_cast<const uint16_t*>(src);
-    if (!o.copy) return hipSuccess;
-    uint16_t* dst = reinterpret_cast<uint16_t*>(ws + o.off);
-    *out = dst;
-    return launch_pad_any(static_cast<const uint16_t*>(src), dst, o.rows, o.cols, o.ld, s);
+// Both operands' places: the caller's memory, or the copies (one launch).
+hipError_t place(const Operand& a, const void* pa, const uint16_t** oa, const Operand& b, const void* pb,
+                 const uint16_t** ob, char* ws, hipStream_t s) {
+    auto one = [ws](const Operand& o, const void* src, const uint16_t** out) {
+        *out = o.copy ? reinterpret_cast<const uint16_t*>(ws + o.off) : static_cast<const uint16_t*>(src);
+        return PadCopy{static_cast<const uint16_t*>(src), const_cast<uint16_t*>(*out), o.copy ? o.rows : 0, o.cols,
+                       o.copy ? o.ld : 0};
+    };
+    const PadCopy ca = one(a, pa, oa), cb = one(b, pb, ob);
+    return a.copy || b.copy ? launch_pad_any(ca, cb, s) : hipSuccess;
 }
 
 // Tile and reduction slices of one product. The ring kernel's round of 256
@@ -78,6 +82,7 @@ struct Shape {
     int tile, splits;
     int64_t k_split;
 };
+constexpr int kSkinny = -1;  // Shape::tile: the kernel for a few rows
 int64_t tiles_of(int tile, int64_t M, int64_t N) {
     const FusedTile& t = kFusedTiles[tile];
     return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
@@ -86,8 +91,8 @@ bool ring_pays(int64_t ring_tiles, int64_t tiles) {
     return ring_tiles >= 96 && (ring_tiles + 255) / 256 * 7 <= (tiles + 511) / 512 * 10;
 }
 Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t lda, int64_t ldb, bool may_split) {
-    Shape sh{M <= 32 && !a_oc ? 1 : 0, 1, up(K, 64)};
-    if (sh.tile == 0 && ring_takes(GRP_NONE, a_oc, b_oc, N, K, lda, ldb) &&
+    Shape sh{a_oc || M > 64 ? 0 : M <= 32 ? 1 : 3, 1, up(K, 64)};
+    if (M > 64 && ring_takes(GRP_NONE, a_oc, b_oc, N, K, lda, ldb) &&
         ring_pays(tiles_of(kRingTile, M, N), tiles_of(0, M, N))) {
         sh.tile = kRingTile;
         return sh;
@@ -102,6 +107,9 @@ Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t ld
     }
     return sh;
 }
+
+// row length of fp32 planes: whole vectors and lines whatever N is
+int64_t plane_ld(int64_t N) { return up(N, 64); }
 
 // FusedArgs::vec_out for rows of ld values
 int vec_rows(int64_t ld, const void* C, bool f32, const void* R, const void* Z) {
@@ -119,16 +127,17 @@ hipError_t run_product(EpiMode mode, const Shape& sh, bool a_oc, bool b_oc, Fuse
     g.k_split = sh.k_split;
     g.splits = sh.splits;
     g.c_split_stride = 0;
+    if (sh.tile == kSkinny) return launch_fused_skinny(g, s);
     if (sh.splits == 1) return launch_fused(mode, GRP_NONE, sh.tile, a_oc, b_oc, g, s);
     FusedArgs p = g;
     p.C = planes;
-    p.ldc = g.N;
+    p.ldc = plane_ld(g.N);
     p.out_f32 = 1;
-    p.vec_out = g.N % 4 == 0;
+    p.vec_out = 2;
     p.accumulate = 0;
-    p.c_split_stride = g.M * g.N;
+    p.c_split_stride = g.M * p.ldc;
     const hipError_t e = launch_fused(EPI_STORE, GRP_NONE, sh.tile, a_oc, b_oc, p, s);
-    return e != hipSuccess ? e : launch_split_epilogue(mode, g, planes, sh.splits, s);
+    return e != hipSuccess ? e : launch_split_epilogue(mode, g, planes, p.ldc, sh.splits, s);
 }
 
 // ---------------------------------------------------------------- act
@@ -148,8 +157,9 @@ ActPlan act_plan(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, bool ali
     p.A = a_oc ? operand(K, M, aligned, &ws) : operand(M, K, aligned, &ws);
     p.B = b_oc ? operand(K, N, aligned, &ws) : operand(N, K, aligned, &ws);
     p.sh = shape_of(M, N, K, a_oc, b_oc, p.A.ld, p.B.ld, true);
+    if (!grad && M <= 32 && !a_oc && !b_oc) p.sh = Shape{kSkinny, 1, K};
     p.planes = ws;
-    if (p.sh.splits > 1) ws += up((int64_t)p.sh.splits * M * N * 4, 256);
+    if (p.sh.splits > 1) ws += (int64_t)p.sh.splits * M * plane_ld(N) * 4;
     p.parts_off = ws;
     p.parts = 0;
     if (grad) {
@@ -218,7 +228,7 @@ XentBwdPlan xent_bwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool align
     p.dw = shape_of(K, p.piece, M, true, true, p.A.ld, p.d_ld, false);
     if (512 * N >= (int64_t)1 << 31) p.dw.tile = 0;  // its rows are N wide in dW
     p.plane_off = ws;
-    if (p.pieces > 1 || p.dx.splits > 1) ws += up((int64_t)p.dx.splits * M * K * 4, 256);
+    if (p.pieces > 1 || p.dx.splits > 1) ws += (int64_t)p.dx.splits * M * plane_ld(K) * 4;
     p.total = ws;
     return p;
 }
@@ -245,7 +255,7 @@ GroupedPlan grouped_plan(int op, int64_t T, int64_t E, int64_t K, int64_t N, int
         p.B = w_order == FC_ROW_MAJOR ? operand(E * K, N, aligned, &ws) : operand(E * N, K, aligned, &ws);
         const bool fwd = op == FC_OP_FWD, b_oc = fwd == (w_order == FC_ROW_MAJOR);
         const int64_t n = fwd ? N : K, k = fwd ? K : N;
-        p.tile = T <= 32 * E ? 1 : 0;
+        p.tile = T <= 32 * E ? 1 : T <= 64 * E ? 3 : 0;
         // a group ends with a partly filled tile: half a tile's rows are lost on average
         if (p.tile == 0 && ring_takes(GRP_ROWS, false, b_oc, n, k, p.A.ld, p.B.ld) &&
             ring_pays(tiles_of(kRingTile, T + 128 * E, n), tiles_of(0, T + 64 * E, n)))
@@ -285,8 +295,7 @@ fc_status grouped_call(int op, const void* P, const void* Q, int w_order, const 
     char* base = static_cast<char*>(ws);
     FusedArgs g;
     hipError_t e;
-    if ((e = place(pl.A, P, base, &g.A, s)) != hipSuccess) return done(e);
-    if ((e = place(pl.B, Q, base, &g.B, s)) != hipSuccess) return done(e);
+    if ((e = place(pl.A, P, &g.A, pl.B, Q, &g.B, base, s)) != hipSuccess) return done(e);
     g.C = out;
     g.lda = pl.A.ld, g.ldb = pl.B.ld;
     g.out_f32 = f32;
@@ -344,8 +353,7 @@ fc_status fc_fwd_act(const void* X, fc_order x_order, const void* W, fc_order w_
     char* base = static_cast<char*>(ws);
     FusedArgs g;
     hipError_t e;
-    if ((e = place(pl.A, X, base, &g.A, s)) != hipSuccess) return done(e);
-    if ((e = place(pl.B, W, base, &g.B, s)) != hipSuccess) return done(e);
+    if ((e = place(pl.A, X, &g.A, pl.B, W, &g.B, base, s)) != hipSuccess) return done(e);
     g.C = Y;
     g.M = M, g.N = N, g.K = K;
     g.lda = pl.A.ld, g.ldb = pl.B.ld, g.ldc = N;
@@ -387,8 +395,7 @@ fc_status fc_bwd_data_act(const void* dY, const void* W, fc_order w_order, const
     char* base = static_cast<char*>(ws);
     FusedArgs g;
     hipError_t e;
-    if ((e = place(pl.A, dY, base, &g.A, s)) != hipSuccess) return done(e);
-    if ((e = place(pl.B, W, base, &g.B, s)) != hipSuccess) return done(e);
+    if ((e = place(pl.A, dY, &g.A, pl.B, W, &g.B, base, s)) != hipSuccess) return done(e);
     g.C = dX;
     g.M = M, g.N = K, g.K = N;
     g.lda = pl.A.ld, g.ldb = pl.B.ld, g.ldc = K;
@@ -454,8 +461,7 @@ fc_status fc_xent_fwd(const void* X, const void* W, fc_order w_order, const int6
     char* base = static_cast<char*>(ws);
     FusedArgs g;
     hipError_t e;
-    if ((e = place(pl.A, X, base, &g.A, s)) != hipSuccess) return done(e);
-    if ((e = place(pl.B, W, base, &g.B, s)) != hipSuccess) return done(e);
+    if ((e = place(pl.A, X, &g.A, pl.B, W, &g.B, base, s)) != hipSuccess) return done(e);
     g.C = nullptr;
     g.M = M, g.N = N, g.K = K;
     g.lda = pl.A.ld, g.ldb = pl.B.ld, g.ldc = N;
@@ -497,8 +503,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
     char* base = static_cast<char*>(ws);
     const uint16_t *x, *w;
     hipError_t e;
-    if ((e = place(pl.A, X, base, &x, s)) != hipSuccess) return done(e);
-    if ((e = place(pl.B, W, base, &w, s)) != hipSuccess) return done(e);
+    if ((e = place(pl.A, X, &x, pl.B, W, &w, base, s)) != hipSuccess) return done(e);
     uint16_t* D = reinterpret_cast<uint16_t*>(base + pl.d_off);
     float* planes = reinterpret_cast<float*>(base + pl.plane_off);
     for (int p = 0; p < pl.pieces; ++p) {
@@ -527,12 +532,13 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         FusedArgs d;
         d.A = D, d.B = wp;
         d.M = M, d.N = K, d.K = c;
-        d.lda = pl.d_ld, d.ldb = pl.B.ld, d.ldc = K;
+        d.lda = pl.d_ld, d.ldb = pl.B.ld;
         const bool last = pl.pieces == 1;
+        d.ldc = last ? K : plane_ld(K);
         d.C = last ? dX : planes;
         d.out_f32 = last ? xf32 : 1;
         d.accumulate = p > 0;
-        d.vec_out = vec_rows(K, d.C, d.out_f32, nullptr, nullptr);
+        d.vec_out = vec_rows(d.ldc, d.C, d.out_f32, nullptr, nullptr);
         Shape sh = pl.dx;
         if (sh.splits == 1) sh.k_split = up(c, 64);
         if (sh.tile == kRingTile && c < 64) sh.tile = 0;  // a last piece of less than one stage
@@ -545,7 +551,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         d.accumulate = 0;
         d.out_f32 = xf32;
         d.vec_out = vec_rows(K, dX, xf32, nullptr, nullptr);
-        e = launch_split_epilogue(EPI_STORE, d, planes, 1, s);
+        e = launch_split_epilogue(EPI_STORE, d, planes, plane_ld(K), 1, s);
     }
     return done(e);
 }

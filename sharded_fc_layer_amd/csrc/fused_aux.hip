@@ -9,19 +9,21 @@
 namespace fcs {
 namespace {
 
-// dst row r = src row r, then zeros up to ld; 8 values per thread and step.
+// dst row r = src row r, then zeros up to ld; 8 values per thread and step,
+// the second copy's after the first's (one launch for both operands).
 // Source rows start anywhere: a thread's 8 values are read one by one (a
 // wave's reads still fall into the same lines).
-__global__ __launch_bounds__(256) void pad_any_kernel(const uint16_t* __restrict__ src, uint16_t* __restrict__ dst,
-                                                      int64_t rows, int64_t cols, int64_t ld) {
-    const int64_t per_row = ld / 8, total = rows * per_row;
+__global__ __launch_bounds__(256) void pad_any_kernel(PadCopy a, PadCopy b) {
+    const int64_t na = a.rows * (a.ld / 8), total = na + b.rows * (b.ld / 8);
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = i / per_row, c = (i - r * per_row) * 8;
-        const uint16_t* p = src + r * cols + c;
+        const PadCopy& p = i < na ? a : b;
+        const int64_t k = i < na ? i : i - na, per_row = p.ld / 8;
+        const int64_t r = k / per_row, c = (k - r * per_row) * 8;
+        const uint16_t* src = p.src + r * p.cols + c;
         u16x8 v;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? p[e] : (uint16_t)0;
-        *reinterpret_cast<u16x8*>(dst + r * ld + c) = v;
+        for (int e = 0; e < 8; ++e) v[e] = c + e < p.cols ? src[e] : (uint16_t)0;
+        *reinterpret_cast<u16x8*>(p.dst + r * p.ld + c) = v;
     }
 }
 
@@ -46,46 +48,48 @@ __global__ __launch_bounds__(1024) void colsum_parts_kernel(const float* __restr
 }
 
 // Sum of a split reduction's planes in order, and the epilogue. A block takes
-// 256 columns (4 per lane) of kSplitRows rows, each wave every fourth row;
-// EPI_DACT's column sums leave one partial row per block of rows.
-constexpr int kSplitRows = 16;
+// 256 columns (4 per lane) of kSplitRows rows, each wave kRowsPerWave of
+// them, whose loads from a plane overlap; EPI_DACT's column sums leave one
+// partial row per block of rows.
+constexpr int kRowsPerWave = 2, kSplitRows = 4 * kRowsPerWave;
 template <EpiMode MODE>
-__global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const float* __restrict__ planes, int splits) {
+__global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const float* __restrict__ planes, int64_t pld,
+                                                             int splits) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t nb = (g.N + 255) / 256;
     const int64_t bm = blockIdx.x / nb, n = (blockIdx.x % nb) * 256 + lane * 4;
     const bool vec = g.vec_out != 0;
     [[maybe_unused]] __shared__ float cs_all[4][256];
     [[maybe_unused]] float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (MODE == EPI_ACT && g.bias && n < g.N) load4(g.bias + n, n, g.N, false, b);
-    const bool pvec = g.N % 4 == 0;
-    if (n < g.N)
-        for (int64_t m = bm * kSplitRows + wave; m < g.M && m < (bm + 1) * kSplitRows; m += 4) {
+    if (n < g.N) {
+        float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (MODE == EPI_ACT && g.bias) load4(g.bias + n, n, g.N, false, b);
+        const int64_t m0 = bm * kSplitRows + wave * kRowsPerWave;
+        const float* p = planes + m0 * pld + n;  // planes have pld columns, a multiple of 4 past N
+        f32x4 sum[kRowsPerWave];
+#pragma unroll
+        for (int r = 0; r < kRowsPerWave; ++r) sum[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s)
+#pragma unroll
+            for (int r = 0; r < kRowsPerWave; ++r)
+                if (m0 + r < g.M) sum[r] += *reinterpret_cast<const f32x4*>(p + (s * g.M + r) * pld);
+#pragma unroll
+        for (int r = 0; r < kRowsPerWave; ++r) {
+            const int64_t m = m0 + r;
+            if (m >= g.M) break;
             const int64_t at = m * g.ldc + n;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int s = 0; s < splits; ++s) {
-                const float* p = planes + ((int64_t)s * g.M + m) * g.N + n;
-                if (pvec) {
-                    const f32x4 w = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] += w[q];
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (n + q < g.N) v[q] += p[q];
-                }
-            }
+            float v[4] = {sum[r][0], sum[r][1], sum[r][2], sum[r][3]};
             if constexpr (MODE == EPI_ACT) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] += b[q];
                 if (g.Z) store4_bf16(g.Z + at, n, g.N, vec, v);
                 act_values(g.act, v);
                 if (g.R) {
-                    float r[4];
-                    load4(g.R + at, n, g.N, vec, r);
+                    float r4[4];
+                    load4(g.R + at, n, g.N, vec, r4);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] += r[q];
+                    for (int q = 0; q < 4; ++q) v[q] += r4[q];
                 }
             } else if constexpr (MODE == EPI_DACT) {
                 float z[4];
@@ -102,6 +106,7 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
             else
                 store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, vec, v);
         }
+    }
     if constexpr (MODE == EPI_DACT) {
         if (g.colpart) {
 #pragma unroll
@@ -153,38 +158,43 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const uint16_t* __restrict
             ((cs_all[0][threadIdx.x] + cs_all[1][threadIdx.x]) + cs_all[2][threadIdx.x]) + cs_all[3][threadIdx.x];
 }
 
-// Rows' maxima and sums joined over the blocks of columns: 16 rows per block,
-// 64 threads for each, every 64th partial to a thread, joined pairwise over
-// the wave (one wave per row). Infinite maxima count as 0 (see EPI_STATS).
+// Maximum and sum of exponentials (relative to it) of two sets joined.
+// Infinite maxima count as 0 (see EPI_STATS); a set of nothing (maximum -inf,
+// sum 0) adds nothing.
+__device__ __forceinline__ void join_sets(float& mx, float& sum, float x, float s) {
+    const float top = fmaxf(mx, x), ref = __builtin_isinf(top) ? 0.0f : top;
+    const float r0 = __builtin_isinf(mx) ? 0.0f : mx, r1 = __builtin_isinf(x) ? 0.0f : x;
+    sum = (sum != 0.0f ? sum * exp_f32(r0 - ref) : 0.0f) + (s != 0.0f ? s * exp_f32(r1 - ref) : 0.0f);
+    mx = top;
+}
+
+// Rows' sets joined over the blocks of columns: 16 rows per block, 64 threads
+// for each with every 64th set, then pairwise in a fixed order.
 __global__ __launch_bounds__(1024) void xent_finish_kernel(const float* __restrict__ stat, int parts,
                                                            const int64_t* __restrict__ targets, int64_t v0,
                                                            int64_t ignore, int64_t M, int64_t N,
                                                            float* __restrict__ lse, float* __restrict__ tlogit,
                                                            float* __restrict__ loss) {
-    // a wave's 64 lanes read 16 neighbouring rows x 4 partials at a time
     __shared__ float smx[64][17], ssum[64][17];
-    const int row = threadIdx.x & 15, sl = threadIdx.x >> 4;  // 64 slices of the partials
+    const int row = threadIdx.x & 15, sl = threadIdx.x >> 4;
     const int64_t m = (int64_t)blockIdx.x * 16 + row;
     float mx = -INFINITY, sum = 0.0f;
-    if (m < M)
-        for (int p = sl; p < parts; p += 64) {
-            const float x = stat[(int64_t)p * M + m], s = stat[(int64_t)(parts + p) * M + m];
-            const float top = fmaxf(mx, x), ref = __builtin_isinf(top) ? 0.0f : top;
-            const float r0 = __builtin_isinf(mx) ? 0.0f : mx, r1 = __builtin_isinf(x) ? 0.0f : x;
-            // a partial of nothing (maximum -inf, sum 0) adds nothing
-            sum = (sum != 0.0f ? sum * exp_f32(r0 - ref) : 0.0f) + (s != 0.0f ? s * exp_f32(r1 - ref) : 0.0f);
-            mx = top;
-        }
+    if (m < M) {
+#pragma unroll 4
+        for (int p = sl; p < parts; p += 64)
+            join_sets(mx, sum, stat[(int64_t)p * M + m], stat[(int64_t)(parts + p) * M + m]);
+    }
     smx[sl][row] = mx, ssum[sl][row] = sum;
     __syncthreads();
-    if (threadIdx.x < 16 && m < M) {
-        for (int q = 1; q < 64; ++q) {
-            const float x = smx[q][row], s = ssum[q][row];
-            const float top = fmaxf(mx, x), ref = __builtin_isinf(top) ? 0.0f : top;
-            const float r0 = __builtin_isinf(mx) ? 0.0f : mx, r1 = __builtin_isinf(x) ? 0.0f : x;
-            sum = (sum != 0.0f ? sum * exp_f32(r0 - ref) : 0.0f) + (s != 0.0f ? s * exp_f32(r1 - ref) : 0.0f);
-            mx = top;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+        if (sl < d) {
+            join_sets(mx, sum, smx[sl + d][row], ssum[sl + d][row]);
+            smx[sl][row] = mx, ssum[sl][row] = sum;
         }
+        __syncthreads();
+    }
+    if (sl == 0 && m < M) {
         const float ref = __builtin_isinf(mx) ? 0.0f : mx;
         const float l = ref + logf(sum);
         const int64_t t = targets[m];
@@ -199,11 +209,13 @@ __global__ __launch_bounds__(1024) void xent_finish_kernel(const float* __restri
 
 }  // namespace
 
-hipError_t launch_pad_any(const uint16_t* src, uint16_t* dst, int64_t rows, int64_t cols, int64_t ld, hipStream_t s) {
-    if (rows <= 0 || ld <= 0) return hipSuccess;
-    if (ld % 8 != 0 || cols > ld || (uintptr_t)dst % 16 != 0) return hipErrorInvalidValue;
-    const int64_t blocks = std::min<int64_t>((rows * (ld / 8) + 255) / 256, 8192);
-    hipLaunchKernelGGL(pad_any_kernel, dim3((unsigned)blocks), dim3(256), 0, s, src, dst, rows, cols, ld);
+hipError_t launch_pad_any(const PadCopy& a, const PadCopy& b, hipStream_t s) {
+    const int64_t work = a.rows * (a.ld / 8) + b.rows * (b.ld / 8);
+    if (work <= 0) return hipSuccess;
+    if (a.ld % 8 != 0 || b.ld % 8 != 0 || (uintptr_t)a.dst % 16 != 0 || (uintptr_t)b.dst % 16 != 0)
+        return hipErrorInvalidValue;
+    const int64_t blocks = std::min<int64_t>((work + 255) / 256, 8192);
+    hipLaunchKernelGGL(pad_any_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, b);
     return hipGetLastError();
 }
 
@@ -214,13 +226,14 @@ hipError_t launch_colsum_parts(const float* part, float* out, int64_t N, int par
 
 int split_epilogue_parts(int64_t M) { return (int)((M + kSplitRows - 1) / kSplitRows); }
 
-hipError_t launch_split_epilogue(EpiMode mode, const FusedArgs& g, const float* planes, int splits, hipStream_t s) {
+hipError_t launch_split_epilogue(EpiMode mode, const FusedArgs& g, const float* planes, int64_t pld, int splits,
+                                 hipStream_t s) {
     const int64_t blocks = ((g.N + 255) / 256) * split_epilogue_parts(g.M);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     const auto fn = mode == EPI_ACT    ? split_epilogue_kernel<EPI_ACT>
                     : mode == EPI_DACT ? split_epilogue_kernel<EPI_DACT>
                                        : split_epilogue_kernel<EPI_STORE>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(256), 0, s, g, planes, splits);
+    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(256), 0, s, g, planes, pld, splits);
     return hipGetLastError();
 }
 

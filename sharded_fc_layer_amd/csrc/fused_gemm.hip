@@ -6,7 +6,7 @@
 
 namespace fcs {
 
-const FusedTile kFusedTiles[kNumFusedTiles] = {{128, 128, 2, 2}, {32, 128, 1, 4}, {256, 256, 2, 2}};
+const FusedTile kFusedTiles[kNumFusedTiles] = {{128, 128, 2, 2}, {32, 128, 1, 4}, {256, 256, 2, 2}, {64, 128, 1, 4}};
 
 bool ring_takes(GroupMode grp, bool a_oc, bool b_oc, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
     const int64_t lim = (int64_t)1 << 31;
@@ -28,7 +28,8 @@ static int head_of(GroupMode grp, int64_t K) {
     template __global__ void fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC>(FusedArgs);
 #define FCF_I2(MODE, GRP, BOC)      \
     FCF_I(MODE, GRP, false, BOC)    \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, false, BOC>(FusedArgs);
+    template __global__ void fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, false, BOC>(FusedArgs); \
+    template __global__ void fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, false, BOC>(FusedArgs);
 namespace {
 FCF_I2(EPI_STORE, GRP_NONE, false) FCF_I2(EPI_STORE, GRP_NONE, true)
 FCF_I2(EPI_STORE, GRP_ROWS, false) FCF_I2(EPI_STORE, GRP_ROWS, true)
@@ -42,7 +43,9 @@ FCF_I(EPI_ACT, GRP_NONE, true, false) FCF_I(EPI_ACT, GRP_NONE, true, true)
 #undef FCF_I
 
 #define FCF_K(MODE, GRP, T, AOC, BOC) \
-    (T == 0 ? (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC> : (FusedFn)fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, AOC, BOC>)
+    (T == 0   ? (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC> \
+     : T == 1 ? (FusedFn)fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, AOC, BOC>  \
+              : (FusedFn)fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, AOC, BOC>)
 
 template <>
 FusedFn fused_kernel<EPI_STORE>(GroupMode grp, int tile, bool a_oc, bool b_oc) {

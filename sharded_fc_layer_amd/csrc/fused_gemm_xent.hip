@@ -7,7 +7,8 @@ namespace fcs {
 namespace {
 #define FCF_I(MODE, BOC)                                                                           \
     template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 128, 128, 2, 2, false, BOC>(FusedArgs); \
-    template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, BOC>(FusedArgs);
+    template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, BOC>(FusedArgs); \
+    template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 64, 128, 1, 4, false, BOC>(FusedArgs);
 FCF_I(EPI_STATS, false) FCF_I(EPI_STATS, true) FCF_I(EPI_DLOGIT, false) FCF_I(EPI_DLOGIT, true)
 #undef FCF_I
 }  // namespace
@@ -19,8 +20,11 @@ FCF_I(EPI_STATS, false) FCF_I(EPI_STATS, true) FCF_I(EPI_DLOGIT, false) FCF_I(EP
         if (tile == 0)                                                                                     \
             return b_oc ? fused_gemm_kernel<MODE, GRP_NONE, 128, 128, 2, 2, false, true>                   \
                         : fused_gemm_kernel<MODE, GRP_NONE, 128, 128, 2, 2, false, false>;                 \
-        return b_oc ? fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, true>                        \
-                    : fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, false>;                      \
+        if (tile == 1)                                                                                     \
+            return b_oc ? fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, true>                    \
+                        : fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, false>;                  \
+        return b_oc ? fused_gemm_kernel<MODE, GRP_NONE, 64, 128, 1, 4, false, true>                        \
+                    : fused_gemm_kernel<MODE, GRP_NONE, 64, 128, 1, 4, false, false>;                      \
     }
 FCF_X(EPI_STATS)
 FCF_X(EPI_DLOGIT)

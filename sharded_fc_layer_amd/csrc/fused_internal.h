@@ -59,7 +59,7 @@ struct FusedArgs : GemmArgs {
 struct FusedTile {
     int bm, bn, wave_rows, wave_cols;  // the 4 waves' grid within the tile
 };
-constexpr int kNumFusedTiles = 3;
+constexpr int kNumFusedTiles = 4;
 constexpr int kRingTile = 2;  // the ring kernel's tile: see ring_takes
 extern const FusedTile kFusedTiles[kNumFusedTiles];
 typedef void (*FusedFn)(FusedArgs);
@@ -106,16 +106,26 @@ bool ring_takes(GroupMode grp, bool a_oc, bool b_oc, int64_t N, int64_t K, int64
 hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc, const FusedArgs& g,
                         hipStream_t s);
 
+// EPI_ACT for at most 32 rows, both operands reduction-contiguous (fused_skinny.hip)
+hipError_t launch_fused_skinny(const FusedArgs& g, hipStream_t s);
+
 // dst (rows x ld) = src (rows x cols) with zeros in columns cols .. ld - 1;
 // any cols and src alignment; ld a multiple of 8, dst 16-byte aligned.
-hipError_t launch_pad_any(const uint16_t* src, uint16_t* dst, int64_t rows, int64_t cols, int64_t ld, hipStream_t s);
+// rows = 0: no copy.
+struct PadCopy {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t rows, cols, ld;
+};
+hipError_t launch_pad_any(const PadCopy& a, const PadCopy& b, hipStream_t s);
 
 // out[j] = sum over p < parts of part[p * N + j], in that order
 hipError_t launch_colsum_parts(const float* part, float* out, int64_t N, int parts, hipStream_t s);
 
-// The epilogue of a split reduction: v = sum of the slices' planes in order,
-// then EPI_STORE, EPI_ACT or EPI_DACT as g says (g.C rows of g.ldc = g.N).
-hipError_t launch_split_epilogue(EpiMode mode, const FusedArgs& g, const float* planes, int splits, hipStream_t s);
+// The epilogue of a split reduction: v = sum of the slices' planes (M rows of
+// pld values, a multiple of 4) in order, then EPI_STORE, EPI_ACT or EPI_DACT.
+hipError_t launch_split_epilogue(EpiMode mode, const FusedArgs& g, const float* planes, int64_t pld, int splits,
+                                 hipStream_t s);
 // rows of its column-sum partials (EPI_DACT)
 int split_epilogue_parts(int64_t M);
 

@@ -229,54 +229,75 @@ def fc_bwd_weight_noalloc(X, dY, x_order: int = ROW, out=None, out_dtype: int = 
 
 # ---- fused operators: activations in the epilogue, the vocabulary's loss, expert layers
 
-def _alloc(shape, dtype, like, stream):
-    """A new tensor, allocated on the stream that the kernels using it run on
-    (None or torch's current stream, or another one: see _out)."""
-    import torch
-    if stream is None or _stream(stream) == torch.cuda.current_stream().cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    ts = stream if isinstance(stream, torch.cuda.Stream) else \
-        torch.cuda.ExternalStream(_stream(stream), device=like.device)
-    with torch.cuda.stream(ts):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+class _On:
+    """The stream of a call: its handle, and where its tensors are allocated
+    (on that stream, so that torch's allocator hands their memory on in its
+    order). These calls may take a few microseconds on the GPU, so the host's
+    share is kept short: the stream is looked up once."""
+    __slots__ = ("handle", "other", "device")
 
+    def __init__(self, stream, like):
+        import torch
+        self.device = like.device
+        current = torch._C._cuda_getCurrentRawStream(like.get_device() if like.is_cuda else 0)
+        self.handle = current if stream is None else _stream(stream)
+        self.other = None
+        if self.handle != current:
+            self.other = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(self.handle, device=like.device)
 
-def _workspace(need: int, what: str, like, stream):
-    """The call's workspace (None if it needs none) and its address. It lives
-    as long as the caller holds it; torch's allocator hands its memory on in
-    the order of the stream that it was allocated on."""
-    import torch
-    if need < 0:
-        raise FcError(FC_E_INVALID, what)
-    if need == 0:
-        return None, None
-    ws = _alloc((need,), torch.uint8, like, stream)
-    return ws, ws.data_ptr()
+    def empty(self, shape, dtype):
+        import torch
+        if self.other is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.other):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def given(self, t, dtype, shape, name):
+        """An output: the caller's tensor, checked, or a new one."""
+        return self.empty(shape, dtype) if t is None else _tensor(t, dtype, shape, name)
+
+    def workspace(self, need, what):
+        """The call's workspace (None if it needs none), its address and size.
+        It may be dropped after the call: its memory is handed on in stream order."""
+        if need <= 0:
+            if need < 0:
+                raise FcError(FC_E_INVALID, what)
+            return None, None, 0
+        import torch
+        ws = self.empty((need,), torch.uint8)
+        return ws, ws.data_ptr(), need
 
 
 def _tensor(t, dtype, shape, name: str):
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
         raise TypeError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA/HIP tensor")
     return t
 
 
-def _given(t, dtype, shape, name: str, like, stream):
-    """An output: the caller's tensor, checked, or a new one."""
-    return _alloc(shape, dtype, like, stream) if t is None else _tensor(t, dtype, shape, name)
+def _here(*ts) -> None:
+    """The library runs on the current device: every tensor must live there."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"a tensor is on {t.device}, but the current device is cuda:{cur}")
 
 
 def _out_type(out_dtype: int, name: str):
     import torch
-    if out_dtype not in (OUT_BF16, OUT_F32):
+    if out_dtype == OUT_BF16:
+        return torch.bfloat16
+    if out_dtype != OUT_F32:
         raise ValueError(f"{name} must be OUT_BF16 or OUT_F32")
-    return torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
+    return torch.float32
 
 
-def _aligned(*ts) -> int:
-    return int(all(t.data_ptr() % 16 == 0 for t in ts))
+def _aligned(a, b) -> int:
+    return int((a.data_ptr() | b.data_ptr()) % 16 == 0)
 
 
 def _ptr(t):
@@ -284,7 +305,7 @@ def _ptr(t):
 
 
 def _order(order: int, name: str) -> int:
-    if order not in (ROW, COL):
+    if order != ROW and order != COL:
         raise ValueError(f"{name} must be ROW or COL")
     return order
 
@@ -304,14 +325,14 @@ def fc_fwd_act(X, W, bias=None, act: int = ACT_NONE, residual=None, x_order: int
         _tensor(bias, torch.bfloat16, (N,), "bias")
     if residual is not None:
         _tensor(residual, torch.bfloat16, (M, N), "residual")
-    Y = _given(out, _out_type(out_dtype, "out_dtype"), (M, N), "out", X, stream)
-    Z = _given(z_out, torch.bfloat16, (M, N), "z_out", X, stream) if keep_z or z_out is not None else None
-    _one_device(*(t for t in (X, W, bias, residual, Y, Z) if t is not None))
-    al = _aligned(X, W)
-    ws, wp = _workspace(lib().fc_fwd_act_ws_bytes(M, K, N, x_order, w_order, al), "fc_fwd_act", X, stream)
-    _check(lib().fc_fwd_act(X.data_ptr(), x_order, W.data_ptr(), w_order, _ptr(bias), _ptr(residual), act, _ptr(Z),
-                            Y.data_ptr(), out_dtype, M, K, N, wp, 0 if ws is None else ws.numel(), _stream(stream)),
-           "fc_fwd_act")
+    on = _On(stream, X)
+    Y = on.given(out, _out_type(out_dtype, "out_dtype"), (M, N), "out")
+    Z = on.given(z_out, torch.bfloat16, (M, N), "z_out") if keep_z or z_out is not None else None
+    _here(X, W, bias, residual, Y, Z)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_fwd_act_ws_bytes(M, K, N, x_order, w_order, _aligned(X, W)), "fc_fwd_act")
+    _check(L.fc_fwd_act(X.data_ptr(), x_order, W.data_ptr(), w_order, _ptr(bias), _ptr(residual), act, _ptr(Z),
+                        Y.data_ptr(), out_dtype, M, K, N, wp, wn, on.handle), "fc_fwd_act")
     return Y if Z is None else (Y, Z)
 
 
@@ -327,15 +348,15 @@ def fc_bwd_data_act(dY, W, Z, act: int, w_order: int = ROW, bias_grad: bool = Fa
     if N2 != N:
         raise ValueError(f"dY is {M}x{N} but W is {K}x{N2}")
     _tensor(Z, torch.bfloat16, (M, K), "Z")
-    dX = _given(out, _out_type(out_dtype, "out_dtype"), (M, K), "out", dY, stream)
+    on = _On(stream, dY)
+    dX = on.given(out, _out_type(out_dtype, "out_dtype"), (M, K), "out")
     if bias_grad or db is not None:
-        db = _given(db, torch.float32, (K,), "db", dY, stream)
-    _one_device(*(t for t in (dY, W, Z, dX, db) if t is not None))
-    al = _aligned(dY, W)
-    ws, wp = _workspace(lib().fc_bwd_data_act_ws_bytes(M, K, N, w_order, al), "fc_bwd_data_act", dY, stream)
-    _check(lib().fc_bwd_data_act(dY.data_ptr(), W.data_ptr(), w_order, Z.data_ptr(), act, dX.data_ptr(), out_dtype,
-                                 _ptr(db), M, K, N, wp, 0 if ws is None else ws.numel(), _stream(stream)),
-           "fc_bwd_data_act")
+        db = on.given(db, torch.float32, (K,), "db")
+    _here(dY, W, Z, dX, db)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_bwd_data_act_ws_bytes(M, K, N, w_order, _aligned(dY, W)), "fc_bwd_data_act")
+    _check(L.fc_bwd_data_act(dY.data_ptr(), W.data_ptr(), w_order, Z.data_ptr(), act, dX.data_ptr(), out_dtype,
+                             _ptr(db), M, K, N, wp, wn, on.handle), "fc_bwd_data_act")
     return dX if db is None else (dX, db)
 
 
@@ -349,14 +370,14 @@ def fc_bwd_act(dY, Z=None, act: int = ACT_NONE, bias_grad: bool = True, keep_dz:
     M, N = dY.shape
     if Z is not None:
         _tensor(Z, torch.bfloat16, (M, N), "Z")
-    dZ = _given(out, torch.bfloat16, (M, N), "out", dY, stream) if keep_dz or out is not None else None
+    on = _On(stream, dY)
+    dZ = on.given(out, torch.bfloat16, (M, N), "out") if keep_dz or out is not None else None
     if bias_grad or db is not None:
-        db = _given(db, torch.float32, (N,), "db", dY, stream)
-    _one_device(*(t for t in (dY, Z, dZ, db) if t is not None))
-    need = lib().fc_bwd_act_ws_bytes(M, N) if db is not None else 0
-    ws, wp = _workspace(need, "fc_bwd_act", dY, stream)
-    _check(lib().fc_bwd_act(dY.data_ptr(), _ptr(Z), act, _ptr(dZ), _ptr(db), M, N, wp,
-                            0 if ws is None else ws.numel(), _stream(stream)), "fc_bwd_act")
+        db = on.given(db, torch.float32, (N,), "db")
+    _here(dY, Z, dZ, db)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_bwd_act_ws_bytes(M, N) if db is not None else 0, "fc_bwd_act")
+    _check(L.fc_bwd_act(dY.data_ptr(), _ptr(Z), act, _ptr(dZ), _ptr(db), M, N, wp, wn, on.handle), "fc_bwd_act")
     return dZ, db
 
 
@@ -377,12 +398,14 @@ def fc_xent_fwd(X, W, targets, w_order: int = ROW, vocab_start: int = 0, ignore_
     the shard of a vocabulary that starts at vocab_start)."""
     import torch
     M, K, N = _xent_operands(X, W, targets, w_order)
-    loss, lse, tlogit = (_alloc((M,), torch.float32, X, stream) for _ in range(3))
-    _one_device(X, W, targets, loss)
-    ws, wp = _workspace(lib().fc_xent_fwd_ws_bytes(M, K, N, w_order, _aligned(X, W)), "fc_xent_fwd", X, stream)
-    _check(lib().fc_xent_fwd(X.data_ptr(), W.data_ptr(), w_order, targets.data_ptr(), vocab_start, ignore_index,
-                             lse.data_ptr(), tlogit.data_ptr(), loss.data_ptr(), M, K, N, wp,
-                             0 if ws is None else ws.numel(), _stream(stream)), "fc_xent_fwd")
+    on = _On(stream, X)
+    loss, lse, tlogit = (on.empty((M,), torch.float32) for _ in range(3))
+    _here(X, W, targets, loss)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_xent_fwd_ws_bytes(M, K, N, w_order, _aligned(X, W)), "fc_xent_fwd")
+    _check(L.fc_xent_fwd(X.data_ptr(), W.data_ptr(), w_order, targets.data_ptr(), vocab_start, ignore_index,
+                         lse.data_ptr(), tlogit.data_ptr(), loss.data_ptr(), M, K, N, wp, wn, on.handle),
+           "fc_xent_fwd")
     return loss, lse, tlogit
 
 
@@ -394,14 +417,26 @@ def fc_xent_bwd(X, W, targets, lse, grad, w_order: int = ROW, vocab_start: int =
     import torch
     M, K, N = _xent_operands(X, W, targets, w_order)
     _tensor(lse, torch.float32, (M,), "lse"), _tensor(grad, torch.float32, (M,), "grad")
-    dX = _given(dX, _out_type(dx_dtype, "dx_dtype"), (M, K), "dX", X, stream)
-    dW = _out(dW, K, N, dw_dtype, X, "dW", stream)
-    _one_device(X, W, targets, lse, grad, dX, dW)
-    ws, wp = _workspace(lib().fc_xent_bwd_ws_bytes(M, K, N, w_order, _aligned(X, W)), "fc_xent_bwd", X, stream)
-    _check(lib().fc_xent_bwd(X.data_ptr(), W.data_ptr(), w_order, targets.data_ptr(), vocab_start, ignore_index,
-                             lse.data_ptr(), grad.data_ptr(), dX.data_ptr(), dx_dtype, dW.data_ptr(), dw_dtype,
-                             M, K, N, wp, 0 if ws is None else ws.numel(), _stream(stream)), "fc_xent_bwd")
+    on = _On(stream, X)
+    dX = on.given(dX, _out_type(dx_dtype, "dx_dtype"), (M, K), "dX")
+    dW = _weight_grad(on, dW, dw_dtype, (K, N), "dW")
+    _here(X, W, targets, lse, grad, dX, dW)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_xent_bwd_ws_bytes(M, K, N, w_order, _aligned(X, W)), "fc_xent_bwd")
+    _check(L.fc_xent_bwd(X.data_ptr(), W.data_ptr(), w_order, targets.data_ptr(), vocab_start, ignore_index,
+                         lse.data_ptr(), grad.data_ptr(), dX.data_ptr(), dx_dtype, dW.data_ptr(), dw_dtype,
+                         M, K, N, wp, wn, on.handle), "fc_xent_bwd")
     return dX, dW
+
+
+def _weight_grad(on, t, dtype: int, shape, name: str):
+    """A weight gradient's output of any type; adding to it needs the tensor."""
+    import torch
+    if dtype == OUT_F32_ACC and t is None:
+        raise ValueError(f"{name}: accumulating needs the existing output tensor")
+    if dtype == OUT_F32_ACC:
+        return _tensor(t, torch.float32, shape, name)
+    return on.given(t, _out_type(dtype, name), shape, name)
 
 
 def _experts(W, w_order: int):
@@ -415,16 +450,15 @@ def _experts(W, w_order: int):
     return (E, r, c) if w_order == ROW else (E, c, r)
 
 
-def _grouped(op: int, fn, P, Q, offsets, out, out_dtype: int, T: int, E: int, K: int, N: int, w_order: int, stream,
+def _grouped(op: int, fn, P, Q, offsets, out, out_dtype: int, T: int, E: int, K: int, N: int, w_order: int, on,
              what: str):
     import torch
     _tensor(offsets, torch.int64, (E + 1,), "offsets")
-    _one_device(P, Q, offsets, out)
-    need = lib().fc_grouped_ws_bytes(op, T, E, K, N, w_order, _aligned(P, Q))
-    ws, wp = _workspace(need, what, P, stream)
+    _here(P, Q, offsets, out)
+    ws, wp, wn = on.workspace(lib().fc_grouped_ws_bytes(op, T, E, K, N, w_order, _aligned(P, Q)), what)
     orders = () if op == OP_BWD_WEIGHT else (w_order,)
-    _check(fn(P.data_ptr(), Q.data_ptr(), *orders, offsets.data_ptr(), out.data_ptr(), out_dtype, T, E, K, N, wp,
-              0 if ws is None else ws.numel(), _stream(stream)), what)
+    _check(fn(P.data_ptr(), Q.data_ptr(), *orders, offsets.data_ptr(), out.data_ptr(), out_dtype, T, E, K, N, wp, wn,
+              on.handle), what)
     return out
 
 
@@ -437,8 +471,9 @@ def fc_grouped_fwd(X, W, offsets, w_order: int = ROW, out=None, out_dtype: int =
     T, K2 = X.shape
     if K2 != K:
         raise ValueError(f"inner dimensions differ: X is {T}x{K2}, W is {K}x{N}")
-    Y = _given(out, _out_type(out_dtype, "out_dtype"), (T, N), "out", X, stream)
-    return _grouped(OP_FWD, lib().fc_grouped_fwd, X, W, offsets, Y, out_dtype, T, E, K, N, w_order, stream,
+    on = _On(stream, X)
+    Y = on.given(out, _out_type(out_dtype, "out_dtype"), (T, N), "out")
+    return _grouped(OP_FWD, lib().fc_grouped_fwd, X, W, offsets, Y, out_dtype, T, E, K, N, w_order, on,
                     "fc_grouped_fwd")
 
 
@@ -449,9 +484,10 @@ def fc_grouped_bwd_data(dY, W, offsets, w_order: int = ROW, out=None, out_dtype:
     T, N2 = dY.shape
     if N2 != N:
         raise ValueError(f"dY is {T}x{N2} but W is {K}x{N}")
-    dX = _given(out, _out_type(out_dtype, "out_dtype"), (T, K), "out", dY, stream)
-    return _grouped(OP_BWD_DATA, lib().fc_grouped_bwd_data, dY, W, offsets, dX, out_dtype, T, E, K, N, w_order,
-                    stream, "fc_grouped_bwd_data")
+    on = _On(stream, dY)
+    dX = on.given(out, _out_type(out_dtype, "out_dtype"), (T, K), "out")
+    return _grouped(OP_BWD_DATA, lib().fc_grouped_bwd_data, dY, W, offsets, dX, out_dtype, T, E, K, N, w_order, on,
+                    "fc_grouped_bwd_data")
 
 
 def fc_grouped_bwd_weight(X, dY, offsets, out=None, out_dtype: int = OUT_BF16, stream=None):
@@ -466,11 +502,10 @@ def fc_grouped_bwd_weight(X, dY, offsets, out=None, out_dtype: int = OUT_BF16, s
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise TypeError("offsets must be a torch.int64 tensor of E + 1 values")
     E = offsets.shape[0] - 1
-    if out_dtype == OUT_F32_ACC and out is None:
-        raise ValueError("out: accumulating needs the existing output tensor (out=)")
-    dW = _given(out, torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32, (E, K, N), "out", X, stream)
-    return _grouped(OP_BWD_WEIGHT, lib().fc_grouped_bwd_weight, X, dY, offsets, dW, out_dtype, T, E, K, N, ROW,
-                    stream, "fc_grouped_bwd_weight")
+    on = _On(stream, X)
+    dW = _weight_grad(on, out, out_dtype, (E, K, N), "out")
+    return _grouped(OP_BWD_WEIGHT, lib().fc_grouped_bwd_weight, X, dY, offsets, dW, out_dtype, T, E, K, N, ROW, on,
+                    "fc_grouped_bwd_weight")
 
 
 STAMP_SLOTS = 8  # values per block written by fc_stamped_call
