@@ -112,9 +112,8 @@ Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t ld
 int64_t plane_ld(int64_t N) { return up(N, 64); }
 
 // FusedArgs::vec_out for rows of ld values
-int vec_rows(int64_t ld, const void* C, bool f32, const void* R, const void* Z) {
-    if (ld % 8 == 0 && !off(C, 16) && !off(R, 16) && !off(Z, 16)) return 2;
-    return ld % 4 == 0 && !off(C, f32 ? 16 : 8) && !off(R, 8) && !off(Z, 8);
+int vec_rows(int64_t ld, const void* C, const void* R, const void* Z) {
+    return ld % 8 == 0 && !off(C, 16) && !off(R, 16) && !off(Z, 16);
 }
 
 bool bad_ws(const void* ws, int64_t have, int64_t need) { return need > 0 && (!ws || have < need || off(ws, 256)); }
@@ -133,7 +132,7 @@ hipError_t run_product(EpiMode mode, const Shape& sh, bool a_oc, bool b_oc, Fuse
     p.C = planes;
     p.ldc = plane_ld(g.N);
     p.out_f32 = 1;
-    p.vec_out = 2;
+    p.vec_out = 1;
     p.accumulate = 0;
     p.c_split_stride = g.M * p.ldc;
     const hipError_t e = launch_fused(EPI_STORE, GRP_NONE, sh.tile, a_oc, b_oc, p, s);
@@ -306,14 +305,14 @@ fc_status grouped_call(int op, const void* P, const void* Q, int w_order, const 
         g.M = K, g.N = N, g.K = T;
         g.ldc = N;
         g.c_stride = K * N;
-        g.vec_out = vec_rows(N, out, f32, nullptr, nullptr);
+        g.vec_out = vec_rows(N, out, nullptr, nullptr);
         return done(launch_fused(EPI_STORE, GRP_RED, pl.tile, true, true, g, s));
     }
     const bool fwd = op == FC_OP_FWD;
     g.M = T, g.N = fwd ? N : K, g.K = fwd ? K : N;
     g.ldc = g.N;
     g.b_stride = (w_order == FC_ROW_MAJOR ? K : N) * pl.B.ld;
-    g.vec_out = vec_rows(g.N, out, f32, nullptr, nullptr);
+    g.vec_out = vec_rows(g.N, out, nullptr, nullptr);
     const bool b_oc = fwd == (w_order == FC_ROW_MAJOR);
     return done(launch_fused(EPI_STORE, GRP_ROWS, pl.tile, false, b_oc, g, s));
 }
@@ -359,7 +358,7 @@ fc_status fc_fwd_act(const void* X, fc_order x_order, const void* W, fc_order w_
     g.lda = pl.A.ld, g.ldb = pl.B.ld, g.ldc = N;
     g.accumulate = 0;
     g.out_f32 = f32;
-    g.vec_out = vec_rows(N, Y, f32, R, Z);
+    g.vec_out = vec_rows(N, Y, R, Z);
     g.act = act;
     g.bias = static_cast<const uint16_t*>(bias);
     g.R = static_cast<const uint16_t*>(R);
@@ -401,7 +400,7 @@ fc_status fc_bwd_data_act(const void* dY, const void* W, fc_order w_order, const
     g.lda = pl.A.ld, g.ldb = pl.B.ld, g.ldc = K;
     g.accumulate = 0;
     g.out_f32 = f32;
-    g.vec_out = vec_rows(K, dX, f32, nullptr, Z);
+    g.vec_out = vec_rows(K, dX, nullptr, Z);
     g.act = act;
     g.Z = static_cast<uint16_t*>(const_cast<void*>(Z));  // read only
     g.colpart = db ? reinterpret_cast<float*>(base + pl.parts_off) : nullptr;
@@ -526,7 +525,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         h.lda = pl.A.ld, h.ldb = pl.d_ld, h.ldc = N;
         h.out_f32 = wf32;
         h.accumulate = dw_dtype == FC_OUT_F32_ACCUMULATE;
-        h.vec_out = vec_rows(N, h.C, wf32, nullptr, nullptr);
+        h.vec_out = vec_rows(N, h.C, nullptr, nullptr);
         if ((e = run_product(EPI_STORE, pl.dw, true, true, h, nullptr, s)) != hipSuccess) return done(e);
         // dX = D W^T: in one go, or summed over the pieces in 32 bits
         FusedArgs d;
@@ -538,7 +537,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         d.C = last ? dX : planes;
         d.out_f32 = last ? xf32 : 1;
         d.accumulate = p > 0;
-        d.vec_out = vec_rows(d.ldc, d.C, d.out_f32, nullptr, nullptr);
+        d.vec_out = vec_rows(d.ldc, d.C, nullptr, nullptr);
         Shape sh = pl.dx;
         if (sh.splits == 1) sh.k_split = up(c, 64);
         if (sh.tile == kRingTile && c < 64) sh.tile = 0;  // a last piece of less than one stage
@@ -550,7 +549,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         d.M = M, d.N = K, d.ldc = K;
         d.accumulate = 0;
         d.out_f32 = xf32;
-        d.vec_out = vec_rows(K, dX, xf32, nullptr, nullptr);
+        d.vec_out = vec_rows(K, dX, nullptr, nullptr);
         e = launch_split_epilogue(EPI_STORE, d, planes, plane_ld(K), 1, s);
     }
     return done(e);

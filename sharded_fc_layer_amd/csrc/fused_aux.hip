@@ -9,21 +9,29 @@
 namespace fcs {
 namespace {
 
-// dst row r = src row r, then zeros up to ld; 8 values per thread and step,
-// the second copy's after the first's (one launch for both operands).
-// Source rows start anywhere: a thread's 8 values are read one by one (a
-// wave's reads still fall into the same lines).
+// dst row r = src row r, then zeros up to ld, the second copy's rows after
+// the first's (one launch for both operands): a wave takes a row at a time,
+// its lanes 8 values each. Source rows start at any element.
+typedef u16x8 u16x8_any __attribute__((aligned(2)));
 __global__ __launch_bounds__(256) void pad_any_kernel(PadCopy a, PadCopy b) {
-    const int64_t na = a.rows * (a.ld / 8), total = na + b.rows * (b.ld / 8);
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const PadCopy& p = i < na ? a : b;
-        const int64_t k = i < na ? i : i - na, per_row = p.ld / 8;
-        const int64_t r = k / per_row, c = (k - r * per_row) * 8;
-        const uint16_t* src = p.src + r * p.cols + c;
-        u16x8 v;
+    const int lane = threadIdx.x & 63;
+    const int64_t waves = (int64_t)gridDim.x * 4, total = a.rows + b.rows;
+    for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < total; i += waves) {
+        const PadCopy& p = i < a.rows ? a : b;
+        const int64_t r = i < a.rows ? i : i - a.rows;
+        const uint16_t* src = p.src + r * p.cols;
+        uint16_t* dst = p.dst + r * p.ld;
+#pragma unroll 4
+        for (int64_t c = lane * 8; c < p.ld; c += 512) {
+            u16x8 v;
+            if (c + 8 <= p.cols) {
+                v = *reinterpret_cast<const u16x8_any*>(src + c);
+            } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < p.cols ? src[e] : (uint16_t)0;
-        *reinterpret_cast<u16x8*>(p.dst + r * p.ld + c) = v;
+                for (int e = 0; e < 8; ++e) v[e] = c + e < p.cols ? src[c + e] : (uint16_t)0;
+            }
+            *reinterpret_cast<u16x8*>(dst + c) = v;
+        }
     }
 }
 
@@ -58,12 +66,11 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t nb = (g.N + 255) / 256;
     const int64_t bm = blockIdx.x / nb, n = (blockIdx.x % nb) * 256 + lane * 4;
-    const bool vec = g.vec_out != 0;
     [[maybe_unused]] __shared__ float cs_all[4][256];
     [[maybe_unused]] float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (n < g.N) {
         float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (MODE == EPI_ACT && g.bias) load4(g.bias + n, n, g.N, false, b);
+        if (MODE == EPI_ACT && g.bias) load4(g.bias + n, n, g.N, b);
         const int64_t m0 = bm * kSplitRows + wave * kRowsPerWave;
         const float* p = planes + m0 * pld + n;  // planes have pld columns, a multiple of 4 past N
         f32x4 sum[kRowsPerWave];
@@ -83,17 +90,17 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
             if constexpr (MODE == EPI_ACT) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] += b[q];
-                if (g.Z) store4_bf16(g.Z + at, n, g.N, vec, v);
+                if (g.Z) store4_bf16(g.Z + at, n, g.N, v);
                 act_values(g.act, v);
                 if (g.R) {
                     float r4[4];
-                    load4(g.R + at, n, g.N, vec, r4);
+                    load4(g.R + at, n, g.N, r4);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) v[q] += r4[q];
                 }
             } else if constexpr (MODE == EPI_DACT) {
                 float z[4];
-                load4(g.Z + at, n, g.N, vec, z);
+                load4(g.Z + at, n, g.N, z);
                 act_slopes(g.act, z);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -102,9 +109,9 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
                 }
             }
             if (g.out_f32)
-                store4_f32(static_cast<float*>(g.C) + at, n, g.N, vec, v, MODE == EPI_STORE && g.accumulate);
+                store4_f32(static_cast<float*>(g.C) + at, n, g.N, v, MODE == EPI_STORE && g.accumulate);
             else
-                store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, vec, v);
+                store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, v);
         }
     }
     if constexpr (MODE == EPI_DACT) {
@@ -125,7 +132,7 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
 // one partial row.
 __global__ __launch_bounds__(256) void act_bwd_kernel(const uint16_t* __restrict__ dY, const uint16_t* __restrict__ Z,
                                                       int act, uint16_t* __restrict__ dZ, float* __restrict__ part,
-                                                      int64_t M, int64_t N, int parts, bool vec) {
+                                                      int64_t M, int64_t N, int parts) {
     __shared__ float cs_all[4][256];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n = (int64_t)blockIdx.x * 256 + lane * 4;
@@ -136,15 +143,15 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const uint16_t* __restrict
         for (int64_t m = m0 + wave; m < m1; m += 4) {
             const int64_t at = m * N + n;
             float v[4];
-            load4(dY + at, n, N, vec, v);
+            load4(dY + at, n, N, v);
             if (Z) {
                 float z[4];
-                load4(Z + at, n, N, vec, z);
+                load4(Z + at, n, N, z);
                 act_slopes(act, z);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] *= z[q];
             }
-            if (dZ) store4_bf16(dZ + at, n, N, vec, v);
+            if (dZ) store4_bf16(dZ + at, n, N, v);
 #pragma unroll
             for (int q = 0; q < 4; ++q) cs[q] += v[q];
         }
@@ -168,26 +175,30 @@ __device__ __forceinline__ void join_sets(float& mx, float& sum, float x, float 
     mx = top;
 }
 
-// Rows' sets joined over the blocks of columns: 16 rows per block, 64 threads
-// for each with every 64th set, then pairwise in a fixed order.
+// Rows' sets joined over the blocks of columns: ROWS rows per block, 1024 /
+// ROWS threads for each with every so many-th set, then pairwise in a fixed
+// order. 16 rows make whole 64-byte pieces of a set's row; 4 give a few rows
+// enough threads.
+template <int ROWS>
 __global__ __launch_bounds__(1024) void xent_finish_kernel(const float* __restrict__ stat, int parts,
                                                            const int64_t* __restrict__ targets, int64_t v0,
                                                            int64_t ignore, int64_t M, int64_t N,
                                                            float* __restrict__ lse, float* __restrict__ tlogit,
                                                            float* __restrict__ loss) {
-    __shared__ float smx[64][17], ssum[64][17];
-    const int row = threadIdx.x & 15, sl = threadIdx.x >> 4;
-    const int64_t m = (int64_t)blockIdx.x * 16 + row;
+    constexpr int S = 1024 / ROWS;
+    __shared__ float smx[S][ROWS + 1], ssum[S][ROWS + 1];
+    const int row = threadIdx.x % ROWS, sl = threadIdx.x / ROWS;
+    const int64_t m = (int64_t)blockIdx.x * ROWS + row;
     float mx = -INFINITY, sum = 0.0f;
     if (m < M) {
 #pragma unroll 4
-        for (int p = sl; p < parts; p += 64)
+        for (int p = sl; p < parts; p += S)
             join_sets(mx, sum, stat[(int64_t)p * M + m], stat[(int64_t)(parts + p) * M + m]);
     }
     smx[sl][row] = mx, ssum[sl][row] = sum;
     __syncthreads();
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
+    for (int d = S / 2; d > 0; d >>= 1) {
         if (sl < d) {
             join_sets(mx, sum, smx[sl + d][row], ssum[sl + d][row]);
             smx[sl][row] = mx, ssum[sl][row] = sum;
@@ -210,11 +221,11 @@ __global__ __launch_bounds__(1024) void xent_finish_kernel(const float* __restri
 }  // namespace
 
 hipError_t launch_pad_any(const PadCopy& a, const PadCopy& b, hipStream_t s) {
-    const int64_t work = a.rows * (a.ld / 8) + b.rows * (b.ld / 8);
-    if (work <= 0) return hipSuccess;
+    const int64_t rows = a.rows + b.rows;
+    if (rows <= 0) return hipSuccess;
     if (a.ld % 8 != 0 || b.ld % 8 != 0 || (uintptr_t)a.dst % 16 != 0 || (uintptr_t)b.dst % 16 != 0)
         return hipErrorInvalidValue;
-    const int64_t blocks = std::min<int64_t>((work + 255) / 256, 8192);
+    const int64_t blocks = std::min<int64_t>((rows + 3) / 4, 8192);
     hipLaunchKernelGGL(pad_any_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, b);
     return hipGetLastError();
 }
@@ -240,16 +251,16 @@ hipError_t launch_split_epilogue(EpiMode mode, const FusedArgs& g, const float* 
 hipError_t launch_act_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16_t* dZ, float* part, int64_t M,
                           int64_t N, int parts, hipStream_t s) {
     if (parts < 1 || parts > 65535) return hipErrorInvalidValue;
-    const bool vec = N % 4 == 0 && (uintptr_t)dY % 8 == 0 && (uintptr_t)Z % 8 == 0 && (uintptr_t)dZ % 8 == 0;
     hipLaunchKernelGGL(act_bwd_kernel, dim3((unsigned)((N + 255) / 256), (unsigned)parts), dim3(256), 0, s, dY, Z,
-                       act, dZ, part, M, N, parts, vec);
+                       act, dZ, part, M, N, parts);
     return hipGetLastError();
 }
 
 hipError_t launch_xent_finish(const float* stat, int parts, const int64_t* targets, int64_t v0, int64_t ignore,
                               int64_t M, int64_t N, float* lse, float* tlogit, float* loss, hipStream_t s) {
-    hipLaunchKernelGGL(xent_finish_kernel, dim3((unsigned)((M + 15) / 16)), dim3(1024), 0, s, stat, parts, targets, v0,
-                       ignore, M, N, lse, tlogit, loss);
+    const int rows = M <= 1024 ? 4 : 16;
+    hipLaunchKernelGGL(rows == 4 ? xent_finish_kernel<4> : xent_finish_kernel<16>, dim3((unsigned)((M + rows - 1) / rows)),
+                       dim3(1024), 0, s, stat, parts, targets, v0, ignore, M, N, lse, tlogit, loss);
     return hipGetLastError();
 }
 

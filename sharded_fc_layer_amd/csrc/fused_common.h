@@ -38,14 +38,25 @@ __device__ __forceinline__ float rcp_f32(float x) { return __builtin_amdgcn_rcpf
 // Either takes one exponential and one reciprocal. In sigma's argument z is
 // clamped to +-64, where sigma is 0 or 1 in fp32 for every kind, so that
 // infinities meet no zeros there; NaNs pass through the final product.
+//
+// ActParams holds sigma's coefficients times -log2(e), for exp(-u) = 2^(e0 +
+// z (e1 + e3 z^2)), and c1 and 3 c3 of the slope.
 struct ActParams {
-    float c0, c1, c3, lo;
+    float e0, e1, e3, c1, c3x3, lo;
 };
 constexpr float kGeluC = 1.5957691216057308f /* 2 sqrt(2 / pi) */, kGeluA = 0.044715f;
 __device__ __forceinline__ ActParams act_params(int act) {
-    if (act == FC_ACT_SILU) return ActParams{0.0f, 1.0f, 0.0f, -INFINITY};
-    if (act == FC_ACT_GELU_TANH) return ActParams{0.0f, kGeluC, kGeluC * kGeluA, -INFINITY};
-    return ActParams{INFINITY, 0.0f, 0.0f, act == FC_ACT_RELU ? 0.0f : -INFINITY};
+    if (act == FC_ACT_SILU) return ActParams{0.0f, -kLog2e, 0.0f, 1.0f, 0.0f, -INFINITY};
+    if (act == FC_ACT_GELU_TANH)
+        return ActParams{0.0f, -kLog2e * kGeluC, -kLog2e * kGeluC * kGeluA, kGeluC, 3.0f * kGeluC * kGeluA, -INFINITY};
+    return ActParams{-INFINITY, 0.0f, 0.0f, 0.0f, 0.0f, act == FC_ACT_RELU ? 0.0f : -INFINITY};
+}
+__device__ __forceinline__ float act_sigma(const ActParams& a, float z, float z2) {
+    return rcp_f32(1.0f + __builtin_amdgcn_exp2f(a.e0 + z * (a.e1 + a.e3 * z2)));
+}
+// z within +-64; a NaN stays one
+__device__ __forceinline__ float clamp64(float z) {
+    return __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -64.0f), 64.0f);
 }
 
 // Phi(z), and exp(-z^2 / 2) in e
@@ -69,8 +80,7 @@ __device__ __forceinline__ float act_value(const ActParams& a, float z) {
         return z * normal_cdf(z, e);
     } else {
         const float zc = __builtin_amdgcn_fmed3f(z, -64.0f, 64.0f);
-        const float v = z * rcp_f32(1.0f + exp_f32(-(a.c0 + zc * (a.c1 + a.c3 * (zc * zc)))));
-        return v < a.lo ? a.lo : v;
+        return __builtin_elementwise_maximum(z * act_sigma(a, zc, zc * zc), a.lo);
     }
 }
 
@@ -78,15 +88,14 @@ __device__ __forceinline__ float act_value(const ActParams& a, float z) {
 // + z phi(z). Beyond +-64 every slope is 0 or 1.
 template <bool ERF>
 __device__ __forceinline__ float act_slope(const ActParams& a, float z) {
-    const float zc = z > 64.0f ? 64.0f : z < -64.0f ? -64.0f : z;  // a NaN stays one
+    const float zc = clamp64(z);
     if constexpr (ERF) {
         float e;
         const float c = normal_cdf(zc, e);
         return c + zc * 0.3989422804014327f * e;
     } else {
-        const float z2 = zc * zc;
-        const float s = rcp_f32(1.0f + exp_f32(-(a.c0 + zc * (a.c1 + a.c3 * z2))));
-        const float d = s + zc * s * (1.0f - s) * (a.c1 + 3.0f * a.c3 * z2);
+        const float z2 = zc * zc, s = act_sigma(a, zc, z2), t = zc * s;
+        const float d = s + (t - t * s) * (a.c1 + a.c3x3 * z2);
         return zc <= a.lo ? 0.0f : d;
     }
 }
@@ -115,11 +124,16 @@ __device__ __forceinline__ void act_slopes(int act, float (&v)[N]) {
     }
 }
 
-// 4 consecutive bf16 values, as a vector where the row allows it; columns
-// from n up to N (those past it read zeros)
-__device__ __forceinline__ void load4(const uint16_t* p, int64_t n, int64_t N, bool vec, float (&v)[4]) {
-    if (vec && n + 4 <= N) {
-        const u16x4 b = *reinterpret_cast<const u16x4*>(p);
+// 4 consecutive values of a row, or those of them that are left of column N
+// (the others read zeros). Rows start anywhere: gfx950 takes global vectors
+// at any element's address.
+typedef u16x4 u16x4_any __attribute__((aligned(2)));
+typedef bf16x4 bf16x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+__device__ __forceinline__ void load4(const uint16_t* p, int64_t n, int64_t N, float (&v)[4]) {
+    if (n + 4 <= N) {
+        const u16x4 b = *reinterpret_cast<const u16x4_any*>(p);
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = bf16_f32(b[q]);
     } else {
@@ -128,10 +142,10 @@ __device__ __forceinline__ void load4(const uint16_t* p, int64_t n, int64_t N, b
     }
 }
 
-__device__ __forceinline__ void store4_bf16(uint16_t* p, int64_t n, int64_t N, bool vec, const float (&v)[4]) {
+__device__ __forceinline__ void store4_bf16(uint16_t* p, int64_t n, int64_t N, const float (&v)[4]) {
     __bf16* c = reinterpret_cast<__bf16*>(p);
-    if (vec && n + 4 <= N) {
-        *reinterpret_cast<bf16x4*>(c) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    if (n + 4 <= N) {
+        *reinterpret_cast<bf16x4_any*>(c) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
     } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -139,11 +153,11 @@ __device__ __forceinline__ void store4_bf16(uint16_t* p, int64_t n, int64_t N, b
     }
 }
 
-__device__ __forceinline__ void store4_f32(float* c, int64_t n, int64_t N, bool vec, const float (&v)[4], bool add) {
-    if (vec && n + 4 <= N) {
+__device__ __forceinline__ void store4_f32(float* c, int64_t n, int64_t N, const float (&v)[4], bool add) {
+    if (n + 4 <= N) {
         f32x4 w{v[0], v[1], v[2], v[3]};
-        if (add) w += *reinterpret_cast<const f32x4*>(c);
-        *reinterpret_cast<f32x4*>(c) = w;
+        if (add) w += *reinterpret_cast<const f32x4_any*>(c);
+        *reinterpret_cast<f32x4_any*>(c) = w;
     } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -269,7 +283,6 @@ __device__ __forceinline__ void fused_store(const FusedArgs& g, const TilePos& t
     const int lr = lane & (MF - 1), lk = MF == 32 ? (lane >> 5) : (lane >> 4);
     const int64_t mb = t.m0 + (int64_t)wave_m * (TM * MF) + lr;
     const int64_t nb = t.n0 + (int64_t)wave_n * (TN * MF) + lk * 4;
-    const bool vec = g.vec_out != 0;
     if constexpr (MODE == EPI_STORE || MODE == EPI_ACT) {
         const int64_t c0 = (GRP == GRP_RED ? (int64_t)t.e * g.c_stride : (int64_t)t.slice * g.c_split_stride);
 #pragma unroll
@@ -280,7 +293,7 @@ __device__ __forceinline__ void fused_store(const FusedArgs& g, const TilePos& t
                 if (n >= g.N) continue;
                 [[maybe_unused]] float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 if constexpr (MODE == EPI_ACT)
-                    if (g.bias) load4(g.bias + n, n, g.N, false, b);
+                    if (g.bias) load4(g.bias + n, n, g.N, b);
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
                     const int64_t m = mb + i * MF;
@@ -292,19 +305,19 @@ __device__ __forceinline__ void fused_store(const FusedArgs& g, const TilePos& t
                     if constexpr (MODE == EPI_ACT) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) v[q] += b[q];
-                        if (g.Z) store4_bf16(g.Z + at, n, g.N, vec, v);
+                        if (g.Z) store4_bf16(g.Z + at, n, g.N, v);
                         act_values(g.act, v);
                         if (g.R) {
                             float r[4];
-                            load4(g.R + at, n, g.N, vec, r);
+                            load4(g.R + at, n, g.N, r);
 #pragma unroll
                             for (int q = 0; q < 4; ++q) v[q] += r[q];
                         }
                     }
                     if (g.out_f32)
-                        store4_f32(static_cast<float*>(g.C) + at, n, g.N, vec, v, MODE == EPI_STORE && g.accumulate);
+                        store4_f32(static_cast<float*>(g.C) + at, n, g.N, v, MODE == EPI_STORE && g.accumulate);
                     else
-                        store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, vec, v);
+                        store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, v);
                 }
             }
     } else if constexpr (MODE == EPI_DACT) {
@@ -320,7 +333,7 @@ __device__ __forceinline__ void fused_store(const FusedArgs& g, const TilePos& t
                     if (m >= t.M || n >= g.N) continue;
                     const int64_t at = m * g.ldc + n;
                     float z[4], v[4];
-                    load4(g.Z + at, n, g.N, vec, z);
+                    load4(g.Z + at, n, g.N, z);
                     act_slopes(g.act, z);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -328,9 +341,9 @@ __device__ __forceinline__ void fused_store(const FusedArgs& g, const TilePos& t
                         cs[q] += v[q];
                     }
                     if (g.out_f32)
-                        store4_f32(static_cast<float*>(g.C) + at, n, g.N, vec, v, false);
+                        store4_f32(static_cast<float*>(g.C) + at, n, g.N, v, false);
                     else
-                        store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, vec, v);
+                        store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, v);
                 }
                 if (g.colpart) {
 #pragma unroll
@@ -409,7 +422,7 @@ __device__ __forceinline__ void fused_store(const FusedArgs& g, const TilePos& t
                         const float p = exp_f32(acc[i][j][gq * 4 + q] - lse);
                         v[q] = counts && n + q < g.N ? w * (n + q == hit ? p - 1.0f : p) : 0.0f;
                     }
-                    store4_bf16(static_cast<uint16_t*>(g.C) + m * g.ldc + n, n, N8, true, v);
+                    store4_bf16(static_cast<uint16_t*>(g.C) + m * g.ldc + n, n, N8, v);
                 }
         }
     }

@@ -93,7 +93,7 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
     if (tile == kRingTile) {
         if (!ring_takes(grp, a_oc, b_oc, g.ldc, g.K, g.lda, g.ldb) || g.splits != 1) return hipErrorInvalidValue;
         const int head = head_of(grp, g.K);
-        const bool vec = g.vec_out == 2, f32 = g.out_f32 != 0, erf = g.act == FC_ACT_GELU;
+        const bool vec = g.vec_out != 0, f32 = g.out_f32 != 0, erf = g.act == FC_ACT_GELU;
         FusedFn fn;
         if (grp != GRP_NONE)
             fn = f32 ? fused_ring_grouped<true>(grp, head, vec, b_oc) : fused_ring_grouped<false>(grp, head, vec, b_oc);

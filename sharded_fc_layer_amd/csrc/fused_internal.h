@@ -31,9 +31,7 @@ enum GroupMode : int {
 // fields of the launch's modes are read.
 struct FusedArgs : GemmArgs {
     int out_f32 = 0;      // C is fp32 (else bf16)
-    // how C's rows (and R's, Z's) start: 2: pieces of 8 columns on 16-byte
-    // boundaries, 1: of 4 columns (8 bytes in bf16, 16 in fp32), 0: anywhere
-    int vec_out = 0;
+    int vec_out = 0;      // the rows of C, R and Z start on 16-byte boundaries, N is a multiple of 8
     int act = 0;          // fc_act
     const uint16_t* bias = nullptr;  // N values, or none
     const uint16_t* R = nullptr;     // M x N, or none

@@ -13,6 +13,7 @@ namespace fcs {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // A buffer over what lies at p, whose accesses at kOOB read zeros and write
 // nothing: rows and columns outside the output take that offset instead of a
@@ -22,16 +23,20 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, p ? 0x7FFFFFFF : 0, kRsrcWord3);
 }
+__device__ __forceinline__ u32x2 pack_bf16(const f32x4& v) {
+    return __builtin_bit_cast(u32x2, bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]});
+}
 __device__ __forceinline__ u32x4 pack_bf16(const float (&v)[8]) {
     return __builtin_bit_cast(u32x4, bf16x8{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3], (__bf16)v[4],
                                             (__bf16)v[5], (__bf16)v[6], (__bf16)v[7]});
 }
 
 // bf16 output whose values are computed where the accumulators lie: the
-// schedule of store_tile_bf16_staged, with value(i, j, v) applied to each
-// 4-column piece on its way into LDS. C has 16-byte rows, N8 columns.
+// schedule of store_tile_bf16_staged, with value(i, j, v) making each
+// 4-column piece on its way into LDS. C has 16-byte rows, N8 columns, of
+// which those from N on become zeros.
 template <int TN, class F>
-__device__ __forceinline__ void store_mapped_bf16(uint16_t* C, int64_t ldc, int64_t M, int64_t N8, int64_t m0,
+__device__ __forceinline__ void store_mapped_bf16(uint16_t* C, int64_t ldc, int64_t M, int64_t N, int64_t m0,
                                                   int64_t n0, int lane, const f32x4 (&acc)[8][TN], char* stage,
                                                   F value) {
     const int lr = lane & 15, lk = lane >> 4;
@@ -39,8 +44,12 @@ __device__ __forceinline__ void store_mapped_bf16(uint16_t* C, int64_t ldc, int6
     const int64_t row0 = m0 + rq, col = n0 + ch * 8;
     __bf16* cp = reinterpret_cast<__bf16*>(C) + row0 * ldc + col;
     const int64_t step = 4 * ldc;
-    const bool col_in = col < N8 && (TN == 8 || ch < 2 * TN);
-    bf16x8 v[2][4];
+    const bool col_in = col < N && (TN == 8 || ch < 2 * TN);
+    u32x4 keep;  // this lane's columns: whole pieces but where N ends
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        keep[q] = (col + 2 * q < N ? 0xFFFFu : 0u) | (col + 2 * q + 1 < N ? 0xFFFF0000u : 0u);
+    u32x4 v[2][4];
 #pragma unroll
     for (int i = 0; i <= 8; ++i) {
         if (i < 8) {  // compute and write group i
@@ -49,21 +58,20 @@ __device__ __forceinline__ void store_mapped_bf16(uint16_t* C, int64_t ldc, int6
             for (int j = 0; j < TN; ++j) {
                 const int cc = j * 16 + lk * 4;
                 const uint32_t at = row * 256 + (((cc >> 3) ^ (row & 15)) << 4) + ((cc & 7) << 1);
-                const f32x4 a = value(i, j, acc[i][j]);
-                *reinterpret_cast<bf16x4*>(stage + at) = bf16x4{(__bf16)a[0], (__bf16)a[1], (__bf16)a[2], (__bf16)a[3]};
+                *reinterpret_cast<u32x2*>(stage + at) = value(i, j, acc[i][j]);
             }
         }
         if (i > 0) {  // store group i - 1
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (col_in && row0 + 16 * (i - 1) + 4 * u < M) *reinterpret_cast<bf16x8*>(cp + u * step) = v[(i - 1) & 1][u];
+                if (col_in && row0 + 16 * (i - 1) + 4 * u < M) *reinterpret_cast<u32x4*>(cp + u * step) = v[(i - 1) & 1][u];
             cp += 4 * step;
         }
         if (i < 8) {  // read group i back
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int row = i * 16 + 4 * u + rq;
-                v[i & 1][u] = *reinterpret_cast<const bf16x8*>(stage + row * 256 + ((ch ^ (row & 15)) << 4));
+                v[i & 1][u] = *reinterpret_cast<const u32x4*>(stage + row * 256 + ((ch ^ (row & 15)) << 4)) & keep;
             }
         }
         asm volatile("" ::: "memory");  // keeps the groups in this order
@@ -73,7 +81,9 @@ __device__ __forceinline__ void store_mapped_bf16(uint16_t* C, int64_t ldc, int6
 // Elementwise epilogues: EPI_ACT, EPI_DACT, and EPI_STORE but for bf16 rows on
 // 16-byte boundaries. The tile goes through LDS in fp32, 16 rows
 // (8 KB, two buffers) at a time, and R, Z or an
-// accumulating output's values are loaded 16 rows ahead of their use; all straight-line (a loop or many branches between accumulators that
+// accumulating output's values are loaded DEPTH times 16 rows ahead of their
+// use (Z one group ahead cost 13 us a round of tiles at M = N = 8192, K =
+// 2048, its latency from HBM); all straight-line (a loop or many branches between accumulators that
 // are still to be read make the compiler spill).
 //
 // VEC: rows on 16-byte boundaries. A lane takes 8 columns of every fourth
@@ -121,14 +131,15 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
             bias[q] = bf16_f32(__builtin_amdgcn_raw_buffer_load_b16(rb, c < cols ? 2u * c : kOOB, 0, 0));
         }
     }
-    [[maybe_unused]] f32x4 old[2][RPG][2];
-    [[maybe_unused]] u16x8 in8[2][RPG];
-    [[maybe_unused]] uint16_t in1[2][RPG][2];
+    constexpr int DEPTH = VEC && MODE != EPI_STORE ? 5 : 2;  // groups whose inputs are held (more would spill)
+    [[maybe_unused]] f32x4 old[DEPTH][RPG][2];
+    [[maybe_unused]] u16x8 in8[DEPTH][RPG];
+    [[maybe_unused]] uint16_t in1[DEPTH][RPG][2];
 #define FCE_FETCH(I)                                                                                              \
     if constexpr (MODE == EPI_STORE && VEC) {                                                                     \
         _Pragma("unroll") for (int u = 0; u < RPG; ++u) _Pragma("unroll") for (int q = 0; q < 2; ++q) {           \
             const int r_ = 16 * (I) + 4 * u + rq;                                                                 \
-            old[(I) & 1][u][q] = __builtin_bit_cast(                                                              \
+            old[(I) % DEPTH][u][q] = __builtin_bit_cast(                                                              \
                 f32x4, __builtin_amdgcn_raw_buffer_load_b128(rold, inside(r_, 0) ? 4u * offset(r_, 0) : kOOB, 16 * q, 0)); \
         }                                                                                                         \
     }                                                                                                             \
@@ -136,21 +147,21 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
         _Pragma("unroll") for (int u = 0; u < RPG; ++u) {                                                         \
             const int r_ = 16 * (I) + (VEC ? 4 * u + rq : u);                                                     \
             if constexpr (VEC)                                                                                    \
-                in8[(I) & 1][u] = __builtin_bit_cast(                                                             \
+                in8[(I) % DEPTH][u] = __builtin_bit_cast(                                                             \
                     u16x8, __builtin_amdgcn_raw_buffer_load_b128(raux, inside(r_, 0) ? 2u * offset(r_, 0) : kOOB, 0, 0)); \
             else                                                                                                  \
-                _Pragma("unroll") for (int q = 0; q < 2; ++q) in1[(I) & 1][u][q] =                                \
+                _Pragma("unroll") for (int q = 0; q < 2; ++q) in1[(I) % DEPTH][u][q] =                                \
                     __builtin_amdgcn_raw_buffer_load_b16(raux, inside(r_, q) ? 2u * offset(r_, q) : kOOB, 0, 0);  \
         }                                                                                                         \
     }
-    FCE_FETCH(0)
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) { FCE_FETCH(i) }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         char* buf = stage + (i & 1) * 8192;
 #pragma unroll
         for (int j = 0; j < TN; ++j)
             *reinterpret_cast<f32x4*>(buf + lr * 512 + (((4 * j + lk) ^ ((lr & 7) << 1)) << 4)) = acc[i][j];
-        if (i + 1 < 8) FCE_FETCH(i + 1)
 #pragma unroll
         for (int u = 0; u < RPG; ++u) {
             const int r = VEC ? 4 * u + rq : u, row = 16 * i + r;
@@ -168,7 +179,7 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
                                                            ((c & 3) << 2));
                 }
             }
-            auto in = [&](int q) { return bf16_f32(VEC ? in8[i & 1][u][q] : in1[i & 1][u][q & 1]); };
+            auto in = [&](int q) { return bf16_f32(VEC ? in8[i % DEPTH][u][q] : in1[i % DEPTH][u][q & 1]); };
             if constexpr (MODE == EPI_ACT) {
 #pragma unroll
                 for (int q = 0; q < W; ++q) v[q] += bias[q];
@@ -196,7 +207,7 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
                 if constexpr (VEC) {
                     const uint32_t o = inside(row, 0) ? 4u * offset(row, 0) : kOOB;
                     f32x4 lo{v[0], v[1], v[2], v[3]}, hi{v[4], v[5], v[6], v[7]};
-                    if constexpr (MODE == EPI_STORE) lo += old[i & 1][u][0], hi += old[i & 1][u][1];
+                    if constexpr (MODE == EPI_STORE) lo += old[i % DEPTH][u][0], hi += old[i % DEPTH][u][1];
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, lo), rc, o, 0, 0);
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, hi), rc, o, 16, 0);
                 } else {
@@ -219,6 +230,7 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
                                                               inside(row, q) ? 2u * offset(row, q) : kOOB, 0, 0);
             }
         }
+        if (i + DEPTH < 8) { FCE_FETCH(i + DEPTH) }
         asm volatile("" ::: "memory");  // keeps the groups in this order
     }
 #undef FCE_FETCH
@@ -245,38 +257,40 @@ __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos&
         fused_store<MODE, GRP, 16, 8, TN, 2, 2>(g, t, wave_m, wave_n, lane, acc);
     } else if constexpr (MODE == EPI_DLOGIT) {
         const int64_t m0 = t.m0 + wave_m * 128, n0 = t.n0 + wave_n * 16 * TN;
-        // this lane's rows 16 i + lane % 16: their weight, lse, and the target
-        // as an offset from this lane's first column
-        const int last = g.N - n0 >= 16 * TN ? 16 * TN : (int)(g.N - n0) - 4 * (lane >> 4);
-        float w[8], lse[8];
-        int hit[8], lim[8];  // columns from lim on are zeros: all of a row that does not count, whatever its logits are
+        // This lane's rows 16 i + lane % 16. exp(z - lse) is one fused
+        // multiply-add and a base-2 exponential (off by |z| 2^-23 at most,
+        // before a rounding to bf16); the target's 1 is subtracted by a
+        // multiply-add with a 0 or 1 for each column of a piece; rows that do
+        // not count are masked, whatever their logits are.
+        float w[8], l2[8];
+        uint32_t live[8];
+        int hit[8];  // the target's column less this lane's first, or -1
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t m = m0 + 16 * i + (lane & 15) < t.M ? m0 + 16 * i + (lane & 15) : t.M - 1;
             const int64_t target = g.targets[m];
             w[i] = g.gw[m];
-            lse[i] = g.lse[m];
-            lim[i] = target == g.ignore ? 0 : last;
+            l2[i] = -kLog2e * g.lse[m];
+            live[i] = target == g.ignore ? 0u : 0xFFFFFFFFu;
             const uint64_t at = (uint64_t)target - (uint64_t)g.v0 - (uint64_t)(n0 + 4 * (lane >> 4));
-            hit[i] = at < (uint64_t)(16 * TN) ? (int)at : -1;
+            hit[i] = at < (uint64_t)(16 * TN) && (at & 15) < 4 ? (int)at : -1;
         }
-        const int64_t N8 = (g.N + 7) / 8 * 8;
-        store_mapped_bf16<TN>(static_cast<uint16_t*>(g.C), g.ldc, t.M, N8, m0, n0, lane, acc, stage,
+        store_mapped_bf16<TN>(static_cast<uint16_t*>(g.C), g.ldc, t.M, g.N, m0, n0, lane, acc, stage,
                               [&](int i, int j, const f32x4& z) {
+                                  const float here = hit[i] >> 4 == j ? 1.0f : 0.0f;
                                   f32x4 d;
 #pragma unroll
                                   for (int q = 0; q < 4; ++q) {
-                                      float p = exp_f32(z[q] - lse[i]);
-                                      p = 16 * j + q == hit[i] ? p - 1.0f : p;
-                                      d[q] = 16 * j + q < lim[i] ? w[i] * p : 0.0f;
+                                      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[q], kLog2e, l2[i]));
+                                      d[q] = w[i] * __builtin_fmaf(-here, (hit[i] & 3) == q ? 1.0f : 0.0f, p);
                                   }
-                                  return d;
+                                  return pack_bf16(d) & live[i];
                               });
     } else if constexpr (MODE == EPI_STORE && VEC && !KIND) {
         const int64_t at = (GRP == GRP_RED ? (int64_t)t.e * g.c_stride : 0) + t.row0 * g.ldc;
         store_mapped_bf16<TN>(static_cast<uint16_t*>(g.C) + at, g.ldc, t.M, g.N, t.m0 + wave_m * 128,
                               t.n0 + wave_n * 16 * TN, lane, acc, stage,
-                              [](int, int, const f32x4& v) { return v; });
+                              [](int, int, const f32x4& v) { return pack_bf16(v); });
     } else {
         ring_elementwise<MODE, GRP, TN, KIND, VEC>(g, t, wave_m, wave_n, lane, acc, stage);
     }

@@ -75,27 +75,26 @@ __global__ __launch_bounds__(64 * WAVES) void fused_skinny_kernel(FusedArgs g) {
     for (int q = 1; q < WAVES; ++q) s += part[q][wave][lane];
     const int64_t m = 16 * wave + lr, n = n0 + 4 * lk;
     if (m >= g.M || n >= g.N) return;
-    const bool vec = g.vec_out != 0;
     const int64_t at = m * g.ldc + n;
     float v[4] = {s[0], s[1], s[2], s[3]};
     if (g.bias) {
         float b[4];
-        load4(g.bias + n, n, g.N, false, b);
+        load4(g.bias + n, n, g.N, b);
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] += b[q];
     }
-    if (g.Z) store4_bf16(g.Z + at, n, g.N, vec, v);
+    if (g.Z) store4_bf16(g.Z + at, n, g.N, v);
     act_values(g.act, v);
     if (g.R) {
         float r[4];
-        load4(g.R + at, n, g.N, vec, r);
+        load4(g.R + at, n, g.N, r);
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] += r[q];
     }
     if (g.out_f32)
-        store4_f32(static_cast<float*>(g.C) + at, n, g.N, vec, v, false);
+        store4_f32(static_cast<float*>(g.C) + at, n, g.N, v, false);
     else
-        store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, vec, v);
+        store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, v);
 }
 
 }  // namespace
