@@ -23,36 +23,40 @@ __device__ __forceinline__ float exp_f32(float x) { return __builtin_amdgcn_exp2
 // 1 / x by the hardware's reciprocal (one ulp)
 __device__ __forceinline__ float rcp_f32(float x) { return __builtin_amdgcn_rcpf(x); }
 
-// The activations are of two kinds, so that an epilogue's code holds one of
-// them without branches between its rows:
+// The activations are of three kinds, so that an epilogue's code holds one of
+// them without branches between its values:
 //
-// * z sigma(z (c1 + c3 z^2)), not below lo: silu (c1 = 1, c3 = 0); gelu by
-//   tanh, since (1 + tanh u) / 2 = sigma(2 u) with u = sqrt(2 / pi) (z +
-//   0.044715 z^3), which written so has no cancellation for negative z; none
-//   and relu as sigma = 1 (c0 = inf), relu with lo = 0.
-// * z Phi(z), gelu with the exact normal distribution function: Phi(z) = 1 -
-//   q(|z|) for z > 0, else q(|z|), where q(x) = exp(-x^2 / 2) P(t) / 2, t =
-//   1 / (1 + 0.3275911 x / sqrt 2), P of degree 5: Abramowitz and Stegun,
+// * kLinear: z, not below lo (none; relu with lo = 0);
+// * kSigmoid: z sigma(u(z)), u = z (c1 + c3 z^2): silu (c1 = 1, c3 = 0) and gelu
+//   by tanh, since (1 + tanh(u / 2)) / 2 = sigma(u) with u / 2 = sqrt(2 / pi) (z
+//   + 0.044715 z^3), which written so has no cancellation for negative z;
+// * kNormal: z Phi(z), gelu with the exact normal distribution function:
+//   Phi(z) = 1 - q(|z|) for z > 0, else q(|z|), where q(x) = exp(-x^2 / 2) P(t) /
+//   2, t = 1 / (1 + 0.3275911 x / sqrt 2), P of degree 5: Abramowitz and Stegun,
 //   Handbook of Mathematical Functions, 7.1.26, off by at most 1.5e-7 in erf.
 //
-// Either takes one exponential and one reciprocal. In sigma's argument z is
-// clamped to +-64, where sigma is 0 or 1 in fp32 for every kind, so that
-// infinities meet no zeros there; NaNs pass through the final product.
-//
-// ActParams holds sigma's coefficients times -log2(e), for exp(-u) = 2^(e0 +
-// z (e1 + e3 z^2)), and c1 and 3 c3 of the slope.
+// The last two take one exponential and one reciprocal. ActParams holds u's
+// coefficients times -log2(e), for exp(-u) = 2^(z (e1 + e3 z^2)), and c1 and 3
+// c3 of the slope. silu's e3 is -1e-30 instead of 0: beneath e1's last bit up
+// to |z| = 1e11 and still no matter beyond, where sigma is 0 or 1, it keeps
+// an overflowing z^2 from meeting a zero.
+enum ActKind : int { kLinear = 0, kSigmoid = 1, kNormal = 2 };
+__host__ __device__ inline int act_kind(int act) {
+    return act == FC_ACT_GELU ? kNormal : act == FC_ACT_GELU_TANH || act == FC_ACT_SILU ? kSigmoid : kLinear;
+}
 struct ActParams {
-    float e0, e1, e3, c1, c3x3, lo;
+    float e1, e3, c1, c3x3, lo, cut;  // cut: the slope is 0 up to there (NaN: nowhere)
 };
 constexpr float kGeluC = 1.5957691216057308f /* 2 sqrt(2 / pi) */, kGeluA = 0.044715f;
 __device__ __forceinline__ ActParams act_params(int act) {
-    if (act == FC_ACT_SILU) return ActParams{0.0f, -kLog2e, 0.0f, 1.0f, 0.0f, -INFINITY};
+    if (act == FC_ACT_SILU) return ActParams{-kLog2e, -1e-30f, 1.0f, 0.0f, 0.0f, 0.0f};
     if (act == FC_ACT_GELU_TANH)
-        return ActParams{0.0f, -kLog2e * kGeluC, -kLog2e * kGeluC * kGeluA, kGeluC, 3.0f * kGeluC * kGeluA, -INFINITY};
-    return ActParams{-INFINITY, 0.0f, 0.0f, 0.0f, 0.0f, act == FC_ACT_RELU ? 0.0f : -INFINITY};
+        return ActParams{-kLog2e * kGeluC, -kLog2e * kGeluC * kGeluA, kGeluC, 3.0f * kGeluC * kGeluA, 0.0f, 0.0f};
+    if (act == FC_ACT_RELU) return ActParams{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    return ActParams{0.0f, 0.0f, 0.0f, 0.0f, -INFINITY, NAN};
 }
 __device__ __forceinline__ float act_sigma(const ActParams& a, float z, float z2) {
-    return rcp_f32(1.0f + __builtin_amdgcn_exp2f(a.e0 + z * (a.e1 + a.e3 * z2)));
+    return rcp_f32(1.0f + __builtin_amdgcn_exp2f(z * (a.e1 + a.e3 * z2)));
 }
 // z within +-64; a NaN stays one
 __device__ __forceinline__ float clamp64(float z) {
@@ -73,54 +77,70 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
     return z > 0.0f ? 1.0f - q : q;
 }
 
-template <bool ERF>
+template <int KIND>
 __device__ __forceinline__ float act_value(const ActParams& a, float z) {
-    if constexpr (ERF) {
+    if constexpr (KIND == kNormal) {
         float e;
         return z * normal_cdf(z, e);
+    } else if constexpr (KIND == kSigmoid) {
+        return z * act_sigma(a, z, z * z);
     } else {
-        const float zc = __builtin_amdgcn_fmed3f(z, -64.0f, 64.0f);
-        return __builtin_elementwise_maximum(z * act_sigma(a, zc, zc * zc), a.lo);
+        return __builtin_elementwise_maximum(z, a.lo);  // a NaN stays one
     }
 }
 
-// d act / dz: with s = sigma(u(z)), s + z s (1 - s) u'(z), 0 up to lo; Phi(z)
-// + z phi(z). Beyond +-64 every slope is 0 or 1.
-template <bool ERF>
+// d act / dz: 1, but 0 up to cut; with s = sigma(u(z)), s + z s (1 - s) u'(z);
+// Phi(z) + z phi(z). Beyond +-64 every slope is 0 or 1 in fp32, and the clamp
+// keeps infinities from meeting zeros.
+template <int KIND>
 __device__ __forceinline__ float act_slope(const ActParams& a, float z) {
+    if constexpr (KIND == kLinear) return z <= a.cut ? 0.0f : 1.0f;
     const float zc = clamp64(z);
-    if constexpr (ERF) {
+    if constexpr (KIND == kNormal) {
         float e;
         const float c = normal_cdf(zc, e);
         return c + zc * 0.3989422804014327f * e;
     } else {
         const float z2 = zc * zc, s = act_sigma(a, zc, z2), t = zc * s;
-        const float d = s + (t - t * s) * (a.c1 + a.c3x3 * z2);
-        return zc <= a.lo ? 0.0f : d;
+        return s + (t - t * s) * (a.c1 + a.c3x3 * z2);
     }
 }
 
-// over several values, with one branch on the kind
-template <int N>
-__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
+// over several values (an array or a vector), with one branch on the kind
+template <class V>
+__device__ __forceinline__ void act_values(int act, V& v) {
+    constexpr int N = sizeof(V) / 4;
     const ActParams a = act_params(act);
-    if (act == FC_ACT_GELU) {
+    switch (act_kind(act)) {
+        case kNormal:
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[q] = act_value<true>(a, v[q]);
-    } else {
+            for (int q = 0; q < N; ++q) v[q] = act_value<kNormal>(a, v[q]);
+            break;
+        case kSigmoid:
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[q] = act_value<false>(a, v[q]);
+            for (int q = 0; q < N; ++q) v[q] = act_value<kSigmoid>(a, v[q]);
+            break;
+        default:
+#pragma unroll
+            for (int q = 0; q < N; ++q) v[q] = act_value<kLinear>(a, v[q]);
     }
 }
-template <int N>
-__device__ __forceinline__ void act_slopes(int act, float (&v)[N]) {
+template <class V>
+__device__ __forceinline__ void act_slopes(int act, V& v) {
+    constexpr int N = sizeof(V) / 4;
     const ActParams a = act_params(act);
-    if (act == FC_ACT_GELU) {
+    switch (act_kind(act)) {
+        case kNormal:
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[q] = act_slope<true>(a, v[q]);
-    } else {
+            for (int q = 0; q < N; ++q) v[q] = act_slope<kNormal>(a, v[q]);
+            break;
+        case kSigmoid:
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[q] = act_slope<false>(a, v[q]);
+            for (int q = 0; q < N; ++q) v[q] = act_slope<kSigmoid>(a, v[q]);
+            break;
+        default:
+#pragma unroll
+            for (int q = 0; q < N; ++q) v[q] = act_slope<kLinear>(a, v[q]);
     }
 }
 
@@ -269,162 +289,6 @@ __device__ __forceinline__ TilePos tile_position(const FusedArgs& g) {
         t.kend = t.kbeg + g.k_split < g.K ? t.kbeg + g.k_split : g.K;
         t.any = true;
         return t;
-    }
-}
-
-// Epilogue of one wave's tile of TM x TN blocks of MF x MF (the B fragment as
-// the MFMA's source A: a lane holds, per block, 4 consecutive columns at
-// 8 grp + 4 lk of row lr). wave_m, wave_n: the wave's place in the block's
-// wave_rows x wave_cols grid.
-template <EpiMode MODE, GroupMode GRP, int MF, int TM, int TN, int WR, int WC>
-__device__ __forceinline__ void fused_store(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
-                                            const typename AccT<MF>::type (&acc)[TM][TN]) {
-    constexpr int GR = MF == 32 ? 4 : 1;
-    const int lr = lane & (MF - 1), lk = MF == 32 ? (lane >> 5) : (lane >> 4);
-    const int64_t mb = t.m0 + (int64_t)wave_m * (TM * MF) + lr;
-    const int64_t nb = t.n0 + (int64_t)wave_n * (TN * MF) + lk * 4;
-    if constexpr (MODE == EPI_STORE || MODE == EPI_ACT) {
-        const int64_t c0 = (GRP == GRP_RED ? (int64_t)t.e * g.c_stride : (int64_t)t.slice * g.c_split_stride);
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int gq = 0; gq < GR; ++gq) {
-                const int64_t n = nb + j * MF + gq * 8;
-                if (n >= g.N) continue;
-                [[maybe_unused]] float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if constexpr (MODE == EPI_ACT)
-                    if (g.bias) load4(g.bias + n, n, g.N, b);
-#pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    const int64_t m = mb + i * MF;
-                    if (m >= t.M) continue;
-                    const int64_t at = c0 + (t.row0 + m) * g.ldc + n;
-                    float v[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = acc[i][j][gq * 4 + q];
-                    if constexpr (MODE == EPI_ACT) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] += b[q];
-                        if (g.Z) store4_bf16(g.Z + at, n, g.N, v);
-                        act_values(g.act, v);
-                        if (g.R) {
-                            float r[4];
-                            load4(g.R + at, n, g.N, r);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) v[q] += r[q];
-                        }
-                    }
-                    if (g.out_f32)
-                        store4_f32(static_cast<float*>(g.C) + at, n, g.N, v, MODE == EPI_STORE && g.accumulate);
-                    else
-                        store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, v);
-                }
-            }
-    } else if constexpr (MODE == EPI_DACT) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int gq = 0; gq < GR; ++gq) {
-                const int64_t n = nb + j * MF + gq * 8;
-                float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    const int64_t m = mb + i * MF;
-                    if (m >= t.M || n >= g.N) continue;
-                    const int64_t at = m * g.ldc + n;
-                    float z[4], v[4];
-                    load4(g.Z + at, n, g.N, z);
-                    act_slopes(g.act, z);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        v[q] = acc[i][j][gq * 4 + q] * z[q];
-                        cs[q] += v[q];
-                    }
-                    if (g.out_f32)
-                        store4_f32(static_cast<float*>(g.C) + at, n, g.N, v, false);
-                    else
-                        store4_bf16(static_cast<uint16_t*>(g.C) + at, n, g.N, v);
-                }
-                if (g.colpart) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                        for (int d = 1; d < MF; d <<= 1) cs[q] += __shfl_xor(cs[q], d);
-                        if (lr == 0 && n + q < g.N)
-                            g.colpart[((int64_t)t.tm * WR + wave_m) * g.N + n + q] = cs[q];
-                    }
-                }
-            }
-    } else if constexpr (MODE == EPI_STATS) {
-        // The sum is taken against the lane group's own maximum; infinite
-        // maxima are replaced by 0 so that no infinity is subtracted from
-        // itself (a row of -inf sums to 0, one with +inf to inf).
-        const int part = t.tn * WC + wave_n;
-        const int parts = (int)((g.N + (WC * TN * MF) - 1) / (WC * TN * MF)) * WC;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int64_t m = mb + i * MF;
-            // unsigned: a target far below v0 wraps past every column
-            const int64_t target = m < t.M ? (int64_t)((uint64_t)g.targets[m] - (uint64_t)g.v0) : -1;
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int gq = 0; gq < GR; ++gq)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int64_t n = nb + j * MF + gq * 8 + q;
-                        if (n < g.N) mx = fmaxf(mx, acc[i][j][gq * 4 + q]);
-                    }
-#pragma unroll
-            for (int d = MF; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-            const float ref = __builtin_isinf(mx) ? 0.0f : mx;
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int gq = 0; gq < GR; ++gq)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int64_t n = nb + j * MF + gq * 8 + q;
-                        const float v = acc[i][j][gq * 4 + q];
-                        if (n < g.N) sum += exp_f32(v - ref);
-                        if (n == target && n < g.N) g.tlogit[m] = v;
-                    }
-#pragma unroll
-            for (int d = MF; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-            if (lk == 0 && m < t.M) {
-                g.stat[(int64_t)part * t.M + m] = mx;
-                g.stat[(int64_t)(parts + part) * t.M + m] = sum;
-            }
-        }
-    } else {  // EPI_DLOGIT
-        // C is a buffer of this library with 16-byte rows: columns from N to
-        // the next multiple of 8 are zeros, for the product that reduces over them
-        const int64_t N8 = (g.N + 7) / 8 * 8;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int64_t m = mb + i * MF;
-            if (m >= t.M) continue;
-            const int64_t target = g.targets[m];
-            const bool counts = target != g.ignore;
-            const int64_t hit = (int64_t)((uint64_t)target - (uint64_t)g.v0);
-            const float w = g.gw[m], lse = g.lse[m];
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int gq = 0; gq < GR; ++gq) {
-                    const int64_t n = nb + j * MF + gq * 8;
-                    if (n >= N8) continue;
-                    float v[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float p = exp_f32(acc[i][j][gq * 4 + q] - lse);
-                        v[q] = counts && n + q < g.N ? w * (n + q == hit ? p - 1.0f : p) : 0.0f;
-                    }
-                    store4_bf16(static_cast<uint16_t*>(g.C) + m * g.ldc + n, n, N8, v);
-                }
-        }
     }
 }
 

@@ -93,21 +93,24 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
     if (tile == kRingTile) {
         if (!ring_takes(grp, a_oc, b_oc, g.ldc, g.K, g.lda, g.ldb) || g.splits != 1) return hipErrorInvalidValue;
         const int head = head_of(grp, g.K);
-        const bool vec = g.vec_out != 0, f32 = g.out_f32 != 0, erf = g.act == FC_ACT_GELU;
+        const bool vec = g.vec_out != 0, f32 = g.out_f32 != 0;
+        const int kind = act_kind(g.act);
         FusedFn fn;
         if (grp != GRP_NONE)
-            fn = f32 ? fused_ring_grouped<true>(grp, head, vec, b_oc) : fused_ring_grouped<false>(grp, head, vec, b_oc);
+            fn = f32 ? fused_ring_grouped<1>(grp, head, vec, b_oc) : fused_ring_grouped<0>(grp, head, vec, b_oc);
         else if (mode == EPI_STORE)
-            fn = f32 ? fused_ring<EPI_STORE, true>(head, vec, a_oc, b_oc)
-                     : fused_ring<EPI_STORE, false>(head, vec, a_oc, b_oc);
+            fn = f32 ? fused_ring<EPI_STORE, 1>(head, vec, a_oc, b_oc) : fused_ring<EPI_STORE, 0>(head, vec, a_oc, b_oc);
         else if (mode == EPI_ACT)
-            fn = erf ? fused_ring<EPI_ACT, true>(head, vec, a_oc, b_oc) : fused_ring<EPI_ACT, false>(head, vec, a_oc, b_oc);
+            fn = kind == kNormal    ? fused_ring<EPI_ACT, kNormal>(head, vec, a_oc, b_oc)
+                 : kind == kSigmoid ? fused_ring<EPI_ACT, kSigmoid>(head, vec, a_oc, b_oc)
+                                    : fused_ring<EPI_ACT, kLinear>(head, vec, a_oc, b_oc);
         else if (mode == EPI_DACT)
-            fn = erf ? fused_ring<EPI_DACT, true>(head, vec, a_oc, b_oc)
-                     : fused_ring<EPI_DACT, false>(head, vec, a_oc, b_oc);
+            fn = kind == kNormal    ? fused_ring<EPI_DACT, kNormal>(head, vec, a_oc, b_oc)
+                 : kind == kSigmoid ? fused_ring<EPI_DACT, kSigmoid>(head, vec, a_oc, b_oc)
+                                    : fused_ring<EPI_DACT, kLinear>(head, vec, a_oc, b_oc);
         else
-            fn = mode == EPI_STATS ? fused_ring<EPI_STATS, false>(head, true, a_oc, b_oc)
-                                   : fused_ring<EPI_DLOGIT, false>(head, true, a_oc, b_oc);
+            fn = mode == EPI_STATS ? fused_ring<EPI_STATS, 0>(head, true, a_oc, b_oc)
+                                   : fused_ring<EPI_DLOGIT, 0>(head, true, a_oc, b_oc);
         if (!fn) return hipErrorInvalidValue;
         hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, g);
         return hipGetLastError();

@@ -11,7 +11,7 @@
 // length may differ from block to block (ragged groups) and may be zero.
 #pragma once
 
-#include "fused_common.h"
+#include "fused_epilogue.h"
 
 namespace fcs {
 namespace {
@@ -153,7 +153,20 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
         }
         waitcnt<0, 0>();  // drain the trailing loads
     }
-    fused_store<MODE, GRP, 32, TM, TN, WR, WC>(g, t, wave_m, wave_n, lane, acc);
+    // the stages become staging space, a wave's rows of WTN fp32 values each:
+    // no wave may still read them
+    __builtin_amdgcn_s_barrier();
+    static_assert(WTM * WTN * 4 * 4 <= (int)sizeof(smem), "staging space");
+    char* stage = smem + wave * (WTM * WTN * 4);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) stage_block<32, WTN>(stage, 32 * i, 32 * j, lane, acc[i][j]);
+    Epilogue<MODE, WTN> e(g, t, t.n0 + wn0, lane);
+    constexpr int kStep = 64 / (WTN / 8);  // rows per access
+    e.template walk<WTM / kStep >= 4 ? 4 : WTM / kStep>(stage, t.m0 + wm0, WTM, output_base<GRP>(g, t), t.tn * WC + wave_n,
+                                                        (int)((g.N + BN - 1) / BN) * WC);
+    e.finish((int64_t)t.tm * WR + wave_m);
 }
 
 

@@ -31,7 +31,7 @@ enum GroupMode : int {
 // fields of the launch's modes are read.
 struct FusedArgs : GemmArgs {
     int out_f32 = 0;      // C is fp32 (else bf16)
-    int vec_out = 0;      // the rows of C, R and Z start on 16-byte boundaries, N is a multiple of 8
+    int vec_out = 0;      // ring kernel: the rows of C, R and Z start on 16-byte boundaries, N is a multiple of 8
     int act = 0;          // fc_act
     const uint16_t* bias = nullptr;  // N values, or none
     const uint16_t* R = nullptr;     // M x N, or none
@@ -67,9 +67,9 @@ template <EpiMode MODE>
 FusedFn fused_kernel(GroupMode grp, int tile, bool a_oc, bool b_oc);
 // The ring kernel's (fused_ring_*.hip), 256 x 256 block tiles: one product, or
 // an expert layer's (EPI_STORE).
-template <EpiMode MODE, bool KIND>
+template <EpiMode MODE, int KIND>
 FusedFn fused_ring(int head, bool vec, bool a_oc, bool b_oc);
-template <bool KIND>
+template <int KIND>
 FusedFn fused_ring_grouped(GroupMode grp, int head, bool vec, bool b_oc);
 #define FCU_DECLARE(MODE) \
     template <>           \
@@ -82,20 +82,22 @@ FCU_DECLARE(EPI_ACT)
 FCU_DECLARE(EPI_DACT)
 FCU_DECLARE(EPI_STATS)
 FCU_DECLARE(EPI_DLOGIT)
-FCU_DECLARE_RING(EPI_STORE, false)
-FCU_DECLARE_RING(EPI_STORE, true)
-FCU_DECLARE_RING(EPI_ACT, false)
-FCU_DECLARE_RING(EPI_ACT, true)
-FCU_DECLARE_RING(EPI_DACT, false)
-FCU_DECLARE_RING(EPI_DACT, true)
-FCU_DECLARE_RING(EPI_STATS, false)
-FCU_DECLARE_RING(EPI_DLOGIT, false)
+FCU_DECLARE_RING(EPI_STORE, 0)
+FCU_DECLARE_RING(EPI_STORE, 1)
+FCU_DECLARE_RING(EPI_ACT, 0)
+FCU_DECLARE_RING(EPI_ACT, 1)
+FCU_DECLARE_RING(EPI_ACT, 2)
+FCU_DECLARE_RING(EPI_DACT, 0)
+FCU_DECLARE_RING(EPI_DACT, 1)
+FCU_DECLARE_RING(EPI_DACT, 2)
+FCU_DECLARE_RING(EPI_STATS, 0)
+FCU_DECLARE_RING(EPI_DLOGIT, 0)
 #undef FCU_DECLARE
 #undef FCU_DECLARE_RING
 template <>
-FusedFn fused_ring_grouped<false>(GroupMode grp, int head, bool vec, bool b_oc);
+FusedFn fused_ring_grouped<0>(GroupMode grp, int head, bool vec, bool b_oc);
 template <>
-FusedFn fused_ring_grouped<true>(GroupMode grp, int head, bool vec, bool b_oc);
+FusedFn fused_ring_grouped<1>(GroupMode grp, int head, bool vec, bool b_oc);
 
 // Whether the ring kernel can run a product: an output-contiguous operand has
 // to lie within 2 GiB, as do 256 rows of a reduction-contiguous one and 128 of

@@ -1,6 +1,6 @@
-// Ring-kernel instances: activation epilogue, exact gelu.
+// Ring-kernel instances: activation epilogue, none and relu.
 #define FCU_MODE EPI_ACT
-#define FCU_KIND true
+#define FCU_KIND 0
 #define FCU_GROUPED 0
 #define FCU_ANY_ROWS 1
 #define FCU_COLUMN_MAJOR_A 1

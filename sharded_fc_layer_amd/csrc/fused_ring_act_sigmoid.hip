@@ -1,0 +1,7 @@
+// Ring-kernel instances: activation epilogue, silu and gelu by tanh.
+#define FCU_MODE EPI_ACT
+#define FCU_KIND 1
+#define FCU_GROUPED 0
+#define FCU_ANY_ROWS 1
+#define FCU_COLUMN_MAJOR_A 1
+#include "fused_ring_table.inc"

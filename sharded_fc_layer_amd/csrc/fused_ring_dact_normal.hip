@@ -1,6 +1,6 @@
 // Ring-kernel instances: activation gradient epilogue, exact gelu.
 #define FCU_MODE EPI_DACT
-#define FCU_KIND true
+#define FCU_KIND 2
 #define FCU_GROUPED 0
 #define FCU_ANY_ROWS 1
 #define FCU_COLUMN_MAJOR_A 0

@@ -1,6 +1,6 @@
 // Ring-kernel instances: cross entropy's gradient of the logits.
 #define FCU_MODE EPI_DLOGIT
-#define FCU_KIND false
+#define FCU_KIND 0
 #define FCU_GROUPED 0
 #define FCU_ANY_ROWS 0
 #define FCU_COLUMN_MAJOR_A 0

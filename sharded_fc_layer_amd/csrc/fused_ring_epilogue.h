@@ -93,9 +93,9 @@ __device__ __forceinline__ void store_mapped_bf16(uint16_t* C, int64_t ldc, int6
 // Either way a lane keeps its columns: the bias is loaded once and the column
 // sums stay in registers.
 //
-// KIND: for EPI_ACT and EPI_DACT, the activation with the exact normal
-// distribution (fused_common.h); for EPI_STORE, an fp32 output.
-template <EpiMode MODE, GroupMode GRP, int TN, bool KIND, bool VEC>
+// KIND: for EPI_ACT and EPI_DACT, the activation's (ActKind); for EPI_STORE, 1
+// for an fp32 output.
+template <EpiMode MODE, GroupMode GRP, int TN, int KIND, bool VEC>
 __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
                                                  const f32x4 (&acc)[8][TN], char* stage) {
     static_assert(TN == 8, "128 columns to a wave");
@@ -109,7 +109,7 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
     const int rows = t.M - m0 > 128 ? 128 : t.M > m0 ? (int)(t.M - m0) : 0;
     const int cols = g.N - n0 > 128 ? 128 : g.N > n0 ? (int)(g.N - n0) : 0;
     const uint32_t ldc = (uint32_t)g.ldc;
-    const bool f32 = MODE == EPI_STORE ? KIND : g.out_f32 != 0;
+    const bool f32 = MODE == EPI_STORE ? KIND != 0 : g.out_f32 != 0;
     const int esz = f32 ? 4 : 2;
     const __amdgpu_buffer_rsrc_t rc = buffer_at(static_cast<char*>(g.C) + at0 * esz);
     // an accumulating output's old values; zeros where there are none
@@ -194,7 +194,11 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
                                                                   inside(row, q) ? 2u * offset(row, q) : kOOB, 0, 0);
                 }
 #pragma unroll
-                for (int q = 0; q < W; ++q) v[q] = act_value<KIND>(a, v[q]) + in(q);
+                for (int q = 0; q < W; ++q) v[q] = act_value<KIND>(a, v[q]);
+                if (g.R) {
+#pragma unroll
+                    for (int q = 0; q < W; ++q) v[q] += in(q);
+                }
             } else if constexpr (MODE == EPI_DACT) {
                 // rows and columns outside are zeros in v: their loads read zeros
 #pragma unroll
@@ -250,19 +254,82 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
     }
 }
 
-template <EpiMode MODE, GroupMode GRP, int TN, bool KIND, bool VEC>
+// The cross entropy's row statistics, where the accumulators lie: a lane has
+// 4 TN values of each of 8 rows, 4 lanes a row. Maximum, then the sum of
+// exponentials against it, as one multiply-add and a base-2 exponential each:
+// the rounding of -max log2(e) scales the whole sum, by max 2^-24, which is
+// less than a last bit of the logarithm that is returned. An infinite maximum
+// is replaced by 0 so that no infinity is subtracted from itself (a row of -inf
+// sums to 0, one with +inf to inf). Only the blocks at the right edge, and
+// only rows whose target is here, take the steps for those.
+template <int TN>
+__device__ __forceinline__ void ring_stats(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
+                                           const f32x4 (&acc)[8][TN]) {
+    const int lr = lane & 15, lk = lane >> 4;
+    const int64_t m0 = t.m0 + wave_m * 128 + lr, n0 = t.n0 + wave_n * 16 * TN + 4 * lk;
+    const bool edge = t.n0 + 32 * TN > g.N;
+    const int last = g.N - n0 >= 16 * TN ? 16 * TN : g.N > n0 ? (int)(g.N - n0) : 0;  // this lane's columns end there
+    const int part = t.tn * 2 + wave_n, parts = (int)((g.N + 32 * TN - 1) / (32 * TN)) * 2;
+    int hit[8];  // the target's column less n0, or -1
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t m = m0 + 16 * i;
+        // unsigned: a target far below v0 wraps past every column
+        const uint64_t at = (uint64_t)g.targets[m < t.M ? m : t.M - 1] - (uint64_t)g.v0 - (uint64_t)n0;
+        hit[i] = at < (uint64_t)last && (at & 15) < 4 && m < t.M ? (int)at : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float z[4 * TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) z[4 * j + q] = acc[i][j][q];
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) z[4 * j + q] = 16 * j + q < last ? z[4 * j + q] : -INFINITY;
+        }
+        float mx = z[0];
+#pragma unroll
+        for (int k = 1; k < 4 * TN; ++k) mx = fmaxf(mx, z[k]);
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        const float ref = __builtin_isinf(mx) ? 0.0f : -kLog2e * mx;
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4 * TN; ++k) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z[k], kLog2e, ref));
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (__any(hit[i] >= 0)) {
+            float h = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4 * TN; ++k) h = hit[i] == 16 * (k >> 2) + (k & 3) ? z[k] : h;
+            if (hit[i] >= 0) g.tlogit[m0 + 16 * i] = h;
+        }
+        const int64_t m = m0 + 16 * i;
+        if (lk == 0 && m < t.M) {
+            g.stat[(int64_t)part * t.M + m] = mx;
+            g.stat[(int64_t)(parts + part) * t.M + m] = sum;
+        }
+        asm volatile("" ::: "memory");  // keeps the groups in this order
+    }
+}
+
+template <EpiMode MODE, GroupMode GRP, int TN, int KIND, bool VEC>
 __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
                                               const f32x4 (&acc)[8][TN], char* stage) {
     if constexpr (MODE == EPI_STATS) {
-        fused_store<MODE, GRP, 16, 8, TN, 2, 2>(g, t, wave_m, wave_n, lane, acc);
+        ring_stats<TN>(g, t, wave_m, wave_n, lane, acc);
     } else if constexpr (MODE == EPI_DLOGIT) {
         const int64_t m0 = t.m0 + wave_m * 128, n0 = t.n0 + wave_n * 16 * TN;
-        // This lane's rows 16 i + lane % 16. exp(z - lse) is one fused
-        // multiply-add and a base-2 exponential (off by |z| 2^-23 at most,
-        // before a rounding to bf16); the target's 1 is subtracted by a
-        // multiply-add with a 0 or 1 for each column of a piece; rows that do
-        // not count are masked, whatever their logits are.
-        float w[8], l2[8];
+        // This lane's rows 16 i + lane % 16. z - lse first: a target that has
+        // all the probability leaves p - 1 = 0, which a multiply-add with -lse
+        // log2(e) would miss by (|z| + |lse|) 2^-24. The target's 1 is
+        // subtracted by a multiply-add with a 0 or 1 for each column of a
+        // piece; rows that do not count are masked, whatever their logits are.
+        float w[8], lse[8];
         uint32_t live[8];
         int hit[8];  // the target's column less this lane's first, or -1
 #pragma unroll
@@ -270,7 +337,7 @@ __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos&
             const int64_t m = m0 + 16 * i + (lane & 15) < t.M ? m0 + 16 * i + (lane & 15) : t.M - 1;
             const int64_t target = g.targets[m];
             w[i] = g.gw[m];
-            l2[i] = -kLog2e * g.lse[m];
+            lse[i] = g.lse[m];
             live[i] = target == g.ignore ? 0u : 0xFFFFFFFFu;
             const uint64_t at = (uint64_t)target - (uint64_t)g.v0 - (uint64_t)(n0 + 4 * (lane >> 4));
             hit[i] = at < (uint64_t)(16 * TN) && (at & 15) < 4 ? (int)at : -1;
@@ -281,12 +348,12 @@ __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos&
                                   f32x4 d;
 #pragma unroll
                                   for (int q = 0; q < 4; ++q) {
-                                      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[q], kLog2e, l2[i]));
+                                      const float p = exp_f32(z[q] - lse[i]);
                                       d[q] = w[i] * __builtin_fmaf(-here, (hit[i] & 3) == q ? 1.0f : 0.0f, p);
                                   }
                                   return pack_bf16(d) & live[i];
                               });
-    } else if constexpr (MODE == EPI_STORE && VEC && !KIND) {
+    } else if constexpr (MODE == EPI_STORE && VEC && KIND == 0) {
         const int64_t at = (GRP == GRP_RED ? (int64_t)t.e * g.c_stride : 0) + t.row0 * g.ldc;
         store_mapped_bf16<TN>(static_cast<uint16_t*>(g.C) + at, g.ldc, t.M, g.N, t.m0 + wave_m * 128,
                               t.n0 + wave_n * 16 * TN, lane, acc, stage,

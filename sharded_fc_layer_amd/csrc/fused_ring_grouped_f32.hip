@@ -1,6 +1,6 @@
 // Ring-kernel instances: expert layer's products, fp32 output.
 #define FCU_MODE EPI_STORE
-#define FCU_KIND true
+#define FCU_KIND 1
 #define FCU_GROUPED 1
 #define FCU_ANY_ROWS 1
 #define FCU_COLUMN_MAJOR_A 0

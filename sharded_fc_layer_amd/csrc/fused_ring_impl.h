@@ -38,7 +38,7 @@
 namespace fcs {
 namespace {
 
-template <EpiMode MODE, GroupMode GRP, bool A_OC, bool B_OC, int BN, int HEAD, int NA, bool KIND, bool VEC>
+template <EpiMode MODE, GroupMode GRP, bool A_OC, bool B_OC, int BN, int HEAD, int NA, int KIND, bool VEC>
 __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(1, 1))) void fused_ring_kernel(
     FusedArgs g) {
     constexpr bool STAMP = false;

@@ -1,6 +1,6 @@
 // Ring-kernel instances: cross entropy's row statistics.
 #define FCU_MODE EPI_STATS
-#define FCU_KIND false
+#define FCU_KIND 0
 #define FCU_GROUPED 0
 #define FCU_ANY_ROWS 0
 #define FCU_COLUMN_MAJOR_A 0
