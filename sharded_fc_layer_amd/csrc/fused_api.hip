@@ -43,17 +43,19 @@ bool overlapping(std::initializer_list<Span> outs, std::initializer_list<Span> i
 }
 bool off(const void* p, int64_t a) { return (uintptr_t)p % (uintptr_t)a != 0; }
 
-// An operand as the kernels read it: in place, or copied into the workspace
-// with rows padded to whole 128-byte lines where its rows do not start on
-// 16-byte boundaries. The copy's padding is zeros, which a reduction may run
-// into.
+// An operand as the kernels read it: in place, or, where the ring kernel would
+// find rows that do not start on 16-byte boundaries, copied into the workspace
+// with rows padded to whole 128-byte lines. The copy's padding is zeros, which
+// a reduction may run into.
 struct Operand {
     int64_t rows, cols;
     bool copy;
     int64_t ld, off;  // row length as read; workspace offset of the copy
 };
-Operand operand(int64_t rows, int64_t cols, bool aligned, int64_t* ws) {
-    Operand o{rows, cols, cols % 8 != 0 || !aligned, cols, 0};
+bool fits(int64_t cols, bool aligned) { return cols % 8 == 0 && aligned; }
+int64_t ring_ld(int64_t cols, bool aligned) { return fits(cols, aligned) ? cols : up(cols, 64); }
+Operand operand(int64_t rows, int64_t cols, bool aligned, bool ring, int64_t* ws) {
+    Operand o{rows, cols, ring && !fits(cols, aligned), cols, 0};
     if (o.copy) {
         o.ld = up(cols, 64);
         o.off = *ws;
@@ -83,6 +85,12 @@ struct Shape {
     int64_t k_split;
 };
 constexpr int kSkinny = -1;  // Shape::tile: the kernel for a few rows
+// row length of fp32 planes: whole vectors and lines whatever N is
+int64_t plane_ld(int64_t N) { return up(N, 64); }
+// the planes of a split reduction
+int64_t planes_bytes(const Shape& sh, int64_t M, int64_t N) {
+    return sh.splits > 1 ? (int64_t)sh.splits * M * plane_ld(N) * 4 : 0;
+}
 int64_t tiles_of(int tile, int64_t M, int64_t N) {
     const FusedTile& t = kFusedTiles[tile];
     return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
@@ -108,8 +116,6 @@ Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t ld
     return sh;
 }
 
-// row length of fp32 planes: whole vectors and lines whatever N is
-int64_t plane_ld(int64_t N) { return up(N, 64); }
 
 // FusedArgs::vec_out for rows of ld values
 int vec_rows(int64_t ld, const void* C, const void* R, const void* Z) {
@@ -153,12 +159,14 @@ struct ActPlan {
 ActPlan act_plan(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, bool aligned, bool grad) {
     ActPlan p;
     int64_t ws = 0;
-    p.A = a_oc ? operand(K, M, aligned, &ws) : operand(M, K, aligned, &ws);
-    p.B = b_oc ? operand(K, N, aligned, &ws) : operand(N, K, aligned, &ws);
-    p.sh = shape_of(M, N, K, a_oc, b_oc, p.A.ld, p.B.ld, true);
+    const int64_t acols = a_oc ? M : K, bcols = b_oc ? N : K;
+    p.sh = shape_of(M, N, K, a_oc, b_oc, ring_ld(acols, aligned), ring_ld(bcols, aligned), true);
     if (!grad && M <= 32 && !a_oc && !b_oc) p.sh = Shape{kSkinny, 1, K};
+    const bool ring = p.sh.tile == kRingTile;
+    p.A = operand(a_oc ? K : M, acols, aligned, ring, &ws);
+    p.B = operand(b_oc ? K : N, bcols, aligned, ring, &ws);
     p.planes = ws;
-    if (p.sh.splits > 1) ws += (int64_t)p.sh.splits * M * plane_ld(N) * 4;
+    ws += planes_bytes(p.sh, M, N);
     p.parts_off = ws;
     p.parts = 0;
     if (grad) {
@@ -186,16 +194,20 @@ struct XentFwdPlan {
     Operand A, B;
     Shape sh;
     int parts;
-    int64_t stat, total;
+    int64_t planes, stat, total;
 };
 XentFwdPlan xent_fwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned) {
     XentFwdPlan p;
     int64_t ws = 0;
-    p.A = operand(M, K, aligned, &ws);
-    p.B = b_oc ? operand(K, N, aligned, &ws) : operand(N, K, aligned, &ws);
-    p.sh = shape_of(M, N, K, false, b_oc, p.A.ld, p.B.ld, false);
+    const int64_t bcols = b_oc ? N : K;
+    p.sh = shape_of(M, N, K, false, b_oc, ring_ld(K, aligned), ring_ld(bcols, aligned), true);
+    const bool ring = p.sh.tile == kRingTile;
+    p.A = operand(M, K, aligned, ring, &ws);
+    p.B = operand(b_oc ? K : N, bcols, aligned, ring, &ws);
+    p.planes = ws;
+    ws += planes_bytes(p.sh, M, N);
     const FusedTile& t = kFusedTiles[p.sh.tile];
-    p.parts = (int)((N + t.bn - 1) / t.bn) * t.wave_cols;
+    p.parts = p.sh.splits > 1 ? split_stats_parts(N) : (int)((N + t.bn - 1) / t.bn) * t.wave_cols;
     p.stat = ws;
     ws += up((int64_t)2 * p.parts * M * 4, 256);
     p.total = ws;
@@ -210,24 +222,28 @@ struct XentBwdPlan {
     int64_t piece, d_ld, d_off;  // columns of a piece (a multiple of 256 but for the last); its buffer
     int pieces;
     Shape logits, dx, dw;        // for a whole piece
-    int64_t plane_off, total;
+    int64_t planes, sum_off, total;  // split products' planes; dX summed over several pieces
 };
 XentBwdPlan xent_bwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned) {
     XentBwdPlan p;
     int64_t ws = 0;
-    p.A = operand(M, K, aligned, &ws);
-    p.B = b_oc ? operand(K, N, aligned, &ws) : operand(N, K, aligned, &ws);
     p.piece = std::min<int64_t>(N, std::max<int64_t>(256, kPieceBytes / (2 * M) / 256 * 256));
     p.pieces = (int)((N + p.piece - 1) / p.piece);
     p.d_ld = up(p.piece, 64);
+    const int64_t bcols = b_oc ? N : K, lda = ring_ld(K, aligned), ldb = ring_ld(bcols, aligned);
+    p.logits = shape_of(M, p.piece, K, false, b_oc, lda, ldb, p.pieces == 1);
+    p.dx = shape_of(M, K, p.piece, false, !b_oc, p.d_ld, ldb, p.pieces == 1);
+    p.dw = shape_of(K, p.piece, M, true, true, lda, p.d_ld, p.pieces == 1);
+    if (512 * N >= (int64_t)1 << 31 && p.dw.tile == kRingTile) p.dw.tile = 0;  // its rows are N wide in dW
+    const bool ring = p.logits.tile == kRingTile || p.dx.tile == kRingTile || p.dw.tile == kRingTile;
+    p.A = operand(M, K, aligned, ring, &ws);
+    p.B = operand(b_oc ? K : N, bcols, aligned, ring, &ws);
     p.d_off = ws;
     ws += up(M * p.d_ld * 2, 256);
-    p.logits = shape_of(M, p.piece, K, false, b_oc, p.A.ld, p.B.ld, false);
-    p.dx = shape_of(M, K, p.piece, false, !b_oc, p.d_ld, p.B.ld, p.pieces == 1);
-    p.dw = shape_of(K, p.piece, M, true, true, p.A.ld, p.d_ld, false);
-    if (512 * N >= (int64_t)1 << 31) p.dw.tile = 0;  // its rows are N wide in dW
-    p.plane_off = ws;
-    if (p.pieces > 1 || p.dx.splits > 1) ws += (int64_t)p.dx.splits * M * plane_ld(K) * 4;
+    p.planes = ws;
+    ws += std::max({planes_bytes(p.logits, M, p.piece), planes_bytes(p.dx, M, K), planes_bytes(p.dw, K, p.piece)});
+    p.sum_off = ws;
+    if (p.pieces > 1) ws += M * plane_ld(K) * 4;
     p.total = ws;
     return p;
 }
@@ -242,24 +258,22 @@ struct GroupedPlan {
 GroupedPlan grouped_plan(int op, int64_t T, int64_t E, int64_t K, int64_t N, int w_order, bool aligned) {
     GroupedPlan p;
     int64_t ws = 0;
-    if (op == FC_OP_BWD_WEIGHT) {
-        p.A = operand(T, K, aligned, &ws);
-        p.B = operand(T, N, aligned, &ws);
-        p.tile = ring_takes(GRP_RED, true, true, N, T, p.A.ld, p.B.ld) &&
-                         ring_pays(E * tiles_of(kRingTile, K, N), E * tiles_of(0, K, N))
-                     ? kRingTile
-                     : 0;
-    } else {
-        p.A = operand(T, op == FC_OP_FWD ? K : N, aligned, &ws);
-        p.B = w_order == FC_ROW_MAJOR ? operand(E * K, N, aligned, &ws) : operand(E * N, K, aligned, &ws);
-        const bool fwd = op == FC_OP_FWD, b_oc = fwd == (w_order == FC_ROW_MAJOR);
-        const int64_t n = fwd ? N : K, k = fwd ? K : N;
-        p.tile = T <= 32 * E ? 1 : T <= 64 * E ? 3 : 0;
-        // a group ends with a partly filled tile: half a tile's rows are lost on average
-        if (p.tile == 0 && ring_takes(GRP_ROWS, false, b_oc, n, k, p.A.ld, p.B.ld) &&
-            ring_pays(tiles_of(kRingTile, T + 128 * E, n), tiles_of(0, T + 64 * E, n)))
-            p.tile = kRingTile;
+    const bool red = op == FC_OP_BWD_WEIGHT, fwd = op == FC_OP_FWD, b_oc = red || fwd == (w_order == FC_ROW_MAJOR);
+    const int64_t acols = op == FC_OP_BWD_DATA ? N : K, bcols = red || w_order == FC_ROW_MAJOR ? N : K;
+    const int64_t n = op == FC_OP_BWD_DATA ? K : N, k = red ? T : fwd ? K : N;  // output columns, reduction
+    const int64_t lda = ring_ld(acols, aligned), ldb = ring_ld(bcols, aligned);
+    p.tile = red || T > 64 * E ? 0 : T <= 32 * E ? 1 : 3;
+    // The experts' weights would be copied for the ring kernel: that takes as
+    // long as its product over some 300 rows of each.
+    const bool copies = !red && !fits(bcols, aligned);
+    if (p.tile == 0 && !(copies && T < 300 * E) && ring_takes(red ? GRP_RED : GRP_ROWS, red, b_oc, n, k, lda, ldb)) {
+        // (a group ends with a partly filled tile: half a tile's rows are lost on average)
+        const int64_t ring = red ? E * tiles_of(kRingTile, K, N) : tiles_of(kRingTile, T + 128 * E, n);
+        const int64_t small = red ? E * tiles_of(0, K, N) : tiles_of(0, T + 64 * E, n);
+        if (ring_pays(ring, small)) p.tile = kRingTile;
     }
+    p.A = operand(T, acols, aligned, p.tile == kRingTile, &ws);
+    p.B = operand(red ? T : w_order == FC_ROW_MAJOR ? E * K : E * N, bcols, aligned, p.tile == kRingTile, &ws);
     p.total = ws;
     return p;
 }
@@ -468,7 +482,7 @@ fc_status fc_xent_fwd(const void* X, const void* W, fc_order w_order, const int6
     g.targets = targets, g.v0 = vocab_start, g.ignore = ignore_index;
     g.stat = reinterpret_cast<float*>(base + pl.stat);
     g.tlogit = tlogit;
-    if ((e = run_product(EPI_STATS, pl.sh, false, b_oc, g, nullptr, s)) != hipSuccess) return done(e);
+    if ((e = run_product(EPI_STATS, pl.sh, false, b_oc, g, reinterpret_cast<float*>(base + pl.planes), s)) != hipSuccess) return done(e);
     return done(launch_xent_finish(g.stat, pl.parts, targets, vocab_start, ignore_index, M, N, lse, tlogit, loss, s));
 }
 
@@ -504,7 +518,8 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
     hipError_t e;
     if ((e = place(pl.A, X, &x, pl.B, W, &w, base, s)) != hipSuccess) return done(e);
     uint16_t* D = reinterpret_cast<uint16_t*>(base + pl.d_off);
-    float* planes = reinterpret_cast<float*>(base + pl.plane_off);
+    float* planes = reinterpret_cast<float*>(base + pl.planes);
+    float* sum = reinterpret_cast<float*>(base + pl.sum_off);
     for (int p = 0; p < pl.pieces; ++p) {
         const int64_t c0 = (int64_t)p * pl.piece, c = std::min(pl.piece, N - c0);
         const uint16_t* wp = w + (w_row ? c0 : c0 * pl.B.ld);
@@ -516,7 +531,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         g.accumulate = 0;
         g.targets = targets, g.v0 = vocab_start + c0, g.ignore = ignore_index;
         g.lse = lse, g.gw = grad;
-        if ((e = run_product(EPI_DLOGIT, pl.logits, false, w_row, g, nullptr, s)) != hipSuccess) return done(e);
+        if ((e = run_product(EPI_DLOGIT, pl.logits, false, w_row, g, planes, s)) != hipSuccess) return done(e);
         // dW = X^T D, this piece's columns
         FusedArgs h;
         h.A = x, h.B = D;
@@ -526,7 +541,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         h.out_f32 = wf32;
         h.accumulate = dw_dtype == FC_OUT_F32_ACCUMULATE;
         h.vec_out = vec_rows(N, h.C, nullptr, nullptr);
-        if ((e = run_product(EPI_STORE, pl.dw, true, true, h, nullptr, s)) != hipSuccess) return done(e);
+        if ((e = run_product(EPI_STORE, pl.dw, true, true, h, planes, s)) != hipSuccess) return done(e);
         // dX = D W^T: in one go, or summed over the pieces in 32 bits
         FusedArgs d;
         d.A = D, d.B = wp;
@@ -534,7 +549,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         d.lda = pl.d_ld, d.ldb = pl.B.ld;
         const bool last = pl.pieces == 1;
         d.ldc = last ? K : plane_ld(K);
-        d.C = last ? dX : planes;
+        d.C = last ? dX : sum;
         d.out_f32 = last ? xf32 : 1;
         d.accumulate = p > 0;
         d.vec_out = vec_rows(d.ldc, d.C, nullptr, nullptr);
@@ -550,7 +565,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         d.accumulate = 0;
         d.out_f32 = xf32;
         d.vec_out = vec_rows(K, dX, nullptr, nullptr);
-        e = launch_split_epilogue(EPI_STORE, d, planes, plane_ld(K), 1, s);
+        e = launch_split_epilogue(EPI_STORE, d, sum, plane_ld(K), 1, s);
     }
     return done(e);
 }

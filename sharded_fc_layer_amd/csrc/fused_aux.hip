@@ -68,7 +68,8 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
     const int64_t bm = blockIdx.x / nb, n = (blockIdx.x % nb) * 256 + lane * 4;
     [[maybe_unused]] __shared__ float cs_all[4][256];
     [[maybe_unused]] float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (n < g.N) {
+    // (the gradient of the logits has zeros up to a multiple of 8 columns)
+    if (n < (MODE == EPI_DLOGIT ? (g.N + 7) / 8 * 8 : g.N)) {
         float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (MODE == EPI_ACT && g.bias) load4(g.bias + n, n, g.N, b);
         const int64_t m0 = bm * kSplitRows + wave * kRowsPerWave;
@@ -87,6 +88,19 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
             if (m >= g.M) break;
             const int64_t at = m * g.ldc + n;
             float v[4] = {sum[r][0], sum[r][1], sum[r][2], sum[r][3]};
+            if constexpr (MODE == EPI_DLOGIT) {  // as in Epilogue::row
+                const int64_t target = g.targets[m], N8 = (g.N + 7) / 8 * 8;
+                const uint64_t hit = (uint64_t)target - (uint64_t)g.v0 - (uint64_t)n;
+                const float lse = g.lse[m], w = g.gw[m];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float p1 = exp_f32(v[q] - lse);
+                    p1 = hit == (uint64_t)q ? p1 - 1.0f : p1;
+                    v[q] = target != g.ignore && n + q < g.N ? w * p1 : 0.0f;
+                }
+                store4_bf16(static_cast<uint16_t*>(g.C) + at, n, N8, v);
+                continue;
+            }
             if constexpr (MODE == EPI_ACT) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] += b[q];
@@ -124,6 +138,53 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
                 g.colpart[bm * g.N + col] = ((cs_all[0][threadIdx.x] + cs_all[1][threadIdx.x]) +
                                              cs_all[2][threadIdx.x]) + cs_all[3][threadIdx.x];
         }
+    }
+}
+
+// EPI_STATS of a split reduction: a wave takes 1024 columns of one row, 4 at a
+// time to a lane.
+constexpr int kStatsCols = 1024;
+__global__ __launch_bounds__(256) void split_stats_kernel(FusedArgs g, const float* __restrict__ planes, int64_t pld,
+                                                          int splits) {
+    const int lane = threadIdx.x & 63;
+    const int parts = (int)((g.N + kStatsCols - 1) / kStatsCols), part = blockIdx.x % parts;
+    const int64_t m = (int64_t)(blockIdx.x / parts) * 4 + (threadIdx.x >> 6);
+    if (m >= g.M) return;  // the whole wave
+    f32x4 z[kStatsCols / 256];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kStatsCols / 256; ++c) {
+        const int64_t n = (int64_t)part * kStatsCols + c * 256 + lane * 4;
+        f32x4 v{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (n < g.N) {
+            const float* p = planes + m * pld + n;
+            v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+            for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(p + s * g.M * pld);
+            const uint64_t hit = (uint64_t)g.targets[m] - (uint64_t)g.v0 - (uint64_t)n;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[q] = n + q < g.N ? v[q] : -INFINITY;
+                if (hit == (uint64_t)q && n + q < g.N) g.tlogit[m] = v[q];
+            }
+        }
+        z[c] = v;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx = fmaxf(mx, v[q]);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+    const float ref = __builtin_isinf(mx) ? 0.0f : mx;
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kStatsCols / 256; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum += exp_f32(z[c][q] - ref);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    if (lane == 0) {
+        g.stat[(int64_t)part * g.M + m] = mx;
+        g.stat[(int64_t)(parts + part) * g.M + m] = sum;
     }
 }
 
@@ -235,14 +296,22 @@ hipError_t launch_colsum_parts(const float* part, float* out, int64_t N, int par
     return hipGetLastError();
 }
 
+int split_stats_parts(int64_t N) { return (int)((N + kStatsCols - 1) / kStatsCols); }
 int split_epilogue_parts(int64_t M) { return (int)((M + kSplitRows - 1) / kSplitRows); }
 
 hipError_t launch_split_epilogue(EpiMode mode, const FusedArgs& g, const float* planes, int64_t pld, int splits,
                                  hipStream_t s) {
+    if (mode == EPI_STATS) {
+        const int64_t blocks = (g.M + 3) / 4 * split_stats_parts(g.N);
+        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(split_stats_kernel, dim3((unsigned)blocks), dim3(256), 0, s, g, planes, pld, splits);
+        return hipGetLastError();
+    }
     const int64_t blocks = ((g.N + 255) / 256) * split_epilogue_parts(g.M);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     const auto fn = mode == EPI_ACT    ? split_epilogue_kernel<EPI_ACT>
                     : mode == EPI_DACT ? split_epilogue_kernel<EPI_DACT>
+                    : mode == EPI_DLOGIT ? split_epilogue_kernel<EPI_DLOGIT>
                                        : split_epilogue_kernel<EPI_STORE>;
     hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(256), 0, s, g, planes, pld, splits);
     return hipGetLastError();

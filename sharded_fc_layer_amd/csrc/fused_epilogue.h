@@ -158,7 +158,6 @@ struct Epilogue {
                 for (int q = 0; q < 8; ++q) v[q] += bf16_f32(in.aux[q]);
             }
         } else if constexpr (MODE == EPI_DACT) {
-            // (rows and columns outside have zeros in v)
             f32x8 z;
 #pragma unroll
             for (int q = 0; q < 8; ++q) z[q] = bf16_f32(in.aux[q]);
@@ -166,7 +165,7 @@ struct Epilogue {
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] *= z[q];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) cs[q] += v[q];
+            for (int q = 0; q < 8; ++q) cs[q] += there ? v[q] : 0.0f;
         } else if constexpr (MODE == EPI_DLOGIT) {
             // z - lse first: a target that has all the probability leaves
             // p - 1 = 0, which a multiply-add with -lse log2(e) would miss by

@@ -24,12 +24,26 @@ static int head_of(GroupMode grp, int64_t K) {
 }
 
 // Explicit instantiations (the host pass emits a launch stub for each).
-#define FCF_I(MODE, GRP, AOC, BOC) \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC>(FusedArgs);
-#define FCF_I2(MODE, GRP, BOC)      \
-    FCF_I(MODE, GRP, false, BOC)    \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, false, BOC>(FusedArgs); \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, false, BOC>(FusedArgs);
+#define FCF_I(MODE, GRP, AOC, BOC)                                                                           \
+    template __global__ void fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, false>(FusedArgs);       \
+    template __global__ void fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, true>(FusedArgs);
+#define FCF_I2(MODE, GRP, BOC)                                                                               \
+    FCF_I(MODE, GRP, false, BOC)                                                                             \
+    template __global__ void fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, false, BOC, false>(FusedArgs);      \
+    template __global__ void fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, false, BOC, false>(FusedArgs);      \
+    template __global__ void fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, false, BOC, true>(FusedArgs);       \
+    template __global__ void fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, false, BOC, true>(FusedArgs);
+#define FCF_K2(MODE, GRP, T, AOC, BOC, ANY)                                          \
+    (T == 0   ? (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, ANY> \
+     : T == 1 ? (FusedFn)fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, AOC, BOC, ANY>  \
+              : (FusedFn)fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, AOC, BOC, ANY>)
+// tiles of every height with the first operand reduction-contiguous
+#define FCF_K(MODE, GRP, BOC) \
+    (any ? FCF_K2(MODE, GRP, tile, false, BOC, true) : FCF_K2(MODE, GRP, tile, false, BOC, false))
+// 128 rows
+#define FCF_K128(MODE, GRP, AOC, BOC)                                                 \
+    (any ? (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, true>      \
+         : (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, false>)
 namespace {
 FCF_I2(EPI_STORE, GRP_NONE, false) FCF_I2(EPI_STORE, GRP_NONE, true)
 FCF_I2(EPI_STORE, GRP_ROWS, false) FCF_I2(EPI_STORE, GRP_ROWS, true)
@@ -39,50 +53,42 @@ FCF_I(EPI_STORE, GRP_NONE, true, false) FCF_I(EPI_STORE, GRP_NONE, true, true)
 FCF_I(EPI_STORE, GRP_RED, true, true)
 FCF_I(EPI_ACT, GRP_NONE, true, false) FCF_I(EPI_ACT, GRP_NONE, true, true)
 }  // namespace
-#undef FCF_I2
-#undef FCF_I
-
-#define FCF_K(MODE, GRP, T, AOC, BOC) \
-    (T == 0   ? (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC> \
-     : T == 1 ? (FusedFn)fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, AOC, BOC>  \
-              : (FusedFn)fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, AOC, BOC>)
 
 template <>
-FusedFn fused_kernel<EPI_STORE>(GroupMode grp, int tile, bool a_oc, bool b_oc) {
-    if (grp == GRP_RED) return tile == 0 && a_oc && b_oc ? fused_gemm_kernel<EPI_STORE, GRP_RED, 128, 128, 2, 2, true, true> : nullptr;
+FusedFn fused_kernel<EPI_STORE>(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any) {
+    if (grp == GRP_RED) return tile == 0 && a_oc && b_oc ? FCF_K128(EPI_STORE, GRP_RED, true, true) : nullptr;
     if (grp == GRP_ROWS) {
         if (a_oc) return nullptr;
-        return b_oc ? FCF_K(EPI_STORE, GRP_ROWS, tile, false, true) : FCF_K(EPI_STORE, GRP_ROWS, tile, false, false);
+        return b_oc ? FCF_K(EPI_STORE, GRP_ROWS, true) : FCF_K(EPI_STORE, GRP_ROWS, false);
     }
     if (a_oc) {
         if (tile != 0) return nullptr;
-        return b_oc ? fused_gemm_kernel<EPI_STORE, GRP_NONE, 128, 128, 2, 2, true, true>
-                    : fused_gemm_kernel<EPI_STORE, GRP_NONE, 128, 128, 2, 2, true, false>;
+        return b_oc ? FCF_K128(EPI_STORE, GRP_NONE, true, true) : FCF_K128(EPI_STORE, GRP_NONE, true, false);
     }
-    return b_oc ? FCF_K(EPI_STORE, GRP_NONE, tile, false, true) : FCF_K(EPI_STORE, GRP_NONE, tile, false, false);
+    return b_oc ? FCF_K(EPI_STORE, GRP_NONE, true) : FCF_K(EPI_STORE, GRP_NONE, false);
 }
 
 template <>
-FusedFn fused_kernel<EPI_ACT>(GroupMode grp, int tile, bool a_oc, bool b_oc) {
+FusedFn fused_kernel<EPI_ACT>(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any) {
     if (grp != GRP_NONE) return nullptr;
     if (a_oc) {
         if (tile != 0) return nullptr;
-        return b_oc ? fused_gemm_kernel<EPI_ACT, GRP_NONE, 128, 128, 2, 2, true, true>
-                    : fused_gemm_kernel<EPI_ACT, GRP_NONE, 128, 128, 2, 2, true, false>;
+        return b_oc ? FCF_K128(EPI_ACT, GRP_NONE, true, true) : FCF_K128(EPI_ACT, GRP_NONE, true, false);
     }
-    return b_oc ? FCF_K(EPI_ACT, GRP_NONE, tile, false, true) : FCF_K(EPI_ACT, GRP_NONE, tile, false, false);
+    return b_oc ? FCF_K(EPI_ACT, GRP_NONE, true) : FCF_K(EPI_ACT, GRP_NONE, false);
 }
 
 template <>
-FusedFn fused_kernel<EPI_DACT>(GroupMode grp, int tile, bool a_oc, bool b_oc) {
+FusedFn fused_kernel<EPI_DACT>(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any) {
     if (grp != GRP_NONE || a_oc) return nullptr;
-    return b_oc ? FCF_K(EPI_DACT, GRP_NONE, tile, false, true) : FCF_K(EPI_DACT, GRP_NONE, tile, false, false);
+    return b_oc ? FCF_K(EPI_DACT, GRP_NONE, true) : FCF_K(EPI_DACT, GRP_NONE, false);
 }
-#undef FCF_K
 
 hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc, const FusedArgs& g,
                         hipStream_t s) {
     if (tile < 0 || tile >= kNumFusedTiles) return hipErrorInvalidValue;
+    // (this one form would spill in its main loop)
+    if (tile == kRingTile && mode == EPI_ACT && a_oc && b_oc && !g.vec_out) tile = 0;
     const FusedTile& t = kFusedTiles[tile];
     const int64_t nbn = (g.N + t.bn - 1) / t.bn;
     // ragged rows: every group may end with one partly filled tile
@@ -115,11 +121,12 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
         hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, g);
         return hipGetLastError();
     }
-    const FusedFn fn = mode == EPI_STORE  ? fused_kernel<EPI_STORE>(grp, tile, a_oc, b_oc)
-                       : mode == EPI_ACT  ? fused_kernel<EPI_ACT>(grp, tile, a_oc, b_oc)
-                       : mode == EPI_DACT ? fused_kernel<EPI_DACT>(grp, tile, a_oc, b_oc)
-                       : mode == EPI_STATS ? fused_kernel<EPI_STATS>(grp, tile, a_oc, b_oc)
-                                           : fused_kernel<EPI_DLOGIT>(grp, tile, a_oc, b_oc);
+    const bool any = g.lda % 8 != 0 || g.ldb % 8 != 0 || (uintptr_t)g.A % 16 != 0 || (uintptr_t)g.B % 16 != 0;
+    const FusedFn fn = mode == EPI_STORE   ? fused_kernel<EPI_STORE>(grp, tile, a_oc, b_oc, any)
+                       : mode == EPI_ACT   ? fused_kernel<EPI_ACT>(grp, tile, a_oc, b_oc, any)
+                       : mode == EPI_DACT  ? fused_kernel<EPI_DACT>(grp, tile, a_oc, b_oc, any)
+                       : mode == EPI_STATS ? fused_kernel<EPI_STATS>(grp, tile, a_oc, b_oc, any)
+                                           : fused_kernel<EPI_DLOGIT>(grp, tile, a_oc, b_oc, any);
     if (!fn) return hipErrorInvalidValue;
     hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, g);
     return hipGetLastError();

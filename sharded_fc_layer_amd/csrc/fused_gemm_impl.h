@@ -8,8 +8,11 @@
 // as every wave has read stage t. Layouts, swizzles and operand reads are
 // those of gemm_common.h. Each stage's buffer descriptor starts at that
 // stage's first row or column, so operands may be of any size. A reduction
-// length may differ from block to block (ragged groups) and may be zero.
+// length may differ from block to block (ragged groups) and may be zero. ANY:
+// rows of the operands start at any element (AnyLoads).
 #pragma once
+
+#include <type_traits>
 
 #include "fused_epilogue.h"
 
@@ -58,7 +61,60 @@ struct StageLoads {
     }
 };
 
-template <EpiMode MODE, GroupMode GRP, int BM, int BN, int WR, int WC, bool A_OC, bool B_OC>
+// The same tile of an operand whose rows start anywhere: through registers
+// (gfx950 takes global vectors at any element's address), into the same places
+// in LDS. Two sets of registers, so that loads have two stages to land.
+//
+// All stages but the last load without masks: rows and columns outside the
+// product load others' values instead (the last row there is, the first
+// columns; a chunk across the last column runs into the next row), which only
+// reach results that nobody stores. The last stage, after which no row may
+// follow, takes its values one by one where a chunk is not whole, and zeros
+// past the end of the reduction.
+template <int R, bool OC>
+struct AnyLoads {
+    typedef StageLoads<R, OC> Places;
+    static constexpr int kInstr = Places::kInstr;
+    uint32_t at[kInstr];        // element offset within a stage
+    int kk[kInstr], n[kInstr];  // reduction index; values inside the product (OC: columns, else row there or not)
+    u16x8 v[2][kInstr];
+
+    __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t rows) {
+#pragma unroll
+        for (int j = 0; j < kInstr; ++j) {
+            if (!OC) {
+                const int i = Places::slot(wave, j) * 16 + (lane >> 2);
+                kk[j] = 8 * ((lane & 3) ^ ((lane >> 4) & 3));
+                n[j] = i < rows;
+                at[j] = (uint32_t)((i < rows ? i : rows - 1) * ld + kk[j]);
+            } else {
+                constexpr int CPR = R / 8, RPI = 64 / CPR;
+                kk[j] = Places::slot(wave, j) * RPI + lane / CPR;
+                const int c = 8 * ((lane % CPR) ^ oc_swizzle(kk[j]));
+                n[j] = c >= rows ? 0 : rows - c < 8 ? (int)(rows - c) : 8;
+                at[j] = (uint32_t)(kk[j] * ld + (c < rows ? c : 0));
+            }
+        }
+    }
+    // `left` values of the reduction from the stage's first on
+    __device__ __forceinline__ void load(int set, const uint16_t* p, int left) {
+        if (left >= kBK + (OC ? 8 : 0)) {  // (a chunk spans up to 8 rows of a very narrow operand)
+#pragma unroll
+            for (int j = 0; j < kInstr; ++j) v[set][j] = *reinterpret_cast<const u16x8_any*>(p + at[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kInstr; ++j)
+                v[set][j] = load8(p + at[j], OC ? (kk[j] < left ? n[j] : 0) : n[j] ? left - kk[j] : 0);
+        }
+    }
+    __device__ __forceinline__ void store(int set, char* region, int wave, int lane) const {
+#pragma unroll
+        for (int j = 0; j < kInstr; ++j)
+            *reinterpret_cast<u16x8*>(region + Places::slot(wave, j) * 1024 + lane * 16) = v[set][j];
+    }
+};
+
+template <EpiMode MODE, GroupMode GRP, int BM, int BN, int WR, int WC, bool A_OC, bool B_OC, bool ANY>
 __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
     static_assert(WR * WC == 4, "four waves");
     constexpr int WTM = BM / WR, WTN = BN / WC, TM = WTM / 32, TN = WTN / 32;
@@ -82,8 +138,8 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
     const uint16_t* pa = g.A + (A_OC ? a0 : a0 * g.lda);
     const uint16_t* pb = g.B + (GRP == GRP_ROWS ? (int64_t)t.e * g.b_stride : 0) + (B_OC ? t.n0 : t.n0 * g.ldb);
     const int64_t sa = A_OC ? g.lda : 1, sb = B_OC ? g.ldb : 1;
-    LoadA da;
-    LoadB db;
+    std::conditional_t<ANY, AnyLoads<BM, A_OC>, LoadA> da;
+    std::conditional_t<ANY, AnyLoads<BN, B_OC>, LoadB> db;
     da.init(wave, lane, g.lda, t.M - t.m0);
     db.init(wave, lane, g.ldb, g.N - t.n0);
 
@@ -100,13 +156,29 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
         pa += t.kbeg * sa, pb += t.kbeg * sb;
         // stages past the end of the reduction read zeros everywhere, so every
         // iteration issues and waits for the same number of loads
+        if constexpr (ANY) {
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) {
-            char* st = smem + s * kStageBytes;
-            da.issue(pa + s * kBK * sa, st, len - s * kBK, wave);
-            db.issue(pb + s * kBK * sb, st + kABytes, len - s * kBK, wave);
+            for (int s = 0; s < 2; ++s) {
+                da.load(s, pa + s * kBK * sa, len - s * kBK);
+                db.load(s, pb + s * kBK * sb, len - s * kBK);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                da.store(s, smem + s * kStageBytes, wave, lane);
+                db.store(s, smem + s * kStageBytes + kABytes, wave, lane);
+                da.load(s, pa + (s + 2) * kBK * sa, len - (s + 2) * kBK);
+                db.load(s, pb + (s + 2) * kBK * sb, len - (s + 2) * kBK);
+            }
+            waitcnt<63, 0>();
+        } else {
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) {
+                char* st = smem + s * kStageBytes;
+                da.issue(pa + s * kBK * sa, st, len - s * kBK, wave);
+                db.issue(pb + s * kBK * sb, st + kABytes, len - s * kBK, wave);
+            }
+            waitcnt<(kStages - 1) * L, 0>();
         }
-        waitcnt<(kStages - 1) * L, 0>();
         __builtin_amdgcn_s_barrier();
 
         bf16x8 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
@@ -117,8 +189,13 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
 
         const uint16_t* na = pa + kStages * kBK * sa;
         const uint16_t* nb = pb + kStages * kBK * sb;
-        for (int k = 0; k < nkt; ++k) {
-            char* st = smem + (k % kStages) * kStageBytes;
+        // (two stages at a time for the register sets' sake; a stage past the
+        // end of an odd count multiplies zeros)
+        for (int k = 0; k < nkt; k += ANY ? 2 : 1)
+#pragma unroll
+        for (int h = 0; h < (ANY ? 2 : 1); ++h) {
+            const int kh = k + h;
+            char* st = smem + (kh % kStages) * kStageBytes;
 #pragma unroll
             for (int i = 0; i < TM; ++i) fa1[i] = fragment<BM, A_OC>(st, wm0 + i * 32, 1, lane);
 #pragma unroll
@@ -131,18 +208,27 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb0[j], fa0[i], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
             // this wave has read all of stage k; stage k + 1 must have landed
-            waitcnt<(kStages - 2) * L, 0>();
+            waitcnt<ANY ? 63 : (kStages - 2) * L, 0>();
             __builtin_amdgcn_s_barrier();
-            const char* nx = smem + ((k + 1) % kStages) * kStageBytes;
+            const char* nx = smem + ((kh + 1) % kStages) * kStageBytes;
 #pragma unroll
             for (int i = 0; i < TM; ++i) fa0[i] = fragment<BM, A_OC>(nx, wm0 + i * 32, 0, lane);
 #pragma unroll
             for (int j = 0; j < TN; ++j) fb0[j] = fragment<BN, B_OC>(nx + kABytes, wn0 + j * 32, 0, lane);
             __builtin_amdgcn_sched_barrier(0);
-            // the loads of stage k + 4 go into stage k's slot
-            const int left = len - (k + kStages) * kBK;
-            da.issue(na, st, left, wave);
-            db.issue(nb, st + kABytes, left, wave);
+            const int left = len - (kh + kStages) * kBK;
+            if constexpr (ANY) {
+                // stage k + 2 into the slot that stage k - 2 left before the
+                // last barrier; the loads of stage k + 4 into its registers
+                char* to = smem + ((kh + 2) % kStages) * kStageBytes;
+                da.store(h, to, wave, lane);
+                db.store(h, to + kABytes, wave, lane);
+                da.load(h, na, left);
+                db.load(h, nb, left);
+            } else {  // the loads of stage k + 4 go into stage k's slot
+                da.issue(na, st, left, wave);
+                db.issue(nb, st + kABytes, left, wave);
+            }
             na += kBK * sa, nb += kBK * sb;
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -5,29 +5,30 @@ namespace fcs {
 
 // Explicit instantiations (the host pass emits a launch stub for each).
 namespace {
-#define FCF_I(MODE, BOC)                                                                           \
-    template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 128, 128, 2, 2, false, BOC>(FusedArgs); \
-    template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, BOC>(FusedArgs); \
-    template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 64, 128, 1, 4, false, BOC>(FusedArgs);
-FCF_I(EPI_STATS, false) FCF_I(EPI_STATS, true) FCF_I(EPI_DLOGIT, false) FCF_I(EPI_DLOGIT, true)
+#define FCF_I(MODE, BOC, ANY)                                                                               \
+    template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 128, 128, 2, 2, false, BOC, ANY>(FusedArgs); \
+    template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, BOC, ANY>(FusedArgs);  \
+    template __global__ void fused_gemm_kernel<MODE, GRP_NONE, 64, 128, 1, 4, false, BOC, ANY>(FusedArgs);
+#define FCF_I4(MODE) FCF_I(MODE, false, false) FCF_I(MODE, true, false) FCF_I(MODE, false, true) FCF_I(MODE, true, true)
+FCF_I4(EPI_STATS) FCF_I4(EPI_DLOGIT)
+#undef FCF_I4
 #undef FCF_I
 }  // namespace
 
-#define FCF_X(MODE)                                                                                        \
-    template <>                                                                                            \
-    FusedFn fused_kernel<MODE>(GroupMode grp, int tile, bool a_oc, bool b_oc) {                            \
-        if (grp != GRP_NONE || a_oc) return nullptr;                                                       \
-        if (tile == 0)                                                                                     \
-            return b_oc ? fused_gemm_kernel<MODE, GRP_NONE, 128, 128, 2, 2, false, true>                   \
-                        : fused_gemm_kernel<MODE, GRP_NONE, 128, 128, 2, 2, false, false>;                 \
-        if (tile == 1)                                                                                     \
-            return b_oc ? fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, true>                    \
-                        : fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, false>;                  \
-        return b_oc ? fused_gemm_kernel<MODE, GRP_NONE, 64, 128, 1, 4, false, true>                        \
-                    : fused_gemm_kernel<MODE, GRP_NONE, 64, 128, 1, 4, false, false>;                      \
+#define FCF_K(MODE, BOC, ANY)                                                                  \
+    (tile == 0   ? (FusedFn)fused_gemm_kernel<MODE, GRP_NONE, 128, 128, 2, 2, false, BOC, ANY> \
+     : tile == 1 ? (FusedFn)fused_gemm_kernel<MODE, GRP_NONE, 32, 128, 1, 4, false, BOC, ANY>  \
+                 : (FusedFn)fused_gemm_kernel<MODE, GRP_NONE, 64, 128, 1, 4, false, BOC, ANY>)
+#define FCF_X(MODE)                                                                                  \
+    template <>                                                                                      \
+    FusedFn fused_kernel<MODE>(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any) {            \
+        if (grp != GRP_NONE || a_oc) return nullptr;                                                 \
+        if (any) return b_oc ? FCF_K(MODE, true, true) : FCF_K(MODE, false, true);                   \
+        return b_oc ? FCF_K(MODE, true, false) : FCF_K(MODE, false, false);                          \
     }
 FCF_X(EPI_STATS)
 FCF_X(EPI_DLOGIT)
 #undef FCF_X
+#undef FCF_K
 
 }  // namespace fcs

@@ -51,9 +51,10 @@ struct FusedArgs : GemmArgs {
 };
 
 // General kernel (fused_gemm.hip): block tiles kFusedTiles[tile], any M, N and
-// K >= 0 with rows of both operands on 16-byte boundaries (lda, ldb multiples
-// of 8, aligned bases); a reduction-contiguous operand has zeros from K to
-// the next multiple of 8.
+// K >= 0, operands at any element's address. Where the rows of both start on
+// 16-byte boundaries (lda, ldb multiples of 8, aligned bases) they go straight
+// into LDS; a reduction-contiguous operand then has zeros from K to the next
+// multiple of 8, which the ring kernel needs too.
 struct FusedTile {
     int bm, bn, wave_rows, wave_cols;  // the 4 waves' grid within the tile
 };
@@ -64,7 +65,7 @@ typedef void (*FusedFn)(FusedArgs);
 // The general kernel's instances of one epilogue (fused_gemm.hip,
 // fused_gemm_xent.hip); nullptr for a combination that no operator uses.
 template <EpiMode MODE>
-FusedFn fused_kernel(GroupMode grp, int tile, bool a_oc, bool b_oc);
+FusedFn fused_kernel(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any);
 // The ring kernel's (fused_ring_*.hip), 256 x 256 block tiles: one product, or
 // an expert layer's (EPI_STORE).
 template <EpiMode MODE, int KIND>
@@ -73,7 +74,7 @@ template <int KIND>
 FusedFn fused_ring_grouped(GroupMode grp, int head, bool vec, bool b_oc);
 #define FCU_DECLARE(MODE) \
     template <>           \
-    FusedFn fused_kernel<MODE>(GroupMode grp, int tile, bool a_oc, bool b_oc);
+    FusedFn fused_kernel<MODE>(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any);
 #define FCU_DECLARE_RING(MODE, KIND) \
     template <>                      \
     FusedFn fused_ring<MODE, KIND>(int head, bool vec, bool a_oc, bool b_oc);
@@ -123,11 +124,12 @@ hipError_t launch_pad_any(const PadCopy& a, const PadCopy& b, hipStream_t s);
 hipError_t launch_colsum_parts(const float* part, float* out, int64_t N, int parts, hipStream_t s);
 
 // The epilogue of a split reduction: v = sum of the slices' planes (M rows of
-// pld values, a multiple of 4) in order, then EPI_STORE, EPI_ACT or EPI_DACT.
+// pld values, a multiple of 4) in order, then what `mode` says.
 hipError_t launch_split_epilogue(EpiMode mode, const FusedArgs& g, const float* planes, int64_t pld, int splits,
                                  hipStream_t s);
-// rows of its column-sum partials (EPI_DACT)
+// rows of its column-sum partials (EPI_DACT); its blocks of columns (EPI_STATS)
 int split_epilogue_parts(int64_t M);
+int split_stats_parts(int64_t N);
 
 // dZ = dY * act'(Z) (dZ and Z may be none) and the column sums of the products
 hipError_t launch_act_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16_t* dZ, float* part, int64_t M,

@@ -8,9 +8,9 @@
 // a lane takes 32 consecutive bytes of its row, which are the reduction
 // values 16 (lane / 16) .. +15 of the piece and serve two MFMAs; the order of
 // the reduction within a piece is the same permutation for X, whose rows past
-// M read zeros. Eight W loads per wave are in flight. The waves' sums meet in
+// M count as zeros. Rows of either start at any element. Eight W loads per wave are in flight. The waves' sums meet in
 // LDS, and the first wave adds them in order and runs the epilogue.
-#include "fused_common.h"
+#include "fused_epilogue.h"
 
 namespace fcs {
 namespace {
@@ -22,28 +22,21 @@ __global__ __launch_bounds__(64 * WAVES) void fused_skinny_kernel(FusedArgs g) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lk = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const __amdgpu_buffer_rsrc_t rw =
-        __builtin_amdgcn_make_buffer_rsrc((void*)(g.B + n0 * g.ldb), 0, 0x7FFFFFFF, kRsrcWord3);
-    const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc((void*)g.A, 0, 0x7FFFFFFF, kRsrcWord3);
-    const int K = (int)g.K;  // rows of both operands hold zeros from K to the next multiple of 8
+    const int K = (int)g.K;
+    const uint16_t* w_row = g.B + (n0 + lr) * g.ldb;
     const bool row_in = n0 + lr < g.N;
-    const uint32_t wrow = (uint32_t)(lr * g.ldb * 2);
-    uint32_t xrow[TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) xrow[i] = (uint32_t)((16 * i + lr) * g.lda * 2);
 
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     f32x4 acc[TM][2];
 #pragma unroll
     for (int i = 0; i < TM; ++i) acc[i][0] = acc[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int p0 = wave * 64; p0 < K; p0 += U * WAVES * 64) {
-        u32x4 w[U][2], x[U][TM][2];
+        u16x8 w[U][2], x[U][TM][2];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = p0 + u * WAVES * 64 + 16 * lk + 8 * h;
-                w[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, row_in && k < K ? wrow + 2u * k : kOOB, 0, 0);
+                w[u][h] = load8(w_row + k, row_in ? K - k : 0);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -52,8 +45,7 @@ __global__ __launch_bounds__(64 * WAVES) void fused_skinny_kernel(FusedArgs g) {
                 const int k = p0 + u * WAVES * 64 + 16 * lk + 8 * h;
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
-                    x[u][i][h] = __builtin_amdgcn_raw_buffer_load_b128(
-                        rx, 16 * i + lr < g.M && k < K ? xrow[i] + 2u * k : kOOB, 0, 0);
+                    x[u][i][h] = load8(g.A + (16 * i + lr) * g.lda + k, 16 * i + lr < g.M ? K - k : 0);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
