@@ -25,8 +25,8 @@ SOURCES = ["gemm_w4_ring256.hip", "gemm_w4_ring192.hip", "gemm_w4_ring256b.hip",
            "fused_ring_act_linear.hip", "fused_ring_dact_linear.hip", "fused_ring_act_sigmoid.hip", "fused_ring_dact_sigmoid.hip",
            "fused_ring_act_normal.hip", "fused_ring_dact_normal.hip", "fused_ring_store.hip", "fused_ring_store_f32.hip",
            "fused_ring_grouped.hip", "fused_ring_grouped_f32.hip", "fused_ring_stats.hip", "fused_ring_dlogit.hip",
-           "fused_gemm.hip", "fused_gemm_xent.hip",
-           "fused_skinny.hip", "fused_aux.hip", "fused_api.hip"]
+           "fused_gemm_dma.hip", "fused_gemm_any.hip",
+           "fused_gemm.hip", "fused_skinny.hip", "fused_aux.hip", "fused_api.hip"]
 
 # packed-fp32 instructions are switched off for all device code
 HIPCC_FLAGS = [

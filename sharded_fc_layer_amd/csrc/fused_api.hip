@@ -75,16 +75,14 @@ hipError_t place(const Operand& a, const void* pa, const uint16_t** oa, const Op
     return a.copy || b.copy ? launch_pad_any(ca, cb, s) : hipSuccess;
 }
 
-// Tile and reduction slices of one product. The ring kernel's round of 256
-// tiles of 256 x 256 takes about as long as 0.7 rounds of the general
-// kernel's 512 tiles of 128 x 128. A product of the general kernel with fewer
-// tiles than the chip holds blocks (two per CU) splits a long reduction, 256
-// values to a slice at least.
+// Tile and reduction slices of one product.
 struct Shape {
     int tile, splits;
     int64_t k_split;
+    double us;  // estimated time
 };
 constexpr int kSkinny = -1;  // Shape::tile: the kernel for a few rows
+
 // row length of fp32 planes: whole vectors and lines whatever N is
 int64_t plane_ld(int64_t N) { return up(N, 64); }
 // the planes of a split reduction
@@ -95,27 +93,70 @@ int64_t tiles_of(int tile, int64_t M, int64_t N) {
     const FusedTile& t = kFusedTiles[tile];
     return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
 }
-bool ring_pays(int64_t ring_tiles, int64_t tiles) {
-    return ring_tiles >= 96 && (ring_tiles + 255) / 256 * 7 <= (tiles + 511) / 512 * 10;
-}
-Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t lda, int64_t ldb, bool may_split) {
-    Shape sh{a_oc || M > 64 ? 0 : M <= 32 ? 1 : 3, 1, up(K, 64)};
-    if (M > 64 && ring_takes(GRP_NONE, a_oc, b_oc, N, K, lda, ldb) &&
-        ring_pays(tiles_of(kRingTile, M, N), tiles_of(0, M, N))) {
-        sh.tile = kRingTile;
-        return sh;
-    }
-    const int64_t tiles = tiles_of(sh.tile, M, N);
-    if (may_split && tiles < 256) {
-        const int64_t want = std::min<int64_t>({512 / tiles, K / 256, 16});
-        if (want > 1) {
-            sh.k_split = up((K + want - 1) / want, 32);
-            sh.splits = (int)((K + sh.k_split - 1) / sh.k_split);
-        }
-    }
-    return sh;
-}
 
+// Estimated times in microseconds, fitted to measurements on one MI355X
+// (outputs 128 x 128 to 8192 x 8192, reductions 40 to 4104):
+//  * a round of up to 256 ring tiles takes 15 and 1.1 for each 64-value stage,
+//    of which a reduction that is not head plus periods has up to 5 more (136
+//    tiles: 19.2 at a reduction of 72, 49.5 at 2056; 1024 tiles at 2048: 213);
+//  * a round of the general kernel's tiles 5 and 0.65 for each 32-value stage
+//    with a block to a CU, 7 and 1.0 with two (255 tiles: 20.5 at 520, 46.7 at
+//    2000; 4096 tiles at 2048: 577); where rows start anywhere 2 more and 1.3 of
+//    the stages' time (84 tiles at 1001: 38); tiles of 32 or 64 rows 0.4 of it
+//    (391 tiles of 64 rows at 2048: 35);
+//  * neither reads, writes or copies faster than 5 TB/s (experts' weights of 403
+//    MB against 48 rows: 61 and 93);
+//  * a launch 3; a split reduction's second launch 4, its planes at 6 TB/s (252
+//    tiles of three slices at 1001: 18.7 and 6.6);
+//  * copies 3, read and written at 3.5 TB/s.
+double ring_us(int64_t tiles, int64_t K, bool ragged, double bytes) {
+    const int64_t n = (K + 63) / 64;
+    const bool head = !ragged && K % 64 == 0 && (n % 6 == 2 || n % 6 == 4) && n > 6;
+    const double stages = ragged ? (double)n + 2.5 : head ? (double)n : (double)up(n, 6);
+    return 3 + std::max((double)((tiles + 255) / 256) * (15 + 1.1 * stages), bytes / 5e6);
+}
+double small_us(int tile, int64_t blocks, int64_t K, bool any, double bytes) {
+    const double stages = (double)((K + 31) / 32) * (tile == 0 ? 1.0 : 0.4) * (any ? 1.3 : 1.0), more = any ? 2 : 0;
+    const double us = blocks <= 256 ? 5 + more + 0.65 * stages : (double)((blocks + 511) / 512) * (7 + more + 1.0 * stages);
+    return 3 + std::max(us, bytes / 5e6);
+}
+double planes_us(int64_t slices, int64_t M, int64_t N) {
+    return 4 + (double)slices * (double)M * (double)plane_ld(N) * 8 / 6e6;
+}
+// what a product reads
+double operand_bytes(int64_t M, int64_t N, int64_t K) { return 2.0 * (double)K * (double)(M + N); }
+double copy_us(int64_t bytes) { return 3 + (double)bytes * 2 / 3.5e6; }
+
+// The general kernel's best form. A product with few tiles may split a long
+// reduction, 128 values to a slice at least.
+Shape small_shape(int64_t M, int64_t N, int64_t K, bool a_oc, bool any, bool may_split) {
+    const int tile = a_oc || M > 64 ? 0 : M <= 32 ? 1 : 3;
+    const int64_t tiles = tiles_of(tile, M, N);
+    const double bytes = operand_bytes(M, N, K);
+    Shape best{tile, 1, up(K, 64), small_us(tile, tiles, K, any, bytes)};
+    if (!may_split || tiles > 256) return best;
+    for (int s = 2; s <= 16; ++s) {
+        const int64_t k_split = up((K + s - 1) / s, 32);
+        if (k_split < 128) break;
+        const int slices = (int)((K + k_split - 1) / k_split);
+        const double us = small_us(tile, tiles * slices, k_split, any, bytes) + planes_us(slices, M, N);
+        if (us < best.us) best = Shape{tile, slices, k_split, us};
+    }
+    return best;
+}
+// The ring kernel's, if it takes the product, without any copies it needs.
+Shape ring_shape(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t lda, int64_t ldb) {
+    const bool takes = ring_takes(GRP_NONE, a_oc, b_oc, N, K, lda, ldb);
+    return Shape{kRingTile, 1, up(K, 64), takes ? ring_us(tiles_of(kRingTile, M, N), K, false, operand_bytes(M, N, K)) : 1e30};
+}
+// The better of both for one product, whose operands' rows are acols and bcols values.
+Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t acols, int64_t bcols, bool aligned) {
+    const Shape small = small_shape(M, N, K, a_oc, !fits(acols, aligned) || !fits(bcols, aligned), true);
+    Shape ring = ring_shape(M, N, K, a_oc, b_oc, ring_ld(acols, aligned), ring_ld(bcols, aligned));
+    const int64_t bytes = (fits(acols, aligned) ? 0 : M * K * 2) + (fits(bcols, aligned) ? 0 : N * K * 2);
+    if (bytes) ring.us += copy_us(bytes);
+    return ring.us < small.us ? ring : small;
+}
 
 // FusedArgs::vec_out for rows of ld values
 int vec_rows(int64_t ld, const void* C, const void* R, const void* Z) {
@@ -147,6 +188,12 @@ hipError_t run_product(EpiMode mode, const Shape& sh, bool a_oc, bool b_oc, Fuse
 
 // ---------------------------------------------------------------- act
 
+// The few-row kernel against the general one (24 rows, outputs 28000: 16.7
+// against 4.8 us at a reduction of 72, 38.5 against 28.3 at 2056; one row, 8192
+// outputs, 2048: 7.0 against 12.3): it reads a narrow W at once, but its blocks
+// of 16 columns cost more where they are many.
+bool skinny_pays(int64_t M, int64_t N, int64_t K) { return N <= (M <= 16 ? 16384 : 8192) && K >= 256; }
+
 struct ActPlan {
     Operand A, B;
     Shape sh;
@@ -160,8 +207,8 @@ ActPlan act_plan(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, bool ali
     ActPlan p;
     int64_t ws = 0;
     const int64_t acols = a_oc ? M : K, bcols = b_oc ? N : K;
-    p.sh = shape_of(M, N, K, a_oc, b_oc, ring_ld(acols, aligned), ring_ld(bcols, aligned), true);
-    if (!grad && M <= 32 && !a_oc && !b_oc) p.sh = Shape{kSkinny, 1, K};
+    p.sh = shape_of(M, N, K, a_oc, b_oc, acols, bcols, aligned);
+    if (!grad && M <= 32 && !a_oc && !b_oc && skinny_pays(M, N, K)) p.sh = Shape{kSkinny, 1, K, 0};
     const bool ring = p.sh.tile == kRingTile;
     p.A = operand(a_oc ? K : M, acols, aligned, ring, &ws);
     p.B = operand(b_oc ? K : N, bcols, aligned, ring, &ws);
@@ -200,7 +247,7 @@ XentFwdPlan xent_fwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool align
     XentFwdPlan p;
     int64_t ws = 0;
     const int64_t bcols = b_oc ? N : K;
-    p.sh = shape_of(M, N, K, false, b_oc, ring_ld(K, aligned), ring_ld(bcols, aligned), true);
+    p.sh = shape_of(M, N, K, false, b_oc, K, bcols, aligned);
     const bool ring = p.sh.tile == kRingTile;
     p.A = operand(M, K, aligned, ring, &ws);
     p.B = operand(b_oc ? K : N, bcols, aligned, ring, &ws);
@@ -231,13 +278,27 @@ XentBwdPlan xent_bwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool align
     p.pieces = (int)((N + p.piece - 1) / p.piece);
     p.d_ld = up(p.piece, 64);
     const int64_t bcols = b_oc ? N : K, lda = ring_ld(K, aligned), ldb = ring_ld(bcols, aligned);
-    p.logits = shape_of(M, p.piece, K, false, b_oc, lda, ldb, p.pieces == 1);
-    p.dx = shape_of(M, K, p.piece, false, !b_oc, p.d_ld, ldb, p.pieces == 1);
-    p.dw = shape_of(K, p.piece, M, true, true, lda, p.d_ld, p.pieces == 1);
-    if (512 * N >= (int64_t)1 << 31 && p.dw.tile == kRingTile) p.dw.tile = 0;  // its rows are N wide in dW
-    const bool ring = p.logits.tile == kRingTile || p.dx.tile == kRingTile || p.dw.tile == kRingTile;
-    p.A = operand(M, K, aligned, ring, &ws);
-    p.B = operand(b_oc ? K : N, bcols, aligned, ring, &ws);
+    // each product's better kernel; the copies, if the operands need them, serve all three
+    const bool split = p.pieces == 1, copies = !fits(K, aligned) || !fits(bcols, aligned);
+    const Shape small[3] = {small_shape(M, p.piece, K, false, copies, split),
+                            small_shape(M, K, p.piece, false, !fits(bcols, aligned), split),
+                            small_shape(K, p.piece, M, true, !fits(K, aligned), split)};
+    Shape ring[3] = {ring_shape(M, p.piece, K, false, b_oc, lda, ldb), ring_shape(M, K, p.piece, false, !b_oc, p.d_ld, ldb),
+                     ring_shape(K, p.piece, M, true, true, lda, p.d_ld)};
+    if (512 * N >= (int64_t)1 << 31) ring[2].us = 1e30;  // dW's rows are N wide
+    Shape* to[3] = {&p.logits, &p.dx, &p.dw};
+    double gain = 0;
+    for (int i = 0; i < 3; ++i) {
+        *to[i] = ring[i].us < small[i].us ? ring[i] : small[i];
+        gain += (small[i].us - to[i]->us) * p.pieces;
+    }
+    const int64_t bytes = (fits(K, aligned) ? 0 : M * K * 2) + (fits(bcols, aligned) ? 0 : N * K * 2);
+    const bool ring_any = gain > 0 && (!copies || gain > copy_us(bytes));
+    if (!ring_any)
+        for (int i = 0; i < 3; ++i) *to[i] = small[i];
+    const bool ring_used = ring_any;
+    p.A = operand(M, K, aligned, ring_used, &ws);
+    p.B = operand(b_oc ? K : N, bcols, aligned, ring_used, &ws);
     p.d_off = ws;
     ws += up(M * p.d_ld * 2, 256);
     p.planes = ws;
@@ -252,8 +313,8 @@ XentBwdPlan xent_bwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool align
 
 struct GroupedPlan {
     Operand A, B;
-    int tile;
-    int64_t total;
+    int tile, slices;
+    int64_t k_split, planes, total;
 };
 GroupedPlan grouped_plan(int op, int64_t T, int64_t E, int64_t K, int64_t N, int w_order, bool aligned) {
     GroupedPlan p;
@@ -262,18 +323,41 @@ GroupedPlan grouped_plan(int op, int64_t T, int64_t E, int64_t K, int64_t N, int
     const int64_t acols = op == FC_OP_BWD_DATA ? N : K, bcols = red || w_order == FC_ROW_MAJOR ? N : K;
     const int64_t n = op == FC_OP_BWD_DATA ? K : N, k = red ? T : fwd ? K : N;  // output columns, reduction
     const int64_t lda = ring_ld(acols, aligned), ldb = ring_ld(bcols, aligned);
+    // (a group ends with a partly filled tile: half a tile's rows are lost on average)
     p.tile = red || T > 64 * E ? 0 : T <= 32 * E ? 1 : 3;
-    // The experts' weights would be copied for the ring kernel: that takes as
-    // long as its product over some 300 rows of each.
-    const bool copies = !red && !fits(bcols, aligned);
-    if (p.tile == 0 && !(copies && T < 300 * E) && ring_takes(red ? GRP_RED : GRP_ROWS, red, b_oc, n, k, lda, ldb)) {
-        // (a group ends with a partly filled tile: half a tile's rows are lost on average)
-        const int64_t ring = red ? E * tiles_of(kRingTile, K, N) : tiles_of(kRingTile, T + 128 * E, n);
-        const int64_t small = red ? E * tiles_of(0, K, N) : tiles_of(0, T + 64 * E, n);
-        if (ring_pays(ring, small)) p.tile = kRingTile;
+    p.slices = 1, p.k_split = k;
+    const int64_t mean = std::max<int64_t>(1, T / E);  // a group's reduction, of the weights' gradient
+    int64_t tiles;
+    if (red)
+        tiles = E * tiles_of(0, K, N);
+    else if (p.tile == 0)
+        tiles = tiles_of(0, T + 64 * E, n);
+    else  // groups of a tile's rows or fewer
+        tiles = std::min(T, E) * ((n + 127) / 128);
+    const bool any = !fits(acols, aligned) || !fits(bcols, aligned);
+    const double moved = 2.0 * (double)T * (double)(K + N) + 2.0 * (double)std::min(T, E) * (double)K * (double)N;
+    double us = small_us(p.tile, tiles, red ? mean : k, any, moved);
+    if (ring_takes(red ? GRP_RED : GRP_ROWS, red, b_oc, n, k, lda, ldb)) {
+        const int64_t rtiles = red ? E * tiles_of(kRingTile, K, N) : tiles_of(kRingTile, T + 128 * E, n);
+        const int64_t bytes = (fits(acols, aligned) ? 0 : T * acols * 2) +
+                              (fits(bcols, aligned) ? 0 : (red ? T * N : E * K * N) * 2);
+        const double ring = ring_us(rtiles, red ? mean : k, red, moved) + (bytes ? copy_us(bytes) : 0);
+        if (ring < us) p.tile = kRingTile, us = ring;
+    }
+    // a few rows against long reductions: slices, as for one product
+    if (!red && p.tile != kRingTile && tiles < 256) {
+        for (int s = 2; s <= 16; ++s) {
+            const int64_t k_split = up((k + s - 1) / s, 32);
+            if (k_split < 128) break;
+            const int slices = (int)((k + k_split - 1) / k_split);
+            const double t = small_us(p.tile, tiles * slices, k_split, any, moved) + planes_us(slices, T, n);
+            if (t < us) p.slices = slices, p.k_split = k_split, us = t;
+        }
     }
     p.A = operand(T, acols, aligned, p.tile == kRingTile, &ws);
     p.B = operand(red ? T : w_order == FC_ROW_MAJOR ? E * K : E * N, bcols, aligned, p.tile == kRingTile, &ws);
+    p.planes = ws;
+    if (p.slices > 1) ws += (int64_t)p.slices * T * plane_ld(n) * 4;
     p.total = ws;
     return p;
 }
@@ -328,7 +412,17 @@ fc_status grouped_call(int op, const void* P, const void* Q, int w_order, const 
     g.b_stride = (w_order == FC_ROW_MAJOR ? K : N) * pl.B.ld;
     g.vec_out = vec_rows(g.N, out, nullptr, nullptr);
     const bool b_oc = fwd == (w_order == FC_ROW_MAJOR);
-    return done(launch_fused(EPI_STORE, GRP_ROWS, pl.tile, false, b_oc, g, s));
+    g.k_split = pl.k_split;
+    if (pl.slices == 1) return done(launch_fused(EPI_STORE, GRP_ROWS, pl.tile, false, b_oc, g, s));
+    FusedArgs p = g;
+    p.C = base + pl.planes;
+    p.ldc = plane_ld(g.N);
+    p.out_f32 = 1;
+    p.splits = pl.slices;
+    p.c_split_stride = T * p.ldc;
+    e = launch_fused(EPI_STORE, GRP_ROWS, pl.tile, false, b_oc, p, s);
+    return done(e != hipSuccess ? e
+                                : launch_split_epilogue(EPI_STORE, g, static_cast<const float*>(p.C), p.ldc, pl.slices, s));
 }
 
 }  // namespace

@@ -68,6 +68,8 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
     const int64_t bm = blockIdx.x / nb, n = (blockIdx.x % nb) * 256 + lane * 4;
     [[maybe_unused]] __shared__ float cs_all[4][256];
     [[maybe_unused]] float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int64_t first = 0, last = g.M;
+    if (MODE == EPI_STORE && g.offsets) first = g.offsets[0], last = g.offsets[g.E];
     // (the gradient of the logits has zeros up to a multiple of 8 columns)
     if (n < (MODE == EPI_DLOGIT ? (g.N + 7) / 8 * 8 : g.N)) {
         float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -86,6 +88,7 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
         for (int r = 0; r < kRowsPerWave; ++r) {
             const int64_t m = m0 + r;
             if (m >= g.M) break;
+            if (m < first || m >= last) continue;  // no group's row: left as it was
             const int64_t at = m * g.ldc + n;
             float v[4] = {sum[r][0], sum[r][1], sum[r][2], sum[r][3]};
             if constexpr (MODE == EPI_DLOGIT) {  // as in Epilogue::row

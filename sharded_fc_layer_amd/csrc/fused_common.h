@@ -225,8 +225,10 @@ __device__ __forceinline__ TilePos find_group_rows(const FusedArgs& g) {
         rows += n;
     }
     const int total = __builtin_amdgcn_readfirstlane(rows) * nbn;
-    const int lin = blockIdx.x;
+    const int each = gridDim.x / g.splits;  // blocks of a reduction slice
+    const int lin = blockIdx.x % each;
     if (lin >= total) return t;
+    t.slice = blockIdx.x / each;
     const int q = total / 8, rem = total % 8, x = lin % 8;
     int id = x * q + (x < rem ? x : rem) + lin / 8;
     for (int c = 0; c < g.E; c += 64) {
@@ -253,7 +255,8 @@ __device__ __forceinline__ TilePos find_group_rows(const FusedArgs& g) {
         t.tm = local % nbm, t.tn = local / nbm;  // rows fastest: neighbours share B's columns
         t.m0 = (int64_t)t.tm * BM, t.n0 = (int64_t)t.tn * BN;
         t.row0 = glo, t.M = ghi - glo;
-        t.kbeg = 0, t.kend = g.K;
+        t.kbeg = (int64_t)t.slice * g.k_split;
+        t.kend = t.kbeg + g.k_split < g.K ? t.kbeg + g.k_split : g.K;
         t.any = true;
         return t;
     }

@@ -1,8 +1,8 @@
-// The general fused kernel's plain and activation instances, and its launch
-// (see fused_gemm_impl.h).
+// The launch of the fused products: the general kernel (fused_gemm_impl.h) or
+// the ring kernel (fused_ring_impl.h).
 #include <algorithm>
 
-#include "fused_gemm_impl.h"
+#include "fused_common.h"
 
 namespace fcs {
 
@@ -23,69 +23,9 @@ static int head_of(GroupMode grp, int64_t K) {
     return grp != GRP_RED && K % 64 == 0 && (n % 6 == 2 || n % 6 == 4) && n > 6 ? (int)(n % 6) : -1;
 }
 
-// Explicit instantiations (the host pass emits a launch stub for each).
-#define FCF_I(MODE, GRP, AOC, BOC)                                                                           \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, false>(FusedArgs);       \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, true>(FusedArgs);
-#define FCF_I2(MODE, GRP, BOC)                                                                               \
-    FCF_I(MODE, GRP, false, BOC)                                                                             \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, false, BOC, false>(FusedArgs);      \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, false, BOC, false>(FusedArgs);      \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, false, BOC, true>(FusedArgs);       \
-    template __global__ void fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, false, BOC, true>(FusedArgs);
-#define FCF_K2(MODE, GRP, T, AOC, BOC, ANY)                                          \
-    (T == 0   ? (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, ANY> \
-     : T == 1 ? (FusedFn)fused_gemm_kernel<MODE, GRP, 32, 128, 1, 4, AOC, BOC, ANY>  \
-              : (FusedFn)fused_gemm_kernel<MODE, GRP, 64, 128, 1, 4, AOC, BOC, ANY>)
-// tiles of every height with the first operand reduction-contiguous
-#define FCF_K(MODE, GRP, BOC) \
-    (any ? FCF_K2(MODE, GRP, tile, false, BOC, true) : FCF_K2(MODE, GRP, tile, false, BOC, false))
-// 128 rows
-#define FCF_K128(MODE, GRP, AOC, BOC)                                                 \
-    (any ? (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, true>      \
-         : (FusedFn)fused_gemm_kernel<MODE, GRP, 128, 128, 2, 2, AOC, BOC, false>)
-namespace {
-FCF_I2(EPI_STORE, GRP_NONE, false) FCF_I2(EPI_STORE, GRP_NONE, true)
-FCF_I2(EPI_STORE, GRP_ROWS, false) FCF_I2(EPI_STORE, GRP_ROWS, true)
-FCF_I2(EPI_ACT, GRP_NONE, false) FCF_I2(EPI_ACT, GRP_NONE, true)
-FCF_I2(EPI_DACT, GRP_NONE, false) FCF_I2(EPI_DACT, GRP_NONE, true)
-FCF_I(EPI_STORE, GRP_NONE, true, false) FCF_I(EPI_STORE, GRP_NONE, true, true)
-FCF_I(EPI_STORE, GRP_RED, true, true)
-FCF_I(EPI_ACT, GRP_NONE, true, false) FCF_I(EPI_ACT, GRP_NONE, true, true)
-}  // namespace
-
-template <>
-FusedFn fused_kernel<EPI_STORE>(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any) {
-    if (grp == GRP_RED) return tile == 0 && a_oc && b_oc ? FCF_K128(EPI_STORE, GRP_RED, true, true) : nullptr;
-    if (grp == GRP_ROWS) {
-        if (a_oc) return nullptr;
-        return b_oc ? FCF_K(EPI_STORE, GRP_ROWS, true) : FCF_K(EPI_STORE, GRP_ROWS, false);
-    }
-    if (a_oc) {
-        if (tile != 0) return nullptr;
-        return b_oc ? FCF_K128(EPI_STORE, GRP_NONE, true, true) : FCF_K128(EPI_STORE, GRP_NONE, true, false);
-    }
-    return b_oc ? FCF_K(EPI_STORE, GRP_NONE, true) : FCF_K(EPI_STORE, GRP_NONE, false);
-}
-
-template <>
-FusedFn fused_kernel<EPI_ACT>(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any) {
-    if (grp != GRP_NONE) return nullptr;
-    if (a_oc) {
-        if (tile != 0) return nullptr;
-        return b_oc ? FCF_K128(EPI_ACT, GRP_NONE, true, true) : FCF_K128(EPI_ACT, GRP_NONE, true, false);
-    }
-    return b_oc ? FCF_K(EPI_ACT, GRP_NONE, true) : FCF_K(EPI_ACT, GRP_NONE, false);
-}
-
-template <>
-FusedFn fused_kernel<EPI_DACT>(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any) {
-    if (grp != GRP_NONE || a_oc) return nullptr;
-    return b_oc ? FCF_K(EPI_DACT, GRP_NONE, true) : FCF_K(EPI_DACT, GRP_NONE, false);
-}
-
-hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc, const FusedArgs& g,
+hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc, const FusedArgs& given,
                         hipStream_t s) {
+    FusedArgs g = given;
     if (tile < 0 || tile >= kNumFusedTiles) return hipErrorInvalidValue;
     // (this one form would spill in its main loop)
     if (tile == kRingTile && mode == EPI_ACT && a_oc && b_oc && !g.vec_out) tile = 0;
@@ -93,7 +33,7 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
     const int64_t nbn = (g.N + t.bn - 1) / t.bn;
     // ragged rows: every group may end with one partly filled tile
     const int64_t nbm = grp == GRP_ROWS ? g.T / t.bm + std::min<int64_t>(g.E, g.T) : (g.M + t.bm - 1) / t.bm;
-    const int64_t blocks = nbm * nbn * (grp == GRP_RED ? g.E : grp == GRP_NONE ? g.splits : 1);
+    const int64_t blocks = nbm * nbn * (grp == GRP_RED ? g.E : g.splits);
     if (blocks <= 0) return hipSuccess;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (tile == kRingTile) {
@@ -121,12 +61,14 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
         hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, g);
         return hipGetLastError();
     }
+    // storage rows and columns of each operand, the last group's where there are several
+    const int64_t ar = grp == GRP_NONE ? (a_oc ? g.K : g.M) : g.T, ac = grp == GRP_ROWS ? g.K : a_oc ? g.M : g.K;
+    const int64_t br = grp == GRP_RED ? g.T : b_oc ? g.K : g.N, bc = b_oc ? g.N : g.K;
+    g.a_end = g.A + (ar - 1) * g.lda + ac;
+    g.b_end = g.B + (grp == GRP_ROWS ? (g.E - 1) * g.b_stride : 0) + (br - 1) * g.ldb + bc;
     const bool any = g.lda % 8 != 0 || g.ldb % 8 != 0 || (uintptr_t)g.A % 16 != 0 || (uintptr_t)g.B % 16 != 0;
-    const FusedFn fn = mode == EPI_STORE   ? fused_kernel<EPI_STORE>(grp, tile, a_oc, b_oc, any)
-                       : mode == EPI_ACT   ? fused_kernel<EPI_ACT>(grp, tile, a_oc, b_oc, any)
-                       : mode == EPI_DACT  ? fused_kernel<EPI_DACT>(grp, tile, a_oc, b_oc, any)
-                       : mode == EPI_STATS ? fused_kernel<EPI_STATS>(grp, tile, a_oc, b_oc, any)
-                                           : fused_kernel<EPI_DLOGIT>(grp, tile, a_oc, b_oc, any);
+    if ((tile != 0 && a_oc) || (grp == GRP_RED && !(a_oc && b_oc)) || (grp == GRP_ROWS && a_oc)) return hipErrorInvalidValue;
+    const FusedFn fn = any ? fused_kernel<true>(mode, grp, tile, a_oc, b_oc) : fused_kernel<false>(mode, grp, tile, a_oc, b_oc);
     if (!fn) return hipErrorInvalidValue;
     hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, g);
     return hipGetLastError();

@@ -1,11 +1,12 @@
 // The general kernel of the fused operators: one tile of a product and its
-// epilogue. Built per epilogue in fused_gemm.hip and fused_gemm_xent.hip.
+// epilogue. Built in fused_gemm_*.hip, through fused_gemm_table.inc.
 //
 // Structure (256 threads = 4 wave64s, block tile BM x BN, 32-value reduction
-// stages in a ring of 4 LDS slots): global data goes straight into LDS with
+// stages in a ring of S = 4 LDS slots): global data goes straight into LDS with
 // 16 bytes per lane, chunks past the tile's rows or the end of the reduction
-// read zeros through an out-of-range offset; stage t + 4 is requested as soon
-// as every wave has read stage t. Layouts, swizzles and operand reads are
+// read zeros through an out-of-range offset; stage t + S is requested as soon
+// as every wave has read stage t. (Eight slots, with a block to a CU,
+// measured the same.) Layouts, swizzles and operand reads are
 // those of gemm_common.h. Each stage's buffer descriptor starts at that
 // stage's first row or column, so operands may be of any size. A reduction
 // length may differ from block to block (ragged groups) and may be zero. ANY:
@@ -63,21 +64,21 @@ struct StageLoads {
 
 // The same tile of an operand whose rows start anywhere: through registers
 // (gfx950 takes global vectors at any element's address), into the same places
-// in LDS. Two sets of registers, so that loads have two stages to land.
+// in LDS. Q sets of registers, so that loads have Q stages to land.
 //
 // All stages but the last load without masks: rows and columns outside the
 // product load others' values instead (the last row there is, the first
 // columns; a chunk across the last column runs into the next row), which only
 // reach results that nobody stores. The last stage, after which no row may
-// follow, takes its values one by one where a chunk is not whole, and zeros
-// past the end of the reduction.
-template <int R, bool OC>
+// follow, reads zeros past the end of the reduction, and takes a chunk that
+// would run past the operand's last value (`end`) one by one.
+template <int R, bool OC, int Q>
 struct AnyLoads {
     typedef StageLoads<R, OC> Places;
     static constexpr int kInstr = Places::kInstr;
     uint32_t at[kInstr];        // element offset within a stage
     int kk[kInstr], n[kInstr];  // reduction index; values inside the product (OC: columns, else row there or not)
-    u16x8 v[2][kInstr];
+    u16x8 v[Q][kInstr];
 
     __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t rows) {
 #pragma unroll
@@ -97,14 +98,27 @@ struct AnyLoads {
         }
     }
     // `left` values of the reduction from the stage's first on
-    __device__ __forceinline__ void load(int set, const uint16_t* p, int left) {
+    __device__ __forceinline__ void load(int set, const uint16_t* p, int left, const uint16_t* end) {
         if (left >= kBK + (OC ? 8 : 0)) {  // (a chunk spans up to 8 rows of a very narrow operand)
 #pragma unroll
             for (int j = 0; j < kInstr; ++j) v[set][j] = *reinterpret_cast<const u16x8_any*>(p + at[j]);
         } else {
 #pragma unroll
-            for (int j = 0; j < kInstr; ++j)
-                v[set][j] = load8(p + at[j], OC ? (kk[j] < left ? n[j] : 0) : n[j] ? left - kk[j] : 0);
+            for (int j = 0; j < kInstr; ++j) {
+                const int there = OC ? (kk[j] < left ? n[j] : 0) : n[j] ? left - kk[j] : 0;
+                u16x8 w{0, 0, 0, 0, 0, 0, 0, 0};
+                if (there > 0) {
+                    if (p + at[j] + 8 <= end)
+                        w = *reinterpret_cast<const u16x8_any*>(p + at[j]);
+                    else
+                        w = load8(p + at[j], there);
+                }
+                if constexpr (!OC) {  // values past the end of the reduction: zeros
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) w[e] = e < there ? w[e] : (uint16_t)0;
+                }
+                v[set][j] = w;
+            }
         }
     }
     __device__ __forceinline__ void store(int set, char* region, int wave, int lane) const {
@@ -117,12 +131,13 @@ struct AnyLoads {
 template <EpiMode MODE, GroupMode GRP, int BM, int BN, int WR, int WC, bool A_OC, bool B_OC, bool ANY>
 __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
     static_assert(WR * WC == 4, "four waves");
+    constexpr int S = kStages;
     constexpr int WTM = BM / WR, WTN = BN / WC, TM = WTM / 32, TN = WTN / 32;
     constexpr int kABytes = BM * kBK * 2, kStageBytes = (BM + BN) * kBK * 2;
     typedef StageLoads<BM, A_OC> LoadA;
     typedef StageLoads<BN, B_OC> LoadB;
     constexpr int L = LoadA::kInstr + LoadB::kInstr;
-    __shared__ __attribute__((aligned(1024))) char smem[kStages * kStageBytes];
+    __shared__ __attribute__((aligned(1024))) char smem[S * kStageBytes];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -138,8 +153,9 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
     const uint16_t* pa = g.A + (A_OC ? a0 : a0 * g.lda);
     const uint16_t* pb = g.B + (GRP == GRP_ROWS ? (int64_t)t.e * g.b_stride : 0) + (B_OC ? t.n0 : t.n0 * g.ldb);
     const int64_t sa = A_OC ? g.lda : 1, sb = B_OC ? g.ldb : 1;
-    std::conditional_t<ANY, AnyLoads<BM, A_OC>, LoadA> da;
-    std::conditional_t<ANY, AnyLoads<BN, B_OC>, LoadB> db;
+    constexpr int Q = S / 2;  // register sets of AnyLoads
+    std::conditional_t<ANY, AnyLoads<BM, A_OC, Q>, LoadA> da;
+    std::conditional_t<ANY, AnyLoads<BN, B_OC, Q>, LoadB> db;
     da.init(wave, lane, g.lda, t.M - t.m0);
     db.init(wave, lane, g.ldb, g.N - t.n0);
 
@@ -157,27 +173,28 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
         // stages past the end of the reduction read zeros everywhere, so every
         // iteration issues and waits for the same number of loads
         if constexpr (ANY) {
+            // stages 0 and 1 go to LDS at once; 2 .. Q + 1 wait in registers
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                da.load(s, pa + s * kBK * sa, len - s * kBK);
-                db.load(s, pb + s * kBK * sb, len - s * kBK);
+            for (int s = 0; s < Q; ++s) {
+                da.load(s, pa + s * kBK * sa, len - s * kBK, g.a_end);
+                db.load(s, pb + s * kBK * sb, len - s * kBK, g.b_end);
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 da.store(s, smem + s * kStageBytes, wave, lane);
                 db.store(s, smem + s * kStageBytes + kABytes, wave, lane);
-                da.load(s, pa + (s + 2) * kBK * sa, len - (s + 2) * kBK);
-                db.load(s, pb + (s + 2) * kBK * sb, len - (s + 2) * kBK);
+                da.load(s, pa + (s + Q) * kBK * sa, len - (s + Q) * kBK, g.a_end);
+                db.load(s, pb + (s + Q) * kBK * sb, len - (s + Q) * kBK, g.b_end);
             }
             waitcnt<63, 0>();
         } else {
 #pragma unroll
-            for (int s = 0; s < kStages; ++s) {
+            for (int s = 0; s < S; ++s) {
                 char* st = smem + s * kStageBytes;
                 da.issue(pa + s * kBK * sa, st, len - s * kBK, wave);
                 db.issue(pb + s * kBK * sb, st + kABytes, len - s * kBK, wave);
             }
-            waitcnt<(kStages - 1) * L, 0>();
+            waitcnt<(S - 1) * L, 0>();
         }
         __builtin_amdgcn_s_barrier();
 
@@ -187,15 +204,16 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) fb0[j] = fragment<BN, B_OC>(smem + kABytes, wn0 + j * 32, 0, lane);
 
-        const uint16_t* na = pa + kStages * kBK * sa;
-        const uint16_t* nb = pb + kStages * kBK * sb;
-        // (two stages at a time for the register sets' sake; a stage past the
-        // end of an odd count multiplies zeros)
-        for (int k = 0; k < nkt; k += ANY ? 2 : 1)
+        constexpr int kAhead = ANY ? Q + 2 : S;
+        const uint16_t* na = pa + kAhead * kBK * sa;
+        const uint16_t* nb = pb + kAhead * kBK * sb;
+        // (Q stages at a time for the register sets' sake; stages past the end
+        // multiply zeros)
+        for (int k = 0; k < nkt; k += ANY ? Q : 1)
 #pragma unroll
-        for (int h = 0; h < (ANY ? 2 : 1); ++h) {
+        for (int h = 0; h < (ANY ? Q : 1); ++h) {
             const int kh = k + h;
-            char* st = smem + (kh % kStages) * kStageBytes;
+            char* st = smem + (kh % S) * kStageBytes;
 #pragma unroll
             for (int i = 0; i < TM; ++i) fa1[i] = fragment<BM, A_OC>(st, wm0 + i * 32, 1, lane);
 #pragma unroll
@@ -208,24 +226,25 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb0[j], fa0[i], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
             // this wave has read all of stage k; stage k + 1 must have landed
-            waitcnt<ANY ? 63 : (kStages - 2) * L, 0>();
+            waitcnt<ANY ? 63 : (S - 2) * L, 0>();
             __builtin_amdgcn_s_barrier();
-            const char* nx = smem + ((kh + 1) % kStages) * kStageBytes;
+            const char* nx = smem + ((kh + 1) % S) * kStageBytes;
 #pragma unroll
             for (int i = 0; i < TM; ++i) fa0[i] = fragment<BM, A_OC>(nx, wm0 + i * 32, 0, lane);
 #pragma unroll
             for (int j = 0; j < TN; ++j) fb0[j] = fragment<BN, B_OC>(nx + kABytes, wn0 + j * 32, 0, lane);
             __builtin_amdgcn_sched_barrier(0);
-            const int left = len - (kh + kStages) * kBK;
+            const int left = len - (kh + kAhead) * kBK;
             if constexpr (ANY) {
-                // stage k + 2 into the slot that stage k - 2 left before the
-                // last barrier; the loads of stage k + 4 into its registers
-                char* to = smem + ((kh + 2) % kStages) * kStageBytes;
-                da.store(h, to, wave, lane);
-                db.store(h, to + kABytes, wave, lane);
-                da.load(h, na, left);
-                db.load(h, nb, left);
-            } else {  // the loads of stage k + 4 go into stage k's slot
+                // stage k + 2 into a slot that was left before the last barrier;
+                // the loads of stage k + 2 + Q into its registers
+                constexpr int kSet = Q == 2 ? 0 : 2;
+                char* to = smem + ((kh + 2) % S) * kStageBytes;
+                da.store((h + kSet) % Q, to, wave, lane);
+                db.store((h + kSet) % Q, to + kABytes, wave, lane);
+                da.load((h + kSet) % Q, na, left, g.a_end);
+                db.load((h + kSet) % Q, nb, left, g.b_end);
+            } else {  // the loads of stage k + S go into stage k's slot
                 da.issue(na, st, left, wave);
                 db.issue(nb, st + kABytes, left, wave);
             }

@@ -30,6 +30,9 @@ enum GroupMode : int {
 // One product with its epilogue, in kernel terms (see GemmArgs). Only the
 // fields of the launch's modes are read.
 struct FusedArgs : GemmArgs {
+    // one past the last value of each operand that may be read (set by launch_fused)
+    const uint16_t* a_end = nullptr;
+    const uint16_t* b_end = nullptr;
     int out_f32 = 0;      // C is fp32 (else bf16)
     int vec_out = 0;      // ring kernel: the rows of C, R and Z start on 16-byte boundaries, N is a multiple of 8
     int act = 0;          // fc_act
@@ -62,27 +65,23 @@ constexpr int kNumFusedTiles = 4;
 constexpr int kRingTile = 2;  // the ring kernel's tile: see ring_takes
 extern const FusedTile kFusedTiles[kNumFusedTiles];
 typedef void (*FusedFn)(FusedArgs);
-// The general kernel's instances of one epilogue (fused_gemm.hip,
-// fused_gemm_xent.hip); nullptr for a combination that no operator uses.
-template <EpiMode MODE>
-FusedFn fused_kernel(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any);
+// The general kernel's instances (fused_gemm_*.hip) by way of loading; nullptr
+// for a combination that no operator uses.
+template <bool ANY>
+FusedFn fused_kernel(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc);
+template <>
+FusedFn fused_kernel<false>(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc);
+template <>
+FusedFn fused_kernel<true>(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc);
 // The ring kernel's (fused_ring_*.hip), 256 x 256 block tiles: one product, or
 // an expert layer's (EPI_STORE).
 template <EpiMode MODE, int KIND>
 FusedFn fused_ring(int head, bool vec, bool a_oc, bool b_oc);
 template <int KIND>
 FusedFn fused_ring_grouped(GroupMode grp, int head, bool vec, bool b_oc);
-#define FCU_DECLARE(MODE) \
-    template <>           \
-    FusedFn fused_kernel<MODE>(GroupMode grp, int tile, bool a_oc, bool b_oc, bool any);
 #define FCU_DECLARE_RING(MODE, KIND) \
     template <>                      \
     FusedFn fused_ring<MODE, KIND>(int head, bool vec, bool a_oc, bool b_oc);
-FCU_DECLARE(EPI_STORE)
-FCU_DECLARE(EPI_ACT)
-FCU_DECLARE(EPI_DACT)
-FCU_DECLARE(EPI_STATS)
-FCU_DECLARE(EPI_DLOGIT)
 FCU_DECLARE_RING(EPI_STORE, 0)
 FCU_DECLARE_RING(EPI_STORE, 1)
 FCU_DECLARE_RING(EPI_ACT, 0)
@@ -93,7 +92,6 @@ FCU_DECLARE_RING(EPI_DACT, 1)
 FCU_DECLARE_RING(EPI_DACT, 2)
 FCU_DECLARE_RING(EPI_STATS, 0)
 FCU_DECLARE_RING(EPI_DLOGIT, 0)
-#undef FCU_DECLARE
 #undef FCU_DECLARE_RING
 template <>
 FusedFn fused_ring_grouped<0>(GroupMode grp, int head, bool vec, bool b_oc);

@@ -35,25 +35,25 @@ def calls(L):
     ws, n = at(20), 1 << 40
     d3 = {p: SIZES for p in (10, 11, 12)}
     return {
-        "fc_fwd_act": (L.fc_fwd_act, [at(0), 0, at(1), 0, at(2), at(3), 3, at(4), at(5), 0, 2601, 101, 2603, ws, n, None],
+        "fc_fwd_act": (L.fc_fwd_act, [at(0), 0, at(1), 0, at(2), at(3), 3, at(4), at(5), 0, 8001, 1001, 8003, ws, n, None],
                        (0, 2, 8), {1: (2, -1), 3: (2, -1), 6: (-1, 5), 9: (-1, 2, 3), **d3}),
-        "fc_bwd_data_act": (L.fc_bwd_data_act, [at(0), at(1), 0, at(2), 1, at(3), 0, at(4), 2601, 2603, 101, ws, n, None],
+        "fc_bwd_data_act": (L.fc_bwd_data_act, [at(0), at(1), 0, at(2), 1, at(3), 0, at(4), 8001, 8003, 1001, ws, n, None],
                             (0, 1, 3, 5), {2: (2, -1), 4: (-1, 5), 6: (-1, 2, 3), 8: SIZES, 9: SIZES, 10: SIZES}),
         "fc_bwd_act": (L.fc_bwd_act, [at(0), at(1), 2, at(2), at(3), 65, 33, ws, n, None],
                        (0, 1), {2: (-1, 5), 5: SIZES, 6: SIZES}),
-        "fc_xent_fwd": (L.fc_xent_fwd, [at(0), at(1), 0, at(2), 0, -100, at(3), at(4), at(5), 2601, 101, 2603, ws, n, None],
+        "fc_xent_fwd": (L.fc_xent_fwd, [at(0), at(1), 0, at(2), 0, -100, at(3), at(4), at(5), 8001, 1001, 8003, ws, n, None],
                         (0, 1, 3, 6, 7), {2: (2, -1), 4: (-1,), 9: SIZES, 10: SIZES, 11: SIZES}),
-        "fc_xent_bwd": (L.fc_xent_bwd, [at(0), at(1), 0, at(2), 0, -100, at(3), at(4), at(5), 0, at(6), 0, 2601, 101, 2603,
+        "fc_xent_bwd": (L.fc_xent_bwd, [at(0), at(1), 0, at(2), 0, -100, at(3), at(4), at(5), 0, at(6), 0, 8001, 1001, 8003,
                                         ws, n, None],
                         (0, 1, 3, 6, 7, 8, 10), {2: (2, -1), 4: (-1,), 9: (-1, 2, 3), 11: (-1, 3), 12: SIZES,
                                                  13: SIZES, 14: SIZES}),
-        "fc_grouped_fwd": (L.fc_grouped_fwd, [at(0), at(1), 0, at(2), at(3), 0, 2601, 3, 2603, 2605, ws, n, None],
+        "fc_grouped_fwd": (L.fc_grouped_fwd, [at(0), at(1), 0, at(2), at(3), 0, 30001, 3, 2603, 2605, ws, n, None],
                            (0, 1, 3, 4), {2: (2, -1), 5: (-1, 2, 3), 6: SIZES, 7: (0, -1, (1 << 20) + 1), 8: SIZES,
                                           9: SIZES}),
-        "fc_grouped_bwd_data": (L.fc_grouped_bwd_data, [at(0), at(1), 1, at(2), at(3), 1, 2601, 3, 2603, 2605, ws, n, None],
+        "fc_grouped_bwd_data": (L.fc_grouped_bwd_data, [at(0), at(1), 1, at(2), at(3), 1, 30001, 3, 2603, 2605, ws, n, None],
                                 (0, 1, 3, 4), {2: (2, -1), 5: (-1, 2, 3), 6: SIZES, 7: (0, -1, (1 << 20) + 1),
                                                8: SIZES, 9: SIZES}),
-        "fc_grouped_bwd_weight": (L.fc_grouped_bwd_weight, [at(0), at(1), at(2), at(3), 2, 2601, 3, 2603, 2605, ws, n, None],
+        "fc_grouped_bwd_weight": (L.fc_grouped_bwd_weight, [at(0), at(1), at(2), at(3), 2, 30001, 3, 2603, 2605, ws, n, None],
                                   (0, 1, 2, 3), {4: (-1, 3), 5: SIZES, 6: (0, -1, (1 << 20) + 1), 7: SIZES,
                                                  8: SIZES}),
     }
@@ -117,14 +117,14 @@ def test_a_call_takes_what_its_query_says(L):
     import torch
     if torch.cuda.is_available():
         pytest.skip("the addresses are made up")
-    for name, query in (("fc_fwd_act", lambda: L.fc_fwd_act_ws_bytes(2601, 101, 2603, 0, 0, 1)),
-                        ("fc_bwd_data_act", lambda: L.fc_bwd_data_act_ws_bytes(2601, 2603, 101, 0, 1)),
+    for name, query in (("fc_fwd_act", lambda: L.fc_fwd_act_ws_bytes(8001, 1001, 8003, 0, 0, 1)),
+                        ("fc_bwd_data_act", lambda: L.fc_bwd_data_act_ws_bytes(8001, 8003, 1001, 0, 1)),
                         ("fc_bwd_act", lambda: L.fc_bwd_act_ws_bytes(65, 33)),
-                        ("fc_xent_fwd", lambda: L.fc_xent_fwd_ws_bytes(2601, 101, 2603, 0, 1)),
-                        ("fc_xent_bwd", lambda: L.fc_xent_bwd_ws_bytes(2601, 101, 2603, 0, 1)),
-                        ("fc_grouped_fwd", lambda: L.fc_grouped_ws_bytes(0, 2601, 3, 2603, 2605, 0, 1)),
-                        ("fc_grouped_bwd_data", lambda: L.fc_grouped_ws_bytes(1, 2601, 3, 2603, 2605, 1, 1)),
-                        ("fc_grouped_bwd_weight", lambda: L.fc_grouped_ws_bytes(2, 2601, 3, 2603, 2605, 0, 1))):
+                        ("fc_xent_fwd", lambda: L.fc_xent_fwd_ws_bytes(8001, 1001, 8003, 0, 1)),
+                        ("fc_xent_bwd", lambda: L.fc_xent_bwd_ws_bytes(8001, 1001, 8003, 0, 1)),
+                        ("fc_grouped_fwd", lambda: L.fc_grouped_ws_bytes(0, 30001, 3, 2603, 2605, 0, 1)),
+                        ("fc_grouped_bwd_data", lambda: L.fc_grouped_ws_bytes(1, 30001, 3, 2603, 2605, 1, 1)),
+                        ("fc_grouped_bwd_weight", lambda: L.fc_grouped_ws_bytes(2, 30001, 3, 2603, 2605, 0, 1))):
         fn, args, _, _ = calls(L)[name]
         need, w = query(), [p for p, a in enumerate(args) if isinstance(a, ctypes.c_void_p)][-1]
         assert need > 0 and need % 256 == 0
@@ -149,8 +149,8 @@ def test_workspace_queries(L):
     assert L.fc_fwd_act_ws_bytes(8192, 2048, 8192, 0, 0, 1) == 0
     assert L.fc_grouped_ws_bytes(0, 8192, 8, 2048, 8192, 0, 1) == 0
     # others are copied where the large tiles run: rows of 1001 values padded to 1024
-    assert L.fc_grouped_ws_bytes(2, 512, 8, 1001, 2048, 0, 1) == 512 * 1024 * 2
-    assert L.fc_grouped_ws_bytes(2, 512, 8, 1024, 2048, 0, 0) == 512 * (1024 + 2048) * 2
+    assert L.fc_grouped_ws_bytes(2, 30000, 8, 1001, 2048, 0, 1) == 30000 * 1024 * 2
+    assert L.fc_grouped_ws_bytes(2, 30000, 8, 1024, 2048, 0, 0) == 30000 * (1024 + 2048) * 2
     # the smaller tiles read them where they are
     assert L.fc_fwd_act_ws_bytes(300, 201, 77, 0, 0, 0) == 0
     assert L.fc_fwd_act_ws_bytes(20, 1001, 4099, 0, 1, 0) == 0
