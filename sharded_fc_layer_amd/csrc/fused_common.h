@@ -252,6 +252,8 @@ __device__ __forceinline__ TilePos find_group_rows(const FusedArgs& g) {
         group_tile_rows<BM>(g, c + l, glo, ghi);
         const int local = id - first;
         t.e = c + l;
+        // (offsets that overlap so much that the sums above overflow end here)
+        if (nbm <= 0 || local < 0 || local / nbm >= nbn) return t;
         t.tm = local % nbm, t.tn = local / nbm;  // rows fastest: neighbours share B's columns
         t.m0 = (int64_t)t.tm * BM, t.n0 = (int64_t)t.tn * BN;
         t.row0 = glo, t.M = ghi - glo;

@@ -209,7 +209,8 @@ def test_slopes_by_differences_and_at_the_ends():
 
 XENT = [(1, 8, 1), (1, 64, 1000), (5, 33, 130), (32, 128, 129), (33, 100, 999), (64, 264, 4001), (130, 72, 520),
         (257, 520, 1032), (300, 65, 2050),
-        (2600, 100, 2600), (2570, 512, 2700), (4100, 640, 1500), (2309, 131, 3001)]
+        (2600, 100, 2600), (2570, 512, 2700), (4100, 640, 1500), (2309, 131, 3001),
+        (96, 2001, 300), (40, 4104, 700)]  # (split reductions)
 
 
 def xent64(X, W, t, v0, ignore, lse=None):
@@ -421,7 +422,12 @@ GROUPED = [  # rows of each expert, first row, rows behind the last, K, N
     ([1100, 900, 0, 1], 0, 0, 1032, 2570), ([2600], 0, 1, 640, 2600), ([700], 0, 0, 264, 300), ([40] * 8, 0, 0, 1001, 129)]
 
 
-@pytest.mark.parametrize("case", GROUPED, ids=lambda c: f"{len(c[0])}x{c[3]}x{c[4]}")
+# few rows against long reductions, which are split
+GROUPED_LONG = [([1], 2, 3, 2000, 136), ([5, 0, 12], 1, 4, 1560, 77), ([40, 0, 61], 3, 2, 4104, 257),
+                ([1, 0, 1], 0, 0, 777, 4100), ([64, 30], 5, 5, 8001, 130)]
+
+
+@pytest.mark.parametrize("case", GROUPED + GROUPED_LONG, ids=lambda c: f"{len(c[0])}x{c[3]}x{c[4]}")
 @pytest.mark.parametrize("wo", [ROW, COL])
 def test_grouped_integers_are_exact(case, wo):
     counts, first, behind, K, N = case
@@ -486,6 +492,77 @@ def test_grouped_bad_offsets_stay_inside():
         assert bool((big[:10] == 9).all()) and bool((big[10 + T:] == 9).all()), bad
         F.fc_grouped_bwd_weight(X, X, off)
     torch.cuda.synchronize()
+
+
+# ---- neighbouring memory
+
+def among_nans(t, offset):
+    """The same values, `offset` elements past a 16-byte boundary, between NaNs."""
+    buf = torch.full((t.numel() + 1024,), float("nan"), dtype=t.dtype, device=t.device)
+    out = buf[256 + offset:256 + offset + t.numel()].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 9, 2), (65, 7, 3), (129, 33, 1), (200, 1, 1), (70, 39, 5), (16, 264, 24),
+                                   (33, 2051, 35), (100, 1000, 136), (2600, 70, 2570)])
+@pytest.mark.parametrize("offset", [0, 1, 4])
+def test_nothing_past_the_operands_counts(shape, offset):
+    M, K, N = shape
+    g = gen(M + K + N)
+    X, W, dY = integers(g, M, K), integers(g, K, N), integers(g, M, N)
+    Y, dX = X.float() @ W.float(), dY.float() @ W.float().t()
+    Z = torch.ones((M, K), dtype=torch.bfloat16, device="cuda")
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    small = 2.0 ** -4  # logits of a few units
+    z = Y.double() * small * small
+    for wo in (ROW, COL):
+        w = among_nans(stored(W, wo), offset)
+        for xo in (ROW, COL):
+            x = among_nans(stored(X, xo), offset)
+            assert torch.equal(F.fc_fwd_act(x, w, x_order=xo, w_order=wo, out_dtype=F.OUT_F32), Y), (xo, wo)
+        got, db = F.fc_bwd_data_act(among_nans(dY, offset), w, Z, F.ACT_RELU, w_order=wo, out_dtype=F.OUT_F32,
+                                    bias_grad=True)
+        assert torch.equal(got, dX) and bool(torch.isfinite(db).all())
+        x, ws = among_nans(X * small, offset), among_nans(stored(W * small, wo), offset)
+        loss, lse, _ = F.fc_xent_fwd(x, ws, t, w_order=wo)
+        want = torch.logsumexp(z, 1)
+        # |z| <= 9 K 2^-8 exactly held (integers over 256); see test_xent_fwd for the sum
+        within(lse, want, 2.0 ** -20 + (N + 16) * U + 4 * U * want.abs(), f"{shape} lse")
+        dX1, dW1 = F.fc_xent_bwd(x, ws, t, lse, torch.ones(M, device="cuda"), w_order=wo)
+        assert bool(torch.isfinite(dX1).all()) and bool(torch.isfinite(dW1).all())
+
+
+@pytest.mark.parametrize("case", [([3, 0, 70, 1], 2, 9, 40, 136), ([300, 17, 0, 64], 5, 3, 135, 264),
+                                  ([1, 2], 3, 2, 1501, 40), ([700, 0, 30, 1500], 3, 5, 1200, 1300)],
+                         ids=lambda c: f"{len(c[0])}x{c[3]}x{c[4]}")
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_rows_and_experts_do_not_meet(case, wo):
+    """Rows that no expert has, and the matrices of experts without rows, are NaN."""
+    counts, first, behind, K, N = case
+    E, T = len(counts), first + sum(counts) + behind
+    g = gen(T)
+    X, dY, W = integers(g, T, K), integers(g, T, N), integers(g, E, K, N)
+    nan = float("nan")
+    for v in (X, dY):
+        v[:first], v[T - behind:] = nan, nan
+    for e in range(E):
+        if counts[e] == 0:
+            W[e] = nan
+    off = offsets_of(counts, first)
+    lo = off.tolist()
+    x, d, w = among_nans(X, 0), among_nans(dY, 0), among_nans(stored(W, wo), 0)
+    Y, dX = torch.zeros((T, N), device="cuda"), torch.zeros((T, K), device="cuda")
+    F.fc_grouped_fwd(x, w, off, w_order=wo, out=Y, out_dtype=F.OUT_F32)
+    F.fc_grouped_bwd_data(d, w, off, w_order=wo, out=dX, out_dtype=F.OUT_F32)
+    dW = F.fc_grouped_bwd_weight(x, d, off, out_dtype=F.OUT_F32)
+    wantY, wantX, wantW = torch.zeros_like(Y), torch.zeros_like(dX), torch.zeros_like(dW)
+    for e in range(E):
+        s = slice(lo[e], lo[e + 1])
+        if counts[e]:
+            wantY[s], wantX[s] = X[s].float() @ W[e].float(), dY[s].float() @ W[e].float().t()
+            wantW[e] = X[s].float().t() @ dY[s].float()
+    assert torch.equal(Y, wantY) and torch.equal(dX, wantX) and torch.equal(dW, wantW)
 
 
 # ---- streams, graphs, several calls at once
