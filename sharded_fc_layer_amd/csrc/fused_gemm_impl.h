@@ -204,6 +204,7 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) fb0[j] = fragment<BN, B_OC>(smem + kABytes, wn0 + j * 32, 0, lane);
 
+        constexpr int kMfmas = TM * TN, kReads = kMfmas == 4 ? 2 : TM + TN;
         constexpr int kAhead = ANY ? Q + 2 : S;
         const uint16_t* na = pa + kAhead * kBK * sa;
         const uint16_t* nb = pb + kAhead * kBK * sb;
@@ -214,47 +215,63 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
         for (int h = 0; h < (ANY ? Q : 1); ++h) {
             const int kh = k + h;
             char* st = smem + (kh % S) * kStageBytes;
+            // MFMAs, LDS reads and loads alternate: a wave waits to issue a
+            // read or a load while the other waves' are taken, and its matrix
+            // unit works meanwhile (reads and loads in front of the MFMAs
+            // measured X)
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa1[i] = fragment<BM, A_OC>(st, wm0 + i * 32, 1, lane);
+            for (int q = 0; q < kMfmas; ++q) {
+                acc[q / TN][q % TN] =
+                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb0[q % TN], fa0[q / TN], acc[q / TN][q % TN], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb1[j] = fragment<BN, B_OC>(st + kABytes, wn0 + j * 32, 1, lane);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb0[j], fa0[i], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int r = q * kReads; r < (q + 1) * kReads && r < TM + TN; ++r)
+                    if (r < TM)
+                        fa1[r] = fragment<BM, A_OC>(st, wm0 + r * 32, 1, lane);
+                    else
+                        fb1[r - TM] = fragment<BN, B_OC>(st + kABytes, wn0 + (r - TM) * 32, 1, lane);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             // this wave has read all of stage k; stage k + 1 must have landed
             waitcnt<ANY ? 63 : (S - 2) * L, 0>();
             __builtin_amdgcn_s_barrier();
             const char* nx = smem + ((kh + 1) % S) * kStageBytes;
-#pragma unroll
-            for (int i = 0; i < TM; ++i) fa0[i] = fragment<BM, A_OC>(nx, wm0 + i * 32, 0, lane);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) fb0[j] = fragment<BN, B_OC>(nx + kABytes, wn0 + j * 32, 0, lane);
-            __builtin_amdgcn_sched_barrier(0);
             const int left = len - (kh + kAhead) * kBK;
-            if constexpr (ANY) {
-                // stage k + 2 into a slot that was left before the last barrier;
-                // the loads of stage k + 2 + Q into its registers
-                constexpr int kSet = Q == 2 ? 0 : 2;
-                char* to = smem + ((kh + 2) % S) * kStageBytes;
-                da.store((h + kSet) % Q, to, wave, lane);
-                db.store((h + kSet) % Q, to + kABytes, wave, lane);
-                da.load((h + kSet) % Q, na, left, g.a_end);
-                db.load((h + kSet) % Q, nb, left, g.b_end);
-            } else {  // the loads of stage k + S go into stage k's slot
-                da.issue(na, st, left, wave);
-                db.issue(nb, st + kABytes, left, wave);
+            // ANY: stage k + 2 into a slot that was left before the last
+            // barrier, the loads of stage k + 2 + Q into its registers;
+            // else the loads of stage k + S into stage k's slot
+            constexpr int kSet = Q == 2 ? 0 : 2;
+            char* to = ANY ? smem + ((kh + 2) % S) * kStageBytes : st;
+#pragma unroll
+            for (int q = 0; q < kMfmas; ++q) {
+                acc[q / TN][q % TN] =
+                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb1[q % TN], fa1[q / TN], acc[q / TN][q % TN], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int r = q * kReads; r < (q + 1) * kReads && r < TM + TN; ++r)
+                    if (r < TM)
+                        fa0[r] = fragment<BM, A_OC>(nx, wm0 + r * 32, 0, lane);
+                    else
+                        fb0[r - TM] = fragment<BN, B_OC>(nx + kABytes, wn0 + (r - TM) * 32, 0, lane);
+                if (q == (kMfmas > 1 ? kMfmas - 2 : 0)) {
+                    if constexpr (ANY) {
+                        da.store((h + kSet) % Q, to, wave, lane);
+                        da.load((h + kSet) % Q, na, left, g.a_end);
+                    } else {
+                        da.issue(na, to, left, wave);
+                    }
+                }
+                if (q == kMfmas - 1) {
+                    if constexpr (ANY) {
+                        db.store((h + kSet) % Q, to + kABytes, wave, lane);
+                        db.load((h + kSet) % Q, nb, left, g.b_end);
+                    } else {
+                        db.issue(nb, to + kABytes, left, wave);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
             na += kBK * sa, nb += kBK * sb;
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb1[j], fa1[i], acc[i][j], 0, 0, 0);
         }
         waitcnt<0, 0>();  // drain the trailing loads
     }
