@@ -100,10 +100,10 @@ int64_t tiles_of(int tile, int64_t M, int64_t N) {
 //    of which a reduction that is not head plus periods has up to 5 more (136
 //    tiles: 19.2 at a reduction of 72, 49.5 at 2056; 1024 tiles at 2048: 213);
 //  * a round of the general kernel's tiles 5 and 0.65 for each 32-value stage
-//    with a block to a CU, 7 and 1.0 with two (255 tiles: 20.5 at 520, 46.7 at
-//    2000; 4096 tiles at 2048: 577); where rows start anywhere 2 more and 1.3 of
-//    the stages' time (84 tiles at 1001: 38); tiles of 32 or 64 rows 0.4 of it
-//    (391 tiles of 64 rows at 2048: 35);
+//    with a block to a CU, 7 and 1.0 with two, from memory (168 tiles at 3904: 73;
+//    4096 tiles at 2048: 577; operands that lie in the caches take 0.37 to 0.5);
+//    where rows start anywhere 2 more and 1.3 of the stages' time; tiles of 32
+//    or 64 rows 0.4 of it (391 tiles of 64 rows at 2048: 35);
 //  * neither reads, writes or copies faster than 5 TB/s (experts' weights of 403
 //    MB against 48 rows: 61 and 93);
 //  * a launch 3; a split reduction's second launch 4, its planes at 6 TB/s (252

@@ -66,7 +66,12 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
     const int64_t br = grp == GRP_RED ? g.T : b_oc ? g.K : g.N, bc = b_oc ? g.N : g.K;
     g.a_end = g.A + (ar - 1) * g.lda + ac;
     g.b_end = g.B + (grp == GRP_ROWS ? (g.E - 1) * g.b_stride : 0) + (br - 1) * g.ldb + bc;
-    const bool any = g.lda % 8 != 0 || g.ldb % 8 != 0 || (uintptr_t)g.A % 16 != 0 || (uintptr_t)g.B % 16 != 0;
+    // (few rows against a long, wide W whose rows are the reduction, a block to
+    // a CU at most: through registers too. 48 rows, 20000 columns, a reduction
+    // of 520, 1000, 2000: 11.4, 19.9, 34.6 us straight into LDS, 12.4, 18.2,
+    // 26.5 through registers; with more blocks 62 against 75)
+    const bool any = g.lda % 8 != 0 || g.ldb % 8 != 0 || (uintptr_t)g.A % 16 != 0 || (uintptr_t)g.B % 16 != 0 ||
+                     (tile != 0 && b_oc && blocks <= 256 && g.k_split >= 768);
     if ((tile != 0 && a_oc) || (grp == GRP_RED && !(a_oc && b_oc)) || (grp == GRP_ROWS && a_oc)) return hipErrorInvalidValue;
     const FusedFn fn = any ? fused_kernel<true>(mode, grp, tile, a_oc, b_oc) : fused_kernel<false>(mode, grp, tile, a_oc, b_oc);
     if (!fn) return hipErrorInvalidValue;

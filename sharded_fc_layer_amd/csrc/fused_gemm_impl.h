@@ -217,8 +217,8 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
             char* st = smem + (kh % S) * kStageBytes;
             // MFMAs, LDS reads and loads alternate: a wave waits to issue a
             // read or a load while the other waves' are taken, and its matrix
-            // unit works meanwhile (reads and loads in front of the MFMAs
-            // measured X)
+            // unit works meanwhile (255 tiles over a reduction of 2000, one to a CU:
+            // 46.7 us with reads and loads in front of the MFMAs, 36.3 so)
 #pragma unroll
             for (int q = 0; q < kMfmas; ++q) {
                 acc[q / TN][q % TN] =
