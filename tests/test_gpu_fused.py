@@ -533,6 +533,28 @@ def test_nothing_past_the_operands_counts(shape, offset):
         assert bool(torch.isfinite(dX1).all()) and bool(torch.isfinite(dW1).all())
 
 
+@pytest.mark.parametrize("shape", [(48, 1000, 20000), (5, 2056, 28008), (20, 776, 32000), (64, 1544, 16392)])
+def test_few_rows_wide_and_long(shape):
+    """A few rows against a wide W whose rows are the reduction, with nothing but NaN around it."""
+    M, K, N = shape
+    g = gen(M + N)
+    X, W = among_nans(integers(g, M, K), 0), integers(g, K, N)
+    Y = X.float() @ W.float()
+    assert torch.equal(F.fc_fwd_act(X, among_nans(W, 0), out_dtype=F.OUT_F32), Y)
+    # the gradient of the layer with K outputs and N inputs, W column-major: the same product
+    Z = torch.ones((M, N), dtype=torch.bfloat16, device="cuda")
+    Z[:, ::3] = -1.0
+    dX, db = F.fc_bwd_data_act(X, among_nans(W, 0), Z, F.ACT_RELU, w_order=COL, out_dtype=F.OUT_F32, bias_grad=True)
+    want = torch.where(Z > 0, Y, 0.0)
+    assert torch.equal(dX, want) and torch.equal(db, want.sum(0))
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    z = Y.double() / 256
+    _, lse, tl = F.fc_xent_fwd((X / 16).contiguous(), (W / 16).contiguous(), t)
+    want = torch.logsumexp(z, 1)
+    within(lse, want, 2.0 ** -20 + (N + 16) * U + 4 * U * want.abs(), f"{shape} lse")
+    assert torch.equal(tl.double(), z.gather(1, t[:, None])[:, 0])
+
+
 @pytest.mark.parametrize("case", [([3, 0, 70, 1], 2, 9, 40, 136), ([300, 17, 0, 64], 5, 3, 135, 264),
                                   ([1, 2], 3, 2, 1501, 40), ([700, 0, 30, 1500], 3, 5, 1200, 1300)],
                          ids=lambda c: f"{len(c[0])}x{c[3]}x{c[4]}")
