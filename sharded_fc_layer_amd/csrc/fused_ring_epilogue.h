@@ -156,6 +156,20 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
     }
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i) { FCE_FETCH(i) }
+    // The column sums take every row of the tile. Rows outside are products of
+    // zeros with B, which are NaN where B is infinite: they are read from a
+    // row of zeros instead, one choice of address for the lane's values of a
+    // row. `there` is `rows` out of the compiler's sight: it would keep the
+    // comparisons that loads and stores make, in scalar registers that it then
+    // spills. It costs 1 us of the 256 that 8192 x 8192 outputs over 2048 take
+    // with gelu by tanh (4 with a choice for each value), and 10 to 18 of the
+    // 284 to 338 of 8187 columns, whose rows are read two values at a time.
+    [[maybe_unused]] char* zeros = stage + 2 * 8192;
+    [[maybe_unused]] int there = rows;
+    if constexpr (MODE == EPI_DACT) {
+        asm("" : "+v"(there));
+        *reinterpret_cast<u32x2*>(zeros + lane * 8) = u32x2{0, 0};
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         char* buf = stage + (i & 1) * 8192;
@@ -165,9 +179,10 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
 #pragma unroll
         for (int u = 0; u < RPG; ++u) {
             const int r = VEC ? 4 * u + rq : u, row = 16 * i + r;
+            const char* src = MODE != EPI_DACT || row < there ? buf + r * 512 : zeros;
             float v[W];
             if constexpr (VEC) {
-                const char* p = buf + r * 512 + (((col >> 2) ^ ((r & 7) << 1)) << 4);
+                const char* p = src + (((col >> 2) ^ ((r & 7) << 1)) << 4);
                 const f32x4 lo = reinterpret_cast<const f32x4*>(p)[0], hi = reinterpret_cast<const f32x4*>(p)[1];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] = lo[q], v[4 + q] = hi[q];
@@ -175,7 +190,7 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
 #pragma unroll
                 for (int q = 0; q < W; ++q) {
                     const int c = col + 64 * q;
-                    v[q] = *reinterpret_cast<const float*>(buf + r * 512 + (((c >> 2) ^ ((r & 7) << 1)) << 4) +
+                    v[q] = *reinterpret_cast<const float*>(src + (((c >> 2) ^ ((r & 7) << 1)) << 4) +
                                                            ((c & 3) << 2));
                 }
             }
@@ -200,7 +215,7 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
                     for (int q = 0; q < W; ++q) v[q] += in(q);
                 }
             } else if constexpr (MODE == EPI_DACT) {
-                // rows and columns outside are zeros in v: their loads read zeros
+                // rows and columns outside are zeros: in v, and what their loads read
 #pragma unroll
                 for (int q = 0; q < W; ++q) {
                     v[q] *= act_slope<KIND>(a, in(q));

@@ -734,3 +734,25 @@ def test_a_step_of_all_of_them():
         rel = ((got.double() - want).norm() / want.norm()).item()
         log(f"  {name}: {rel:.3g}")
         assert rel <= 16 * H, name
+
+
+# ---- values at the ends of the types
+
+@pytest.mark.parametrize("shape", [(4000, 640, 4104), (4001, 640, 4099), (333, 611, 1531), (40, 512, 264)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_bias_gradient_of_infinite_weights(shape, wo):
+    """Column sums of infinities are infinities: a tile's rows past the last one, whose products of zeros
+    with infinite weights are NaN, are not in them."""
+    M, N, K = shape
+    g = gen(M)
+    dY = torch.randint(1, 4, (M, N), device="cuda", generator=g).to(torch.bfloat16)
+    W, Z = integers(g, K, N), torch.ones((M, K), dtype=torch.bfloat16, device="cuda")
+    up = dY.double() @ W.double().t()
+    W[3, 5], W[K - 1, 0] = float("inf"), -float("inf")
+    up[:, 3], up[:, K - 1] = float("inf"), -float("inf")  # dY is positive
+    for act in ACTS:  # every slope is positive at 1
+        dX, db = F.fc_bwd_data_act(dY, stored(W, wo), Z, act, w_order=wo, out_dtype=F.OUT_F32, bias_grad=True)
+        assert db[3].item() == float("inf") and db[K - 1].item() == -float("inf"), ACT_NAMES[act]
+        assert bool(torch.isfinite(db[4:K - 1]).all()) and bool(torch.isfinite(db[:3]).all()), ACT_NAMES[act]
+        if act in (F.ACT_NONE, F.ACT_RELU):  # sums of integers below 2^24
+            assert torch.equal(dX.double(), up) and torch.equal(db.double(), up.sum(0))
