@@ -16,6 +16,7 @@ Integer inputs, whose products and sums fit fp32, are compared bit for bit.
 """
 from __future__ import annotations
 
+import math
 import sys
 
 import pytest
@@ -756,3 +757,35 @@ def test_bias_gradient_of_infinite_weights(shape, wo):
         assert bool(torch.isfinite(db[4:K - 1]).all()) and bool(torch.isfinite(db[:3]).all()), ACT_NAMES[act]
         if act in (F.ACT_NONE, F.ACT_RELU):  # sums of integers below 2^24
             assert torch.equal(dX.double(), up) and torch.equal(db.double(), up.sum(0))
+
+
+@pytest.mark.parametrize("shape", [(4100, 640, 1500), (130, 72, 520), (96, 2001, 300)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_xent_logits_of_any_size(shape, wo):
+    """Logits up to the type's largest and lowest values (a mask's), in some columns or in all."""
+    M, K, N = shape
+    g = gen(N)
+    X, W = normal(g, M, K), normal(g, K, N, scale=0.3)
+    X[:, 0] = (1 + torch.arange(M, device="cuda") % 128 / 128.0).to(torch.bfloat16)  # 1 <= x < 2, held exactly
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    for big in (-1e6, -1e10, -3e37, -1.6e38):
+        W[0] = 0.0
+        W[0, N // 4:N // 2 + 3] = big
+        W[0, N - 1] = big
+        rest = W[0] == 0
+        z = X.double() @ W.double()
+        _, lse, tl = F.fc_xent_fwd(X, stored(W, wo), t, w_order=wo)
+        want = torch.logsumexp(z, 1)  # of the columns that are not masked: the others' terms are below e^-10^5
+        ez = (K + 16) * U * (X.double().abs() @ W[:, rest].double().abs()).max(1).values
+        within(lse, want, ez + 2.0 ** -20 + (N + 16) * U + 4 * U * want.abs(), f"{shape} {wo} {big:g} in places")
+        hit = z.gather(1, t[:, None])[:, 0]
+        assert bool(((tl.double() - hit).abs() <= (K + 16) * U * (X.double().abs() @ W.double().abs()).max(1).values).all())
+    # one value in all columns: lse = z + log N, whose two additions round
+    Xs = torch.zeros_like(X)
+    Xs[:, 0] = X[:, 0]
+    for big in (-1.6e38, -1e10, -1e6, -30.0, 0.0, 30.0, 1e6, 1e10, 1.6e38):
+        W[0] = big
+        z = Xs[:, 0].double() * W[0, 0].double()
+        _, lse, _ = F.fc_xent_fwd(Xs, stored(W, wo), t, w_order=wo)
+        want = z + math.log(N)
+        within(lse, want, 2.0 ** -20 + (N + 16) * U + 4 * U * want.abs(), f"{shape} {wo} {big:g} everywhere")
