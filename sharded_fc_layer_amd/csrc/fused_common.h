@@ -31,9 +31,12 @@ __device__ __forceinline__ float rcp_f32(float x) { return __builtin_amdgcn_rcpf
 //   by tanh, since (1 + tanh(u / 2)) / 2 = sigma(u) with u / 2 = sqrt(2 / pi) (z
 //   + 0.044715 z^3), which written so has no cancellation for negative z;
 // * kNormal: z Phi(z), gelu with the exact normal distribution function:
-//   Phi(z) = 1 - q(|z|) for z > 0, else q(|z|), where q(x) = exp(-x^2 / 2) P(t) /
-//   2, t = 1 / (1 + 0.3275911 x / sqrt 2), P of degree 5: Abramowitz and Stegun,
-//   Handbook of Mathematical Functions, 7.1.26, off by at most 1.5e-7 in erf.
+//   Phi(z) = 1 - q(|z|) for z > 0, else q(|z|), where q(x) = exp(-x^2 / 2) t P(t),
+//   t = 1 / (1 + 0.304 x), and P of degree 7 is a minimax fit to exp(x^2 / 2)
+//   Phi(-x) / t over 0 <= x <= 13.5 (past which q is less than fp32 holds),
+//   relative to it: off by at most 8.4e-8, in fp32 by 8 (1 + z^2) 2^-24
+//   relative. So small values far below zero keep their digits; a fit with a
+//   bound on erf itself loses them (at z = -6 one of 1.5e-7 errs by 0.4 %).
 //
 // The last two take one exponential and one reciprocal. ActParams holds u's
 // coefficients times -log2(e), for exp(-u) = 2^(z (e1 + e3 z^2)), and c1 and 3
@@ -66,13 +69,16 @@ __device__ __forceinline__ float clamp64(float z) {
 // Phi(z), and exp(-z^2 / 2) in e
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
     const float x = fabsf(z);
-    const float t = rcp_f32(1.0f + 0.23164189f * x);  // 0.3275911 / sqrt 2
+    const float t = rcp_f32(1.0f + 0.304f * x);
     e = __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
-    float p = 0.5f * 1.061405429f;
-    p = p * t - 0.5f * 1.453152027f;
-    p = p * t + 0.5f * 1.421413741f;
-    p = p * t - 0.5f * 0.284496736f;
-    p = p * t + 0.5f * 0.254829592f;
+    float p = 0.036859006f;
+    p = p * t - 0.1553007f;
+    p = p * t + 0.1921915f;
+    p = p * t - 0.04313204f;
+    p = p * t + 0.123554595f;
+    p = p * t + 0.10242222f;
+    p = p * t + 0.1221708f;
+    p = p * t + 0.12123468f;
     const float q = p * t * e;
     return z > 0.0f ? 1.0f - q : q;
 }

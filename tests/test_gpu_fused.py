@@ -789,3 +789,26 @@ def test_xent_logits_of_any_size(shape, wo):
         _, lse, _ = F.fc_xent_fwd(Xs, stored(W, wo), t, w_order=wo)
         want = z + math.log(N)
         within(lse, want, 2.0 ** -20 + (N + 16) * U + 4 * U * want.abs(), f"{shape} {wo} {big:g} everywhere")
+
+
+@pytest.mark.parametrize("shape", [(20, 1, 1), (30, 256, 72), (4096, 512, 4096)])
+def test_gelu_of_negative_values(shape):
+    """The negative tail of z Phi(z) and its slope against erfc, relative to the value. exp(-z^2 / 2)
+    comes from an argument with three roundings, 1.5 z^2 u relative; the fit, its evaluation, the reciprocal,
+    the exponential and the products 16 u."""
+    M, K, N = shape
+    zs = torch.linspace(-12.5, -0.25, 4001, device="cuda").to(torch.bfloat16)
+    for z in zs.split(M) if M < 64 else (zs,):
+        m = z.numel()
+        X, W = torch.zeros((m, K), dtype=torch.bfloat16, device="cuda"), torch.zeros((K, N), dtype=torch.bfloat16, device="cuda")
+        X[:, 0], W[0] = z, 1.0
+        zd = z.double()
+        cdf, pdf = 0.5 * torch.special.erfc(-zd * 0.5 ** 0.5), torch.exp(-0.5 * zd * zd) / (2 * math.pi) ** 0.5
+        rel = 16 * U + 2 * zd * zd * U
+        Y = F.fc_fwd_act(X, W, act=F.ACT_GELU, out_dtype=F.OUT_F32)
+        within(Y, (zd * cdf)[:, None].expand(m, N), (rel * (zd * cdf).abs())[:, None], f"{shape} gelu")
+        # dX = (dY W^T) slope(Z), dY W^T = 1
+        dY, Wd = X[:, :1].clone().fill_(1.0), torch.ones((N, 1), dtype=torch.bfloat16, device="cuda")
+        Z = z[:, None].expand(m, N).contiguous()
+        dX = F.fc_bwd_data_act(dY, Wd, Z, F.ACT_GELU, out_dtype=F.OUT_F32)
+        within(dX, (cdf + zd * pdf)[:, None].expand(m, N), (rel * (cdf + zd.abs() * pdf))[:, None], f"{shape} slope")
