@@ -257,6 +257,13 @@ class _On:
         """An output: the caller's tensor, checked, or a new one."""
         return self.empty(shape, dtype) if t is None else _tensor(t, dtype, shape, name)
 
+    def zero(self, t):
+        import torch
+        if self.other is None:
+            return t.zero_()
+        with torch.cuda.stream(self.other):
+            return t.zero_()
+
     def workspace(self, need, what):
         """The call's workspace (None if it needs none), its address and size.
         It may be dropped after the call: its memory is handed on in stream order."""
@@ -455,6 +462,10 @@ def _grouped(op: int, fn, P, Q, offsets, out, out_dtype: int, T: int, E: int, K:
     import torch
     _tensor(offsets, torch.int64, (E + 1,), "offsets")
     _here(P, Q, offsets, out)
+    if T == 0:  # no row for any expert: the library's sizes start at 1, the answer is known
+        if lib().fc_grouped_ws_bytes(op, 1, E, K, N, w_order, 1) < 0:
+            raise FcError(FC_E_INVALID, what)
+        return on.zero(out) if op == OP_BWD_WEIGHT and out_dtype != OUT_F32_ACC else out
     ws, wp, wn = on.workspace(lib().fc_grouped_ws_bytes(op, T, E, K, N, w_order, _aligned(P, Q)), what)
     orders = () if op == OP_BWD_WEIGHT else (w_order,)
     _check(fn(P.data_ptr(), Q.data_ptr(), *orders, offsets.data_ptr(), out.data_ptr(), out_dtype, T, E, K, N, wp, wn,
@@ -465,7 +476,8 @@ def _grouped(op: int, fn, P, Q, offsets, out, out_dtype: int, T: int, E: int, K:
 def fc_grouped_fwd(X, W, offsets, w_order: int = ROW, out=None, out_dtype: int = OUT_BF16, stream=None):
     """Y = X . W[e] for the rows offsets[e] .. offsets[e + 1] - 1 of each expert
     e: X is T x K, W is E x K x N (COL: E x N x K), offsets E + 1 int64 values
-    on the GPU. Rows outside offsets[0] .. offsets[E] of `out` are left as they were."""
+    on the GPU. Rows outside offsets[0] .. offsets[E] of `out` are left as they were.
+    T may be 0 in all three calls."""
     _bf16_2d(X, "X")
     E, K, N = _experts(W, w_order)
     T, K2 = X.shape

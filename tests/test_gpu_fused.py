@@ -812,3 +812,46 @@ def test_gelu_of_negative_values(shape):
         Z = z[:, None].expand(m, N).contiguous()
         dX = F.fc_bwd_data_act(dY, Wd, Z, F.ACT_GELU, out_dtype=F.OUT_F32)
         within(dX, (cdf + zd * pdf)[:, None].expand(m, N), (rel * (cdf + zd.abs() * pdf))[:, None], f"{shape} slope")
+
+
+@pytest.mark.parametrize("other", [False, True])
+def test_expert_layers_without_rows(other):
+    """A step in which no row came: empty outputs, weight gradients of zeros (or left as they were)."""
+    E, K, N = 3, 24, 40
+    g = gen(6)
+    X, dY = torch.empty((0, K), dtype=torch.bfloat16, device="cuda"), torch.empty((0, N), dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int64, device="cuda")
+    k = {"stream": torch.cuda.Stream()} if other else {}
+    torch.cuda.synchronize()
+    for wo in (ROW, COL):
+        W = stored(normal(g, E, K, N), wo)
+        for od, dt in ((F.OUT_BF16, torch.bfloat16), (F.OUT_F32, torch.float32)):
+            Y, dX = F.fc_grouped_fwd(X, W, off, w_order=wo, out_dtype=od, **k), F.fc_grouped_bwd_data(dY, W, off, w_order=wo, out_dtype=od, **k)
+            assert Y.shape == (0, N) and dX.shape == (0, K) and Y.dtype == dX.dtype == dt
+            dW = torch.full((E, K, N), 5.0, dtype=dt, device="cuda")
+            torch.cuda.synchronize()
+            assert F.fc_grouped_bwd_weight(X, dY, off, out=dW, out_dtype=od, **k) is dW
+            torch.cuda.synchronize()
+            assert bool((dW == 0).all())
+    acc = torch.full((E, K, N), 5.0, device="cuda")
+    F.fc_grouped_bwd_weight(X, dY, off, out=acc, out_dtype=F.OUT_F32_ACC, **k)
+    torch.cuda.synchronize()
+    assert bool((acc == 5).all())
+    with pytest.raises(TypeError, match="offsets"):  # checked as with rows
+        F.fc_grouped_fwd(X, W, off[:2], w_order=COL)
+    with pytest.raises(ValueError, match="accumulating"):
+        F.fc_grouped_bwd_weight(X, dY, off, out_dtype=F.OUT_F32_ACC)
+
+
+def test_expert_layers_without_rows_in_a_graph():
+    E, K, N = 2, 16, 24
+    X, dY = torch.empty((0, K), dtype=torch.bfloat16, device="cuda"), torch.empty((0, N), dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int64, device="cuda")
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        dW = F.fc_grouped_bwd_weight(X, dY, off)
+    for _ in range(3):
+        dW.fill_(1.0)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert bool((dW == 0).all())
