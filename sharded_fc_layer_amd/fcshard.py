@@ -239,6 +239,8 @@ class _On:
     def __init__(self, stream, like):
         import torch
         self.device = like.device
+        if isinstance(stream, torch.cuda.Stream) and stream.device_index != like.get_device():
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {like.device}")
         current = torch._C._cuda_getCurrentRawStream(like.get_device() if like.is_cuda else 0)
         self.handle = current if stream is None else _stream(stream)
         self.other = None

@@ -855,3 +855,11 @@ def test_expert_layers_without_rows_in_a_graph():
         gr.replay()
         torch.cuda.synchronize()
         assert bool((dW == 0).all())
+
+
+def test_a_stream_of_another_device_is_refused():
+    g = gen(1)
+    X, W = normal(g, 8, 16), normal(g, 16, 24)
+    far = torch.cuda.Stream(stream_id=0, device_index=X.get_device() + 1, device_type=torch.cuda.current_stream().device_type)
+    with pytest.raises(ValueError, match="stream"):
+        F.fc_fwd_act(X, W, stream=far)
