@@ -296,9 +296,8 @@ XentBwdPlan xent_bwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool align
     const bool ring_any = gain > 0 && (!copies || gain > copy_us(bytes));
     if (!ring_any)
         for (int i = 0; i < 3; ++i) *to[i] = small[i];
-    const bool ring_used = ring_any;
-    p.A = operand(M, K, aligned, ring_used, &ws);
-    p.B = operand(b_oc ? K : N, bcols, aligned, ring_used, &ws);
+    p.A = operand(M, K, aligned, ring_any, &ws);
+    p.B = operand(b_oc ? K : N, bcols, aligned, ring_any, &ws);
     p.d_off = ws;
     ws += up(M * p.d_ld * 2, 256);
     p.planes = ws;
