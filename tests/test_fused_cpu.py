@@ -181,3 +181,51 @@ def test_binding_refuses_what_is_not_on_the_gpu():
         F.fc_xent_fwd(x, w, torch.zeros(4, dtype=torch.int64))
     with pytest.raises(ValueError, match="CUDA"):
         F.fc_grouped_fwd(x, w[None], torch.zeros(2, dtype=torch.int64))
+
+
+# ---- which kernel the planner takes, as the workspaces show it
+
+def up(v, a):
+    return -(-v // a) * a
+
+
+def copied(rows, cols, aligned=True):
+    """Bytes of an operand's copy for the 256 x 256 tiles: rows padded to 64 values, none if they fit as they are."""
+    return 0 if cols % 8 == 0 and aligned else up(rows * up(cols, 64) * 2, 256)
+
+
+def weight(K, N, order, aligned=True):
+    return copied(K, N, aligned) if order == F.ROW else copied(N, K, aligned)
+
+
+def test_shapes_of_the_large_tiles_go_there(L):
+    """The GPU tests of the 256 x 256 tiles use shapes that the planner sends there. Those leave two rows of
+    column sums for 256 rows, two statistics for 256 columns (the 128 x 128 tiles four), planes never, and
+    copies where rows do not fit, which the smaller tiles do not make."""
+    import test_gpu_fused as G
+    for order in (F.ROW, F.COL):
+        for M, N, K in G.RING + [(4096, 100, 4096)]:  # fc_bwd_data_act: the reduction is N
+            assert L.fc_bwd_data_act_ws_bytes(M, K, N, order, 1) == \
+                copied(M, N) + weight(K, N, order) + up(2 * -(-M // 256) * K * 4, 256), (M, N, K)
+        for M, K, N in G.RING + [(4100, 640, 1500)]:
+            # fc_fwd_act and fc_xent_fwd are planned alike; the statistics show it where nothing is copied
+            w = copied(M, K) + weight(K, N, order)
+            assert L.fc_xent_fwd_ws_bytes(M, K, N, order, 1) == w + up(2 * 2 * -(-N // 256) * M * 4, 256), (M, K, N)
+            assert L.fc_fwd_act_ws_bytes(M, K, N, F.ROW, order, 1) == w
+            assert L.fc_fwd_act_ws_bytes(M, K, N, F.COL, order, 1) == copied(K, M) + weight(K, N, order)
+        for M, K, N in G.RING_XENT_BWD:
+            assert L.fc_xent_bwd_ws_bytes(M, K, N, order, 1) == \
+                copied(M, K) + weight(K, N, order) + up(M * up(N, 64) * 2, 256), (M, K, N)
+        for counts, first, behind, K, N in G.RING_GROUPED:
+            E, T = len(counts), first + sum(counts) + behind
+            for op, A in ((F.OP_FWD, K), (F.OP_BWD_DATA, N), (F.OP_BWD_WEIGHT, K)):
+                if K < 1000 and op != F.OP_FWD:
+                    continue  # few outputs: not worth the copies
+                b = copied(T, N, False) if op == F.OP_BWD_WEIGHT else \
+                    copied(E * K, N, False) if order == F.ROW else copied(E * N, K, False)
+                assert L.fc_grouped_ws_bytes(op, T, E, K, N, order, 0) == copied(T, A, False) + b, (T, E, K, N, op)
+        for M, K, N in G.LAST_PIECE:  # the last piece has 33 columns; the copy shows the large tiles
+            piece = (1 << 28) // (2 * M) // 256 * 256
+            assert 0 < N % piece < 64 and N > piece
+            assert L.fc_xent_bwd_ws_bytes(M, K, N, order, 1) == \
+                weight(K, N, order) + up(M * piece * 2, 256) + M * up(K, 64) * 4

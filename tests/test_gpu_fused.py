@@ -863,3 +863,112 @@ def test_a_stream_of_another_device_is_refused():
     far = torch.cuda.Stream(stream_id=0, device_index=X.get_device() + 1, device_type=torch.cuda.current_stream().device_type)
     with pytest.raises(ValueError, match="stream"):
         F.fc_fwd_act(X, W, stream=far)
+
+
+# ---- the 256 x 256 tiles: shapes that the planner sends there (test_fused_cpu.py asks it)
+
+# whole reductions of 8 and 10 stages of 64 (2 and 4 past a period of 6), a partial last stage, and
+# rows of 8 values' multiples or not
+RING = [(4096, 512, 4096), (4000, 640, 4104), (4000, 600, 4104), (4001, 600, 4099)]
+RING_XENT_BWD = [(4096, 2048, 4096), (4352, 2048, 4352), (4100, 2056, 4104), (4099, 2049, 4103)]
+RING_GROUPED = [([1100, 900, 0, 2000], 0, 0, 1024, 4096), ([1600, 0, 70, 1800, 513], 3, 14, 2056, 4104),
+                ([1103, 900, 1500, 497], 1, 2, 1031, 4103), ([1100, 900, 0, 2000], 0, 0, 512, 4096)]
+
+
+@pytest.mark.parametrize("shape", RING)
+@pytest.mark.parametrize("xo, wo", [(ROW, ROW), (ROW, COL), (COL, ROW), (COL, COL)])
+def test_fwd_act_in_large_tiles(shape, xo, wo):
+    test_fwd_act(shape, xo, wo)
+
+
+@pytest.mark.parametrize("shape", RING + [(4096, 100, 4096)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_bwd_data_act_in_large_tiles(shape, wo):
+    test_bwd_data_act(shape, wo)
+
+
+@pytest.mark.parametrize("shape", RING)
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_xent_fwd_in_large_tiles(shape, wo):
+    test_xent_fwd(shape, wo)
+
+
+@pytest.mark.parametrize("shape", RING_XENT_BWD)
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_xent_bwd_in_large_tiles(shape, wo):
+    test_xent_bwd(shape, wo)
+
+
+@pytest.mark.parametrize("case", RING_GROUPED, ids=lambda c: f"{len(c[0])}x{c[3]}x{c[4]}")
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_grouped_in_large_tiles(case, wo):
+    test_grouped_integers_are_exact(case, wo)
+
+
+@pytest.mark.parametrize("shape", [RING[0], RING[3]])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_xent_rows_that_do_not_count_in_large_tiles(shape, wo):
+    """Rows of NaN and infinities whose targets are to be ignored: no loss, no gradient, no other row disturbed."""
+    M, K, N = shape
+    g = gen(K)
+    X, W = normal(g, M, K), normal(g, K, N, scale=0.1)
+    t = torch.arange(M, device="cuda") % N
+    out = torch.tensor([5, 128, 255, 256, M - 1], device="cuda")
+    X[out[::2]], X[out[1::2]] = float("nan"), float("inf")
+    t[out] = -100
+    counts = t != -100
+    z = X[counts].double() @ W.double()
+    ez = (K + 16) * U * (X[counts].double().abs() @ W.double().abs()).max(1).values
+    loss, lse, _ = F.fc_xent_fwd(X, stored(W, wo), t, w_order=wo)
+    want = torch.logsumexp(z, 1)
+    within(lse[counts], want, ez + 2.0 ** -20 + (N + 16) * U + 4 * U * want.abs(), f"{shape} lse")
+    assert bool((loss[~counts] == 0).all()) and bool(torch.isfinite(loss).all())
+    dX, _ = F.fc_xent_bwd(X, stored(W, wo), t, lse, torch.ones(M, device="cuda"), w_order=wo)
+    assert bool((dX[~counts] == 0).all()) and bool(torch.isfinite(dX).all())
+
+
+# pieces of 7936 columns, the last of 33
+LAST_PIECE = [(16500, 40, 15905), (16500, 128, 15905)]
+
+
+@pytest.mark.parametrize("shape", LAST_PIECE)
+def test_xent_bwd_with_a_short_last_piece(shape):
+    """A last piece of fewer columns than a stage of the large tiles' reduction."""
+    M, K, N = shape
+    g = gen(9)
+    X, W = normal(g, M, K), normal(g, K, N, scale=0.3)
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    t[:40] = torch.arange(N - 40, N, device="cuda")
+    lse = torch.full((M,), 12.0, device="cuda")
+    w = torch.full((M,), 1.0 / M, device="cuda")
+    for wo in (ROW, COL):
+        dX, dW = F.fc_xent_bwd(X, stored(W, wo), t, lse, w, w_order=wo, dx_dtype=F.OUT_F32, dw_dtype=F.OUT_F32)
+        wW, tW = (torch.zeros((K, N), dtype=torch.float64, device="cuda") for _ in range(2))
+        for r in torch.split(torch.arange(M, device="cuda"), 4096):
+            z = X[r].double() @ W.double()
+            p = torch.exp(z - 12.0)
+            ez = (K + 16) * U * (X[r].double().abs() @ W.double().abs())
+            ep = p * torch.expm1(ez + 2.0 ** -22 * (13 + z.abs()))
+            p[torch.arange(len(r)), t[r]] -= 1
+            D = p / M
+            eD = (ep + 2 * U * (p.abs() + 1)) / M
+            eD = eD + H * (D.abs() + eD)
+            aD, aW, aX = D.abs() + eD, W.double().abs(), X[r].double().abs()
+            within(dX[r], D @ W.double().t(), (eD + (N + 16) * U * aD) @ aW.t(), f"{shape} {wo} dX")
+            wW += X[r].double().t() @ D
+            tW += aX.t() @ (eD + (M + 16) * U * aD)
+        within(dW, wW, tW, f"{shape} {wo} dW")
+
+
+# tiles of 32 and 64 rows whose operands go straight into LDS, and the few-row kernel with more than 256
+# blocks of columns (16 rows and 32)
+@pytest.mark.parametrize("shape", [(20, 128, 520), (64, 72, 520), (5, 264, 5000), (30, 264, 5000)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_fwd_act_of_few_rows(shape, wo):
+    test_fwd_act(shape, ROW, wo)
+
+
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_xent_of_few_rows(wo):
+    test_xent_fwd((64, 72, 4000), wo)
+    test_xent_bwd((64, 72, 4000), wo)
