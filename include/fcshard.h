@@ -385,7 +385,10 @@ int64_t fc_xent_fwd_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, 
  *   dW = X^T . D (K x N row-major, any output type)
  * The logits are computed again, a piece of the vocabulary at a time; a
  * piece's D is rounded to bf16 for the two products, as every gradient
- * between this library's products is. The workspace holds one piece.
+ * between this library's products is, but for a common factor of the weights,
+ * which the products' fp32 results are multiplied by. The workspace holds one
+ * piece. (A row that does not count still enters dW, as X's row times zeros:
+ * NaN or infinities there are NaN in dW.)
  */
 fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int64_t* targets, int64_t vocab_start,
                       int64_t ignore_index, const float* lse, const float* grad, void* dX, fc_out_dtype dx_dtype,

@@ -181,6 +181,7 @@ hipError_t run_product(EpiMode mode, const Shape& sh, bool a_oc, bool b_oc, Fuse
     p.out_f32 = 1;
     p.vec_out = 1;
     p.accumulate = 0;
+    p.wscale = nullptr;
     p.c_split_stride = g.M * p.ldc;
     const hipError_t e = launch_fused(EPI_STORE, GRP_NONE, sh.tile, a_oc, b_oc, p, s);
     return e != hipSuccess ? e : launch_split_epilogue(mode, g, planes, p.ldc, sh.splits, s);
@@ -269,7 +270,7 @@ struct XentBwdPlan {
     int64_t piece, d_ld, d_off;  // columns of a piece (a multiple of 256 but for the last); its buffer
     int pieces;
     Shape logits, dx, dw;        // for a whole piece
-    int64_t planes, sum_off, total;  // split products' planes; dX summed over several pieces
+    int64_t scale_off, planes, sum_off, total;  // weight_scale; split products' planes; dX summed over several pieces
 };
 XentBwdPlan xent_bwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned) {
     XentBwdPlan p;
@@ -300,6 +301,8 @@ XentBwdPlan xent_bwd_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool align
     p.B = operand(b_oc ? K : N, bcols, aligned, ring_any, &ws);
     p.d_off = ws;
     ws += up(M * p.d_ld * 2, 256);
+    p.scale_off = ws;
+    ws += 256;
     p.planes = ws;
     ws += std::max({planes_bytes(p.logits, M, p.piece), planes_bytes(p.dx, M, K), planes_bytes(p.dw, K, p.piece)});
     p.sum_off = ws;
@@ -613,6 +616,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
     uint16_t* D = reinterpret_cast<uint16_t*>(base + pl.d_off);
     float* planes = reinterpret_cast<float*>(base + pl.planes);
     float* sum = reinterpret_cast<float*>(base + pl.sum_off);
+    float* scale = reinterpret_cast<float*>(base + pl.scale_off);
     for (int p = 0; p < pl.pieces; ++p) {
         const int64_t c0 = (int64_t)p * pl.piece, c = std::min(pl.piece, N - c0);
         const uint16_t* wp = w + (w_row ? c0 : c0 * pl.B.ld);
@@ -623,7 +627,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         g.lda = pl.A.ld, g.ldb = pl.B.ld, g.ldc = pl.d_ld;
         g.accumulate = 0;
         g.targets = targets, g.v0 = vocab_start + c0, g.ignore = ignore_index;
-        g.lse = lse, g.gw = grad;
+        g.lse = lse, g.gw = grad, g.wscale = scale;
         if ((e = run_product(EPI_DLOGIT, pl.logits, false, w_row, g, planes, s)) != hipSuccess) return done(e);
         // dW = X^T D, this piece's columns
         FusedArgs h;
@@ -634,6 +638,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         h.out_f32 = wf32;
         h.accumulate = dw_dtype == FC_OUT_F32_ACCUMULATE;
         h.vec_out = vec_rows(N, h.C, nullptr, nullptr);
+        h.wscale = scale;
         if ((e = run_product(EPI_STORE, pl.dw, true, true, h, planes, s)) != hipSuccess) return done(e);
         // dX = D W^T: in one go, or summed over the pieces in 32 bits
         FusedArgs d;
@@ -646,6 +651,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         d.out_f32 = last ? xf32 : 1;
         d.accumulate = p > 0;
         d.vec_out = vec_rows(d.ldc, d.C, nullptr, nullptr);
+        d.wscale = scale;
         Shape sh = pl.dx;
         if (sh.splits == 1) sh.k_split = up(c, 64);
         if (sh.tile == kRingTile && c < 64) sh.tile = 0;  // a last piece of less than one stage

@@ -69,6 +69,12 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
     [[maybe_unused]] __shared__ float cs_all[4][256];
     [[maybe_unused]] float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int64_t first = 0, last = g.M;
+    [[maybe_unused]] float scale = 1.0f;
+    if constexpr (MODE == EPI_DLOGIT) {
+        scale = weight_scale(g);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *g.wscale = scale;
+    }
+    if constexpr (MODE == EPI_STORE) scale = g.wscale ? *g.wscale : 1.0f;
     if (MODE == EPI_STORE && g.offsets) first = g.offsets[0], last = g.offsets[g.E];
     // (the gradient of the logits has zeros up to a multiple of 8 columns)
     if (n < (MODE == EPI_DLOGIT ? (g.N + 7) / 8 * 8 : g.N)) {
@@ -94,7 +100,7 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
             if constexpr (MODE == EPI_DLOGIT) {  // as in Epilogue::row
                 const int64_t target = g.targets[m], N8 = (g.N + 7) / 8 * 8;
                 const uint64_t hit = (uint64_t)target - (uint64_t)g.v0 - (uint64_t)n;
-                const float lse = g.lse[m], w = g.gw[m];
+                const float lse = g.lse[m], w = g.gw[m] * rcp_f32(scale);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float p1 = exp_f32(v[q] - lse);
@@ -104,7 +110,10 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
                 store4_bf16(static_cast<uint16_t*>(g.C) + at, n, N8, v);
                 continue;
             }
-            if constexpr (MODE == EPI_ACT) {
+            if constexpr (MODE == EPI_STORE) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] *= scale;
+            } else if constexpr (MODE == EPI_ACT) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] += b[q];
                 if (g.Z) store4_bf16(g.Z + at, n, g.N, v);

@@ -150,6 +150,37 @@ __device__ __forceinline__ void act_slopes(int act, V& v) {
     }
 }
 
+// A factor s of all rows' weights (1 <= s < 2) that the bf16 gradient of the
+// logits leaves to the two products that read it: their epilogues multiply by
+// it in fp32. Most losses weigh every row that counts alike, and nearly all of
+// that gradient lies in the targets' columns, at values near minus the weight.
+// Rounded with it, all of them err alike, by up to 2^-8, and so do dX and dW as
+// wholes (8192 x 2048 -> 32000, fp32 outputs, relative to 64 bits: 0.0012 to
+// 0.0032 by the weight, 0.00005 without it, when they are near powers of two).
+// bf16 is what the matrix units take; the two parts of a longer D would double
+// both products. s is the mantissa of the first weight that
+// counts among 256 rows spread over all of them (straight-line code, for the
+// ring's sake); rows of other weights round as any number does. All lanes of a wave
+// call it.
+__device__ __forceinline__ float weight_scale(const FusedArgs& g) {
+    const int lane = threadIdx.x & 63;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t m = (g.M * (k * 64 + lane)) >> 8;
+        const uint32_t b = __builtin_bit_cast(uint32_t, g.gw[m]) & 0x7FFFFFFFu;
+        w[k] = g.targets[m] != g.ignore && b < 0x7F800000u ? b : 0u;
+    }
+    uint32_t s = 0;
+#pragma unroll
+    for (int k = 3; k >= 0; --k) {
+        const unsigned long long there = __ballot(w[k] != 0);
+        const uint32_t first = __builtin_amdgcn_readlane(w[k], there ? __builtin_ctzll(there) : 0);
+        s = there ? first : s;
+    }
+    return __builtin_bit_cast(float, (s & 0x7FFFFFu) | 0x3F800000u);
+}
+
 // 4 consecutive values of a row, or those of them that are left of column N
 // (the others read zeros). Rows start anywhere: gfx950 takes global vectors
 // at any element's address.

@@ -89,6 +89,7 @@ struct Epilogue {
     int64_t n;      // the lane's first column
     int left;       // its columns inside the output, up to 8
     float bias[8], cs[8];
+    float scale;    // EPI_DLOGIT: weight_scale; EPI_STORE: the factor of the results
 
     __device__ __forceinline__ Epilogue(const FusedArgs& g_, const TilePos& t_, int64_t n0, int lane_) : g(g_), t(t_) {
         lane = lane_, rq = lane / kLanes, ch = lane % kLanes;
@@ -98,6 +99,9 @@ struct Epilogue {
         if (MODE == EPI_ACT && g.bias) b = load8(g.bias + n, left);
 #pragma unroll
         for (int q = 0; q < 8; ++q) bias[q] = bf16_f32(b[q]), cs[q] = 0.0f;
+        scale = 1.0f;
+        if constexpr (MODE == EPI_DLOGIT) scale = weight_scale(g);
+        if constexpr (MODE == EPI_STORE) scale = g.wscale ? *g.wscale : 1.0f;
     }
 
     // Inputs of one row: 8 values of Z or R, or the row's target, weight and lse.
@@ -174,15 +178,19 @@ struct Epilogue {
             // rows: columns from N to the next multiple of 8 are zeros, for
             // the product that reduces over them.
             const bool counts = in.target != g.ignore;
+            const float w = in.w * rcp_f32(scale);
             const uint64_t hit = (uint64_t)in.target - (uint64_t)g.v0 - (uint64_t)n;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 float p = exp_f32(v[q] - in.lse);
                 p = hit == (uint64_t)q ? p - 1.0f : p;
-                v[q] = counts && q < left ? in.w * p : 0.0f;
+                v[q] = counts && q < left ? w * p : 0.0f;
             }
             store8(static_cast<uint16_t*>(g.C) + at, cols > 0 ? 8 : 0, v);
             return;
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] *= scale;
         }
         if (g.out_f32)
             store8(static_cast<float*>(g.C) + at, cols, v, MODE == EPI_STORE && g.accumulate);
@@ -219,8 +227,11 @@ struct Epilogue {
         }
     }
 
-    // after all rows: the column sums of this wave's rows, partial row `at`
+    // after all rows: the column sums of this wave's rows, partial row `at`; weight_scale once
     __device__ __forceinline__ void finish(int64_t at) {
+        if constexpr (MODE == EPI_DLOGIT) {
+            if (blockIdx.x == 0 && threadIdx.x == 0) *g.wscale = scale;
+        }
         if constexpr (MODE == EPI_DACT) {
             if (!g.colpart) return;
 #pragma unroll

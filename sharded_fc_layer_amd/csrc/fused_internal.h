@@ -16,7 +16,7 @@ enum EpiMode : int {
     EPI_ACT = 1,    // z = v + bias; Z = z; C = act(z) + R
     EPI_DACT = 2,   // C = v * act'(Z); column sums of C per block of rows
     EPI_STATS = 3,  // per row and block of columns: maximum and sum of exponentials; the target's value
-    EPI_DLOGIT = 4, // C = w (exp(v - lse) - [column = target])
+    EPI_DLOGIT = 4, // C = w / s (exp(v - lse) - [column = target]), s of weight_scale
     kNumEpiModes = 5
 };
 
@@ -45,6 +45,7 @@ struct FusedArgs : GemmArgs {
     int64_t ignore = 0;   // target of a row that takes no part
     const float* lse = nullptr;
     const float* gw = nullptr;       // EPI_DLOGIT: the rows' weights
+    float* wscale = nullptr;         // EPI_DLOGIT: s, written; EPI_STORE: a factor of v, or none
     float* stat = nullptr;           // EPI_STATS: [block of columns][M] maxima, then as many sums
     float* tlogit = nullptr;
     const int64_t* offsets = nullptr;  // E + 1 values on the device

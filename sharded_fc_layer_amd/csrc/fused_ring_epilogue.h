@@ -118,6 +118,7 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
     const __amdgpu_buffer_rsrc_t raux = buffer_at(auxp ? auxp + at0 : nullptr);
     const __amdgpu_buffer_rsrc_t rz = buffer_at(MODE == EPI_ACT && g.Z ? g.Z + at0 : nullptr);
     const ActParams a = act_params(g.act);
+    [[maybe_unused]] const float scale = MODE == EPI_STORE && GRP == GRP_NONE && g.wscale ? *g.wscale : 1.0f;
     // element offset of row r, column col + 64 c, and whether it is inside
     auto inside = [&](int r, int c) { return r < rows && col + 64 * c < cols; };
     auto offset = [&](int r, int c) { return (uint32_t)r * ldc + (uint32_t)(col + 64 * c); };
@@ -221,6 +222,10 @@ __device__ __forceinline__ void ring_elementwise(const FusedArgs& g, const TileP
                     v[q] *= act_slope<KIND>(a, in(q));
                     cs[q] += v[q];
                 }
+            }
+            if constexpr (MODE == EPI_STORE && GRP == GRP_NONE) {
+#pragma unroll
+                for (int q = 0; q < W; ++q) v[q] *= scale;
             }
             if (f32) {
                 if constexpr (VEC) {
@@ -346,6 +351,7 @@ __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos&
         // log2(e) would miss by (|z| + |lse|) 2^-24. The target's 1 is
         // subtracted by a multiply-add with a 0 or 1 for each column of a
         // piece; rows that do not count are masked, whatever their logits are.
+        const float scale = weight_scale(g), unscale = rcp_f32(scale);
         float w[8], lse[8];
         uint32_t live[8];
         int hit[8];  // the target's column less this lane's first, or -1
@@ -353,7 +359,7 @@ __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos&
         for (int i = 0; i < 8; ++i) {
             const int64_t m = m0 + 16 * i + (lane & 15) < t.M ? m0 + 16 * i + (lane & 15) : t.M - 1;
             const int64_t target = g.targets[m];
-            w[i] = g.gw[m];
+            w[i] = g.gw[m] * unscale;
             lse[i] = g.lse[m];
             live[i] = target == g.ignore ? 0u : 0xFFFFFFFFu;
             const uint64_t at = (uint64_t)target - (uint64_t)g.v0 - (uint64_t)(n0 + 4 * (lane >> 4));
@@ -370,11 +376,15 @@ __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos&
                                   }
                                   return pack_bf16(d) & live[i];
                               });
+        if (blockIdx.x == 0 && threadIdx.x == 0) *g.wscale = scale;
     } else if constexpr (MODE == EPI_STORE && VEC && KIND == 0) {
         const int64_t at = (GRP == GRP_RED ? (int64_t)t.e * g.c_stride : 0) + t.row0 * g.ldc;
+        const float scale = GRP == GRP_NONE && g.wscale ? *g.wscale : 1.0f;
         store_mapped_bf16<TN>(static_cast<uint16_t*>(g.C) + at, g.ldc, t.M, g.N, t.m0 + wave_m * 128,
-                              t.n0 + wave_n * 16 * TN, lane, acc, stage,
-                              [](int, int, const f32x4& v) { return pack_bf16(v); });
+                              t.n0 + wave_n * 16 * TN, lane, acc, stage, [&](int, int, const f32x4& v) {
+                                  if constexpr (GRP == GRP_NONE) return pack_bf16(v * scale);
+                                  return pack_bf16(v);
+                              });
     } else {
         ring_elementwise<MODE, GRP, TN, KIND, VEC>(g, t, wave_m, wave_n, lane, acc, stage);
     }

@@ -215,7 +215,7 @@ def test_shapes_of_the_large_tiles_go_there(L):
             assert L.fc_fwd_act_ws_bytes(M, K, N, F.COL, order, 1) == copied(K, M) + weight(K, N, order)
         for M, K, N in G.RING_XENT_BWD:
             assert L.fc_xent_bwd_ws_bytes(M, K, N, order, 1) == \
-                copied(M, K) + weight(K, N, order) + up(M * up(N, 64) * 2, 256), (M, K, N)
+                copied(M, K) + weight(K, N, order) + up(M * up(N, 64) * 2, 256) + 256, (M, K, N)
         for counts, first, behind, K, N in G.RING_GROUPED:
             E, T = len(counts), first + sum(counts) + behind
             for op, A in ((F.OP_FWD, K), (F.OP_BWD_DATA, N), (F.OP_BWD_WEIGHT, K)):
@@ -228,4 +228,4 @@ def test_shapes_of_the_large_tiles_go_there(L):
             piece = (1 << 28) // (2 * M) // 256 * 256
             assert 0 < N % piece < 64 and N > piece
             assert L.fc_xent_bwd_ws_bytes(M, K, N, order, 1) == \
-                weight(K, N, order) + up(M * piece * 2, 256) + M * up(K, 64) * 4
+                weight(K, N, order) + up(M * piece * 2, 256) + 256 + M * up(K, 64) * 4

@@ -972,3 +972,45 @@ def test_fwd_act_of_few_rows(shape, wo):
 def test_xent_of_few_rows(wo):
     test_xent_fwd((64, 72, 4000), wo)
     test_xent_bwd((64, 72, 4000), wo)
+
+
+@pytest.mark.parametrize("shape", [(4096, 640, 4096), (130, 72, 520), (96, 2001, 300), (700, 40, 4001)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_xent_bwd_with_equal_weights(shape, wo):
+    """Rows of one weight (a mean over the rows that count): the targets' values of the logits' gradient, w (p - 1),
+    which make up nearly all of it, are held as p - 1, whose rounding is at most p, instead of all erring by
+    the weight's rounding. Most rows, the first ones among them, do not count and have another weight."""
+    M, K, N = shape
+    g = gen(M + N)
+    X, W = normal(g, M, K), normal(g, K, N, scale=0.1 * K ** -0.5)
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    t[:M // 2], t[::3] = -100, -100
+    counts = t != -100
+    z = X.double() @ W.double()
+    ez = (K + 16) * U * (X.double().abs() @ W.double().abs())
+    lse = torch.logsumexp(z, 1).float()
+    p = torch.exp(z - lse.double()[:, None])
+    ep = p * torch.expm1(ez + 2.0 ** -22 * (1 + z.abs() + lse.double().abs()[:, None]))
+    hot = torch.zeros_like(p)
+    hot[counts, t[counts]] = 1.0
+    aX, aW = X.double().abs(), W.double().abs()
+    for weight in (1.0 / 7782, 1.0 / 3, -0.7, 1.9921875):
+        w = torch.where(counts, torch.tensor(weight, device="cuda"), 1.0)
+        wd = torch.where(counts, w.double(), 0.0)[:, None]
+        D = wd * (p - hot)
+        # p rounds by H p; p - 1 by H (1 - p), but by no more than p where -1 is nearest; the factor and its use by 8 u
+        eD = wd.abs() * (ep + torch.where(hot > 0, torch.minimum(H * (1 - p + ep), p + ep), H * (p + ep)) + 8 * U * (p + hot))
+        aD = D.abs() + eD
+        tx = (eD + (N + 16) * U * aD) @ aW.t() + 2.0 ** -126
+        tw = aX.t() @ (eD + (M + 16) * U * aD) + 2.0 ** -126
+        dX, dW = F.fc_xent_bwd(X, stored(W, wo), t, lse, w, w_order=wo, dx_dtype=F.OUT_F32, dw_dtype=F.OUT_F32)
+        within(dX, D @ W.double().t(), tx, f"{shape} {wo} {weight:.3g} dX")
+        within(dW, X.double().t() @ D, tw, f"{shape} {wo} {weight:.3g} dW")
+        acc = torch.ones((K, N), device="cuda")
+        F.fc_xent_bwd(X, stored(W, wo), t, lse, w, w_order=wo, dW=acc, dw_dtype=F.OUT_F32_ACC)
+        within(acc, X.double().t() @ D + 1, tw + U * (2 + tw), "dW accumulated")
+    # no row counts, weights of zero, infinite weights of rows that do not count
+    for w, t2 in ((torch.ones(M, device="cuda"), torch.full_like(t, -100)), (torch.zeros(M, device="cuda"), t),
+                  (torch.where(counts, 0.0, math.inf), t)):
+        dX, dW = F.fc_xent_bwd(X, stored(W, wo), t2, lse, w, w_order=wo)
+        assert bool((dX == 0).all()) and bool((dW == 0).all())
