@@ -63,10 +63,13 @@ Operand operand(int64_t rows, int64_t cols, bool aligned, bool ring, int64_t* ws
     }
     return o;
 }
-// Both operands' places: the caller's memory, or the copies (one launch).
-hipError_t place(const Operand& a, const void* pa, const uint16_t** oa, const Operand& b, const void* pb,
-                 const uint16_t** ob, char* ws, hipStream_t s) {
-    auto one = [ws](const Operand& o, const void* src, const uint16_t** out) {
+// Both operands' places: the caller's memory, or the copies (one launch). A
+// plan says `aligned` of both or of neither; an operand that fits as it is
+// stays where it is, whatever the other one does.
+hipError_t place(Operand& a, const void* pa, const uint16_t** oa, Operand& b, const void* pb, const uint16_t** ob,
+                 char* ws, hipStream_t s) {
+    auto one = [ws](Operand& o, const void* src, const uint16_t** out) {
+        if (o.copy && fits(o.cols, !off(src, 16))) o.copy = false, o.ld = o.cols;
         *out = o.copy ? reinterpret_cast<const uint16_t*>(ws + o.off) : static_cast<const uint16_t*>(src);
         return PadCopy{static_cast<const uint16_t*>(src), const_cast<uint16_t*>(*out), o.copy ? o.rows : 0, o.cols,
                        o.copy ? o.ld : 0};
@@ -382,7 +385,7 @@ fc_status grouped_call(int op, const void* P, const void* Q, int w_order, const 
     const int64_t qbytes = op == FC_OP_BWD_WEIGHT ? T * N * 2 : E * K * N * 2;
     const int64_t obytes = esz * (op == FC_OP_FWD ? T * N : op == FC_OP_BWD_DATA ? T * K : E * K * N);
     const bool aligned = !off(P, 16) && !off(Q, 16);
-    const GroupedPlan pl = grouped_plan(op, T, E, K, N, w_order, aligned);
+    GroupedPlan pl = grouped_plan(op, T, E, K, N, w_order, aligned);
     if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
     if (overlapping({{out, obytes}, {pl.total ? ws : nullptr, pl.total}},
                     {{P, pbytes}, {Q, qbytes}, {offsets, 8 * (E + 1)}}))
@@ -450,7 +453,7 @@ fc_status fc_fwd_act(const void* X, fc_order x_order, const void* W, fc_order w_
     if (off(X, 2) || off(W, 2) || off(bias, 2) || off(R, 2) || off(Z, 2) || off(Y, f32 ? 4 : 2)) return FC_E_INVALID;
     const bool aligned = !off(X, 16) && !off(W, 16);
     const bool a_oc = x_order == FC_COL_MAJOR, b_oc = w_order == FC_ROW_MAJOR;
-    const ActPlan pl = act_plan(M, N, K, a_oc, b_oc, aligned, false);
+    ActPlan pl = act_plan(M, N, K, a_oc, b_oc, aligned, false);
     if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
     if (overlapping({{Y, M * N * (f32 ? 4 : 2)}, {Z, M * N * 2}, {pl.total ? ws : nullptr, pl.total}},
                     {{X, M * K * 2}, {W, K * N * 2}, {bias, N * 2}, {R, M * N * 2}}))
@@ -492,7 +495,7 @@ fc_status fc_bwd_data_act(const void* dY, const void* W, fc_order w_order, const
     if (off(dY, 2) || off(W, 2) || off(Z, 2) || off(db, 4) || off(dX, f32 ? 4 : 2)) return FC_E_INVALID;
     const bool aligned = !off(dY, 16) && !off(W, 16);
     const bool b_oc = w_order == FC_COL_MAJOR;
-    const ActPlan pl = act_plan(M, K, N, false, b_oc, aligned, true);
+    ActPlan pl = act_plan(M, K, N, false, b_oc, aligned, true);
     if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
     if (overlapping({{dX, M * K * (f32 ? 4 : 2)}, {db, K * 4}, {ws, pl.total}},
                     {{dY, M * N * 2}, {W, K * N * 2}, {Z, M * K * 2}}))
@@ -558,7 +561,7 @@ fc_status fc_xent_fwd(const void* X, const void* W, fc_order w_order, const int6
     if (off(X, 2) || off(W, 2) || off(targets, 8) || off(lse, 4) || off(tlogit, 4) || off(loss, 4))
         return FC_E_INVALID;
     const bool aligned = !off(X, 16) && !off(W, 16), b_oc = w_order == FC_ROW_MAJOR;
-    const XentFwdPlan pl = xent_fwd_plan(M, K, N, b_oc, aligned);
+    XentFwdPlan pl = xent_fwd_plan(M, K, N, b_oc, aligned);
     if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
     if (overlapping({{lse, M * 4}, {tlogit, M * 4}, {loss, M * 4}, {ws, pl.total}},
                     {{X, M * K * 2}, {W, K * N * 2}, {targets, M * 8}}))
@@ -600,7 +603,7 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
         off(dW, wf32 ? 4 : 2))
         return FC_E_INVALID;
     const bool aligned = !off(X, 16) && !off(W, 16), w_row = w_order == FC_ROW_MAJOR;
-    const XentBwdPlan pl = xent_bwd_plan(M, K, N, w_row, aligned);
+    XentBwdPlan pl = xent_bwd_plan(M, K, N, w_row, aligned);
     if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
     if (overlapping({{dX, M * K * (xf32 ? 4 : 2)}, {dW, K * N * (wf32 ? 4 : 2)}, {ws, pl.total}},
                     {{X, M * K * 2}, {W, K * N * 2}, {targets, M * 8}, {lse, M * 4}, {grad, M * 4}}))

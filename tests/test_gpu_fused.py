@@ -1014,3 +1014,55 @@ def test_xent_bwd_with_equal_weights(shape, wo):
                   (torch.where(counts, 0.0, math.inf), t)):
         dX, dW = F.fc_xent_bwd(X, stored(W, wo), t2, lse, w, w_order=wo)
         assert bool((dX == 0).all()) and bool((dW == 0).all())
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_one_unaligned_operand_is_copied_alone(which, wo):
+    """Of two operands whose rows fit the large tiles, one at an odd address: the other's part of the
+    workspace stays untouched."""
+    M, K, N = RING[0]
+    g = gen(which)
+    X, W = integers(g, M, K), stored(integers(g, K, N), wo)
+    want = X.double() @ (W if wo == ROW else W.t()).double()
+    x, w = (shifted(X), W) if which == 0 else (X, shifted(W))
+    L = F.lib()
+    need = L.fc_fwd_act_ws_bytes(M, K, N, ROW, wo, 0)
+    assert need == 2 * (M * K + K * N)  # a copy of each
+    ws = torch.full((need,), 171, dtype=torch.uint8, device="cuda")
+    Y = torch.empty((M, N), device="cuda")
+    assert L.fc_fwd_act(x.data_ptr(), ROW, w.data_ptr(), wo, None, None, F.ACT_NONE, None, Y.data_ptr(), F.OUT_F32,
+                        M, K, N, ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == F.FC_OK
+    torch.cuda.synchronize()
+    assert torch.equal(Y.double(), want)
+    copies = ws[:2 * M * K], ws[2 * M * K:]
+    assert not bool((copies[which] == 171).all()) and bool((copies[1 - which] == 171).all())
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_one_unaligned_operand(which, wo):
+    """The same in the other operators, where both operands' copies serve several products."""
+    move = (shifted, lambda t: t) if which == 0 else (lambda t: t, shifted)
+    M, K, N = RING[1]
+    g = gen(which + 2)
+    dY, W = integers(g, M, N), integers(g, K, N)
+    Z = torch.ones((M, K), dtype=torch.bfloat16, device="cuda")
+    dX = F.fc_bwd_data_act(move[0](dY), move[1](stored(W, wo)), Z, F.ACT_RELU, w_order=wo, out_dtype=F.OUT_F32)
+    assert torch.equal(dX.double(), dY.double() @ W.double().t())
+    M, K, N = RING_XENT_BWD[1]
+    X, W = normal(g, M, K), stored(normal(g, K, N, scale=0.02), wo)
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    w = torch.rand(M, device="cuda", generator=g)
+    fwd = F.fc_xent_fwd(X, W, t, w_order=wo)
+    assert same(F.fc_xent_fwd(move[0](X), move[1](W), t, w_order=wo), fwd)  # the same kernels, the same bits
+    assert same(F.fc_xent_bwd(move[0](X), move[1](W), t, fwd[1], w, w_order=wo),
+                F.fc_xent_bwd(X, W, t, fwd[1], w, w_order=wo))
+    counts, first, behind, K, N = RING_GROUPED[1]
+    T, off = first + sum(counts) + behind, offsets_of(counts, first)
+    X, dY, W = integers(g, T, K), integers(g, T, N), stored(integers(g, len(counts), K, N), wo)
+    rows = slice(first, T - behind)
+    assert torch.equal(F.fc_grouped_fwd(move[0](X), move[1](W), off, w_order=wo)[rows], F.fc_grouped_fwd(X, W, off, w_order=wo)[rows])
+    assert torch.equal(F.fc_grouped_bwd_data(move[0](dY), move[1](W), off, w_order=wo)[rows],
+                       F.fc_grouped_bwd_data(dY, W, off, w_order=wo)[rows])
+    assert torch.equal(F.fc_grouped_bwd_weight(move[0](X), move[1](dY), off), F.fc_grouped_bwd_weight(X, dY, off))
