@@ -307,10 +307,12 @@ fc_status fc_stamped_call(fc_op op, const void* P, fc_order p_order, const void*
  * the same arguments, 256-byte aligned; NULL where the query returns 0. It
  * holds nothing that a later call needs. Calls that can run at the same time
  * need workspaces of their own. `aligned` says whether both bf16 matrices of
- * the product (X and W, dY and W, X and dY) start on 16-byte boundaries; if
- * not, or if their rows are not a multiple of 8 values, they are copied into
- * the workspace with padded rows first. The queries return -1 for arguments
- * that the call would refuse.
+ * the product (X and W, dY and W, X and dY) start on 16-byte boundaries. The
+ * size is the query's to say: besides partial results it holds a copy with
+ * padded rows of a matrix that does not, or whose rows are not a multiple of 8
+ * values, but only where the call runs in its largest tiles; the smaller ones
+ * read every matrix where it is. The queries return -1 for arguments that the
+ * call would refuse.
  *
  * Sizes are 1 .. 2^22. No output may overlap an input, another output or the
  * workspace. FC_E_INVALID for arguments outside this text, FC_E_UNSUPPORTED
@@ -360,8 +362,10 @@ int64_t fc_bwd_act_ws_bytes(int64_t M, int64_t N);
 
 /*
  * Softmax cross entropy of the vocabulary projection z = X . W, X: M x K
- * row-major, W: K x N, whose logits z are never stored. W is the vocabulary's
- * columns vocab_start .. vocab_start + N - 1: all of it, or one GPU's shard.
+ * row-major, W: K x N, whose logits z are not kept: most calls never store
+ * them; where a few rows split their reduction, the workspace holds partial
+ * sums of them while the call runs. W is the vocabulary's columns vocab_start
+ * .. vocab_start + N - 1: all of it, or one GPU's shard.
  * For each row i:
  *   lse[i]    = log sum_j exp(z_ij) over the columns given here
  *   tlogit[i] = z_ij at j = targets[i] - vocab_start; 0 if that column is not

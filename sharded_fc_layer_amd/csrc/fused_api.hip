@@ -106,9 +106,10 @@ int64_t tiles_of(int tile, int64_t M, int64_t N) {
 //    with a block to a CU, 7 and 1.0 with two, from memory (168 tiles at 3904: 73;
 //    4096 tiles at 2048: 577; operands that lie in the caches take 0.37 to 0.5);
 //    where rows start anywhere 2 more and 1.3 of the stages' time; tiles of 32
-//    or 64 rows 0.4 of it (391 tiles of 64 rows at 2048: 35);
-//  * neither reads, writes or copies faster than 5 TB/s (experts' weights of 403
-//    MB against 48 rows: 61 and 93);
+//    or 64 rows 0.4 of it (391 tiles of 64 rows at 2048: 36 with W in the
+//    caches, 55 from memory, where the next bound says 44);
+//  * neither reads, writes or copies faster than 5 TB/s (16 experts' weights of
+//    403 MB against 48 rows: 70);
 //  * a launch 3; a split reduction's second launch 4, its planes at 6 TB/s (252
 //    tiles of three slices at 1001: 18.7 and 6.6);
 //  * copies 3, read and written at 3.5 TB/s.
