@@ -44,9 +44,10 @@ MFMA_BF16_PEAK_TFLOPS = 2500.0  # MI355X dense bf16
 HBM_PEAK_GBS = 8000.0
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 CSRC = os.path.join(ROOT, "sharded_fc_layer_amd", "csrc")
-# every source with device code (the C-ABI layer, fcshard_api.hip, is host code only)
+# every source with device code of the products timed here (the C-ABI layer,
+# fcshard_api.hip, is host code only; fused_* are other operators' kernels)
 KERNEL_SOURCES = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
-                        if f.endswith((".hip", ".h", ".inc")) and f != "fcshard_api.hip")
+                        if f.endswith((".hip", ".h", ".inc")) and f != "fcshard_api.hip" and not f.startswith("fused_"))
 
 
 def kernel_source_hash(sources=None) -> str:

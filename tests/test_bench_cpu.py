@@ -66,3 +66,12 @@ def test_traffic_weighs_this_runs_calls_by_launch_grid(tmp_path, monkeypatch):
     assert bench.measured_traffic("k", "w", [1024, 2048]) == 300.0
     assert bench.measured_traffic("k", "w", [None]) == 300.0
     assert bench.measured_traffic("k", "w") == 300.0
+
+
+def test_the_committed_traffic_is_of_the_current_device_code():
+    """The benchmark line reports measured traffic only while it is: counter runs are taken again, or shown
+    to hold (the same machine code), whenever the products' device code changes."""
+    with open(bench.TRAFFIC_FILE) as f:
+        assert json.load(f)["source_hash"] == bench.kernel_source_hash()
+    assert bench.measured_traffic("gemm_w4k64r_kernel<false, true, false, 256, 2, 3>", bench.WORKLOAD_NAMES[5]) > 1e9
+    assert not any(os.path.basename(f).startswith("fused_") for f in bench.KERNEL_SOURCES)
