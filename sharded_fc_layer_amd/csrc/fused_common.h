@@ -156,11 +156,11 @@ __device__ __forceinline__ void act_slopes(int act, V& v) {
 // that gradient lies in the targets' columns, at values near minus the weight.
 // Rounded with it, all of them err alike, by up to 2^-8, and so do dX and dW as
 // wholes (8192 x 2048 -> 32000, fp32 outputs, relative to 64 bits: 0.0012 to
-// 0.0032 by the weight, 0.00005 without it, when they are near powers of two).
-// bf16 is what the matrix units take; the two parts of a longer D would double
-// both products. s is the mantissa of the first weight that
-// counts among 256 rows spread over all of them (straight-line code, for the
-// ring's sake); rows of other weights round as any number does. All lanes of a wave
+// 0.0032 by the weight; 0.00005 without it, when they are near powers of two).
+// bf16 is what the matrix units take; the two parts of a longer gradient would
+// double both products. s is the mantissa of the first weight that counts
+// among 256 rows spread over all of them (straight-line code, for the ring's
+// sake); rows of other weights round as any number does. All lanes of a wave
 // call it.
 __device__ __forceinline__ float weight_scale(const FusedArgs& g) {
     const int lane = threadIdx.x & 63;
