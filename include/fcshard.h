@@ -294,8 +294,8 @@ fc_status fc_stamped_call(fc_op op, const void* P, fc_order p_order, const void*
 /* ------------------------------------------------------ fused operators
  *
  * The FC layer's products with what a language model does around them:
- * activations in the epilogue, the loss over a vocabulary projection, and
- * expert layers. Matrices are laid out as above (tightly packed, bf16 unless
+ * activations in the epilogue, the loss over a vocabulary projection, expert
+ * layers, gated layers, log probabilities and distillation. Matrices are laid out as above (tightly packed, bf16 unless
  * stated), sums are held in fp32 and rounded once on output unless stated.
  * Calls enqueue kernels on `stream` and return: they neither allocate nor
  * synchronize, keep nothing between calls and may be captured into graphs.
@@ -427,6 +427,109 @@ fc_status fc_grouped_bwd_weight(const void* X, const void* dY, const int64_t* of
                                 int64_t ws_bytes, void* stream);
 /* op: FC_OP_FWD, FC_OP_BWD_DATA or FC_OP_BWD_WEIGHT (which does not read w_order) */
 int64_t fc_grouped_ws_bytes(fc_op op, int64_t T, int64_t E, int64_t K, int64_t N, fc_order w_order, int aligned);
+
+/*
+ * Gated layers. W (K x 2N) holds the gate's columns 0 .. N - 1, then the up
+ * projection's; Z = X . W + bias = [G | U] (M x 2N, bias 2N bf16 values or
+ * NULL), X row-major, and
+ *   Y = act(G) * U                                   M x N, bf16 or fp32
+ * Z (bf16, what the backward pass needs) may be NULL. Y is computed from the
+ * fp32 Z, not from the rounded one.
+ */
+fc_status fc_fwd_glu(const void* X, const void* W, fc_order w_order, const void* bias, fc_act act, void* Z, void* Y,
+                     fc_out_dtype y_dtype, int64_t M, int64_t K, int64_t N, void* ws, int64_t ws_bytes, void* stream);
+int64_t fc_fwd_glu_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned);
+
+/*
+ * The gradient through a product and the gated layer below it, whose
+ * fc_fwd_glu left Z = [G | U] (bf16, M x 2K): with dH = dY[M x N] . W[K x N]^T,
+ *   dZ = [dH * U * act'(G) | dH * act(G)]            M x 2K, bf16
+ *   H  = act(G) * U, the layer's output again        M x K, bf16, or NULL
+ *   db = the sums of dZ's columns before rounding    2K fp32 values, or NULL
+ * fc_bwd_data and fc_bwd_weight of dZ (as the gradient of a layer of 2K
+ * outputs) are the gated layer's own gradients, fc_bwd_weight of H and dY that
+ * of W; so the layer's output need not be kept.
+ */
+fc_status fc_bwd_data_glu(const void* dY, const void* W, fc_order w_order, const void* Z, fc_act act, void* dZ, void* H,
+                          float* db, int64_t M, int64_t K, int64_t N, void* ws, int64_t ws_bytes, void* stream);
+int64_t fc_bwd_data_glu_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned);
+
+/*
+ * The same from the gradient dY (bf16, M x N) of fc_fwd_glu's output itself:
+ *   dZ = [dY * U * act'(G) | dY * act(G)], Y = act(G) * U, db = dZ's column sums
+ * of which dZ, Y (bf16) and db (fp32, 2N) may be NULL, not all. No workspace is
+ * needed without db.
+ */
+fc_status fc_bwd_glu(const void* dY, const void* Z, fc_act act, void* dZ, void* Y, float* db, int64_t M, int64_t N,
+                     void* ws, int64_t ws_bytes, void* stream);
+int64_t fc_bwd_glu_ws_bytes(int64_t M, int64_t N);
+
+/*
+ * Log probabilities under the vocabulary projection z = X . W, X: M x K
+ * row-major, W: K x N (vocabulary columns vocab_start .. vocab_start + N - 1:
+ * all of it, or one GPU's shard), at a temperature T of 2^-10 .. 2^10. For
+ * each row i, over the columns given here:
+ *   lse[i]      = log sum_j exp(z_ij / T)
+ *   logp[i]     = z_ij / T - lse[i] at j = targets[i] - vocab_start; -inf if
+ *                 that column is not here, 0 if targets[i] = ignore_index
+ *   entropy[i]  = - sum_j p_ij log p_ij, p_ij = exp(z_ij / T - lse[i])
+ *   top_ids[i, r], top_logp[i, r], r < top_k: the most likely columns' indices
+ *                 (vocab_start + j) and log probabilities, most likely first,
+ *                 equal logits by lowest index
+ * targets and logp may be NULL together; entropy may be NULL. top_k is 0 ..
+ * 128, at most N. (top_ids int64, the others fp32.) A shard's logp and
+ * top_logp become the whole vocabulary's by adding its lse and subtracting the
+ * logarithm L of the summed exponentials of all shards' lse; with pi = exp(lse
+ * - L), the whole entropy is the sum of pi (entropy + L - lse). In rows whose
+ * logits are not finite numbers, NaN ranks with -inf, and top_ids are columns
+ * of this call whatever they hold.
+ *
+ * The workspace holds the logits of some rows at a time, at most 512 MiB of
+ * them, or 256 rows where those are more.
+ */
+fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64_t* targets, int64_t vocab_start,
+                     int64_t ignore_index, float temperature, float* logp, float* entropy, float* lse, float* top_logp,
+                     int64_t* top_ids, int top_k, int64_t M, int64_t K, int64_t N, void* ws, int64_t ws_bytes,
+                     void* stream);
+int64_t fc_logprob_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int top_k, int aligned);
+
+/*
+ * Distillation from a teacher's top logits. Row i lists top_n (1 .. 128)
+ * tokens of the vocabulary, ids[i, r], with the teacher's logits tlogits[i, r]
+ * (fp32; log probabilities do as well: a constant per row drops out). A token
+ * with a negative id or a logit of -inf is absent; ids of other shards count.
+ *   p_ir = softmax over the listed tokens of tlogits[i, r] / T
+ * With the student's logits z = X . W as above:
+ *   lse[i]        = log sum_j exp(z_ij / T) over the columns given here
+ *   slogits[i, r] = z_ij at j = ids[i, r] - vocab_start; 0 if that column is
+ *                   not here or the token is absent
+ *   loss[i]       = sum_r p_ir (log p_ir - slogits[i, r] / T + lse[i]): for a
+ *                   whole vocabulary, the divergence of the student's softmax
+ *                   of z / T from p; 0 for a row without tokens
+ * (fp32). A token listed twice counts with both its probabilities. With a
+ * sharded vocabulary the loss is this formula of the shards' joined lse and
+ * the sum of their slogits.
+ */
+fc_status fc_distill_fwd(const void* X, const void* W, fc_order w_order, const int64_t* ids, const float* tlogits,
+                         int top_n, int64_t vocab_start, float temperature, float* lse, float* slogits, float* loss,
+                         int64_t M, int64_t K, int64_t N, void* ws, int64_t ws_bytes, void* stream);
+int64_t fc_distill_fwd_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned);
+
+/*
+ * Its gradient. With the rows' weights grad[i] (the gradient of each row's
+ * loss), and slogits and lse as fc_distill_fwd left them (lse over the whole
+ * vocabulary, if it is sharded),
+ *   D_ij = grad[i] / T (exp(z_ij / T - lse[i]) - sum of p_ir at ids[i, r] = vocab_start + j),
+ * rows of zeros where a row has no tokens;
+ *   dX = D . W^T (M x K, bf16 or fp32; a shard's share of the sum)
+ *   dW = X^T . D (K x N row-major, any output type)
+ * The logits are computed again and D is rounded to bf16 as in fc_xent_bwd.
+ */
+fc_status fc_distill_bwd(const void* X, const void* W, fc_order w_order, const int64_t* ids, const float* tlogits,
+                         int top_n, int64_t vocab_start, float temperature, const float* slogits, const float* lse,
+                         const float* grad, void* dX, fc_out_dtype dx_dtype, void* dW, fc_out_dtype dw_dtype, int64_t M,
+                         int64_t K, int64_t N, void* ws, int64_t ws_bytes, void* stream);
+int64_t fc_distill_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int top_n, int aligned);
 
 /* static text for a status; never NULL */
 const char* fc_status_str(fc_status status);

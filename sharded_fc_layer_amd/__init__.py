@@ -24,12 +24,18 @@ from .fcshard import (  # noqa: F401
     fc_bwd_act,
     fc_bwd_data,
     fc_bwd_data_act,
+    fc_bwd_data_glu,
+    fc_bwd_glu,
     fc_bwd_weight,
+    fc_distill_bwd,
+    fc_distill_fwd,
     fc_fwd,
     fc_fwd_act,
+    fc_fwd_glu,
     fc_grouped_bwd_data,
     fc_grouped_bwd_weight,
     fc_grouped_fwd,
+    fc_logprob,
     fc_plan_count,
     fc_plan_describe,
     fc_plans_load,

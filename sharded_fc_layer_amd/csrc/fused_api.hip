@@ -4,200 +4,12 @@
 // Every plan here is a function of sizes, orders, types and operand alignment
 // alone, so that the workspace queries and the calls agree. Nothing is
 // allocated, kept or synchronized: workspaces are the caller's.
-#include <algorithm>
-#include <initializer_list>
-
-#include "fused_internal.h"
+#include "fused_plan.h"
 
 namespace fcs {
 namespace {
 
-constexpr int64_t kMaxSize = (int64_t)1 << 22;   // largest M, K, N, T: 128 rows of it stay within 2 GiB
-constexpr int64_t kMaxCount = (int64_t)1 << 46;  // largest element count of the experts' weights
-constexpr int kMaxExperts = 1 << 20;
-
-int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-
-bool bad_order(int o) { return o != FC_ROW_MAJOR && o != FC_COL_MAJOR; }
-bool bad_act(int a) { return a < FC_ACT_NONE || a > FC_ACT_SILU; }
-bool bad_size(int64_t v) { return v < 1 || v > kMaxSize; }
-
-struct Span {
-    const void* p;
-    int64_t bytes;
-};
-bool meets(const Span& a, const Span& b) {
-    if (!a.p || !b.p) return false;
-    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    return a0 < b0 + (uintptr_t)b.bytes && b0 < a0 + (uintptr_t)a.bytes;
-}
-// outputs must not meet each other or an input
-bool overlapping(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-    for (auto o = outs.begin(); o != outs.end(); ++o) {
-        for (const Span& i : ins)
-            if (meets(*o, i)) return true;
-        for (auto q = o + 1; q != outs.end(); ++q)
-            if (meets(*o, *q)) return true;
-    }
-    return false;
-}
-bool off(const void* p, int64_t a) { return (uintptr_t)p % (uintptr_t)a != 0; }
-
-// An operand as the kernels read it: in place, or, where the ring kernel would
-// find rows that do not start on 16-byte boundaries, copied into the workspace
-// with rows padded to whole 128-byte lines. The copy's padding is zeros, which
-// a reduction may run into.
-struct Operand {
-    int64_t rows, cols;
-    bool copy;
-    int64_t ld, off;  // row length as read; workspace offset of the copy
-};
-bool fits(int64_t cols, bool aligned) { return cols % 8 == 0 && aligned; }
-int64_t ring_ld(int64_t cols, bool aligned) { return fits(cols, aligned) ? cols : up(cols, 64); }
-Operand operand(int64_t rows, int64_t cols, bool aligned, bool ring, int64_t* ws) {
-    Operand o{rows, cols, ring && !fits(cols, aligned), cols, 0};
-    if (o.copy) {
-        o.ld = up(cols, 64);
-        o.off = *ws;
-        *ws += up(rows * o.ld * 2, 256);
-    }
-    return o;
-}
-// Both operands' places: the caller's memory, or the copies (one launch). A
-// plan says `aligned` of both or of neither; an operand that fits as it is
-// stays where it is, whatever the other one does.
-hipError_t place(Operand& a, const void* pa, const uint16_t** oa, Operand& b, const void* pb, const uint16_t** ob,
-                 char* ws, hipStream_t s) {
-    auto one = [ws](Operand& o, const void* src, const uint16_t** out) {
-        if (o.copy && fits(o.cols, !off(src, 16))) o.copy = false, o.ld = o.cols;
-        *out = o.copy ? reinterpret_cast<const uint16_t*>(ws + o.off) : static_cast<const uint16_t*>(src);
-        return PadCopy{static_cast<const uint16_t*>(src), const_cast<uint16_t*>(*out), o.copy ? o.rows : 0, o.cols,
-                       o.copy ? o.ld : 0};
-    };
-    const PadCopy ca = one(a, pa, oa), cb = one(b, pb, ob);
-    return a.copy || b.copy ? launch_pad_any(ca, cb, s) : hipSuccess;
-}
-
-// Tile and reduction slices of one product.
-struct Shape {
-    int tile, splits;
-    int64_t k_split;
-    double us;  // estimated time
-};
-constexpr int kSkinny = -1;  // Shape::tile: the kernel for a few rows
-
-// row length of fp32 planes: whole vectors and lines whatever N is
-int64_t plane_ld(int64_t N) { return up(N, 64); }
-// the planes of a split reduction
-int64_t planes_bytes(const Shape& sh, int64_t M, int64_t N) {
-    return sh.splits > 1 ? (int64_t)sh.splits * M * plane_ld(N) * 4 : 0;
-}
-int64_t tiles_of(int tile, int64_t M, int64_t N) {
-    const FusedTile& t = kFusedTiles[tile];
-    return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
-}
-
-// Estimated times in microseconds, fitted to measurements on one MI355X
-// (outputs 128 x 128 to 8192 x 8192, reductions 40 to 4104):
-//  * a round of up to 256 ring tiles takes 15 and 1.1 for each 64-value stage,
-//    of which a reduction that is not head plus periods has up to 5 more (136
-//    tiles: 19.2 at a reduction of 72, 49.5 at 2056; 1024 tiles at 2048: 213);
-//  * a round of the general kernel's tiles 5 and 0.65 for each 32-value stage
-//    with a block to a CU, 7 and 1.0 with two, from memory (168 tiles at 3904: 73;
-//    4096 tiles at 2048: 577; operands that lie in the caches take 0.37 to 0.5);
-//    where rows start anywhere 2 more and 1.3 of the stages' time; tiles of 32
-//    or 64 rows 0.4 of it (391 tiles of 64 rows at 2048: 36 with W in the
-//    caches, 55 from memory, where the next bound says 44);
-//  * neither reads, writes or copies faster than 5 TB/s (16 experts' weights of
-//    403 MB against 48 rows: 70);
-//  * a launch 3; a split reduction's second launch 4, its planes at 6 TB/s (252
-//    tiles of three slices at 1001: 18.7 and 6.6);
-//  * copies 3, read and written at 3.5 TB/s.
-double ring_us(int64_t tiles, int64_t K, bool ragged, double bytes) {
-    const int64_t n = (K + 63) / 64;
-    const bool head = !ragged && K % 64 == 0 && (n % 6 == 2 || n % 6 == 4) && n > 6;
-    const double stages = ragged ? (double)n + 2.5 : head ? (double)n : (double)up(n, 6);
-    return 3 + std::max((double)((tiles + 255) / 256) * (15 + 1.1 * stages), bytes / 5e6);
-}
-double small_us(int tile, int64_t blocks, int64_t K, bool any, double bytes) {
-    const double stages = (double)((K + 31) / 32) * (tile == 0 ? 1.0 : 0.4) * (any ? 1.3 : 1.0), more = any ? 2 : 0;
-    const double us = blocks <= 256 ? 5 + more + 0.65 * stages : (double)((blocks + 511) / 512) * (7 + more + 1.0 * stages);
-    return 3 + std::max(us, bytes / 5e6);
-}
-double planes_us(int64_t slices, int64_t M, int64_t N) {
-    return 4 + (double)slices * (double)M * (double)plane_ld(N) * 8 / 6e6;
-}
-// what a product reads
-double operand_bytes(int64_t M, int64_t N, int64_t K) { return 2.0 * (double)K * (double)(M + N); }
-double copy_us(int64_t bytes) { return 3 + (double)bytes * 2 / 3.5e6; }
-
-// The general kernel's best form. A product with few tiles may split a long
-// reduction, 128 values to a slice at least.
-Shape small_shape(int64_t M, int64_t N, int64_t K, bool a_oc, bool any, bool may_split) {
-    const int tile = a_oc || M > 64 ? 0 : M <= 32 ? 1 : 3;
-    const int64_t tiles = tiles_of(tile, M, N);
-    const double bytes = operand_bytes(M, N, K);
-    Shape best{tile, 1, up(K, 64), small_us(tile, tiles, K, any, bytes)};
-    if (!may_split || tiles > 256) return best;
-    for (int s = 2; s <= 16; ++s) {
-        const int64_t k_split = up((K + s - 1) / s, 32);
-        if (k_split < 128) break;
-        const int slices = (int)((K + k_split - 1) / k_split);
-        const double us = small_us(tile, tiles * slices, k_split, any, bytes) + planes_us(slices, M, N);
-        if (us < best.us) best = Shape{tile, slices, k_split, us};
-    }
-    return best;
-}
-// The ring kernel's, if it takes the product, without any copies it needs.
-Shape ring_shape(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t lda, int64_t ldb) {
-    const bool takes = ring_takes(GRP_NONE, a_oc, b_oc, N, K, lda, ldb);
-    return Shape{kRingTile, 1, up(K, 64), takes ? ring_us(tiles_of(kRingTile, M, N), K, false, operand_bytes(M, N, K)) : 1e30};
-}
-// The better of both for one product, whose operands' rows are acols and bcols values.
-Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t acols, int64_t bcols, bool aligned) {
-    const Shape small = small_shape(M, N, K, a_oc, !fits(acols, aligned) || !fits(bcols, aligned), true);
-    Shape ring = ring_shape(M, N, K, a_oc, b_oc, ring_ld(acols, aligned), ring_ld(bcols, aligned));
-    const int64_t bytes = (fits(acols, aligned) ? 0 : M * K * 2) + (fits(bcols, aligned) ? 0 : N * K * 2);
-    if (bytes) ring.us += copy_us(bytes);
-    return ring.us < small.us ? ring : small;
-}
-
-// FusedArgs::vec_out for rows of ld values
-int vec_rows(int64_t ld, const void* C, const void* R, const void* Z) {
-    return ld % 8 == 0 && !off(C, 16) && !off(R, 16) && !off(Z, 16);
-}
-
-bool bad_ws(const void* ws, int64_t have, int64_t need) { return need > 0 && (!ws || have < need || off(ws, 256)); }
-
-fc_status done(hipError_t e) { return e == hipSuccess ? FC_OK : FC_E_HIP; }
-
-// The common end of a split product: the slices' planes, then the epilogue.
-hipError_t run_product(EpiMode mode, const Shape& sh, bool a_oc, bool b_oc, FusedArgs g, float* planes,
-                       hipStream_t s) {
-    g.k_split = sh.k_split;
-    g.splits = sh.splits;
-    g.c_split_stride = 0;
-    if (sh.tile == kSkinny) return launch_fused_skinny(g, s);
-    if (sh.splits == 1) return launch_fused(mode, GRP_NONE, sh.tile, a_oc, b_oc, g, s);
-    FusedArgs p = g;
-    p.C = planes;
-    p.ldc = plane_ld(g.N);
-    p.out_f32 = 1;
-    p.vec_out = 1;
-    p.accumulate = 0;
-    p.wscale = nullptr;
-    p.c_split_stride = g.M * p.ldc;
-    const hipError_t e = launch_fused(EPI_STORE, GRP_NONE, sh.tile, a_oc, b_oc, p, s);
-    return e != hipSuccess ? e : launch_split_epilogue(mode, g, planes, p.ldc, sh.splits, s);
-}
-
 // ---------------------------------------------------------------- act
-
-// The few-row kernel against the general one (24 rows, outputs 28000: 16.7
-// against 4.8 us at a reduction of 72, 38.5 against 28.3 at 2056; one row, 8192
-// outputs, 2048: 7.0 against 12.3): it reads a narrow W at once, but its blocks
-// of 16 columns cost more where they are many.
-bool skinny_pays(int64_t M, int64_t N, int64_t K) { return N <= (M <= 16 ? 16384 : 8192) && K >= 256; }
 
 struct ActPlan {
     Operand A, B;
@@ -228,16 +40,6 @@ ActPlan act_plan(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, bool ali
     }
     p.total = ws;
     return p;
-}
-
-bool bad_sizes(int64_t M, int64_t K, int64_t N) {
-    return bad_size(M) || bad_size(K) || bad_size(N);
-}
-
-int bwd_act_parts(int64_t M, int64_t N) {
-    // about 2048 blocks, at least 16 rows to each
-    const int64_t cols = (N + 255) / 256;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({(M + 15) / 16, 2048 / cols, 65535}));
 }
 
 // --------------------------------------------------------------- xent
@@ -432,6 +234,76 @@ fc_status grouped_call(int op, const void* P, const void* Q, int w_order, const 
 }
 
 }  // namespace
+
+int64_t logits_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, int w_order, bool aligned) {
+    return xent_bwd_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned).total;
+}
+
+hipError_t run_logits_bwd(const LogitsBwd& b, char* base, hipStream_t s) {
+    const int64_t M = b.M, K = b.K, N = b.N;
+    const bool w_row = b.w_order == FC_ROW_MAJOR, wf32 = b.dw_dtype != FC_OUT_BF16;
+    XentBwdPlan pl = xent_bwd_plan(M, K, N, w_row, !off(b.X, 16) && !off(b.W, 16));
+    const uint16_t *x, *w;
+    hipError_t e;
+    if ((e = place(pl.A, b.X, &x, pl.B, b.W, &w, base, s)) != hipSuccess) return e;
+    uint16_t* D = reinterpret_cast<uint16_t*>(base + pl.d_off);
+    float* planes = reinterpret_cast<float*>(base + pl.planes);
+    float* sum = reinterpret_cast<float*>(base + pl.sum_off);
+    float* scale = reinterpret_cast<float*>(base + pl.scale_off);
+    for (int p = 0; p < pl.pieces; ++p) {
+        const int64_t c0 = (int64_t)p * pl.piece, c = std::min(pl.piece, N - c0);
+        const uint16_t* wp = w + (w_row ? c0 : c0 * pl.B.ld);
+        // the piece's logits again, and their gradient
+        FusedArgs g;
+        g.A = x, g.B = wp, g.C = D;
+        g.M = M, g.N = c, g.K = K;
+        g.lda = pl.A.ld, g.ldb = pl.B.ld, g.ldc = pl.d_ld;
+        g.accumulate = 0;
+        g.targets = b.targets, g.v0 = b.v0 + c0, g.ignore = b.ignore;
+        g.lse = b.lse, g.gw = b.gw, g.inv_t = b.inv_t, g.wscale = scale;
+        if ((e = run_product(EPI_DLOGIT, pl.logits, false, w_row, g, planes, s)) != hipSuccess) return e;
+        if (b.listed && (e = launch_listed_grad(*b.listed, b.lse, b.gw, b.inv_t, scale, D, pl.d_ld, g.v0, c, M, s)) != hipSuccess)
+            return e;
+        // dW = X^T D, this piece's columns
+        FusedArgs h;
+        h.A = x, h.B = D;
+        h.C = static_cast<char*>(b.dW) + c0 * (wf32 ? 4 : 2);
+        h.M = K, h.N = c, h.K = M;
+        h.lda = pl.A.ld, h.ldb = pl.d_ld, h.ldc = N;
+        h.out_f32 = wf32;
+        h.accumulate = b.dw_dtype == FC_OUT_F32_ACCUMULATE;
+        h.vec_out = vec_rows(N, h.C, nullptr, nullptr);
+        h.wscale = scale;
+        if ((e = run_product(EPI_STORE, pl.dw, true, true, h, planes, s)) != hipSuccess) return e;
+        // dX = D W^T: in one go, or summed over the pieces in 32 bits
+        FusedArgs d;
+        d.A = D, d.B = wp;
+        d.M = M, d.N = K, d.K = c;
+        d.lda = pl.d_ld, d.ldb = pl.B.ld;
+        const bool last = pl.pieces == 1;
+        d.ldc = last ? K : plane_ld(K);
+        d.C = last ? b.dX : sum;
+        d.out_f32 = last ? b.dx_f32 : 1;
+        d.accumulate = p > 0;
+        d.vec_out = vec_rows(d.ldc, d.C, nullptr, nullptr);
+        d.wscale = scale;
+        Shape sh = pl.dx;
+        if (sh.splits == 1) sh.k_split = up(c, 64);
+        if (sh.tile == kRingTile && c < 64) sh.tile = 0;  // a last piece of less than one stage
+        if ((e = run_product(EPI_STORE, sh, false, !w_row, d, planes, s)) != hipSuccess) return e;
+    }
+    if (pl.pieces > 1) {
+        FusedArgs d;
+        d.C = b.dX;
+        d.M = M, d.N = K, d.ldc = K;
+        d.accumulate = 0;
+        d.out_f32 = b.dx_f32;
+        d.vec_out = vec_rows(K, b.dX, nullptr, nullptr);
+        e = launch_split_epilogue(EPI_STORE, d, sum, plane_ld(K), 1, s);
+    }
+    return e;
+}
+
 }  // namespace fcs
 
 using namespace fcs;
@@ -588,7 +460,7 @@ fc_status fc_xent_fwd(const void* X, const void* W, fc_order w_order, const int6
 
 int64_t fc_xent_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned) {
     if (bad_sizes(M, K, N) || bad_order(w_order)) return -1;
-    return xent_bwd_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned != 0).total;
+    return logits_bwd_ws_bytes(M, K, N, w_order, aligned != 0);
 }
 
 fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int64_t* targets, int64_t vocab_start,
@@ -603,74 +475,21 @@ fc_status fc_xent_bwd(const void* X, const void* W, fc_order w_order, const int6
     if (off(X, 2) || off(W, 2) || off(targets, 8) || off(lse, 4) || off(grad, 4) || off(dX, xf32 ? 4 : 2) ||
         off(dW, wf32 ? 4 : 2))
         return FC_E_INVALID;
-    const bool aligned = !off(X, 16) && !off(W, 16), w_row = w_order == FC_ROW_MAJOR;
-    XentBwdPlan pl = xent_bwd_plan(M, K, N, w_row, aligned);
-    if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
-    if (overlapping({{dX, M * K * (xf32 ? 4 : 2)}, {dW, K * N * (wf32 ? 4 : 2)}, {ws, pl.total}},
+    const int64_t need = logits_bwd_ws_bytes(M, K, N, w_order, !off(X, 16) && !off(W, 16));
+    if (bad_ws(ws, ws_bytes, need)) return FC_E_INVALID;
+    if (overlapping({{dX, M * K * (xf32 ? 4 : 2)}, {dW, K * N * (wf32 ? 4 : 2)}, {ws, need}},
                     {{X, M * K * 2}, {W, K * N * 2}, {targets, M * 8}, {lse, M * 4}, {grad, M * 4}}))
         return FC_E_INVALID;
     const fc_status st = current_device_status();
     if (st != FC_OK) return st;
     (void)hipGetLastError();
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    char* base = static_cast<char*>(ws);
-    const uint16_t *x, *w;
-    hipError_t e;
-    if ((e = place(pl.A, X, &x, pl.B, W, &w, base, s)) != hipSuccess) return done(e);
-    uint16_t* D = reinterpret_cast<uint16_t*>(base + pl.d_off);
-    float* planes = reinterpret_cast<float*>(base + pl.planes);
-    float* sum = reinterpret_cast<float*>(base + pl.sum_off);
-    float* scale = reinterpret_cast<float*>(base + pl.scale_off);
-    for (int p = 0; p < pl.pieces; ++p) {
-        const int64_t c0 = (int64_t)p * pl.piece, c = std::min(pl.piece, N - c0);
-        const uint16_t* wp = w + (w_row ? c0 : c0 * pl.B.ld);
-        // the piece's logits again, and their gradient
-        FusedArgs g;
-        g.A = x, g.B = wp, g.C = D;
-        g.M = M, g.N = c, g.K = K;
-        g.lda = pl.A.ld, g.ldb = pl.B.ld, g.ldc = pl.d_ld;
-        g.accumulate = 0;
-        g.targets = targets, g.v0 = vocab_start + c0, g.ignore = ignore_index;
-        g.lse = lse, g.gw = grad, g.wscale = scale;
-        if ((e = run_product(EPI_DLOGIT, pl.logits, false, w_row, g, planes, s)) != hipSuccess) return done(e);
-        // dW = X^T D, this piece's columns
-        FusedArgs h;
-        h.A = x, h.B = D;
-        h.C = static_cast<char*>(dW) + c0 * (wf32 ? 4 : 2);
-        h.M = K, h.N = c, h.K = M;
-        h.lda = pl.A.ld, h.ldb = pl.d_ld, h.ldc = N;
-        h.out_f32 = wf32;
-        h.accumulate = dw_dtype == FC_OUT_F32_ACCUMULATE;
-        h.vec_out = vec_rows(N, h.C, nullptr, nullptr);
-        h.wscale = scale;
-        if ((e = run_product(EPI_STORE, pl.dw, true, true, h, planes, s)) != hipSuccess) return done(e);
-        // dX = D W^T: in one go, or summed over the pieces in 32 bits
-        FusedArgs d;
-        d.A = D, d.B = wp;
-        d.M = M, d.N = K, d.K = c;
-        d.lda = pl.d_ld, d.ldb = pl.B.ld;
-        const bool last = pl.pieces == 1;
-        d.ldc = last ? K : plane_ld(K);
-        d.C = last ? dX : sum;
-        d.out_f32 = last ? xf32 : 1;
-        d.accumulate = p > 0;
-        d.vec_out = vec_rows(d.ldc, d.C, nullptr, nullptr);
-        d.wscale = scale;
-        Shape sh = pl.dx;
-        if (sh.splits == 1) sh.k_split = up(c, 64);
-        if (sh.tile == kRingTile && c < 64) sh.tile = 0;  // a last piece of less than one stage
-        if ((e = run_product(EPI_STORE, sh, false, !w_row, d, planes, s)) != hipSuccess) return done(e);
-    }
-    if (pl.pieces > 1) {
-        FusedArgs d;
-        d.C = dX;
-        d.M = M, d.N = K, d.ldc = K;
-        d.accumulate = 0;
-        d.out_f32 = xf32;
-        d.vec_out = vec_rows(K, dX, nullptr, nullptr);
-        e = launch_split_epilogue(EPI_STORE, d, sum, plane_ld(K), 1, s);
-    }
-    return done(e);
+    LogitsBwd b;
+    b.X = X, b.W = W, b.w_order = w_order;
+    b.targets = targets, b.v0 = vocab_start, b.ignore = ignore_index;
+    b.lse = lse, b.gw = grad;
+    b.dX = dX, b.dx_f32 = xf32, b.dW = dW, b.dw_dtype = dw_dtype;
+    b.M = M, b.K = K, b.N = N;
+    return done(run_logits_bwd(b, static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }
 
 int64_t fc_grouped_ws_bytes(fc_op op, int64_t T, int64_t E, int64_t K, int64_t N, fc_order w_order, int aligned) {

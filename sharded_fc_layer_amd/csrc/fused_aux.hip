@@ -103,7 +103,7 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(FusedArgs g, const 
                 const float lse = g.lse[m], w = g.gw[m] * rcp_f32(scale);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    float p1 = exp_f32(v[q] - lse);
+                    float p1 = exp_f32(v[q] * g.inv_t - lse);
                     p1 = hit == (uint64_t)q ? p1 - 1.0f : p1;
                     v[q] = target != g.ignore && n + q < g.N ? w * p1 : 0.0f;
                 }

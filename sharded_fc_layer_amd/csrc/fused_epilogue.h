@@ -182,7 +182,7 @@ struct Epilogue {
             const uint64_t hit = (uint64_t)in.target - (uint64_t)g.v0 - (uint64_t)n;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                float p = exp_f32(v[q] - in.lse);
+                float p = exp_f32(v[q] * g.inv_t - in.lse);
                 p = hit == (uint64_t)q ? p - 1.0f : p;
                 v[q] = counts && q < left ? w * p : 0.0f;
             }

@@ -1,0 +1,175 @@
+// Gated layers around their products (gfx950): the epilogues of split (or not
+// yet fused) products from their fp32 planes, and the elementwise gradient.
+//
+// With G the gate and U the up values, Y = act(G) U, and for a gradient d of Y
+//   dG = d U act'(G),  dU = d act(G).
+// Bound by memory: every value is read and written once, 4 columns of G and
+// the same 4 of U to a lane.
+#include <algorithm>
+
+#include "fused_common.h"
+
+namespace fcs {
+namespace {
+
+// v: the gate in, act(gate) out; s: its slope
+__device__ __forceinline__ void act_and_slope(int act, float (&v)[4], float (&s)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[q] = v[q];
+    act_slopes(act, s);
+    act_values(act, v);
+}
+
+// Sums of 4 columns of each lane over a block's four waves, in order, into `to`
+// (columns n .. n + 3 of a row of N, by lane of wave 0).
+__device__ __forceinline__ void block_colsum(float (*all)[256], const float (&cs)[4], float* to, int64_t n, int64_t N) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) all[wave][lane * 4 + q] = cs[q];
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int c = lane * 4 + q;
+            if (n + q < N) to[n + q] = ((all[0][c] + all[1][c]) + all[2][c]) + all[3][c];
+        }
+    }
+    __syncthreads();
+}
+
+constexpr int kRowsPerWave = 2, kSplitRows = 4 * kRowsPerWave;  // as split_epilogue_parts counts them
+
+// EPI_GLU: planes of 2 N columns, of which a lane takes 4 and the 4 that lie N
+// further. EPI_DGLU: planes of N columns.
+template <EpiMode MODE>
+__global__ __launch_bounds__(256) void split_glu_kernel(FusedArgs g, const float* __restrict__ planes, int64_t pld,
+                                                        int splits) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t nb = (g.N + 255) / 256, N = g.N;
+    const int64_t bm = blockIdx.x / nb, n = (blockIdx.x % nb) * 256 + lane * 4;
+    [[maybe_unused]] __shared__ float cs_all[4][256];
+    [[maybe_unused]] float csg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, csu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n < N) {
+        [[maybe_unused]] float bg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, bu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (MODE == EPI_GLU && g.bias) {
+            load4(g.bias + n, n, N, bg);
+            load4(g.bias + N + n, n, N, bu);
+        }
+#pragma unroll
+        for (int r = 0; r < kRowsPerWave; ++r) {
+            const int64_t m = bm * kSplitRows + wave * kRowsPerWave + r;
+            if (m >= g.M) break;
+            const float* p = planes + m * pld + n;
+            // (the up columns start at any address; past the last one lie others, or the plane's padding)
+            f32x4 sg{0.0f, 0.0f, 0.0f, 0.0f};
+            [[maybe_unused]] f32x4 su{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+            for (int s = 0; s < splits; ++s) {
+                sg += *reinterpret_cast<const f32x4_any*>(p + s * g.M * pld);
+                if constexpr (MODE == EPI_GLU) {
+                    if (n + 4 <= N) {
+                        su += *reinterpret_cast<const f32x4_any*>(p + s * g.M * pld + N);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (n + q < N) su[q] += p[s * g.M * pld + N + q];
+                    }
+                }
+            }
+            float vg[4], vu[4];
+            if constexpr (MODE == EPI_GLU) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) vg[q] = sg[q] + bg[q], vu[q] = su[q] + bu[q];
+                if (g.Z) {
+                    store4_bf16(g.Z + m * 2 * N + n, n, N, vg);
+                    store4_bf16(g.Z + m * 2 * N + N + n, n, N, vu);
+                }
+                act_values(g.act, vg);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) vg[q] *= vu[q];
+                if (g.out_f32)
+                    store4_f32(static_cast<float*>(g.C) + m * g.ldc + n, n, N, vg, false);
+                else
+                    store4_bf16(static_cast<uint16_t*>(g.C) + m * g.ldc + n, n, N, vg);
+            } else {
+                float sl[4], y[4];
+                load4(g.Z + m * 2 * N + n, n, N, vg);
+                load4(g.Z + m * 2 * N + N + n, n, N, vu);
+                act_and_slope(g.act, vg, sl);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    y[q] = vg[q] * vu[q];
+                    vu[q] = sg[q] * vu[q] * sl[q];  // dG
+                    vg[q] = sg[q] * vg[q];          // dU
+                    csg[q] += vu[q], csu[q] += vg[q];
+                }
+                uint16_t* d = static_cast<uint16_t*>(g.C) + m * 2 * N + n;
+                store4_bf16(d, n, N, vu);
+                store4_bf16(d + N, n, N, vg);
+                if (g.Y) store4_bf16(g.Y + m * N + n, n, N, y);
+            }
+        }
+    }
+    if constexpr (MODE == EPI_DGLU) {
+        if (!g.colpart) return;
+        block_colsum(cs_all, csg, g.colpart + bm * 2 * N, n, N);
+        block_colsum(cs_all, csu, g.colpart + bm * 2 * N + N, n, N);
+    }
+}
+
+// The elementwise gradient: a block takes 256 columns (4 per lane) of a range
+// of rows (4 at a time, one per wave), and leaves one partial row.
+__global__ __launch_bounds__(256) void glu_bwd_kernel(const uint16_t* __restrict__ dY, const uint16_t* __restrict__ Z,
+                                                      int act, uint16_t* __restrict__ dZ, uint16_t* __restrict__ Y,
+                                                      float* __restrict__ part, int64_t M, int64_t N, int parts) {
+    __shared__ float cs_all[4][256];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = (int64_t)blockIdx.x * 256 + lane * 4;
+    const int64_t rows = (M + parts - 1) / parts, m0 = blockIdx.y * rows;
+    const int64_t m1 = m0 + rows < M ? m0 + rows : M;
+    float csg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, csu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n < N)
+        for (int64_t m = m0 + wave; m < m1; m += 4) {
+            float d[4], gate[4], up[4], sl[4], y[4];
+            load4(dY + m * N + n, n, N, d);
+            load4(Z + m * 2 * N + n, n, N, gate);
+            load4(Z + m * 2 * N + N + n, n, N, up);
+            act_and_slope(act, gate, sl);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                y[q] = gate[q] * up[q];
+                up[q] = d[q] * up[q] * sl[q];
+                gate[q] = d[q] * gate[q];
+                csg[q] += up[q], csu[q] += gate[q];
+            }
+            if (dZ) {
+                store4_bf16(dZ + m * 2 * N + n, n, N, up);
+                store4_bf16(dZ + m * 2 * N + N + n, n, N, gate);
+            }
+            if (Y) store4_bf16(Y + m * N + n, n, N, y);
+        }
+    if (!part) return;
+    block_colsum(cs_all, csg, part + (int64_t)blockIdx.y * 2 * N, n, N);
+    block_colsum(cs_all, csu, part + (int64_t)blockIdx.y * 2 * N + N, n, N);
+}
+
+}  // namespace
+
+hipError_t launch_split_glu(EpiMode mode, const FusedArgs& g, const float* planes, int64_t pld, int splits,
+                            hipStream_t s) {
+    const int64_t blocks = ((g.N + 255) / 256) * split_epilogue_parts(g.M);
+    if (blocks > 0x7FFFFFFF || split_epilogue_parts(kSplitRows) != 1) return hipErrorInvalidValue;
+    const auto fn = mode == EPI_GLU ? split_glu_kernel<EPI_GLU> : split_glu_kernel<EPI_DGLU>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(256), 0, s, g, planes, pld, splits);
+    return hipGetLastError();
+}
+
+hipError_t launch_glu_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16_t* dZ, uint16_t* Y, float* part,
+                          int64_t M, int64_t N, int parts, hipStream_t s) {
+    if (parts < 1 || parts > 65535) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(glu_bwd_kernel, dim3((unsigned)((N + 255) / 256), (unsigned)parts), dim3(256), 0, s, dY, Z, act,
+                       dZ, Y, part, M, N, parts);
+    return hipGetLastError();
+}
+
+}  // namespace fcs

@@ -17,7 +17,10 @@ enum EpiMode : int {
     EPI_DACT = 2,   // C = v * act'(Z); column sums of C per block of rows
     EPI_STATS = 3,  // per row and block of columns: maximum and sum of exponentials; the target's value
     EPI_DLOGIT = 4, // C = w / s (exp(v - lse) - [column = target]), s of weight_scale
-    kNumEpiModes = 5
+    EPI_GLU = 5,    // z = v + bias over 2 N columns [gate | up]; Z = z; C = act(gate) * up, N columns
+    EPI_DGLU = 6,   // C = [v * up * act'(gate) | v * act(gate)], 2 N columns, Z = [gate | up]; Y = act(gate) * up; column sums of C
+    EPI_LOGITS = 7, // per row and block of columns: maximum, sum of exponentials, their mean logit; C = v or none; the target's value
+    kNumEpiModes = 8
 };
 
 // Which rows a product's tiles cover.
@@ -48,6 +51,8 @@ struct FusedArgs : GemmArgs {
     float* wscale = nullptr;         // EPI_DLOGIT: s, written; EPI_STORE: a factor of v, or none
     float* stat = nullptr;           // EPI_STATS: [block of columns][M] maxima, then as many sums
     float* tlogit = nullptr;
+    float inv_t = 1.0f;              // EPI_DLOGIT, EPI_LOGITS: one over the temperature, a factor of the logits
+    uint16_t* Y = nullptr;           // EPI_DGLU: M x N, written, or none
     const int64_t* offsets = nullptr;  // E + 1 values on the device
     int E = 1;
     int64_t T = 0;        // rows that offsets may reach
@@ -137,5 +142,83 @@ hipError_t launch_act_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16
 // lse, target value and loss of every row from EPI_STATS' partials
 hipError_t launch_xent_finish(const float* stat, int parts, const int64_t* targets, int64_t v0, int64_t ignore,
                               int64_t M, int64_t N, float* lse, float* tlogit, float* loss, hipStream_t s);
+
+// ---- gated layers (fused_glu.hip)
+
+// The epilogues of gated products from the planes of a plain one (EPI_GLU: of
+// 2 N columns). EPI_DGLU leaves split_epilogue_parts(M) rows of 2 N column sums.
+hipError_t launch_split_glu(EpiMode mode, const FusedArgs& g, const float* planes, int64_t pld, int splits,
+                            hipStream_t s);
+// dZ = [dY * up * act'(gate) | dY * act(gate)] and Y = act(gate) * up from Z =
+// [gate | up] (dZ and Y may be none), and the column sums of dZ in `parts` rows
+hipError_t launch_glu_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16_t* dZ, uint16_t* Y, float* part,
+                          int64_t M, int64_t N, int parts, hipStream_t s);
+
+// ---- the vocabulary's logits (fused_vocab.hip)
+
+// EPI_LOGITS from the planes of a plain product: the sum of a row's planes
+// goes to plane 0, the statistics of each kLogitCols columns to g.stat.
+constexpr int kLogitCols = 256;
+hipError_t launch_row_logits(const FusedArgs& g, float* planes, int64_t pld, int splits, hipStream_t s);
+
+// M rows of logits with their statistics (EPI_LOGITS: 3 x parts x M values,
+// `width` columns to a part, a power of two from 32 to 256).
+struct RowLogits {
+    const float* z;  // M x ld, or none
+    int64_t ld;
+    const float* stat;
+    int parts, width;
+    int64_t M, N, v0;
+    float inv_t;
+};
+constexpr int kMaxTop = 128;  // most alternatives and most listed tokens of a row
+
+// What fc_logprob returns of these rows.
+struct LogprobOut {
+    const int64_t* targets;  // or none
+    int64_t ignore;
+    const float* tlogit;
+    float *logp, *entropy, *lse, *top_logp;  // logp and entropy may be none
+    int64_t* top_ids;
+    int k;
+};
+hipError_t launch_logprob_finish(const RowLogits& r, const LogprobOut& o, hipStream_t s);
+
+// A teacher's n listed tokens of each row.
+struct Listed {
+    const int64_t* ids;      // M x n
+    const float* tlogits;    // M x n
+    int n;
+    const float* slogits;    // M x n: the student's logits there
+    const float* p;          // M x n (launch_listed_prep)
+};
+hipError_t launch_distill_finish(const RowLogits& r, const Listed& t, float* lse, float* slogits, float* loss,
+                                 hipStream_t s);
+// For the gradient: p = the listed tokens' probabilities, a token's summed at
+// its first place (-1 at the others and where none is); gw = grad / T; targets
+// = -1 in rows that count, INT64_MIN in the others.
+hipError_t launch_listed_prep(const Listed& t, const float* grad, float inv_t, int64_t M, float* p, float* gw,
+                              int64_t* targets, hipStream_t s);
+// Columns v0 .. v0 + c - 1 of D (bf16, rows of ld) at the listed tokens:
+// gw / *scale (exp(z / T - lse) - p).
+hipError_t launch_listed_grad(const Listed& t, const float* lse, const float* gw, float inv_t, const float* scale,
+                              uint16_t* D, int64_t ld, int64_t v0, int64_t c, int64_t M, hipStream_t s);
+
+// The two gradients of a loss over a vocabulary projection (fused_api.hip):
+// D = gw (exp(z / T - lse) - [column = target]), and at the listed tokens as above.
+struct LogitsBwd {
+    const void *X, *W;
+    int w_order;
+    const int64_t* targets;
+    int64_t v0, ignore;
+    const float *lse, *gw;
+    float inv_t = 1.0f;
+    const Listed* listed = nullptr;
+    void *dX, *dW;
+    int dx_f32, dw_dtype;
+    int64_t M, K, N;
+};
+int64_t logits_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, int w_order, bool aligned);
+hipError_t run_logits_bwd(const LogitsBwd& b, char* ws, hipStream_t s);
 
 }  // namespace fcs

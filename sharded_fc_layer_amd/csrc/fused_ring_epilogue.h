@@ -371,7 +371,7 @@ __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos&
                                   f32x4 d;
 #pragma unroll
                                   for (int q = 0; q < 4; ++q) {
-                                      const float p = exp_f32(z[q] - lse[i]);
+                                      const float p = exp_f32(z[q] * g.inv_t - lse[i]);
                                       d[q] = w[i] * __builtin_fmaf(-here, (hit[i] & 3) == q ? 1.0f : 0.0f, p);
                                   }
                                   return pack_bf16(d) & live[i];

@@ -90,13 +90,27 @@ def lib() -> ctypes.CDLL:
         L.fc_fwd_act_ws_bytes.argtypes = [i64, i64, i64, ci, ci, ci]
         L.fc_bwd_act_ws_bytes.argtypes = [i64, i64]
         L.fc_grouped_ws_bytes.argtypes = [ci, i64, i64, i64, i64, ci, ci]
-        for f in (L.fc_bwd_data_act_ws_bytes, L.fc_xent_fwd_ws_bytes, L.fc_xent_bwd_ws_bytes):
+        cf = ctypes.c_float
+        L.fc_fwd_glu.argtypes = [vp, vp, ci, vp, ci, vp, vp, ci, i64, i64, i64, vp, i64, vp]
+        L.fc_bwd_data_glu.argtypes = [vp, vp, ci, vp, ci, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+        L.fc_bwd_glu.argtypes = [vp, vp, ci, vp, vp, vp, i64, i64, vp, i64, vp]
+        L.fc_logprob.argtypes = [vp, vp, ci, vp, i64, i64, cf, vp, vp, vp, vp, vp, ci, i64, i64, i64, vp, i64, vp]
+        L.fc_distill_fwd.argtypes = [vp, vp, ci, vp, vp, ci, i64, cf, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+        L.fc_distill_bwd.argtypes = [vp, vp, ci, vp, vp, ci, i64, cf, vp, vp, vp, vp, ci, vp, ci, i64, i64, i64, vp,
+                                     i64, vp]
+        L.fc_bwd_glu_ws_bytes.argtypes = [i64, i64]
+        L.fc_logprob_ws_bytes.argtypes = [i64, i64, i64, ci, ci, ci]
+        L.fc_distill_bwd_ws_bytes.argtypes = [i64, i64, i64, ci, ci, ci]
+        for f in (L.fc_bwd_data_act_ws_bytes, L.fc_xent_fwd_ws_bytes, L.fc_xent_bwd_ws_bytes, L.fc_fwd_glu_ws_bytes,
+                  L.fc_bwd_data_glu_ws_bytes, L.fc_distill_fwd_ws_bytes):
             f.argtypes = [i64, i64, i64, ci, ci]
         for f in (L.fc_fwd_act_ws_bytes, L.fc_bwd_data_act_ws_bytes, L.fc_bwd_act_ws_bytes, L.fc_xent_fwd_ws_bytes,
-                  L.fc_xent_bwd_ws_bytes, L.fc_grouped_ws_bytes):
+                  L.fc_xent_bwd_ws_bytes, L.fc_grouped_ws_bytes, L.fc_fwd_glu_ws_bytes, L.fc_bwd_data_glu_ws_bytes,
+                  L.fc_bwd_glu_ws_bytes, L.fc_logprob_ws_bytes, L.fc_distill_fwd_ws_bytes, L.fc_distill_bwd_ws_bytes):
             f.restype = i64
         for f in (L.fc_fwd_act, L.fc_bwd_data_act, L.fc_bwd_act, L.fc_xent_fwd, L.fc_xent_bwd, L.fc_grouped_fwd,
-                  L.fc_grouped_bwd_data, L.fc_grouped_bwd_weight):
+                  L.fc_grouped_bwd_data, L.fc_grouped_bwd_weight, L.fc_fwd_glu, L.fc_bwd_data_glu, L.fc_bwd_glu,
+                  L.fc_logprob, L.fc_distill_fwd, L.fc_distill_bwd):
             f.restype = ci
         for f in (L.fc_fwd, L.fc_bwd_data, L.fc_bwd_weight, L.fc_bwd_weight_noalloc, L.fc_tune, L.fc_set_plan, L.fc_plan_describe,
                   L.fc_plan_count, L.fc_release, L.fc_plans_save, L.fc_plans_load, L.fc_mfma_probe,
@@ -520,6 +534,176 @@ def fc_grouped_bwd_weight(X, dY, offsets, out=None, out_dtype: int = OUT_BF16, s
     dW = _weight_grad(on, out, out_dtype, (E, K, N), "out")
     return _grouped(OP_BWD_WEIGHT, lib().fc_grouped_bwd_weight, X, dY, offsets, dW, out_dtype, T, E, K, N, ROW, on,
                     "fc_grouped_bwd_weight")
+
+
+# ---- gated layers, log probabilities, distillation
+
+def fc_fwd_glu(X, W, bias=None, act: int = ACT_SILU, w_order: int = ROW, keep_z: bool = False, out=None, z=None,
+               out_dtype: int = OUT_BF16, stream=None):
+    """Y = act(G) * U with [G | U] = Z = X . W + bias on the GPU: W is K x 2N, the
+    gate's columns before the up projection's (COL: 2N x K, their rows one after
+    the other). Returns Y (M x N), or (Y, Z) with keep_z."""
+    import torch
+    _bf16_2d(X, "X"), _bf16_2d(W, "W"), _order(w_order, "w_order")
+    M, K = X.shape
+    K2, N2 = _logical(W, w_order)
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: X is {M}x{K}, W is {K2}x{N2}")
+    if N2 % 2:
+        raise ValueError(f"W has {N2} columns: the gate's and as many of the up projection")
+    if bias is not None:
+        _tensor(bias, torch.bfloat16, (N2,), "bias")
+    on = _On(stream, X)
+    Y = on.given(out, _out_type(out_dtype, "out_dtype"), (M, N2 // 2), "out")
+    Z = on.given(z, torch.bfloat16, (M, N2), "z") if keep_z or z is not None else None
+    _here(X, W, bias, Y, Z)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_fwd_glu_ws_bytes(M, K, N2 // 2, w_order, _aligned(X, W)), "fc_fwd_glu")
+    _check(L.fc_fwd_glu(X.data_ptr(), W.data_ptr(), w_order, _ptr(bias), act, _ptr(Z), Y.data_ptr(), out_dtype, M, K,
+                        N2 // 2, wp, wn, on.handle), "fc_fwd_glu")
+    return Y if Z is None else (Y, Z)
+
+
+def fc_bwd_data_glu(dY, W, Z, act: int = ACT_SILU, w_order: int = ROW, keep_y: bool = False, bias_grad: bool = False,
+                    out=None, y=None, db=None, stream=None):
+    """The gradient through a product and the gated layer below it: dH = dY . W^T,
+    dZ = [dH * U * act'(G) | dH * act(G)], where Z = [G | U] (M x 2K) is what the
+    layer's fc_fwd_glu left and W (K x N) is the product's. Returns dZ (M x 2K);
+    with keep_y also the layer's output act(G) * U (M x K), with bias_grad also
+    dZ's column sums (fp32, 2K), as a tuple in this order."""
+    import torch
+    _bf16_2d(dY, "dY"), _bf16_2d(W, "W"), _order(w_order, "w_order")
+    M, N = dY.shape
+    K, N2 = _logical(W, w_order)
+    if N2 != N:
+        raise ValueError(f"dY is {M}x{N} but W is {K}x{N2}")
+    _tensor(Z, torch.bfloat16, (M, 2 * K), "Z")
+    on = _On(stream, dY)
+    dZ = on.given(out, torch.bfloat16, (M, 2 * K), "out")
+    if keep_y or y is not None:
+        y = on.given(y, torch.bfloat16, (M, K), "y")
+    if bias_grad or db is not None:
+        db = on.given(db, torch.float32, (2 * K,), "db")
+    _here(dY, W, Z, dZ, y, db)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_bwd_data_glu_ws_bytes(M, K, N, w_order, _aligned(dY, W)), "fc_bwd_data_glu")
+    _check(L.fc_bwd_data_glu(dY.data_ptr(), W.data_ptr(), w_order, Z.data_ptr(), act, dZ.data_ptr(), _ptr(y), _ptr(db),
+                             M, K, N, wp, wn, on.handle), "fc_bwd_data_glu")
+    given = tuple(t for t in (dZ, y, db) if t is not None)
+    return given if len(given) > 1 else dZ
+
+
+def fc_bwd_glu(dY, Z, act: int = ACT_SILU, keep_dz: bool = True, keep_y: bool = False, bias_grad: bool = False,
+               out=None, y=None, db=None, stream=None):
+    """dZ = [dY * U * act'(G) | dY * act(G)] from the gradient dY (M x N) of
+    fc_fwd_glu's output and its Z = [G | U]: returns (dZ, Y, db), None for what
+    was not asked for: Y = act(G) * U again (keep_y), db = dZ's column sums
+    (fp32, 2N; bias_grad)."""
+    import torch
+    _bf16_2d(dY, "dY")
+    M, N = dY.shape
+    _tensor(Z, torch.bfloat16, (M, 2 * N), "Z")
+    on = _On(stream, dY)
+    dZ = on.given(out, torch.bfloat16, (M, 2 * N), "out") if keep_dz or out is not None else None
+    if keep_y or y is not None:
+        y = on.given(y, torch.bfloat16, (M, N), "y")
+    if bias_grad or db is not None:
+        db = on.given(db, torch.float32, (2 * N,), "db")
+    _here(dY, Z, dZ, y, db)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_bwd_glu_ws_bytes(M, N) if db is not None else 0, "fc_bwd_glu")
+    _check(L.fc_bwd_glu(dY.data_ptr(), Z.data_ptr(), act, _ptr(dZ), _ptr(y), _ptr(db), M, N, wp, wn, on.handle),
+           "fc_bwd_glu")
+    return dZ, y, db
+
+
+def _vocabulary(X, W, w_order: int):
+    _bf16_2d(X, "X"), _bf16_2d(W, "W"), _order(w_order, "w_order")
+    M, K = X.shape
+    K2, N = _logical(W, w_order)
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: X is {M}x{K}, W is {K2}x{N}")
+    return M, K, N
+
+
+def fc_logprob(X, W, targets=None, w_order: int = ROW, vocab_start: int = 0, ignore_index: int = -100,
+               temperature: float = 1.0, top_k: int = 0, stream=None):
+    """Log probabilities under softmax(X . W / temperature), without its logits:
+    returns (logp, entropy, lse, top_logp, top_ids): the targets' log
+    probabilities (None without targets), the entropy and the logarithm of the
+    normaliser, M fp32 values each, and the top_k most likely columns' (M x
+    top_k) log probabilities and int64 indices (see fcshard.h)."""
+    import torch
+    M, K, N = _vocabulary(X, W, w_order)
+    if targets is not None:
+        _tensor(targets, torch.int64, (M,), "targets")
+    if not 0 <= top_k <= min(N, 128):
+        raise ValueError(f"top_k must be 0 .. {min(N, 128)}")
+    on = _On(stream, X)
+    logp = None if targets is None else on.empty((M,), torch.float32)
+    entropy, lse = on.empty((M,), torch.float32), on.empty((M,), torch.float32)
+    top_logp, top_ids = on.empty((M, top_k), torch.float32), on.empty((M, top_k), torch.int64)
+    _here(X, W, targets, lse)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_logprob_ws_bytes(M, K, N, w_order, top_k, _aligned(X, W)), "fc_logprob")
+    _check(L.fc_logprob(X.data_ptr(), W.data_ptr(), w_order, _ptr(targets), vocab_start, ignore_index, temperature,
+                        _ptr(logp), entropy.data_ptr(), lse.data_ptr(), top_logp.data_ptr() if top_k else None,
+                        top_ids.data_ptr() if top_k else None, top_k, M, K, N, wp, wn, on.handle), "fc_logprob")
+    return logp, entropy, lse, top_logp, top_ids
+
+
+def _listed(ids, tlogits, M: int):
+    import torch
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise TypeError("ids must be a 2-D torch.int64 tensor")
+    n = ids.shape[1]
+    _tensor(ids, torch.int64, (M, n), "ids"), _tensor(tlogits, torch.float32, (M, n), "tlogits")
+    if not 1 <= n <= 128:
+        raise ValueError("ids must list 1 .. 128 tokens for each row")
+    return n
+
+
+def fc_distill_fwd(X, W, ids, tlogits, w_order: int = ROW, vocab_start: int = 0, temperature: float = 1.0,
+                   stream=None):
+    """The divergence of softmax(X . W / temperature) from a teacher's distribution
+    over its listed tokens: ids (int64) and tlogits (fp32), M x n each, a
+    negative id for an absent one. Returns (loss, lse, slogits): M fp32 values
+    each, and the student's logits of the listed tokens (M x n; see fcshard.h)."""
+    import torch
+    M, K, N = _vocabulary(X, W, w_order)
+    n = _listed(ids, tlogits, M)
+    on = _On(stream, X)
+    loss, lse, slogits = on.empty((M,), torch.float32), on.empty((M,), torch.float32), on.empty((M, n), torch.float32)
+    _here(X, W, ids, tlogits, loss)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_distill_fwd_ws_bytes(M, K, N, w_order, _aligned(X, W)), "fc_distill_fwd")
+    _check(L.fc_distill_fwd(X.data_ptr(), W.data_ptr(), w_order, ids.data_ptr(), tlogits.data_ptr(), n, vocab_start,
+                            temperature, lse.data_ptr(), slogits.data_ptr(), loss.data_ptr(), M, K, N, wp, wn,
+                            on.handle), "fc_distill_fwd")
+    return loss, lse, slogits
+
+
+def fc_distill_bwd(X, W, ids, tlogits, slogits, lse, grad, w_order: int = ROW, vocab_start: int = 0,
+                   temperature: float = 1.0, dX=None, dx_dtype: int = OUT_BF16, dW=None, dw_dtype: int = OUT_BF16,
+                   stream=None):
+    """Gradients of fc_distill_fwd's loss: grad (fp32, M) weighs the rows, slogits
+    and lse are what it returned (lse over the whole vocabulary). Returns (dX,
+    dW): M x K, and K x N row-major; dw_dtype = OUT_F32_ACC adds to the given dW."""
+    import torch
+    M, K, N = _vocabulary(X, W, w_order)
+    n = _listed(ids, tlogits, M)
+    _tensor(slogits, torch.float32, (M, n), "slogits")
+    _tensor(lse, torch.float32, (M,), "lse"), _tensor(grad, torch.float32, (M,), "grad")
+    on = _On(stream, X)
+    dX = on.given(dX, _out_type(dx_dtype, "dx_dtype"), (M, K), "dX")
+    dW = _weight_grad(on, dW, dw_dtype, (K, N), "dW")
+    _here(X, W, ids, tlogits, slogits, lse, grad, dX, dW)
+    L = lib()
+    ws, wp, wn = on.workspace(L.fc_distill_bwd_ws_bytes(M, K, N, w_order, n, _aligned(X, W)), "fc_distill_bwd")
+    _check(L.fc_distill_bwd(X.data_ptr(), W.data_ptr(), w_order, ids.data_ptr(), tlogits.data_ptr(), n, vocab_start,
+                            temperature, slogits.data_ptr(), lse.data_ptr(), grad.data_ptr(), dX.data_ptr(), dx_dtype,
+                            dW.data_ptr(), dw_dtype, M, K, N, wp, wn, on.handle), "fc_distill_bwd")
+    return dX, dW
 
 
 STAMP_SLOTS = 8  # values per block written by fc_stamped_call
