@@ -112,6 +112,14 @@ __device__ __forceinline__ float act_slope(const ActParams& a, float z) {
     }
 }
 
+// One logit's share of its row's statistics: e = exp((z - ref) / T), and e (z -
+// ref) / T, where a distance past 1e4 below (-inf too) counts as 1e4: e is 0.
+__device__ __forceinline__ void add_exp(float z, float ref, float inv_t, float& sum, float& mean) {
+    const float d = (z - ref) * inv_t, e = exp_f32(d);
+    sum += e;
+    mean = __builtin_fmaf(e, fmaxf(d, -1e4f), mean);
+}
+
 // over several values (an array or a vector), with one branch on the kind
 template <class V>
 __device__ __forceinline__ void act_values(int act, V& v) {

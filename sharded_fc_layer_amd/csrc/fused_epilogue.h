@@ -117,6 +117,7 @@ struct Epilogue {
         // (a row past the end takes the last one's: nothing of it is stored)
         const int64_t mc = there ? m : t.M - 1;
         if constexpr (MODE == EPI_STATS || MODE == EPI_DLOGIT) r.target = g.targets[mc];
+        if constexpr (MODE == EPI_LOGITS) r.target = g.targets ? g.targets[mc] : -1;
         if constexpr (MODE == EPI_DLOGIT) r.lse = g.lse[mc], r.w = g.gw[mc];
     }
 
@@ -148,6 +149,38 @@ struct Epilogue {
             if (there && ch == 0) {
                 g.stat[(int64_t)part * t.M + m] = mx;
                 g.stat[(int64_t)(parts + part) * t.M + m] = sum;
+            }
+            return;
+        }
+        if constexpr (MODE == EPI_LOGITS) {
+            // as EPI_STATS, with the mean distance from the maximum; C's rows
+            // are padded to whole vectors
+            float mx = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                v[q] = q < left ? v[q] : -INFINITY;
+                mx = fmaxf(mx, v[q]);
+            }
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+            const float ref = __builtin_isinf(mx) ? 0.0f : mx;
+            float sum = 0.0f, mean = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) add_exp(v[q], ref, g.inv_t, sum, mean);
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor(sum, d), mean += __shfl_xor(mean, d);
+            const uint64_t hit = (uint64_t)in.target - (uint64_t)g.v0 - (uint64_t)n;
+            float z = v[0];
+#pragma unroll
+            for (int q = 1; q < 8; ++q) z = hit == (uint64_t)q ? v[q] : z;
+            if (g.targets && hit < (uint64_t)cols) g.tlogit[m] = z;
+            if (g.C) store8(static_cast<float*>(g.C) + m * g.ldc + n, cols > 0 ? 8 : 0, v, false);
+            if (there && ch == 0) {
+                float* st = g.stat + (int64_t)part * t.M + m;
+                const int64_t step = (int64_t)parts * t.M;
+                st[0] = mx;
+                st[step] = sum;
+                st[2 * step] = mean;
             }
             return;
         }

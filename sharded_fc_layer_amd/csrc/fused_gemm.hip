@@ -54,6 +54,8 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
             fn = kind == kNormal    ? fused_ring<EPI_DACT, kNormal>(head, vec, a_oc, b_oc)
                  : kind == kSigmoid ? fused_ring<EPI_DACT, kSigmoid>(head, vec, a_oc, b_oc)
                                     : fused_ring<EPI_DACT, kLinear>(head, vec, a_oc, b_oc);
+        else if (mode == EPI_LOGITS)
+            fn = g.C ? fused_ring<EPI_LOGITS, 1>(head, true, a_oc, b_oc) : fused_ring<EPI_LOGITS, 0>(head, true, a_oc, b_oc);
         else
             fn = mode == EPI_STATS ? fused_ring<EPI_STATS, 0>(head, true, a_oc, b_oc)
                                    : fused_ring<EPI_DLOGIT, 0>(head, true, a_oc, b_oc);

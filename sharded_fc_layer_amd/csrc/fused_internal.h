@@ -37,7 +37,7 @@ struct FusedArgs : GemmArgs {
     const uint16_t* a_end = nullptr;
     const uint16_t* b_end = nullptr;
     int out_f32 = 0;      // C is fp32 (else bf16)
-    int vec_out = 0;      // ring kernel: the rows of C, R and Z start on 16-byte boundaries, N is a multiple of 8
+    int vec_out = 0;      // ring kernel: the rows of C, R, Y and Z start on 16-byte boundaries, N is a multiple of 8
     int act = 0;          // fc_act
     const uint16_t* bias = nullptr;  // N values, or none
     const uint16_t* R = nullptr;     // M x N, or none
@@ -98,6 +98,8 @@ FCU_DECLARE_RING(EPI_DACT, 1)
 FCU_DECLARE_RING(EPI_DACT, 2)
 FCU_DECLARE_RING(EPI_STATS, 0)
 FCU_DECLARE_RING(EPI_DLOGIT, 0)
+FCU_DECLARE_RING(EPI_LOGITS, 0)
+FCU_DECLARE_RING(EPI_LOGITS, 1)
 #undef FCU_DECLARE_RING
 template <>
 FusedFn fused_ring_grouped<0>(GroupMode grp, int head, bool vec, bool b_oc);

@@ -44,24 +44,30 @@ constexpr int64_t kLogitBytes = (int64_t)512 << 20;
 struct LogitsPlan {
     Operand A, B;
     Shape sh;
+    bool keep;     // the logits are stored: they are read again, or a split reduction's planes
     int64_t rows;  // of a chunk: a multiple of 256, or all
     int64_t z_ld, z_off, stat_off, t_off, total;
     int parts, width;
 };
-LogitsPlan logits_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned) {
+LogitsPlan logits_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned, bool read_again) {
     LogitsPlan p;
     int64_t ws = 0;
     p.z_ld = plane_ld(N);
-    p.rows = std::min<int64_t>(M, std::max<int64_t>(256, kLogitBytes / (4 * p.z_ld) / 256 * 256));
+    const int64_t fit = std::max<int64_t>(256, kLogitBytes / (4 * p.z_ld) / 256 * 256);
     const int64_t bcols = b_oc ? N : K;
+    p.rows = read_again ? std::min(M, fit) : M;
     p.sh = shape_of(p.rows, N, K, false, b_oc, K, bcols, aligned);
-    const bool ring = p.sh.tile == kRingTile;
+    if (512 * p.z_ld >= (int64_t)1 << 31 && p.sh.tile == kRingTile)
+        p.sh = small_shape(p.rows, N, K, false, !fits(K, aligned) || !fits(bcols, aligned), false);
+    const bool ring = p.sh.tile == kRingTile, split = p.sh.splits > 1;
+    p.keep = read_again || split;
     p.A = operand(M, K, aligned, ring, &ws);
     p.B = operand(b_oc ? K : N, bcols, aligned, ring, &ws);
-    p.width = kLogitCols;
-    p.parts = (int)((N + p.width - 1) / p.width);
+    const FusedTile& t = kFusedTiles[p.sh.tile];
+    p.width = split ? kLogitCols : t.bn / t.wave_cols;
+    p.parts = split ? (int)((N + p.width - 1) / p.width) : (int)((N + t.bn - 1) / t.bn) * t.wave_cols;
     p.z_off = ws;
-    ws += p.sh.splits * p.rows * p.z_ld * 4;
+    if (p.keep) ws += p.sh.splits * p.rows * p.z_ld * 4;
     p.stat_off = ws;
     ws += up((int64_t)3 * p.parts * p.rows * 4, 256);
     p.t_off = ws;
@@ -92,7 +98,12 @@ hipError_t run_logits(const LogitsPlan& pl, const LogitsCall& c, const uint16_t*
     g.tlogit = reinterpret_cast<float*>(base + pl.t_off);
     float* z = reinterpret_cast<float*>(base + pl.z_off);
     *out = RowLogits{z, pl.z_ld, g.stat, pl.parts, pl.width, rows, c.N, c.v0, c.inv_t};
-    return run_planes(EPI_LOGITS, pl.sh, false, c.w_order == FC_ROW_MAJOR, g, c.N, z, s);
+    const bool b_oc = c.w_order == FC_ROW_MAJOR;
+    if (pl.sh.splits > 1) return run_planes(EPI_LOGITS, pl.sh, false, b_oc, g, c.N, z, s);
+    g.C = pl.keep ? z : nullptr;
+    g.ldc = pl.z_ld;
+    g.k_split = pl.sh.k_split, g.splits = 1, g.c_split_stride = 0;
+    return launch_fused(EPI_LOGITS, GRP_NONE, pl.sh.tile, false, b_oc, g, s);
 }
 
 }  // namespace
@@ -205,7 +216,7 @@ fc_status fc_bwd_glu(const void* dY, const void* Z, fc_act act, void* dZ, void* 
 
 int64_t fc_logprob_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int top_k, int aligned) {
     if (bad_sizes(M, K, N) || bad_order(w_order) || top_k < 0 || top_k > kMaxTop || top_k > N) return -1;
-    return logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned != 0).total;
+    return logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned != 0, top_k > 0).total;
 }
 
 fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64_t* targets, int64_t vocab_start,
@@ -219,7 +230,7 @@ fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64
         off(top_logp, 4) || off(top_ids, 8))
         return FC_E_INVALID;
     const bool aligned = !off(X, 16) && !off(W, 16);
-    LogitsPlan pl = logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned);
+    LogitsPlan pl = logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned, top_k > 0);
     if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
     if (overlapping({{logp, M * 4}, {entropy, M * 4}, {lse, M * 4}, {top_k ? top_logp : nullptr, M * top_k * 4},
                      {top_k ? top_ids : nullptr, M * top_k * 8}, {ws, pl.total}},
@@ -247,7 +258,7 @@ fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64
 
 int64_t fc_distill_fwd_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned) {
     if (bad_sizes(M, K, N) || bad_order(w_order)) return -1;
-    return logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned != 0).total;
+    return logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned != 0, true).total;
 }
 
 fc_status fc_distill_fwd(const void* X, const void* W, fc_order w_order, const int64_t* ids, const float* tlogits,
@@ -259,7 +270,7 @@ fc_status fc_distill_fwd(const void* X, const void* W, fc_order w_order, const i
     if (off(X, 2) || off(W, 2) || off(ids, 8) || off(tlogits, 4) || off(lse, 4) || off(slogits, 4) || off(loss, 4))
         return FC_E_INVALID;
     const bool aligned = !off(X, 16) && !off(W, 16);
-    LogitsPlan pl = logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned);
+    LogitsPlan pl = logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned, true);
     if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
     if (overlapping({{lse, M * 4}, {slogits, M * top_n * 4}, {loss, M * 4}, {ws, pl.total}},
                     {{X, M * K * 2}, {W, K * N * 2}, {ids, M * top_n * 8}, {tlogits, M * top_n * 4}}))

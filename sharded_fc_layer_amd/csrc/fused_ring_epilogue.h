@@ -339,11 +339,90 @@ __device__ __forceinline__ void ring_stats(const FusedArgs& g, const TilePos& t,
     }
 }
 
+// EPI_LOGITS where the accumulators lie: ring_stats with the mean distance from
+// the maximum; KEEP: the logits are stored too, 16 rows x 64 bytes to an
+// access, into rows that are padded to 64 columns.
+template <int TN, bool KEEP>
+__device__ __forceinline__ void ring_logits(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
+                                            const f32x4 (&acc)[8][TN]) {
+    const int lr = lane & 15, lk = lane >> 4;
+    const int64_t m0 = t.m0 + wave_m * 128 + lr, n0 = t.n0 + wave_n * 16 * TN + 4 * lk;
+    const bool edge = t.n0 + 32 * TN > g.N;
+    const int last = g.N - n0 >= 16 * TN ? 16 * TN : g.N > n0 ? (int)(g.N - n0) : 0;  // this lane's columns end there
+    const int part = t.tn * 2 + wave_n, parts = (int)((g.N + 32 * TN - 1) / (32 * TN)) * 2;
+    const float inv_t = g.inv_t;
+    [[maybe_unused]] const int room = g.ldc - n0 >= 16 * TN ? 16 * TN : g.ldc > n0 ? (int)(g.ldc - n0) : 0;
+    [[maybe_unused]] const __amdgpu_buffer_rsrc_t rc =
+        buffer_at(KEEP ? static_cast<float*>(g.C) + (t.m0 + wave_m * 128) * g.ldc + t.n0 + wave_n * 16 * TN : nullptr);
+    int hit[8];  // the target's column less n0, or -1
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t m = m0 + 16 * i;
+        hit[i] = -1;
+        if (g.targets) {
+            // unsigned: a target far below v0 wraps past every column
+            const uint64_t at = (uint64_t)g.targets[m < t.M ? m : t.M - 1] - (uint64_t)g.v0 - (uint64_t)n0;
+            hit[i] = at < (uint64_t)last && (at & 15) < 4 && m < t.M ? (int)at : -1;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t m = m0 + 16 * i;
+        float z[4 * TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) z[4 * j + q] = acc[i][j][q];
+        if constexpr (KEEP) {
+            const uint32_t row = (uint32_t)(16 * i + lr) * (uint32_t)g.ldc * 4 + 16 * lk;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), rc,
+                                                       m < t.M && 16 * j < room ? row : kOOB, 64 * j, 0);
+        }
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) z[4 * j + q] = 16 * j + q < last ? z[4 * j + q] : -INFINITY;
+        }
+        float mx = z[0];
+#pragma unroll
+        for (int k = 1; k < 4 * TN; ++k) mx = fmaxf(mx, z[k]);
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        const float ref = __builtin_isinf(mx) ? 0.0f : mx;
+        float sum = 0.0f, mean = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4 * TN; ++k) add_exp(z[k], ref, inv_t, sum, mean);
+        sum += __shfl_xor(sum, 16);
+        mean += __shfl_xor(mean, 16);
+        sum += __shfl_xor(sum, 32);
+        mean += __shfl_xor(mean, 32);
+        if (__any(hit[i] >= 0)) {
+            float h = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4 * TN; ++k) h = hit[i] == 16 * (k >> 2) + (k & 3) ? z[k] : h;
+            if (hit[i] >= 0) g.tlogit[m0 + 16 * i] = h;
+        }
+        if (lk == 0 && m < t.M) {
+            float* st = g.stat + (int64_t)part * t.M + m;
+            const int64_t step = (int64_t)parts * t.M;
+            st[0] = mx;
+            st[step] = sum;
+            st[2 * step] = mean;
+        }
+        asm volatile("" ::: "memory");  // keeps the groups in this order
+    }
+}
+
 template <EpiMode MODE, GroupMode GRP, int TN, int KIND, bool VEC>
 __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
                                               const f32x4 (&acc)[8][TN], char* stage) {
     if constexpr (MODE == EPI_STATS) {
         ring_stats<TN>(g, t, wave_m, wave_n, lane, acc);
+    } else if constexpr (MODE == EPI_LOGITS) {
+        ring_logits<TN, KIND != 0>(g, t, wave_m, wave_n, lane, acc);
     } else if constexpr (MODE == EPI_DLOGIT) {
         const int64_t m0 = t.m0 + wave_m * 128, n0 = t.n0 + wave_n * 16 * TN;
         // This lane's rows 16 i + lane % 16. z - lse first: a target that has

@@ -72,11 +72,7 @@ __global__ __launch_bounds__(256) void row_logits_kernel(FusedArgs g, float* __r
     const float ref = finite_ref(mx);
     float sum = 0.0f, mean = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float d = (z[q] - ref) * g.inv_t, e = exp_f32(d);
-        sum += e;
-        mean += e * fmaxf(d, -1e4f);
-    }
+    for (int q = 0; q < 4; ++q) add_exp(z[q], ref, g.inv_t, sum, mean);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d), mean += __shfl_xor(mean, d);
     if (lane == 0) {
