@@ -39,10 +39,6 @@ __device__ __forceinline__ void join_stats(Stats& a, const Stats& b, float inv_t
     a.sum = a.sum * fa + b.sum * fb;
     a.mx = top;
 }
-__device__ __forceinline__ Stats shuffled(const Stats& a, int d) {
-    return Stats{__shfl_xor(a.mx, d), __shfl_xor(a.sum, d), __shfl_xor(a.mean, d)};
-}
-
 // The planes of a product, 256 columns of one row to a wave, 4 to a lane: their
 // sum, which is left in plane 0, and its statistics.
 __global__ __launch_bounds__(256) void row_logits_kernel(FusedArgs g, float* __restrict__ planes, int64_t pld,
@@ -84,20 +80,66 @@ __global__ __launch_bounds__(256) void row_logits_kernel(FusedArgs g, float* __r
     }
 }
 
-// The statistics of a row from its parts: those of every 64 SUBS-th part from
-// 64 sub + lane on, joined over the wave. All lanes get the same.
-__device__ __forceinline__ Stats row_stats(const RowLogits& r, int64_t m, int sub, int subs, int lane) {
-    Stats a{-INFINITY, 0.0f, 0.0f};
-    const int64_t step = (int64_t)r.parts * r.M;
-    for (int p = sub * 64 + lane; p < r.parts; p += 64 * subs) {
-        const float* st = r.stat + (int64_t)p * r.M + m;
-        join_stats(a, Stats{st[0], st[step], st[2 * step]}, r.inv_t);
-    }
+__device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) join_stats(a, shuffled(a, d), r.inv_t);
-    // (a sum of two products may round differently the other way round)
-    auto first = [](float v) { return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v))); };
-    return Stats{first(a.mx), first(a.sum), first(a.mean)};
+    for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ float wave_min(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v = fminf(v, __shfl_xor(v, d));
+    return v;
+}
+// the smaller one, but -inf and NaN do not count
+__device__ __forceinline__ float least_number(float low, float v) { return v > -INFINITY && v < low ? v : low; }
+
+constexpr int kFinishThreads = 1024;
+
+// The statistics of the ROWS rows from m0 on, by a block: thread (row, slice)
+// joins every so many-th part of its row, so that with 16 rows a wave's reads
+// are whole 64-byte pieces (4096 rows of 250 parts: 30 us with the parts of a
+// row over the lanes of a wave, 7 so), then pairwise in a fixed order. Rows past the last
+// one repeat it. `maxima` (LDS, ROWS x parts, or none) receives the parts' maxima.
+template <int ROWS>
+__device__ __forceinline__ void block_stats(const RowLogits& r, int64_t m0, Stats (*s)[ROWS + 1], float* maxima) {
+    constexpr int S = kFinishThreads / ROWS;
+    const int row = threadIdx.x % ROWS, sl = threadIdx.x / ROWS;
+    const int64_t m = m0 + row < r.M ? m0 + row : r.M - 1, step = (int64_t)r.parts * r.M;
+    Stats a{-INFINITY, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int p = sl; p < r.parts; p += S) {
+        const float* st = r.stat + (int64_t)p * r.M + m;
+        const Stats b{st[0], st[step], st[2 * step]};
+        if (maxima) maxima[row * r.parts + p] = b.mx;
+        join_stats(a, b, r.inv_t);
+    }
+    // 64 slices to LDS at most, the others' through the lanes of a wave first
+    constexpr int T = S > 64 ? 64 : S;
+    if constexpr (S > T) {
+#pragma unroll
+        for (int d = ROWS; d < ROWS * (S / T); d <<= 1) {
+            const Stats b{__shfl_xor(a.mx, d), __shfl_xor(a.sum, d), __shfl_xor(a.mean, d)};
+            join_stats(a, b, r.inv_t);
+        }
+    }
+    static_assert(ROWS * (S / T) <= 64, "within a wave");
+    const int at = sl / (S / T);
+    if (sl % (S / T) == 0) s[at][row] = a;
+    __syncthreads();
+#pragma unroll
+    for (int d = T / 2; d > 0; d >>= 1) {
+        if (sl % (S / T) == 0 && at < d) {
+            join_stats(a, s[at + d][row], r.inv_t);
+            s[at][row] = a;
+        }
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------- the largest of a row
@@ -156,44 +198,96 @@ struct TopList {
     }
 };
 
-constexpr int kFinishWaves = 16;
+// Whole 32-bit order of values: that of order_key's upper half.
+__device__ __forceinline__ uint32_t order_of(float z) { return (uint32_t)(order_key(z, 0) >> 32); }
 
-// Rows' lists of SUBS waves each made one, in lists[row's first wave]: all
-// waves of the block call it.
-template <int SUBS, int R>
-__device__ __forceinline__ void join_lists(TopList<R>& top, uint64_t (*lists)[64 * R], int wave, int sub, int k,
-                                           int lane) {
-    __syncthreads();  // the lists' last readers are done
-#pragma unroll
-    for (int r = 0; r < R; ++r) lists[wave][64 * r + lane] = top.v[r];
-    __syncthreads();
-    if (SUBS > 1 && sub == 0) {
-        for (int w = 1; w < SUBS; ++w)
-#pragma unroll
-            for (int r = 0; r < R; ++r) top.offer(lists[wave + w][64 * r + lane], k, 0, lane);
-#pragma unroll
-        for (int r = 0; r < R; ++r) lists[wave][64 * r + lane] = top.v[r];
+// What a row's SUBS waves have, joined by all of them: a sum, or the smallest,
+// of a value that is the same in a wave's lanes. `slot` is LDS for 2 x 16
+// values, used in turn, so that one barrier lies between a value's writes and
+// the next but one's. All waves of the block call it.
+template <int SUBS>
+struct RowJoin {
+    int (*slot)[16];
+    int wave, first, turn;
+    __device__ __forceinline__ void put(int v) {
+        if constexpr (SUBS > 1) {
+            if ((threadIdx.x & 63) == 0) slot[turn][wave] = v;
+            __syncthreads();
+        }
     }
-    if (SUBS > 1) __syncthreads();
+    __device__ __forceinline__ int sum(int v) {
+        if constexpr (SUBS == 1) return v;
+        put(v);
+        int s = 0;
+#pragma unroll
+        for (int w = 0; w < SUBS; ++w) s += slot[turn][first + w];
+        turn ^= 1;
+        return __builtin_amdgcn_readfirstlane(s);
+    }
+    __device__ __forceinline__ float smallest(float v) {
+        if constexpr (SUBS == 1) return v;
+        put(__builtin_bit_cast(int, v));
+        float s = INFINITY;
+#pragma unroll
+        for (int w = 0; w < SUBS; ++w) s = fminf(s, __builtin_bit_cast(float, slot[turn][first + w]));
+        turn ^= 1;
+        return s;
+    }
+};
+
+__device__ __forceinline__ float value_of(uint32_t order) { return key_value((uint64_t)order << 32); }
+
+// An order v >= least (which at least k of a row's values reach) that at least
+// k, and at most `most`, of its values reach; or, where equal values leave no
+// such one, the k-th largest value's. n: how many reach it. By halving between
+// low (about the smallest value that is a number) and high (the largest), as
+// floats first, where values lie close together, then as orders.
+// reach(c): the wave's number of values with an order of at least c.
+template <int SUBS, class F>
+__device__ __forceinline__ uint32_t reached_by(int k, int most, uint32_t least, float low, float high, RowJoin<SUBS>& join,
+                                               int& n, F reach) {
+    uint32_t lo = least, hi = order_of(high) + 1;  // k values reach lo, fewer reach hi
+    n = 0;
+    bool done = false;
+    for (int round = 0;; ++round) {
+        uint32_t c = order_of(0.5f * low + 0.5f * high);
+        if (round >= 8 || c <= lo || c >= hi) c = lo + (hi - lo) / 2;
+        const int here = join.sum(done ? 0 : reach(c));
+        if (!done) {
+            if (here >= k)
+                lo = c, n = here, low = value_of(c);
+            else
+                hi = c, high = value_of(c);
+            done = (n >= k && n <= most) || hi - lo <= 1;
+        }
+        // (rows of a block end together)
+        if (SUBS == 1 ? done : SUBS == 16 ? done : __syncthreads_and(done)) break;
+    }
+    return lo;
 }
 
-// SUBS waves to a row. R = 0: no alternatives.
-template <int SUBS, int R>
-__global__ __launch_bounds__(64 * kFinishWaves) void logprob_finish_kernel(RowLogits in, LogprobOut out) {
-    __shared__ Stats stats[kFinishWaves];
+// SUBS waves to a row, 16 / SUBS rows to a block. TOP: the largest as well, in
+// four steps: a value that k blocks' maxima or a few more reach, by halving;
+// those blocks (of equal maxima the first ones); their columns' values that
+// reach it, into LDS; the place of each by counting those in front of it. Where
+// more than kCandidates reach it, what k of the first kCandidates reach takes
+// its place; if that is no more (equal values), one wave keeps a sorted list
+// instead.
+constexpr int kCandidates = 256, kMostBlocks = kMaxTop * 3 / 2;
+constexpr int64_t kMaximaBytes = 56 << 10;
+template <int SUBS, bool TOP>
+__global__ __launch_bounds__(kFinishThreads) void logprob_finish_kernel(RowLogits in, LogprobOut out, int in_lds) {
+    constexpr int ROWS = 16 / SUBS;
+    __shared__ Stats stats[64][ROWS + 1];
+    extern __shared__ float maxima[];  // ROWS x parts, where they fit
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int sub = wave % SUBS, first = wave - sub;
-    const int64_t m_ = (int64_t)blockIdx.x * (kFinishWaves / SUBS) + wave / SUBS;
-    const bool there = m_ < in.M;
-    const int64_t m = there ? m_ : in.M - 1;  // (waves past the last row do its work again and store nothing)
+    const int sub = wave % SUBS, first = wave - sub, row = wave / SUBS;
+    const int64_t m0 = (int64_t)blockIdx.x * ROWS;
+    const bool there = m0 + row < in.M;
+    const int64_t m = there ? m0 + row : in.M - 1;  // (waves past the last row do its work again and store nothing)
 
-    Stats a = row_stats(in, m, sub, SUBS, lane);
-    if (SUBS > 1) {
-        if (lane == 0) stats[wave] = a;
-        __syncthreads();
-        a = stats[first];
-        for (int w = 1; w < SUBS; ++w) join_stats(a, stats[first + w], in.inv_t);
-    }
+    block_stats<ROWS>(in, m0, stats, TOP && in_lds ? maxima : nullptr);
+    const Stats a = stats[0][row];
     const float ref = finite_ref(a.mx), log_sum = logf(a.sum);
     if (there && sub == 0 && lane == 0) {
         out.lse[m] = ref * in.inv_t + log_sum;
@@ -205,61 +299,151 @@ __global__ __launch_bounds__(64 * kFinishWaves) void logprob_finish_kernel(RowLo
                                                  : (out.tlogit[m] - ref) * in.inv_t - log_sum;
         }
     }
-    if constexpr (R > 0) {
-        __shared__ uint64_t lists[kFinishWaves][64 * R];
-        const int k = out.k;
-        TopList<R> top;
-        top.clear();
-        // (loops of as many rounds in every wave; nothing beyond the end)
-        for (int p0 = 0; p0 < in.parts; p0 += 64 * SUBS) {
-            const int p = p0 + sub * 64 + lane;
-            top.offer(p < in.parts ? order_key(in.stat[(int64_t)p * in.M + m], p) : 0, k, 0, lane);
+    if constexpr (TOP) {
+        __shared__ int slots[2][16];
+        __shared__ int taken[16][2];
+        __shared__ uint32_t chosen[ROWS][kMostBlocks];
+        __shared__ uint64_t found[ROWS][kCandidates];
+        __shared__ int found_n[ROWS];
+        RowJoin<SUBS> join{slots, wave, first, 0};
+        const int k = out.k, parts = in.parts;
+        auto maximum = [&](int p) { return order_of(in_lds ? maxima[row * parts + p] : in.stat[(int64_t)p * in.M + m]); };
+
+        // the blocks: a wave's share of them is consecutive
+        const int per = (parts + SUBS - 1) / SUBS, p0 = sub * per, p1 = p0 + per < parts ? p0 + per : parts;
+        const int most = k + k / 2;
+        uint32_t least = 0;
+        int count = parts;  // blocks to be read
+        if (parts > most) {
+            float low = INFINITY;
+            for (int p = p0 + lane; p < p1; p += 64) low = least_number(low, value_of(maximum(p)));
+            low = join.smallest(wave_min(low));
+            least = reached_by<SUBS>(k, most, 0, low, a.mx, join, count, [&](uint32_t c) {
+                int n = 0;
+                for (int p = p0; p < p1; p += 64) n += __popcll(__ballot(p + lane < p1 && maximum(p + lane) >= c));
+                return n;
+            });
+            if (count > most || count < k) count = k;
         }
-        join_lists<SUBS, R>(top, lists, wave, sub, k, lane);
-        // the chosen blocks' columns; k of them have maxima that are no less
-        // than the last one's, so nothing below that is among the k first
-        const uint64_t last = lists[first][k - 1];
-        const uint64_t least = last ? (last >> 32 << 32) - 1 : 0;
-        const int count = k < in.parts ? k : in.parts, total = count * in.width;
-        top.clear();
-        const float* z = in.z + m * in.ld;
-        for (int e0 = 0; e0 < total; e0 += 64 * SUBS) {
-            const int e = e0 + sub * 64 + lane, c = e / in.width;
-            uint64_t key = 0;
-            if (e < total) {
-                const int64_t col = (int64_t)key_index(lists[first][c]) * in.width + e % in.width;
-                if (col < in.N) key = order_key(z[col], (uint32_t)col);
-            }
-            top.offer(key, k, least, lane);
+        // those above it, and of those that are equal the first ones
+        int above = 0, equal = 0;
+        for (int p = p0; p < p1; p += 64) {
+            const uint32_t o = p + lane < p1 ? maximum(p + lane) : 0;
+            above += __popcll(__ballot(p + lane < p1 && o > least));
+            equal += __popcll(__ballot(p + lane < p1 && o == least));
         }
-        join_lists<SUBS, R>(top, lists, wave, sub, k, lane);
-        if (there && sub == 0) {
+        if (lane == 0) taken[wave][0] = above, taken[wave][1] = equal;
+        __syncthreads();
+        int at = 0, equal_at = 0, all_above = 0;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int i = 64 * r + lane;
-                if (i < k) {
-                    const uint64_t key = top.v[r];
-                    out.top_ids[m * k + i] = (int64_t)key_index(key) + in.v0;
-                    out.top_logp[m * k + i] =
-                        a.sum == 0.0f ? -INFINITY : (key_value(key) - ref) * in.inv_t - log_sum;
+        for (int w = 0; w < SUBS; ++w) {
+            all_above += taken[first + w][0];
+            if (w < sub) at += taken[first + w][0], equal_at += taken[first + w][1];
+        }
+        const int room = count - all_above;       // of them with a maximum of `least`
+        at += equal_at < room ? equal_at : room;
+        for (int p = p0; p < p1; p += 64) {
+            const uint32_t o = p + lane < p1 ? maximum(p + lane) : 0;
+            const unsigned long long below = (1ull << lane) - 1, eq = __ballot(p + lane < p1 && o == least);
+            const bool take = p + lane < p1 && (o > least || (o == least && equal_at + __popcll(eq & below) < room));
+            const unsigned long long t = __ballot(take);
+            if (take) chosen[row][at + __popcll(t & below)] = (uint32_t)(p + lane);
+            at += __popcll(t);
+            equal_at += __popcll(eq);
+        }
+        if (sub == 0 && lane == 0) found_n[row] = 0;
+        __syncthreads();
+
+        // their columns, two to a lane, four loads ahead
+        const float* z = in.z + m * in.ld;
+        const int total = count * in.width, shift = 31 - __builtin_clz(in.width);
+        int n;
+        bool sorted = false;
+        for (;;) {
+            for (int e0 = 2 * (sub * 64); e0 < total; e0 += 4 * 128 * SUBS) {
+                float v[4][2];
+                int64_t col[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int e = e0 + u * 128 * SUBS + 2 * lane;
+                    col[u] = e < total ? ((int64_t)chosen[row][e >> shift] << shift) + (e & (in.width - 1)) : in.N;
+                    // (rows are padded to whole vectors)
+                    const float2 w = col[u] < in.N ? *reinterpret_cast<const float2*>(z + col[u]) : float2{0.0f, 0.0f};
+                    v[u][0] = w.x, v[u][1] = w.y;
                 }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t key = order_key(v[u][h], (uint32_t)(col[u] + h));
+                        const bool take = col[u] + h < in.N && (uint32_t)(key >> 32) >= least;
+                        const unsigned long long t = __ballot(take);
+                        if (t == 0) continue;
+                        int base = 0;
+                        if (lane == 0) base = atomicAdd(&found_n[row], (int)__popcll(t));
+                        base = __builtin_amdgcn_readfirstlane(base) + (int)__popcll(t & ((1ull << lane) - 1));
+                        if (take && base < kCandidates) found[row][base] = key;
+                    }
+            }
+            __syncthreads();
+            n = found_n[row];
+            // (all rows of the block go round while one has too many)
+            const bool full = n > kCandidates && !sorted;
+            if (!__syncthreads_or(full)) break;
+            const int have = n < kCandidates ? n : kCandidates;
+            float low = INFINITY;
+            for (int i = sub * 64 + lane; i < have; i += 64 * SUBS) low = least_number(low, key_value(found[row][i]));
+            low = join.smallest(wave_min(low));
+            int reached;
+            const uint32_t v = reached_by<SUBS>(full ? k : 0, most, least, low, a.mx, join, reached, [&](uint32_t c) {
+                int r = 0;
+                for (int i = sub * 64; i < have; i += 64 * SUBS)
+                    r += __popcll(__ballot(i + lane < have && (uint32_t)(found[row][i + lane] >> 32) >= c));
+                return r;
+            });
+            const uint32_t more = full ? v : least;
+            if (full && more == least) sorted = true;  // equal values
+            least = more;
+            __syncthreads();
+            if (sub == 0 && lane == 0) found_n[row] = 0;
+            __syncthreads();
+        }
+        if (n > kCandidates) {
+            if (sub != 0) return;  // (no barrier follows)
+            TopList<kMaxTop / 64> top;
+            top.clear();
+            for (int e0 = 0; e0 < total; e0 += 64) {
+                const int e = e0 + lane;
+                uint64_t key = 0;
+                if (e < total) {
+                    const int64_t c = ((int64_t)chosen[row][e >> shift] << shift) + (e & (in.width - 1));
+                    if (c < in.N) key = order_key(z[c], (uint32_t)c);
+                }
+                top.offer(key, k, 0, lane);
+            }
+#pragma unroll
+            for (int r = 0; r < kMaxTop / 64; ++r)
+                if (there && 64 * r + lane < k) {
+                    out.top_ids[m * k + 64 * r + lane] = (int64_t)key_index(top.v[r]) + in.v0;
+                    out.top_logp[m * k + 64 * r + lane] =
+                        a.sum == 0.0f ? -INFINITY : (key_value(top.v[r]) - ref) * in.inv_t - log_sum;
+                }
+            return;
+        }
+        for (int i = sub * 64 + lane; i < n; i += 64 * SUBS) {
+            const uint64_t key = found[row][i];
+            int rank = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) rank += found[row][j] > key;
+            if (there && rank < k) {
+                out.top_ids[m * k + rank] = (int64_t)key_index(key) + in.v0;
+                out.top_logp[m * k + rank] = a.sum == 0.0f ? -INFINITY : (key_value(key) - ref) * in.inv_t - log_sum;
             }
         }
     }
 }
 
 // ------------------------------------------------- a teacher's tokens
-
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
-}
 
 constexpr int kPer = kMaxTop / 64;  // listed tokens to a lane: 64 r + lane
 
@@ -292,13 +476,17 @@ __device__ __forceinline__ bool teacher_row(const Listed& t, float inv_t, int64_
     return any;
 }
 
-// One wave to a row.
-__global__ __launch_bounds__(256) void distill_finish_kernel(RowLogits in, Listed t, float* __restrict__ lse,
-                                                             float* __restrict__ slogits, float* __restrict__ loss) {
-    const int lane = threadIdx.x & 63;
-    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (m >= in.M) return;  // the whole wave
-    const Stats a = row_stats(in, m, 0, 1, lane);
+// ROWS rows to a block; their teachers' tokens, a wave to a row.
+template <int ROWS>
+__global__ __launch_bounds__(kFinishThreads) void distill_finish_kernel(RowLogits in, Listed t, float* __restrict__ lse,
+                                                                        float* __restrict__ slogits,
+                                                                        float* __restrict__ loss) {
+    __shared__ Stats stats[64][ROWS + 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    block_stats<ROWS>(in, (int64_t)blockIdx.x * ROWS, stats, nullptr);
+    const int64_t m = (int64_t)blockIdx.x * ROWS + wave;
+    if (wave >= ROWS || m >= in.M) return;  // the whole wave
+    const Stats a = stats[0][wave];
     const float l = finite_ref(a.mx) * in.inv_t + logf(a.sum);
     int64_t id[kPer];
     float p[kPer], logp[kPer];
@@ -322,23 +510,31 @@ __global__ __launch_bounds__(256) void distill_finish_kernel(RowLogits in, Liste
 __global__ __launch_bounds__(256) void listed_prep_kernel(Listed t, const float* __restrict__ grad, float inv_t,
                                                           int64_t M, float* __restrict__ p_out, float* __restrict__ gw,
                                                           int64_t* __restrict__ targets) {
-    const int lane = threadIdx.x & 63;
-    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (m >= M) return;  // the whole wave
+    __shared__ int64_t ids[4][kMaxTop];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m = (int64_t)blockIdx.x * 4 + wave;
+    if (m >= M) return;  // the whole wave, which has its own LDS
     int64_t id[kPer];
     float p[kPer], logp[kPer], total[kPer];
     bool firsts[kPer];
     const bool any = teacher_row(t, inv_t, m, lane, id, p, logp);
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) total[r] = 0.0f, firsts[r] = id[r] >= 0;
-    // tokens that are listed several times count together, at their first place
+    for (int r = 0; r < kPer; ++r) {
+        total[r] = p[r], firsts[r] = id[r] >= 0;
+        ids[wave][64 * r + lane] = id[r];
+    }
+    __builtin_amdgcn_wave_barrier();
+    // tokens that are listed several times count together, in order, at their first place
     for (int i = 0; i < t.n; ++i) {
-        const int src = i & 63;
-        const int64_t other = i < 64 ? __shfl(id[0], src) : __shfl(id[kPer - 1], src);
-        const float q = i < 64 ? __shfl(p[0], src) : __shfl(p[kPer - 1], src);
+        const int64_t other = ids[wave][i];
+        bool again = false;
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) again |= other == id[r] && other >= 0 && i != 64 * r + lane;
+        if (!__ballot(again)) continue;
+        const float q = i < 64 ? __shfl(p[0], i) : __shfl(p[kPer - 1], i - 64);
 #pragma unroll
         for (int r = 0; r < kPer; ++r)
-            if (other == id[r]) {
+            if (other == id[r] && i != 64 * r + lane) {
                 total[r] += q;
                 if (i < 64 * r + lane) firsts[r] = false;
             }
@@ -380,11 +576,13 @@ hipError_t launch_row_logits(const FusedArgs& g, float* planes, int64_t pld, int
 
 template <int SUBS>
 static hipError_t logprob_finish(const RowLogits& r, const LogprobOut& o, hipStream_t s) {
-    const int rows = kFinishWaves / SUBS;
-    const auto fn = o.k == 0    ? logprob_finish_kernel<SUBS, 0>
-                    : o.k <= 64 ? logprob_finish_kernel<SUBS, 1>
-                                : logprob_finish_kernel<SUBS, 2>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)((r.M + rows - 1) / rows)), dim3(64 * kFinishWaves), 0, s, r, o);
+    const int rows = 16 / SUBS;
+    // the maxima of the parts in LDS, unless they are more than it holds beside the rest (44 KB with 16 rows ...)
+    const int64_t bytes = (int64_t)rows * r.parts * 4;
+    const bool in_lds = o.k > 0 && bytes <= kMaximaBytes;
+    const auto fn = o.k > 0 ? logprob_finish_kernel<SUBS, true> : logprob_finish_kernel<SUBS, false>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)((r.M + rows - 1) / rows)), dim3(kFinishThreads), in_lds ? (unsigned)bytes : 0u, s,
+                       r, o, in_lds ? 1 : 0);
     return hipGetLastError();
 }
 
@@ -396,7 +594,9 @@ hipError_t launch_logprob_finish(const RowLogits& r, const LogprobOut& o, hipStr
 hipError_t launch_distill_finish(const RowLogits& r, const Listed& t, float* lse, float* slogits, float* loss,
                                  hipStream_t s) {
     if (t.n < 1 || t.n > kMaxTop) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(distill_finish_kernel, dim3((unsigned)((r.M + 3) / 4)), dim3(256), 0, s, r, t, lse, slogits, loss);
+    const int rows = r.M <= 1024 ? 4 : 16;
+    hipLaunchKernelGGL(rows == 4 ? distill_finish_kernel<4> : distill_finish_kernel<16>,
+                       dim3((unsigned)((r.M + rows - 1) / rows)), dim3(kFinishThreads), 0, s, r, t, lse, slogits, loss);
     return hipGetLastError();
 }
 

@@ -305,6 +305,24 @@ def test_logprob_ties(shape, k):
         within(x, (s * log_n).expand(x.shape), torch.full_like(x, 2.0 ** -19 + (N + 16) * U, dtype=torch.float64), "log N")
 
 
+@pytest.mark.parametrize("shape", [(40, 3000), (1100, 4096), (4200, 4000), (9, 40000)])
+@pytest.mark.parametrize("k", [5, 64, 128])
+def test_logprob_of_sorted_rows(shape, k):
+    """Rising, falling and interleaved rows of different values, and steps: what comes first is not what counts."""
+    M, N = shape
+    i = torch.arange(N, device="cuda")
+    orders = torch.stack([i, N - 1 - i, (i * 7919) % N, i // 150, (N - 1 - i) // 150, i % 2 * 1000 + i // 300])
+    W = torch.cat([orders // 128, orders % 128]).to(torch.bfloat16)  # exact: under 256 each
+    X = torch.zeros((M, 12), dtype=torch.bfloat16, device="cuda")
+    r = torch.arange(M, device="cuda")
+    X[r, r % 6], X[r, 6 + r % 6] = 1.0, 2.0 ** -7
+    if N > 32768:
+        W[:6] = W[:6] * (W[:6] < 256)  # (bf16 holds these, but no more digits)
+    t = r % N
+    for wo in (ROW, COL):
+        check_logprob(X, stored(W, wo), W, wo, t, 0, 1.0, k, what=f"{shape} {wo} {k}")
+
+
 def test_logprob_of_rows_that_are_not_finite():
     """NaN and infinities: their own rows alone, and indices that are columns."""
     for M, K, N in ((6, 16, 300), (2600, 72, 2600), (600, 16, 1000)):
