@@ -25,7 +25,8 @@ SOURCES = ["gemm_w4_ring256.hip", "gemm_w4_ring192.hip", "gemm_w4_ring256b.hip",
            "fused_ring_act_linear.hip", "fused_ring_dact_linear.hip", "fused_ring_act_sigmoid.hip", "fused_ring_dact_sigmoid.hip",
            "fused_ring_act_normal.hip", "fused_ring_dact_normal.hip", "fused_ring_store.hip", "fused_ring_store_f32.hip",
            "fused_ring_grouped.hip", "fused_ring_grouped_f32.hip", "fused_ring_stats.hip", "fused_ring_dlogit.hip",
-           "fused_ring_logits.hip", "fused_ring_logits_kept.hip",
+           "fused_ring_logits.hip", "fused_ring_logits_kept.hip", "fused_ring_glu_linear.hip", "fused_ring_glu_sigmoid.hip",
+           "fused_ring_glu_normal.hip", "fused_ring_dglu_linear.hip", "fused_ring_dglu_sigmoid.hip", "fused_ring_dglu_normal.hip",
            "fused_gemm_dma.hip", "fused_gemm_any.hip",
            "fused_gemm.hip", "fused_skinny.hip", "fused_aux.hip", "fused_glu.hip", "fused_vocab.hip", "fused_api.hip",
            "fused_lm_api.hip"]

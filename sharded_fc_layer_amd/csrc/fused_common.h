@@ -112,6 +112,37 @@ __device__ __forceinline__ float act_slope(const ActParams& a, float z) {
     }
 }
 
+// Both at once, from one exponential and one reciprocal. Past +-64 the value is
+// z or, within e^-59, 0.
+template <int KIND>
+__device__ __forceinline__ void act_value_slope(const ActParams& a, float z, float& v, float& s) {
+    if constexpr (KIND == kLinear) {
+        v = act_value<KIND>(a, z);
+        s = act_slope<KIND>(a, z);
+        return;
+    }
+    const float zc = clamp64(z);
+    float c;
+    if constexpr (KIND == kNormal) {
+        float e;
+        c = normal_cdf(zc, e);
+        s = c + zc * 0.3989422804014327f * e;
+    } else {
+        const float z2 = zc * zc;
+        c = act_sigma(a, zc, z2);
+        const float t = zc * c;
+        s = c + (t - t * c) * (a.c1 + a.c3x3 * z2);
+    }
+    v = z == zc ? z * c : __builtin_elementwise_maximum(z, 0.0f);  // a NaN stays one
+}
+
+// Gated products (EPI_GLU): a tile of B's columns holds the gate's and the up
+// projection's for the same outputs, 16 and 16 in turn, so that both meet in
+// one wave's accumulators. Column i of the tile is column pair_column(i) of
+// its half of the outputs, and pair_up(i) says which of the two.
+__host__ __device__ constexpr int pair_column(int i) { return (i >> 5) * 16 + (i & 15); }
+__host__ __device__ constexpr bool pair_up(int i) { return (i & 16) != 0; }
+
 // One logit's share of its row's statistics: e = exp((z - ref) / T), and e (z -
 // ref) / T, where a distance past 1e4 below (-inf too) counts as 1e4: e is 0.
 __device__ __forceinline__ void add_exp(float z, float ref, float inv_t, float& sum, float& mean) {
@@ -331,6 +362,7 @@ __device__ __forceinline__ TilePos tile_position(const FusedArgs& g) {
         return t;
     } else {
         TilePos t{};
+        // (BN: output columns, of a gated product half the tile's)
         const BlockTile b = map_block<BM, BN>(g);
         t.slice = b.slice, t.m0 = b.m0, t.n0 = b.n0;
         t.tm = (int)(b.m0 / BM), t.tn = (int)(b.n0 / BN);

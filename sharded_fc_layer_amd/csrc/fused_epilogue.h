@@ -89,6 +89,7 @@ struct Epilogue {
     int64_t n;      // the lane's first column
     int left;       // its columns inside the output, up to 8
     float bias[8], cs[8];
+    float cs_up[8];  // EPI_DGLU: of the up half
     float scale;    // EPI_DLOGIT: weight_scale; EPI_STORE: the factor of the results
 
     __device__ __forceinline__ Epilogue(const FusedArgs& g_, const TilePos& t_, int64_t n0, int lane_) : g(g_), t(t_) {
@@ -98,7 +99,7 @@ struct Epilogue {
         u16x8 b{0, 0, 0, 0, 0, 0, 0, 0};
         if (MODE == EPI_ACT && g.bias) b = load8(g.bias + n, left);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) bias[q] = bf16_f32(b[q]), cs[q] = 0.0f;
+        for (int q = 0; q < 8; ++q) bias[q] = bf16_f32(b[q]), cs[q] = cs_up[q] = 0.0f;
         scale = 1.0f;
         if constexpr (MODE == EPI_DLOGIT) scale = weight_scale(g);
         if constexpr (MODE == EPI_STORE) scale = g.wscale ? *g.wscale : 1.0f;
@@ -106,7 +107,7 @@ struct Epilogue {
 
     // Inputs of one row: 8 values of Z or R, or the row's target, weight and lse.
     struct Row {
-        u16x8 aux;
+        u16x8 aux, aux_up;
         int64_t target;
         float lse, w;
     };
@@ -114,11 +115,29 @@ struct Epilogue {
         const bool there = m < t.M;
         if constexpr (MODE == EPI_DACT) r.aux = load8(g.Z + m * g.ldc + n, there ? left : 0);
         if constexpr (MODE == EPI_ACT) r.aux = load8(g.R + m * g.ldc + n, there && g.R ? left : 0);
+        if constexpr (MODE == EPI_DGLU) {
+            r.aux = load8(g.Z + m * 2 * g.N + n, there ? left : 0);
+            r.aux_up = load8(g.Z + m * 2 * g.N + g.N + n, there ? left : 0);
+        }
         // (a row past the end takes the last one's: nothing of it is stored)
         const int64_t mc = there ? m : t.M - 1;
         if constexpr (MODE == EPI_STATS || MODE == EPI_DLOGIT) r.target = g.targets[mc];
         if constexpr (MODE == EPI_LOGITS) r.target = g.targets ? g.targets[mc] : -1;
         if constexpr (MODE == EPI_DLOGIT) r.lse = g.lse[mc], r.w = g.gw[mc];
+    }
+
+    // v: the gradient of the layer's output in, of the gate out
+    template <int KIND>
+    static __device__ __forceinline__ void glu_row(const ActParams& a, const Row& in, f32x8& v, f32x8& du, f32x8& y) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float up = bf16_f32(in.aux_up[q]), d = v[q];
+            float value, slope;
+            act_value_slope<KIND>(a, bf16_f32(in.aux[q]), value, slope);
+            y[q] = value * up;
+            v[q] = d * up * slope;
+            du[q] = d * value;
+        }
     }
 
     __device__ __forceinline__ void row(int64_t m, f32x8 v, const Row& in, int64_t c0, int part, int parts) {
@@ -182,6 +201,22 @@ struct Epilogue {
                 st[step] = sum;
                 st[2 * step] = mean;
             }
+            return;
+        }
+        if constexpr (MODE == EPI_DGLU) {
+            f32x8 y, du;
+            const ActParams a = act_params(g.act);
+            switch (act_kind(g.act)) {
+                case kNormal: glu_row<kNormal>(a, in, v, du, y); break;
+                case kSigmoid: glu_row<kSigmoid>(a, in, v, du, y); break;
+                default: glu_row<kLinear>(a, in, v, du, y);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) cs[q] += there ? v[q] : 0.0f, cs_up[q] += there ? du[q] : 0.0f;
+            uint16_t* d = static_cast<uint16_t*>(g.C) + m * 2 * g.N + n;
+            store8(d, cols, v);
+            store8(d + g.N, cols, du);
+            if (g.Y) store8(g.Y + m * g.N + n, cols, y);
             return;
         }
         const int64_t at = c0 + (t.row0 + m) * g.ldc + n;
@@ -260,10 +295,22 @@ struct Epilogue {
         }
     }
 
-    // after all rows: the column sums of this wave's rows, partial row `at`; weight_scale once
+    // after all rows: the column sums of this wave's rows, partial row `at` (EPI_DGLU: 2 N wide); weight_scale once
     __device__ __forceinline__ void finish(int64_t at) {
         if constexpr (MODE == EPI_DLOGIT) {
             if (blockIdx.x == 0 && threadIdx.x == 0) *g.wscale = scale;
+        }
+        if constexpr (MODE == EPI_DGLU) {
+            if (!g.colpart) return;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+#pragma unroll
+                for (int d = kLanes; d < 64; d <<= 1) cs[q] += __shfl_xor(cs[q], d), cs_up[q] += __shfl_xor(cs_up[q], d);
+                if (rq == 0 && q < left) {
+                    g.colpart[at * 2 * g.N + n + q] = cs[q];
+                    g.colpart[at * 2 * g.N + g.N + n + q] = cs_up[q];
+                }
+            }
         }
         if constexpr (MODE == EPI_DACT) {
             if (!g.colpart) return;
@@ -275,6 +322,56 @@ struct Epilogue {
             }
         }
     }
+};
+
+// EPI_GLU: a wave's COLS staged columns are the gate and the up projection of
+// COLS / 2 outputs, 16 and 16 in turn (pair_column). A lane takes 8 outputs.
+template <int COLS>
+struct GluEpilogue {
+    static constexpr int kLanes = COLS / 16, kRows = 64 / kLanes;
+    const FusedArgs& g;
+    const TilePos& t;
+    int lane, rq, ch;
+    int64_t n;
+    int left;
+    u16x8 bg, bu;
+
+    __device__ __forceinline__ GluEpilogue(const FusedArgs& g_, const TilePos& t_, int64_t n0, int lane_) : g(g_), t(t_) {
+        lane = lane_, rq = lane / kLanes, ch = lane % kLanes;
+        n = n0 + 8 * ch;
+        left = n >= g.N ? 0 : g.N - n < 8 ? (int)(g.N - n) : 8;
+        bg = load8(g.bias + n, g.bias ? left : 0);
+        bu = load8(g.bias + g.N + n, g.bias ? left : 0);
+    }
+    template <int UN>
+    __device__ __forceinline__ void walk(const char* stage, int64_t m0, int rows, int64_t, int, int) const {
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += kRows) {
+            const int r = r0 + rq;
+            const int64_t m = m0 + r;
+            const int cols = m < t.M ? left : 0, c = (ch >> 1) * 8 + (ch & 1) * 2;
+            const f32x4* pg = reinterpret_cast<const f32x4*>(stage + stage_offset<COLS>(r, c));
+            const f32x4* pu = reinterpret_cast<const f32x4*>(stage + stage_offset<COLS>(r, c + 4));
+            f32x8 gate, up;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                gate[q] = pg[0][q] + bf16_f32(bg[q]), gate[4 + q] = pg[1][q] + bf16_f32(bg[4 + q]);
+                up[q] = pu[0][q] + bf16_f32(bu[q]), up[4 + q] = pu[1][q] + bf16_f32(bu[4 + q]);
+            }
+            if (g.Z) {
+                store8(g.Z + m * 2 * g.N + n, cols, gate);
+                store8(g.Z + m * 2 * g.N + g.N + n, cols, up);
+            }
+            act_values(g.act, gate);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) gate[q] *= up[q];
+            if (g.out_f32)
+                store8(static_cast<float*>(g.C) + m * g.ldc + n, cols, gate, false);
+            else
+                store8(static_cast<uint16_t*>(g.C) + m * g.ldc + n, cols, gate);
+        }
+    }
+    __device__ __forceinline__ void finish(int64_t) const {}
 };
 
 template <GroupMode GRP>

@@ -29,8 +29,11 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
     if (tile < 0 || tile >= kNumFusedTiles) return hipErrorInvalidValue;
     // (this one form would spill in its main loop)
     if (tile == kRingTile && mode == EPI_ACT && a_oc && b_oc && !g.vec_out) tile = 0;
+    const bool pairs = mode == EPI_GLU;
+    // (outputs whose rows do not start on 16 bytes)
+    if (tile == kRingTile && (pairs || mode == EPI_DGLU) && !g.vec_out) tile = 0;
     const FusedTile& t = kFusedTiles[tile];
-    const int64_t nbn = (g.N + t.bn - 1) / t.bn;
+    const int64_t bn = pairs ? t.bn / 2 : t.bn, nbn = (g.N + bn - 1) / bn;
     // ragged rows: every group may end with one partly filled tile
     const int64_t nbm = grp == GRP_ROWS ? g.T / t.bm + std::min<int64_t>(g.E, g.T) : (g.M + t.bm - 1) / t.bm;
     const int64_t blocks = nbm * nbn * (grp == GRP_RED ? g.E : g.splits);
@@ -54,6 +57,14 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
             fn = kind == kNormal    ? fused_ring<EPI_DACT, kNormal>(head, vec, a_oc, b_oc)
                  : kind == kSigmoid ? fused_ring<EPI_DACT, kSigmoid>(head, vec, a_oc, b_oc)
                                     : fused_ring<EPI_DACT, kLinear>(head, vec, a_oc, b_oc);
+        else if (mode == EPI_GLU)
+            fn = kind == kNormal    ? fused_ring<EPI_GLU, kNormal>(head, true, a_oc, b_oc)
+                 : kind == kSigmoid ? fused_ring<EPI_GLU, kSigmoid>(head, true, a_oc, b_oc)
+                                    : fused_ring<EPI_GLU, kLinear>(head, true, a_oc, b_oc);
+        else if (mode == EPI_DGLU)
+            fn = kind == kNormal    ? fused_ring<EPI_DGLU, kNormal>(head, true, a_oc, b_oc)
+                 : kind == kSigmoid ? fused_ring<EPI_DGLU, kSigmoid>(head, true, a_oc, b_oc)
+                                    : fused_ring<EPI_DGLU, kLinear>(head, true, a_oc, b_oc);
         else if (mode == EPI_LOGITS)
             fn = g.C ? fused_ring<EPI_LOGITS, 1>(head, true, a_oc, b_oc) : fused_ring<EPI_LOGITS, 0>(head, true, a_oc, b_oc);
         else
@@ -65,7 +76,8 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
     }
     // storage rows and columns of each operand, the last group's where there are several
     const int64_t ar = grp == GRP_NONE ? (a_oc ? g.K : g.M) : g.T, ac = grp == GRP_ROWS ? g.K : a_oc ? g.M : g.K;
-    const int64_t br = grp == GRP_RED ? g.T : b_oc ? g.K : g.N, bc = b_oc ? g.N : g.K;
+    const int64_t bcols = pairs ? 2 * g.N : g.N;
+    const int64_t br = grp == GRP_RED ? g.T : b_oc ? g.K : bcols, bc = b_oc ? bcols : g.K;
     g.a_end = g.A + (ar - 1) * g.lda + ac;
     g.b_end = g.B + (grp == GRP_ROWS ? (g.E - 1) * g.b_stride : 0) + (br - 1) * g.ldb + bc;
     // (few rows against a long, wide W whose rows are the reduction, a block to
@@ -73,6 +85,7 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
     // of 520, 1000, 2000: 11.4, 19.9, 34.6 us straight into LDS, 12.4, 18.2,
     // 26.5 through registers; with more blocks 62 against 75)
     const bool any = g.lda % 8 != 0 || g.ldb % 8 != 0 || (uintptr_t)g.A % 16 != 0 || (uintptr_t)g.B % 16 != 0 ||
+                     (pairs && b_oc && g.N % 8 != 0) ||
                      (tile != 0 && b_oc && blocks <= 256 && g.k_split >= 768);
     if ((tile != 0 && a_oc) || (grp == GRP_RED && !(a_oc && b_oc)) || (grp == GRP_ROWS && a_oc)) return hipErrorInvalidValue;
     const FusedFn fn = any ? fused_kernel<true>(mode, grp, tile, a_oc, b_oc) : fused_kernel<false>(mode, grp, tile, a_oc, b_oc);

@@ -56,6 +56,25 @@ struct StageLoads {
         }
     }
 
+    // a tile of column pairs (pair_column), the up projection's `up` elements further
+    __device__ __forceinline__ void init_pairs(int wave, int lane, int64_t ld, int64_t rows, int64_t up) {
+#pragma unroll
+        for (int j = 0; j < kInstr; ++j) {
+            if (!OC) {
+                const int i = slot(wave, j) * 16 + (lane >> 2), r = pair_column(i);
+                const int c = (lane & 3) ^ ((lane >> 4) & 3);
+                kk[j] = 8 * c;
+                base[j] = r < rows ? (uint32_t)((r * ld + (pair_up(i) ? up : 0) + 8 * c) * 2) : kOOB;
+            } else {
+                constexpr int CPR = R / 8, RPI = 64 / CPR;
+                const int k = slot(wave, j) * RPI + lane / CPR;
+                const int i = 8 * ((lane % CPR) ^ oc_swizzle(k)), r = pair_column(i);
+                kk[j] = k;
+                base[j] = r < rows ? (uint32_t)((k * ld + r + (pair_up(i) ? up : 0)) * 2) : kOOB;
+            }
+        }
+    }
+
     // `p`: the tile's first row at the stage's first reduction value; `left`:
     // reduction values from there to the end (none: every chunk reads zeros,
     // and nothing is read at p)
@@ -100,6 +119,23 @@ struct AnyLoads {
                 const int c = 8 * ((lane % CPR) ^ oc_swizzle(kk[j]));
                 n[j] = c >= rows ? 0 : rows - c < 8 ? (int)(rows - c) : 8;
                 at[j] = (uint32_t)(kk[j] * ld + (c < rows ? c : 0));
+            }
+        }
+    }
+    __device__ __forceinline__ void init_pairs(int wave, int lane, int64_t ld, int64_t rows, int64_t up) {
+#pragma unroll
+        for (int j = 0; j < kInstr; ++j) {
+            if (!OC) {
+                const int i = Places::slot(wave, j) * 16 + (lane >> 2), r = pair_column(i);
+                kk[j] = 8 * ((lane & 3) ^ ((lane >> 4) & 3));
+                n[j] = r < rows;
+                at[j] = (uint32_t)((r < rows ? r : rows - 1) * ld + (pair_up(i) ? up : 0) + kk[j]);
+            } else {
+                constexpr int CPR = R / 8, RPI = 64 / CPR;
+                kk[j] = Places::slot(wave, j) * RPI + lane / CPR;
+                const int i = 8 * ((lane % CPR) ^ oc_swizzle(kk[j])), r = pair_column(i);
+                n[j] = r >= rows ? 0 : rows - r < 8 ? (int)(rows - r) : 8;
+                at[j] = (uint32_t)(kk[j] * ld + (r < rows ? r : 0) + (pair_up(i) ? up : 0));
             }
         }
     }
@@ -150,7 +186,8 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
     const int wave_m = wave / WC, wave_n = wave % WC;
     const int wm0 = wave_m * WTM, wn0 = wave_n * WTN;
 
-    const TilePos t = tile_position<BM, BN, GRP>(g);
+    constexpr bool kPairs = MODE == EPI_GLU;
+    const TilePos t = tile_position<BM, kPairs ? BN / 2 : BN, GRP>(g);
     if (!t.any) return;  // the whole block: no wave waits for another yet
     const int nkt = (int)((t.kend - t.kbeg + kBK - 1) / kBK);
 
@@ -163,7 +200,10 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
     std::conditional_t<ANY, AnyLoads<BM, A_OC, Q>, LoadA> da;
     std::conditional_t<ANY, AnyLoads<BN, B_OC, Q>, LoadB> db;
     da.init(wave, lane, g.lda, t.M - t.m0);
-    db.init(wave, lane, g.ldb, g.N - t.n0);
+    if constexpr (kPairs)
+        db.init_pairs(wave, lane, g.ldb, g.N - t.n0, B_OC ? g.N : g.N * g.ldb);
+    else
+        db.init(wave, lane, g.ldb, g.N - t.n0);
 
     f32x16 acc[TM][TN];
 #pragma unroll
@@ -290,8 +330,9 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) stage_block<32, WTN>(stage, 32 * i, 32 * j, lane, acc[i][j]);
-    Epilogue<MODE, WTN> e(g, t, t.n0 + wn0, lane);
-    constexpr int kStep = 64 / (WTN / 8);  // rows per access
+    typedef std::conditional_t<kPairs, GluEpilogue<WTN>, Epilogue<MODE, WTN>> E;
+    E e(g, t, t.n0 + (kPairs ? wn0 / 2 : wn0), lane);
+    constexpr int kStep = E::kRows;  // rows per access
     e.template walk<WTM / kStep >= 4 ? 4 : WTM / kStep>(stage, t.m0 + wm0, WTM, output_base<GRP>(g, t), t.tn * WC + wave_n,
                                                         (int)((g.N + BN - 1) / BN) * WC);
     e.finish((int64_t)t.tm * WR + wave_m);

@@ -12,12 +12,22 @@
 namespace fcs {
 namespace {
 
-// v: the gate in, act(gate) out; s: its slope
+// v: the gate in, act(gate) out; s: its slope; one branch on the kind
 __device__ __forceinline__ void act_and_slope(int act, float (&v)[4], float (&s)[4]) {
+    const ActParams a = act_params(act);
+    switch (act_kind(act)) {
+        case kNormal:
 #pragma unroll
-    for (int q = 0; q < 4; ++q) s[q] = v[q];
-    act_slopes(act, s);
-    act_values(act, v);
+            for (int q = 0; q < 4; ++q) act_value_slope<kNormal>(a, v[q], v[q], s[q]);
+            break;
+        case kSigmoid:
+#pragma unroll
+            for (int q = 0; q < 4; ++q) act_value_slope<kSigmoid>(a, v[q], v[q], s[q]);
+            break;
+        default:
+#pragma unroll
+            for (int q = 0; q < 4; ++q) act_value_slope<kLinear>(a, v[q], v[q], s[q]);
+    }
 }
 
 // Sums of 4 columns of each lane over a block's four waves, in order, into `to`

@@ -100,6 +100,12 @@ FCU_DECLARE_RING(EPI_STATS, 0)
 FCU_DECLARE_RING(EPI_DLOGIT, 0)
 FCU_DECLARE_RING(EPI_LOGITS, 0)
 FCU_DECLARE_RING(EPI_LOGITS, 1)
+FCU_DECLARE_RING(EPI_GLU, 0)
+FCU_DECLARE_RING(EPI_GLU, 1)
+FCU_DECLARE_RING(EPI_GLU, 2)
+FCU_DECLARE_RING(EPI_DGLU, 0)
+FCU_DECLARE_RING(EPI_DGLU, 1)
+FCU_DECLARE_RING(EPI_DGLU, 2)
 #undef FCU_DECLARE_RING
 template <>
 FusedFn fused_ring_grouped<0>(GroupMode grp, int head, bool vec, bool b_oc);

@@ -12,24 +12,46 @@ namespace {
 struct GluPlan {
     Operand A, B;
     Shape sh;
+    bool fused;  // the epilogue in the product's kernel, else from planes
     int64_t planes, parts_off, total;
     int parts;  // rows of column-sum partials, 2 N wide
 };
 GluPlan glu_plan(int64_t M, int64_t N, int64_t K, bool b_oc, bool aligned, bool grad) {
     GluPlan p;
     int64_t ws = 0;
-    const int64_t cols = grad ? N : 2 * N, bcols = b_oc ? cols : K;
-    p.sh = shape_of(M, cols, K, false, b_oc, K, bcols, aligned);
-    const bool ring = p.sh.tile == kRingTile;
-    p.A = operand(M, K, aligned, ring, &ws);
-    p.B = operand(b_oc ? K : cols, bcols, aligned, ring, &ws);
+    const int64_t cols = grad ? N : 2 * N, bcols = b_oc ? cols : K, ldb = ring_ld(bcols, aligned);
+    const int64_t limit = (int64_t)1 << 31;
+    // (the two halves of W are read through one descriptor; Z's rows are 2 N wide)
+    const bool near = grad || 2 * (b_oc ? K : cols) * ldb < limit;
+    p.sh = small_shape(M, cols, K, false, !fits(K, aligned) || !fits(bcols, aligned) || (b_oc && !grad && N % 8 != 0), true);
+    p.fused = near && p.sh.splits == 1;
+    if (!near) p.sh.us += planes_us(1, M, cols);
+    // the large tiles: fused where rows of N values are whole vectors, else with planes
+    Shape ring = ring_shape(M, cols, K, false, b_oc, ring_ld(K, aligned), ldb);
+    const bool ring_fused = near && N % 8 == 0 && 512 * 2 * N < limit;
+    const int64_t copies = (fits(K, aligned) ? 0 : M * K * 2) + (fits(bcols, aligned) ? 0 : cols * K * 2);
+    if (copies) ring.us += copy_us(copies);
+    if (!ring_fused) ring.us += planes_us(1, M, cols);
+    if (512 * plane_ld(cols) < limit && ring.us < p.sh.us) p.sh = ring, p.fused = ring_fused;
+    const bool large = p.sh.tile == kRingTile;
+    p.A = operand(M, K, aligned, large, &ws);
+    p.B = operand(b_oc ? K : cols, bcols, aligned, large, &ws);
     p.planes = ws;
-    ws += up((int64_t)p.sh.splits * M * plane_ld(cols) * 4, 256);
+    if (!p.fused) ws += up((int64_t)p.sh.splits * M * plane_ld(cols) * 4, 256);
     p.parts_off = ws;
-    p.parts = grad ? split_epilogue_parts(M) : 0;
-    ws += up((int64_t)p.parts * 2 * N * 4, 256);
+    const FusedTile& t = kFusedTiles[p.sh.tile];
+    p.parts = !grad ? 0 : !p.fused ? split_epilogue_parts(M) : (int)((M + t.bm - 1) / t.bm) * t.wave_rows;
+    // (a launch that falls back from the large tiles to the first ones leaves more rows)
+    const int rows = large && grad && p.fused ? (int)((M + 127) / 128) * 2 : p.parts;
+    ws += up((int64_t)rows * 2 * N * 4, 256);
     p.total = ws;
     return p;
+}
+// The product with its epilogue.
+hipError_t run_glu(EpiMode mode, const GluPlan& pl, bool b_oc, FusedArgs g, int64_t cols, char* base, hipStream_t s) {
+    if (!pl.fused) return run_planes(mode, pl.sh, false, b_oc, g, cols, reinterpret_cast<float*>(base + pl.planes), s);
+    g.k_split = pl.sh.k_split, g.splits = 1, g.c_split_stride = 0;
+    return launch_fused(mode, GRP_NONE, pl.sh.tile, false, b_oc, g, s);
 }
 
 int64_t glu_bwd_bytes(int64_t M, int64_t N) { return up((int64_t)bwd_act_parts(M, N) * 2 * N * 4, 256); }
@@ -147,7 +169,8 @@ fc_status fc_fwd_glu(const void* X, const void* W, fc_order w_order, const void*
     g.act = act;
     g.bias = static_cast<const uint16_t*>(bias);
     g.Z = static_cast<uint16_t*>(Z);
-    return done(run_planes(EPI_GLU, pl.sh, false, b_oc, g, 2 * N, reinterpret_cast<float*>(base + pl.planes), s));
+    g.vec_out = vec_rows(N, Y, nullptr, Z);
+    return done(run_glu(EPI_GLU, pl, b_oc, g, 2 * N, base, s));
 }
 
 int64_t fc_bwd_data_glu_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned) {
@@ -182,8 +205,11 @@ fc_status fc_bwd_data_glu(const void* dY, const void* W, fc_order w_order, const
     g.Z = static_cast<uint16_t*>(const_cast<void*>(Z));  // read only
     g.Y = static_cast<uint16_t*>(H);
     g.colpart = db ? reinterpret_cast<float*>(base + pl.parts_off) : nullptr;
-    e = run_planes(EPI_DGLU, pl.sh, false, b_oc, g, K, reinterpret_cast<float*>(base + pl.planes), s);
-    if (e == hipSuccess && db) e = launch_colsum_parts(g.colpart, db, 2 * K, pl.parts, s);
+    g.vec_out = vec_rows(K, dZ, H, Z);
+    // (the large tiles fall back to the first ones where outputs are not aligned: their partial rows)
+    const int parts = pl.fused && pl.sh.tile == kRingTile && !g.vec_out ? (int)((M + 127) / 128) * 2 : pl.parts;
+    e = run_glu(EPI_DGLU, pl, b_oc, g, K, base, s);
+    if (e == hipSuccess && db) e = launch_colsum_parts(g.colpart, db, 2 * K, parts, s);
     return done(e);
 }
 

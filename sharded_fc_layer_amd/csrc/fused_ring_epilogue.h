@@ -416,11 +416,171 @@ __device__ __forceinline__ void ring_logits(const FusedArgs& g, const TilePos& t
     }
 }
 
+// EPI_GLU: blocks 2 p and 2 p + 1 of a wave's accumulators are the gate and
+// the up projection of outputs 16 p .. 16 p + 15 of its 64. Z's values (64 of
+// either half) and Y's are made where the accumulators lie and go through LDS,
+// 16 rows at a time in two buffers of 8 KB, so that stores are whole lines of
+// each half. Rows on 16-byte boundaries, N a multiple of 8; outputs that are
+// not wanted are descriptors of no size.
+template <int KIND>
+__device__ __forceinline__ void ring_glu(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
+                                         const f32x4 (&acc)[8][8], char* stage) {
+    const int lr = lane & 15, lk = lane >> 4;
+    const int64_t n0 = t.n0 + wave_n * 64, m0 = t.m0 + wave_m * 128;
+    const int rows = t.M - m0 > 128 ? 128 : t.M > m0 ? (int)(t.M - m0) : 0;
+    const int cols = g.N - n0 > 64 ? 64 : g.N > n0 ? (int)(g.N - n0) : 0;
+    const bool f32 = g.out_f32 != 0;
+    const uint32_t ldc = (uint32_t)g.ldc, ldz = 2 * (uint32_t)g.N;
+    const __amdgpu_buffer_rsrc_t rz = buffer_at(g.Z ? g.Z + m0 * 2 * g.N + n0 : nullptr);
+    const __amdgpu_buffer_rsrc_t rzu = buffer_at(g.Z ? g.Z + m0 * 2 * g.N + g.N + n0 : nullptr);
+    const __amdgpu_buffer_rsrc_t ry = buffer_at(static_cast<char*>(g.C) + (m0 * g.ldc + n0) * (f32 ? 4 : 2));
+    const ActParams a = act_params(g.act);
+    f32x4 bg[4], bu[4];
+    const __amdgpu_buffer_rsrc_t rb = buffer_at(g.bias ? g.bias + n0 : nullptr);
+    const __amdgpu_buffer_rsrc_t rbu = buffer_at(g.bias ? g.bias + g.N + n0 : nullptr);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int c = 16 * p + 4 * lk;
+        const u16x4 x = __builtin_bit_cast(u16x4, __builtin_amdgcn_raw_buffer_load_b64(rb, c < cols ? 2u * c : kOOB, 0, 0));
+        const u16x4 y = __builtin_bit_cast(u16x4, __builtin_amdgcn_raw_buffer_load_b64(rbu, c < cols ? 2u * c : kOOB, 0, 0));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bg[p][q] = bf16_f32(x[q]), bu[p][q] = bf16_f32(y[q]);
+    }
+    // reading back: Z's 16-byte chunk ch of rows 4 u + rq; Y's (bf16: 8 chunks to a row, fp32: 16)
+    const int rq = lane >> 4, ch = lane & 15;
+    const int yrq = f32 ? lane >> 4 : lane >> 3, ych = f32 ? lane & 15 : lane & 7, ystep = f32 ? 4 : 8;
+    const bool z_in = 8 * (ch & 7) < cols, y_in = (f32 ? 4 : 8) * ych < cols;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        char* zs = stage + (i & 1) * 8192;
+        char* ys = zs + 4096;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const f32x4 gate = acc[i][2 * p] + bg[p], up = acc[i][2 * p + 1] + bu[p];
+            f32x4 y;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] = act_value<KIND>(a, gate[q]) * up[q];
+            const int c = 2 * (16 * p + 4 * lk);  // byte in a half's 128
+            *reinterpret_cast<u32x2*>(zs + lr * 256 + ((((c >> 4)) ^ lr) << 4) + (c & 15)) = pack_bf16(gate);
+            *reinterpret_cast<u32x2*>(zs + lr * 256 + ((((c >> 4) + 8) ^ lr) << 4) + (c & 15)) = pack_bf16(up);
+            // rows of 256 bytes; of a bf16 output's chunks the first 8 are used
+            if (f32)
+                *reinterpret_cast<f32x4*>(ys + lr * 256 + (((4 * p + lk) ^ lr) << 4)) = y;
+            else
+                *reinterpret_cast<u32x2*>(ys + lr * 256 + (((c >> 4) ^ (lr & 7)) << 4) + (c & 15)) = pack_bf16(y);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = 4 * u + rq, row = 16 * i + r;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(zs + r * 256 + ((ch ^ r) << 4));
+            const uint32_t o = row < rows && z_in ? 2 * ((uint32_t)row * ldz + 8 * (ch & 7)) : kOOB;
+            __builtin_amdgcn_raw_buffer_store_b128(v, rz, ch < 8 ? o : kOOB, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(v, rzu, ch < 8 ? kOOB : o, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = ystep * u + yrq, row = 16 * i + r;  // (bf16: two accesses, the others past the group)
+            const u32x4 v = *reinterpret_cast<const u32x4*>(ys + (r & 15) * 256 + ((f32 ? ych ^ (r & 15) : ych ^ (r & 7)) << 4));
+            const uint32_t o = f32 ? 4 * ((uint32_t)row * ldc + 4 * ych) : 2 * ((uint32_t)row * ldc + 8 * ych);
+            __builtin_amdgcn_raw_buffer_store_b128(v, ry, r < 16 && row < rows && y_in ? o : kOOB, 0, 0);
+        }
+        asm volatile("" ::: "memory");  // keeps the groups in this order
+    }
+}
+
+// EPI_DGLU: the schedule of ring_elementwise. A lane takes 8 columns of every
+// fourth row; Z's two halves are loaded DEPTH groups of 16 rows ahead. Rows on
+// 16-byte boundaries, N a multiple of 8. Column sums as there: rows outside
+// are read from a row of zeros, since they may be products with infinities.
+template <int KIND>
+__device__ __forceinline__ void ring_dglu(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
+                                          const f32x4 (&acc)[8][8], char* stage) {
+    const int lr = lane & 15, lk = lane >> 4, rq = lane >> 4, col = (lane & 15) * 8;
+    const int64_t n0 = t.n0 + wave_n * 128, m0 = t.m0 + wave_m * 128, at0 = m0 * 2 * g.N + n0;
+    const int rows = t.M - m0 > 128 ? 128 : t.M > m0 ? (int)(t.M - m0) : 0;
+    const int cols = g.N - n0 > 128 ? 128 : g.N > n0 ? (int)(g.N - n0) : 0;
+    const uint32_t ld = 2 * (uint32_t)g.N, ldy = (uint32_t)g.N;
+    uint16_t* C = static_cast<uint16_t*>(g.C);
+    const __amdgpu_buffer_rsrc_t rdg = buffer_at(C + at0), rdu = buffer_at(C + at0 + g.N);
+    const __amdgpu_buffer_rsrc_t rg = buffer_at(g.Z + at0), ru = buffer_at(g.Z + at0 + g.N);
+    const __amdgpu_buffer_rsrc_t ry = buffer_at(g.Y ? g.Y + m0 * g.N + n0 : nullptr);
+    const ActParams a = act_params(g.act);
+    float csg[8] = {}, csu[8] = {};
+    constexpr int DEPTH = 4;
+    u16x8 ing[DEPTH][4], inu[DEPTH][4];
+    const bool in = col < cols;
+#define FCE_FETCH(I)                                                                                               \
+    _Pragma("unroll") for (int u = 0; u < 4; ++u) {                                                                \
+        const int r_ = 16 * (I) + 4 * u + rq;                                                                      \
+        const uint32_t o_ = r_ < rows && in ? 2 * ((uint32_t)r_ * ld + col) : kOOB;                                \
+        ing[(I) % DEPTH][u] = __builtin_bit_cast(u16x8, __builtin_amdgcn_raw_buffer_load_b128(rg, o_, 0, 0));      \
+        inu[(I) % DEPTH][u] = __builtin_bit_cast(u16x8, __builtin_amdgcn_raw_buffer_load_b128(ru, o_, 0, 0));      \
+    }
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) { FCE_FETCH(i) }
+    char* zeros = stage + 2 * 8192;
+    int there = rows;
+    asm("" : "+v"(there));
+    *reinterpret_cast<u32x2*>(zeros + lane * 8) = u32x2{0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        char* buf = stage + (i & 1) * 8192;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<f32x4*>(buf + lr * 512 + (((4 * j + lk) ^ ((lr & 7) << 1)) << 4)) = acc[i][j];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = 4 * u + rq, row = 16 * i + r;
+            const char* p = (row < there ? buf + r * 512 : zeros) + (((col >> 2) ^ ((r & 7) << 1)) << 4);
+            const f32x4 lo = reinterpret_cast<const f32x4*>(p)[0], hi = reinterpret_cast<const f32x4*>(p)[1];
+            float dg[8], du[8], y[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float d = q < 4 ? lo[q & 3] : hi[q & 3];
+                const float gate = bf16_f32(ing[i % DEPTH][u][q]), up = bf16_f32(inu[i % DEPTH][u][q]);
+                float v, s;
+                act_value_slope<KIND>(a, gate, v, s);
+                y[q] = v * up;
+                dg[q] = d * up * s;
+                du[q] = d * v;
+                csg[q] += dg[q];
+                csu[q] += du[q];
+            }
+            const uint32_t o = row < rows && in ? 2 * ((uint32_t)row * ld + col) : kOOB;
+            __builtin_amdgcn_raw_buffer_store_b128(pack_bf16(dg), rdg, o, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(pack_bf16(du), rdu, o, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(pack_bf16(y), ry, row < rows && in ? 2 * ((uint32_t)row * ldy + col) : kOOB, 0, 0);
+        }
+        // (the sums stay here: moved into the branch behind the loop, every value
+        // would wait for them, 128 registers spilled)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) asm("" : "+v"(csg[q]), "+v"(csu[q]));
+        if (i + DEPTH < 8) { FCE_FETCH(i + DEPTH) }
+        asm volatile("" ::: "memory");  // keeps the groups in this order
+    }
+#undef FCE_FETCH
+    if (g.colpart) {
+        float* part = g.colpart + ((int64_t)t.tm * 2 + wave_m) * 2 * g.N + n0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            csg[q] += __shfl_xor(csg[q], 16);
+            csu[q] += __shfl_xor(csu[q], 16);
+            csg[q] += __shfl_xor(csg[q], 32);
+            csu[q] += __shfl_xor(csu[q], 32);
+            if (rq == 0 && col + q < cols) part[col + q] = csg[q], part[g.N + col + q] = csu[q];
+        }
+    }
+}
+
 template <EpiMode MODE, GroupMode GRP, int TN, int KIND, bool VEC>
 __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
                                               const f32x4 (&acc)[8][TN], char* stage) {
     if constexpr (MODE == EPI_STATS) {
         ring_stats<TN>(g, t, wave_m, wave_n, lane, acc);
+    } else if constexpr (MODE == EPI_GLU) {
+        ring_glu<KIND>(g, t, wave_m, wave_n, lane, acc, stage);
+    } else if constexpr (MODE == EPI_DGLU) {
+        ring_dglu<KIND>(g, t, wave_m, wave_n, lane, acc, stage);
     } else if constexpr (MODE == EPI_LOGITS) {
         ring_logits<TN, KIND != 0>(g, t, wave_m, wave_n, lane, acc);
     } else if constexpr (MODE == EPI_DLOGIT) {

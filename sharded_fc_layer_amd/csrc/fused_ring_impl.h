@@ -16,7 +16,8 @@
 // matrix or rows) and ends with the last row that the tile may read, so that
 // only one tile's rows, or one group's, have to lie within 2 GiB.
 #define FCR_SETUP                                                                                                   \
-    const TilePos pos = tile_position<256, BN, GRP>(g);                                                             \
+    constexpr int kOut = MODE == EPI_GLU ? BN / 2 : BN; /* output columns */                                        \
+    const TilePos pos = tile_position<256, kOut, GRP>(g);                                                           \
     if (!pos.any) return; /* the whole block */                                                                     \
     W4Setup w;                                                                                                      \
     w.lane = threadIdx.x & 63;                                                                                      \
@@ -27,7 +28,7 @@
     w.kbeg = 0, w.kend = pos.kend - pos.kbeg;                                                                       \
     w.nkt = (int)((w.kend + BKP - 1) / BKP);                                                                        \
     const int64_t a0_ = pos.row0 + pos.m0, rows_ = pos.M - pos.m0 < 256 ? pos.M - pos.m0 : 256;                     \
-    const int64_t cols_ = g.N - pos.n0 < BN ? g.N - pos.n0 : BN;                                                    \
+    const int64_t cols_ = (g.N - pos.n0 < kOut ? g.N - pos.n0 : kOut) + (MODE == EPI_GLU ? g.N : 0);                \
     const uint16_t* pa_ = g.A + (A_OC ? pos.kbeg * g.lda + a0_ : a0_ * g.lda + pos.kbeg);                           \
     const uint16_t* pb_ = g.B + (GRP == GRP_ROWS ? (int64_t)pos.e * g.b_stride : 0) +                               \
                           (B_OC ? pos.kbeg * g.ldb + pos.n0 : pos.n0 * g.ldb + pos.kbeg);                           \
@@ -37,6 +38,11 @@
         (void*)pb_, 0, (int)(2 * (B_OC ? w.kend * g.ldb - pos.n0 : cols_ * g.ldb - pos.kbeg)), kRsrcWord3);
 #define FCR_ROWS (pos.M - pos.m0)
 #define FCR_COLS (g.N - pos.n0)
+#define FCR_INIT_B                                                                                                  \
+    if constexpr (MODE == EPI_GLU)                                                                                  \
+        db.init_pairs(wave, lane, g.ldb, FCR_COLS, B_OC ? g.N : g.N * g.ldb, pair_column, pair_up);                 \
+    else                                                                                                            \
+        db.init(wave, lane, g.ldb, w.n0, FCR_COLS);
 #define FCR_SHORT (GRP == GRP_RED)
 #define FCR_EPILOGUE ring_epilogue<MODE, GRP, TN, KIND, VEC>(g, pos, wave >> 1, wave & 1, lane, acc, stage);
 

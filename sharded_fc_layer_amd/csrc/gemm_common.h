@@ -165,6 +165,33 @@ struct DmaPP {
         }
     }
 
+    // The same for a tile whose column i is column of(i).first of the operand's,
+    // `up` elements further where of(i).second: pairs of 16 columns that lie
+    // apart (16-byte chunks do not cross them). `rows`: columns there are of each.
+    template <class F, class G>
+    __device__ __forceinline__ void init_pairs(int wq, int lane, int64_t ld, int64_t rows, int64_t up, F column,
+                                               G is_up) {
+        const uint32_t ld32 = (uint32_t)ld, nrows = (uint32_t)rows, up32 = (uint32_t)up;
+#pragma unroll
+        for (int j = 0; j < kInstr; ++j) {
+            const uint32_t p = (uint32_t)((wq * kInstr + j) * 64 + lane);
+            if (!OC) {
+                constexpr uint32_t CPR = BKP / 8;
+                const int i = (int)(p / CPR);
+                const uint32_t c = (p % CPR) ^ (uint32_t)rc_swizzle<BKP>(i), r = (uint32_t)column(i);
+                kk[j] = (int)(8 * c);
+                base[j] = r < nrows ? (r * ld32 + (is_up(i) ? up32 : 0) + 8 * c) * 2 : kOOB;
+            } else {
+                constexpr uint32_t CPR = R / 8;
+                const uint32_t k = p / CPR;
+                const int i = (int)(8 * ((p % CPR) ^ (uint32_t)oc_swizzle_r<R>((int)k)));
+                const uint32_t r = (uint32_t)column(i);
+                kk[j] = (int)k;
+                base[j] = r < nrows ? (k * ld32 + r + (is_up(i) ? up32 : 0)) * 2 : kOOB;
+            }
+        }
+    }
+
     __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t rsrc, char* region, int64_t k0, int64_t kend,
                                           int64_t ld, int wq) const {
         const uint32_t step = OC ? (uint32_t)(k0 * ld * 2) : (uint32_t)(k0 * 2);

@@ -16,6 +16,7 @@
 #define FCR_SETUP const W4Setup w = w4_setup<A_OC, B_OC, BKP, BN>(g);
 #define FCR_ROWS g.M
 #define FCR_COLS g.N
+#define FCR_INIT_B db.init(wave, lane, g.ldb, w.n0, FCR_COLS);
 #define FCR_SHORT false
 #define FCR_EPILOGUE                                                              \
     if constexpr (OUT_F32)                                                        \
