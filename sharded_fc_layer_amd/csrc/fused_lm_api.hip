@@ -33,14 +33,18 @@ GluPlan glu_plan(int64_t M, int64_t N, int64_t K, bool b_oc, bool aligned, bool 
     if (copies) ring.us += copy_us(copies);
     if (!ring_fused) ring.us += planes_us(1, M, cols);
     if (512 * plane_ld(cols) < limit && ring.us < p.sh.us) p.sh = ring, p.fused = ring_fused;
+    if (!grad && M <= 32 && !b_oc && skinny_pays(M, N, K)) p.sh = Shape{kSkinny, 1, K, 0}, p.fused = true;
     const bool large = p.sh.tile == kRingTile;
     p.A = operand(M, K, aligned, large, &ws);
     p.B = operand(b_oc ? K : cols, bcols, aligned, large, &ws);
     p.planes = ws;
     if (!p.fused) ws += up((int64_t)p.sh.splits * M * plane_ld(cols) * 4, 256);
     p.parts_off = ws;
-    const FusedTile& t = kFusedTiles[p.sh.tile];
-    p.parts = !grad ? 0 : !p.fused ? split_epilogue_parts(M) : (int)((M + t.bm - 1) / t.bm) * t.wave_rows;
+    p.parts = 0;
+    if (grad) {
+        const FusedTile& t = kFusedTiles[p.sh.tile];
+        p.parts = p.fused ? (int)((M + t.bm - 1) / t.bm) * t.wave_rows : split_epilogue_parts(M);
+    }
     // (a launch that falls back from the large tiles to the first ones leaves more rows)
     const int rows = large && grad && p.fused ? (int)((M + 127) / 128) * 2 : p.parts;
     ws += up((int64_t)rows * 2 * N * 4, 256);
@@ -50,6 +54,7 @@ GluPlan glu_plan(int64_t M, int64_t N, int64_t K, bool b_oc, bool aligned, bool 
 // The product with its epilogue.
 hipError_t run_glu(EpiMode mode, const GluPlan& pl, bool b_oc, FusedArgs g, int64_t cols, char* base, hipStream_t s) {
     if (!pl.fused) return run_planes(mode, pl.sh, false, b_oc, g, cols, reinterpret_cast<float*>(base + pl.planes), s);
+    if (pl.sh.tile == kSkinny) return launch_fused_skinny_glu(g, s);
     g.k_split = pl.sh.k_split, g.splits = 1, g.c_split_stride = 0;
     return launch_fused(mode, GRP_NONE, pl.sh.tile, false, b_oc, g, s);
 }
