@@ -52,6 +52,7 @@ struct FusedArgs : GemmArgs {
     float* stat = nullptr;           // EPI_STATS: [block of columns][M] maxima, then as many sums
     float* tlogit = nullptr;
     float inv_t = 1.0f;              // EPI_DLOGIT, EPI_LOGITS: one over the temperature, a factor of the logits
+    const uint32_t* need = nullptr;  // EPI_LOGITS, ring kernel: bit p % 32 of need[p / 32][row]: the logits of part p are read (none: all)
     uint16_t* Y = nullptr;           // EPI_DGLU: M x N, written, or none
     const int64_t* offsets = nullptr;  // E + 1 values on the device
     int E = 1;
@@ -201,6 +202,9 @@ struct Listed {
     const float* slogits;    // M x n: the student's logits there
     const float* p;          // M x n (launch_listed_prep)
 };
+// need[p / 32][row], a bit for each part of `width` columns (FusedArgs::need): where the listed tokens lie
+hipError_t launch_listed_need(const Listed& t, int64_t M, int64_t N, int64_t v0, int width, int parts, uint32_t* need,
+                              hipStream_t s);
 hipError_t launch_distill_finish(const RowLogits& r, const Listed& t, float* lse, float* slogits, float* loss,
                                  hipStream_t s);
 // For the gradient: p = the listed tokens' probabilities, a token's summed at

@@ -7,6 +7,14 @@ namespace {
 
 // -------------------------------------------------------------- gated
 
+// The few-row kernel against the general one (us, W from memory; from the
+// caches): 2048 -> 8192 one row 16.0 and 19.8 (12.4; 16.2), 16 rows 19.4 and
+// 22.5 (14.9; 17.4), 32 rows 23.1 and 23.0; 4096 -> 14336 one row 49.6 and 55.8
+// (39.3; 35.1), 4 rows 51.9 and 60.6 (40.2; 34.8), 16 rows 60.5 and 57.2.
+bool few_rows_pay(int64_t M, int64_t N, int64_t K) {
+    return N <= (M <= 8 ? 16384 : M <= 16 ? 8192 : 4096) && K >= 256;
+}
+
 // A gated product: the plain one of 2 N columns (forward) or of N (its data
 // gradient, `grad`), whose epilogue reads or writes 2 N columns of Z.
 struct GluPlan {
@@ -33,7 +41,7 @@ GluPlan glu_plan(int64_t M, int64_t N, int64_t K, bool b_oc, bool aligned, bool 
     if (copies) ring.us += copy_us(copies);
     if (!ring_fused) ring.us += planes_us(1, M, cols);
     if (512 * plane_ld(cols) < limit && ring.us < p.sh.us) p.sh = ring, p.fused = ring_fused;
-    if (!grad && M <= 32 && !b_oc && skinny_pays(M, N, K)) p.sh = Shape{kSkinny, 1, K, 0}, p.fused = true;
+    if (!grad && M <= 32 && !b_oc && few_rows_pay(M, N, K)) p.sh = Shape{kSkinny, 1, K, 0}, p.fused = true;
     const bool large = p.sh.tile == kRingTile;
     p.A = operand(M, K, aligned, large, &ws);
     p.B = operand(b_oc ? K : cols, bcols, aligned, large, &ws);
@@ -73,10 +81,11 @@ struct LogitsPlan {
     Shape sh;
     bool keep;     // the logits are stored: they are read again, or a split reduction's planes
     int64_t rows;  // of a chunk: a multiple of 256, or all
-    int64_t z_ld, z_off, stat_off, t_off, total;
+    int64_t z_ld, z_off, stat_off, t_off, need_off, total;
     int parts, width;
+    bool need;     // of listed tokens: which parts are stored
 };
-LogitsPlan logits_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned, bool read_again) {
+LogitsPlan logits_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned, bool read_again, bool listed) {
     LogitsPlan p;
     int64_t ws = 0;
     p.z_ld = plane_ld(N);
@@ -99,6 +108,9 @@ LogitsPlan logits_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned,
     ws += up((int64_t)3 * p.parts * p.rows * 4, 256);
     p.t_off = ws;
     ws += up(p.rows * 4, 256);
+    p.need = listed && ring;
+    p.need_off = ws;
+    if (p.need) ws += up((int64_t)((p.parts + 31) / 32) * p.rows * 4, 256);
     p.total = ws;
     return p;
 }
@@ -111,6 +123,7 @@ struct LogitsCall {
     int64_t v0;
     float inv_t;
     int64_t M, K, N;
+    const Listed* listed;    // of these rows, or none
 };
 hipError_t run_logits(const LogitsPlan& pl, const LogitsCall& c, const uint16_t* x, const uint16_t* w, int64_t m0,
                       int64_t rows, char* base, RowLogits* out, hipStream_t s) {
@@ -127,6 +140,12 @@ hipError_t run_logits(const LogitsPlan& pl, const LogitsCall& c, const uint16_t*
     *out = RowLogits{z, pl.z_ld, g.stat, pl.parts, pl.width, rows, c.N, c.v0, c.inv_t};
     const bool b_oc = c.w_order == FC_ROW_MAJOR;
     if (pl.sh.splits > 1) return run_planes(EPI_LOGITS, pl.sh, false, b_oc, g, c.N, z, s);
+    if (pl.need && c.listed) {
+        uint32_t* need = reinterpret_cast<uint32_t*>(base + pl.need_off);
+        const hipError_t e = launch_listed_need(*c.listed, rows, c.N, c.v0, pl.width, pl.parts, need, s);
+        if (e != hipSuccess) return e;
+        g.need = need;
+    }
     g.C = pl.keep ? z : nullptr;
     g.ldc = pl.z_ld;
     g.k_split = pl.sh.k_split, g.splits = 1, g.c_split_stride = 0;
@@ -247,7 +266,7 @@ fc_status fc_bwd_glu(const void* dY, const void* Z, fc_act act, void* dZ, void* 
 
 int64_t fc_logprob_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int top_k, int aligned) {
     if (bad_sizes(M, K, N) || bad_order(w_order) || top_k < 0 || top_k > kMaxTop || top_k > N) return -1;
-    return logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned != 0, top_k > 0).total;
+    return logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned != 0, top_k > 0, false).total;
 }
 
 fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64_t* targets, int64_t vocab_start,
@@ -261,7 +280,7 @@ fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64
         off(top_logp, 4) || off(top_ids, 8))
         return FC_E_INVALID;
     const bool aligned = !off(X, 16) && !off(W, 16);
-    LogitsPlan pl = logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned, top_k > 0);
+    LogitsPlan pl = logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned, top_k > 0, false);
     if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
     if (overlapping({{logp, M * 4}, {entropy, M * 4}, {lse, M * 4}, {top_k ? top_logp : nullptr, M * top_k * 4},
                      {top_k ? top_ids : nullptr, M * top_k * 8}, {ws, pl.total}},
@@ -275,7 +294,7 @@ fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64
     const uint16_t *x, *w;
     hipError_t e;
     if ((e = place(pl.A, X, &x, pl.B, W, &w, base, s)) != hipSuccess) return done(e);
-    const LogitsCall call{X, W, w_order, targets, vocab_start, 1.0f / temperature, M, K, N};
+    const LogitsCall call{X, W, w_order, targets, vocab_start, 1.0f / temperature, M, K, N, nullptr};
     for (int64_t m0 = 0; m0 < M; m0 += pl.rows) {
         RowLogits r;
         if ((e = run_logits(pl, call, x, w, m0, std::min(pl.rows, M - m0), base, &r, s)) != hipSuccess) return done(e);
@@ -289,7 +308,7 @@ fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64
 
 int64_t fc_distill_fwd_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, int aligned) {
     if (bad_sizes(M, K, N) || bad_order(w_order)) return -1;
-    return logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned != 0, true).total;
+    return logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned != 0, true, true).total;
 }
 
 fc_status fc_distill_fwd(const void* X, const void* W, fc_order w_order, const int64_t* ids, const float* tlogits,
@@ -301,7 +320,7 @@ fc_status fc_distill_fwd(const void* X, const void* W, fc_order w_order, const i
     if (off(X, 2) || off(W, 2) || off(ids, 8) || off(tlogits, 4) || off(lse, 4) || off(slogits, 4) || off(loss, 4))
         return FC_E_INVALID;
     const bool aligned = !off(X, 16) && !off(W, 16);
-    LogitsPlan pl = logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned, true);
+    LogitsPlan pl = logits_plan(M, K, N, w_order == FC_ROW_MAJOR, aligned, true, true);
     if (bad_ws(ws, ws_bytes, pl.total)) return FC_E_INVALID;
     if (overlapping({{lse, M * 4}, {slogits, M * top_n * 4}, {loss, M * 4}, {ws, pl.total}},
                     {{X, M * K * 2}, {W, K * N * 2}, {ids, M * top_n * 8}, {tlogits, M * top_n * 4}}))
@@ -314,11 +333,11 @@ fc_status fc_distill_fwd(const void* X, const void* W, fc_order w_order, const i
     const uint16_t *x, *w;
     hipError_t e;
     if ((e = place(pl.A, X, &x, pl.B, W, &w, base, s)) != hipSuccess) return done(e);
-    const LogitsCall call{X, W, w_order, nullptr, vocab_start, 1.0f / temperature, M, K, N};
     for (int64_t m0 = 0; m0 < M; m0 += pl.rows) {
+        const Listed t{ids + m0 * top_n, tlogits + m0 * top_n, top_n, nullptr, nullptr};
+        const LogitsCall call{X, W, w_order, nullptr, vocab_start, 1.0f / temperature, M, K, N, &t};
         RowLogits r;
         if ((e = run_logits(pl, call, x, w, m0, std::min(pl.rows, M - m0), base, &r, s)) != hipSuccess) return done(e);
-        const Listed t{ids + m0 * top_n, tlogits + m0 * top_n, top_n, nullptr, nullptr};
         if ((e = launch_distill_finish(r, t, lse + m0, slogits + m0 * top_n, loss + m0, s)) != hipSuccess) return done(e);
     }
     return FC_OK;

@@ -19,7 +19,7 @@ namespace {
 
 template <int TM, int WAVES, int HALVES>
 __global__ __launch_bounds__(64 * WAVES) void fused_skinny_kernel(FusedArgs g) {
-    constexpr int U = 4 / HALVES;  // pieces in flight
+    constexpr int U = 4 / HALVES;  // pieces in flight (a gated layer: 4 measured slower, 13.8 us against 12.5)
     __shared__ f32x4 part[WAVES][TM * HALVES][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lk = lane >> 4;

@@ -507,6 +507,30 @@ __global__ __launch_bounds__(kFinishThreads) void distill_finish_kernel(RowLogit
     }
 }
 
+// A wave to a row, 1024 words of it at a time in LDS.
+constexpr int kNeedWords = 1024;
+__global__ __launch_bounds__(256) void listed_need_kernel(Listed t, int64_t M, int64_t N, int64_t v0, int shift, int words,
+                                                          uint32_t* __restrict__ need) {
+    __shared__ uint32_t bits[4][kNeedWords];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m = (int64_t)blockIdx.x * 4 + wave;
+    if (m >= M) return;  // the whole wave, which has its own LDS
+    for (int w0 = 0; w0 < words; w0 += kNeedWords) {
+        const int here = words - w0 < kNeedWords ? words - w0 : kNeedWords;
+        for (int w = lane; w < here; w += 64) bits[wave][w] = 0;
+        __builtin_amdgcn_wave_barrier();
+        for (int i = lane; i < t.n; i += 64) {
+            const int64_t id = t.ids[m * t.n + i];
+            const uint64_t at = (uint64_t)id - (uint64_t)v0;
+            if (id < 0 || at >= (uint64_t)N) continue;
+            const int part = (int)(at >> shift), w = (part >> 5) - w0;
+            if (w >= 0 && w < here) atomicOr(&bits[wave][w], 1u << (part & 31));
+        }
+        __builtin_amdgcn_wave_barrier();
+        for (int w = lane; w < here; w += 64) need[(int64_t)(w0 + w) * M + m] = bits[wave][w];
+    }
+}
+
 __global__ __launch_bounds__(256) void listed_prep_kernel(Listed t, const float* __restrict__ grad, float inv_t,
                                                           int64_t M, float* __restrict__ p_out, float* __restrict__ gw,
                                                           int64_t* __restrict__ targets) {
@@ -597,6 +621,14 @@ hipError_t launch_distill_finish(const RowLogits& r, const Listed& t, float* lse
     const int rows = r.M <= 1024 ? 4 : 16;
     hipLaunchKernelGGL(rows == 4 ? distill_finish_kernel<4> : distill_finish_kernel<16>,
                        dim3((unsigned)((r.M + rows - 1) / rows)), dim3(kFinishThreads), 0, s, r, t, lse, slogits, loss);
+    return hipGetLastError();
+}
+
+hipError_t launch_listed_need(const Listed& t, int64_t M, int64_t N, int64_t v0, int width, int parts, uint32_t* need,
+                              hipStream_t s) {
+    if (t.n < 1 || t.n > kMaxTop || width < 1 || (width & (width - 1))) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(listed_need_kernel, dim3((unsigned)((M + 3) / 4)), dim3(256), 0, s, t, M, N, v0,
+                       31 - __builtin_clz((unsigned)width), (parts + 31) / 32, need);
     return hipGetLastError();
 }
 
