@@ -484,7 +484,7 @@ int64_t fc_bwd_glu_ws_bytes(int64_t M, int64_t N);
  * logits are not finite numbers, NaN ranks with -inf, and top_ids are columns
  * of this call whatever they hold.
  *
- * The workspace holds the logits of some rows at a time, at most 512 MiB of
+ * The workspace holds the logits of some rows at a time, at most 1 GiB of
  * them, or 256 rows where those are more.
  */
 fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64_t* targets, int64_t vocab_start,

@@ -112,8 +112,8 @@ __device__ __forceinline__ float act_slope(const ActParams& a, float z) {
     }
 }
 
-// Both at once, from one exponential and one reciprocal. Past +-64 the value is
-// z or, within e^-59, 0.
+// Both at once, from one exponential and one reciprocal: the slope at z within
+// +-64, the value at z not below -64 (where it is 0 within e^-59).
 template <int KIND>
 __device__ __forceinline__ void act_value_slope(const ActParams& a, float z, float& v, float& s) {
     if constexpr (KIND == kLinear) {
@@ -121,7 +121,7 @@ __device__ __forceinline__ void act_value_slope(const ActParams& a, float z, flo
         s = act_slope<KIND>(a, z);
         return;
     }
-    const float zc = clamp64(z);
+    const float zl = __builtin_elementwise_maximum(z, -64.0f), zc = __builtin_elementwise_minimum(zl, 64.0f);
     float c;
     if constexpr (KIND == kNormal) {
         float e;
@@ -133,7 +133,7 @@ __device__ __forceinline__ void act_value_slope(const ActParams& a, float z, flo
         const float t = zc * c;
         s = c + (t - t * c) * (a.c1 + a.c3x3 * z2);
     }
-    v = z == zc ? z * c : __builtin_elementwise_maximum(z, 0.0f);  // a NaN stays one
+    v = zl * c;
 }
 
 // Gated products (EPI_GLU): a tile of B's columns holds the gate's and the up
@@ -143,13 +143,15 @@ __device__ __forceinline__ void act_value_slope(const ActParams& a, float z, flo
 __host__ __device__ constexpr int pair_column(int i) { return (i >> 5) * 16 + (i & 15); }
 __host__ __device__ constexpr bool pair_up(int i) { return (i & 16) != 0; }
 
-// One logit's share of its row's statistics: e = exp((z - ref) / T), and e (z -
-// ref) / T, where a distance past 1e4 below (-inf too) counts as 1e4: e is 0.
-__device__ __forceinline__ void add_exp(float z, float ref, float inv_t, float& sum, float& mean) {
-    const float d = (z - ref) * inv_t, e = exp_f32(d);
+// One logit's share of its row's statistics: e = exp((z - ref) / T), and e times
+// that distance in powers of two (c = log2(e) / T), where one past 2^14 below
+// (-inf too) counts as 2^14: e is 0.
+__device__ __forceinline__ void add_exp(float z, float ref, float c, float& sum, float& mean) {
+    const float d = (z - ref) * c, e = __builtin_amdgcn_exp2f(d);
     sum += e;
-    mean = __builtin_fmaf(e, fmaxf(d, -1e4f), mean);
+    mean = __builtin_fmaf(e, fmaxf(d, -16384.0f), mean);
 }
+constexpr float kLn2 = 0.6931471805599453f;  // of the mean distance, in the end
 
 // over several values (an array or a vector), with one branch on the kind
 template <class V>

@@ -183,9 +183,10 @@ struct Epilogue {
 #pragma unroll
             for (int d = 1; d < kLanes; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
             const float ref = __builtin_isinf(mx) ? 0.0f : mx;
+            const float c = g.inv_t * kLog2e;
             float sum = 0.0f, mean = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) add_exp(v[q], ref, g.inv_t, sum, mean);
+            for (int q = 0; q < 8; ++q) add_exp(v[q], ref, c, sum, mean);
 #pragma unroll
             for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor(sum, d), mean += __shfl_xor(mean, d);
             const uint64_t hit = (uint64_t)in.target - (uint64_t)g.v0 - (uint64_t)n;
@@ -199,7 +200,7 @@ struct Epilogue {
                 const int64_t step = (int64_t)parts * t.M;
                 st[0] = mx;
                 st[step] = sum;
-                st[2 * step] = mean;
+                st[2 * step] = mean * kLn2;
             }
             return;
         }

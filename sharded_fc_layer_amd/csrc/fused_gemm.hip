@@ -23,6 +23,18 @@ static int head_of(GroupMode grp, int64_t K) {
     return grp != GRP_RED && K % 64 == 0 && (n % 6 == 2 || n % 6 == 4) && n > 6 ? (int)(n % 6) : -1;
 }
 
+// FusedArgs::stagger: half the time in which the memory serves a quarter of a
+// round's epilogues (at 5 TB/s), for the one that moves most, EPI_DGLU with 10
+// bytes a value. Outputs 8192 wide over 2048: 4096 rows (two rounds of tiles)
+// 190 us without, 170 with it, 8192 rows 335 and 322, 16384 rows 669 and 654;
+// over 6144 no difference. All of that time or more of it gains less, and none
+// of the others gains (EPI_LOGITS that stores 8192 x 32000: 948 and 949).
+static int ring_stagger_ticks(EpiMode mode, const FusedArgs& g, int64_t blocks) {
+    if (mode != EPI_DGLU || blocks < 512) return 0;
+    const double bytes = 65536 * (8.0 + (g.Y ? 2.0 : 0.0));  // of a tile's epilogue
+    return (int)(0.5 * bytes * 64 / 5e12 * 1e8);
+}
+
 hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc, const FusedArgs& given,
                         hipStream_t s) {
     FusedArgs g = given;
@@ -71,6 +83,7 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
             fn = mode == EPI_STATS ? fused_ring<EPI_STATS, 0>(head, true, a_oc, b_oc)
                                    : fused_ring<EPI_DLOGIT, 0>(head, true, a_oc, b_oc);
         if (!fn) return hipErrorInvalidValue;
+        g.stagger = ring_stagger_ticks(mode, g, blocks);
         hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, g);
         return hipGetLastError();
     }

@@ -54,6 +54,7 @@ struct FusedArgs : GemmArgs {
     float inv_t = 1.0f;              // EPI_DLOGIT, EPI_LOGITS: one over the temperature, a factor of the logits
     const uint32_t* need = nullptr;  // EPI_LOGITS, ring kernel: bit p % 32 of need[p / 32][row]: the logits of part p are read (none: all)
     uint16_t* Y = nullptr;           // EPI_DGLU: M x N, written, or none
+    int stagger = 0;      // ring kernel: how far the four phases of the first blocks start apart, in 10 ns
     const int64_t* offsets = nullptr;  // E + 1 values on the device
     int E = 1;
     int64_t T = 0;        // rows that offsets may reach

@@ -75,7 +75,7 @@ bool bad_temperature(float t) { return !(t >= 0x1p-10f && t <= 0x1p10f); }
 
 // A row's logits and their statistics, a chunk of rows at a time: the workspace
 // holds the chunk's logits.
-constexpr int64_t kLogitBytes = (int64_t)512 << 20;
+constexpr int64_t kLogitBytes = (int64_t)1024 << 20;
 struct LogitsPlan {
     Operand A, B;
     Shape sh;

@@ -351,7 +351,7 @@ __device__ __forceinline__ void ring_logits(const FusedArgs& g, const TilePos& t
     const bool edge = t.n0 + 32 * TN > g.N;
     const int last = g.N - n0 >= 16 * TN ? 16 * TN : g.N > n0 ? (int)(g.N - n0) : 0;  // this lane's columns end there
     const int part = t.tn * 2 + wave_n, parts = (int)((g.N + 32 * TN - 1) / (32 * TN)) * 2;
-    const float inv_t = g.inv_t;
+    const float c = g.inv_t * kLog2e;
     [[maybe_unused]] const int room = g.ldc - n0 >= 16 * TN ? 16 * TN : g.ldc > n0 ? (int)(g.ldc - n0) : 0;
     [[maybe_unused]] const __amdgpu_buffer_rsrc_t rc =
         buffer_at(KEEP ? static_cast<float*>(g.C) + (t.m0 + wave_m * 128) * g.ldc + t.n0 + wave_n * 16 * TN : nullptr);
@@ -404,7 +404,7 @@ __device__ __forceinline__ void ring_logits(const FusedArgs& g, const TilePos& t
         const float ref = __builtin_isinf(mx) ? 0.0f : mx;
         float sum = 0.0f, mean = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 4 * TN; ++k) add_exp(z[k], ref, inv_t, sum, mean);
+        for (int k = 0; k < 4 * TN; ++k) add_exp(z[k], ref, c, sum, mean);
         sum += __shfl_xor(sum, 16);
         mean += __shfl_xor(mean, 16);
         sum += __shfl_xor(sum, 32);
@@ -420,7 +420,7 @@ __device__ __forceinline__ void ring_logits(const FusedArgs& g, const TilePos& t
             const int64_t step = (int64_t)parts * t.M;
             st[0] = mx;
             st[step] = sum;
-            st[2 * step] = mean;
+            st[2 * step] = mean * kLn2;
         }
         asm volatile("" ::: "memory");  // keeps the groups in this order
     }

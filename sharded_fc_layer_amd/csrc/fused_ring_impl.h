@@ -16,6 +16,7 @@
 // matrix or rows) and ends with the last row that the tile may read, so that
 // only one tile's rows, or one group's, have to lie within 2 GiB.
 #define FCR_SETUP                                                                                                   \
+    if constexpr (MODE == EPI_DGLU) ring_stagger(g);                                                                \
     constexpr int kOut = MODE == EPI_GLU ? BN / 2 : BN; /* output columns */                                        \
     const TilePos pos = tile_position<256, kOut, GRP>(g);                                                           \
     if (!pos.any) return; /* the whole block */                                                                     \
@@ -48,6 +49,18 @@
 
 namespace fcs {
 namespace {
+
+// Blocks that start together end together, round after round, so all CUs'
+// epilogues would ask for the memory at once and leave it idle during the main
+// loops. A quarter of the first round's blocks (of every XCD) starts g.stagger
+// later than the one before (launch_fused says how long, and what it gains).
+// The wait ends by a counter that always advances.
+__device__ __forceinline__ void ring_stagger(const FusedArgs& g) {
+    if (g.stagger <= 0 || blockIdx.x >= 256) return;
+    const unsigned long long ticks = (unsigned long long)g.stagger * ((blockIdx.x >> 3) & 3);
+    const unsigned long long start = __builtin_amdgcn_s_memrealtime();
+    while (__builtin_amdgcn_s_memrealtime() - start < ticks) __builtin_amdgcn_s_sleep(16);
+}
 
 template <EpiMode MODE, GroupMode GRP, bool A_OC, bool B_OC, int BN, int HEAD, int NA, int KIND, bool VEC>
 __global__ __launch_bounds__(kW4Threads) __attribute__((amdgpu_waves_per_eu(1, 1))) void fused_ring_kernel(

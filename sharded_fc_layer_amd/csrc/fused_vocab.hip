@@ -68,7 +68,7 @@ __global__ __launch_bounds__(256) void row_logits_kernel(FusedArgs g, float* __r
     const float ref = finite_ref(mx);
     float sum = 0.0f, mean = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) add_exp(z[q], ref, g.inv_t, sum, mean);
+    for (int q = 0; q < 4; ++q) add_exp(z[q], ref, g.inv_t * kLog2e, sum, mean);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d), mean += __shfl_xor(mean, d);
     if (lane == 0) {
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void row_logits_kernel(FusedArgs g, float* __r
         const int64_t step = (int64_t)parts * g.M;
         st[0] = mx;
         st[step] = sum;
-        st[2 * step] = mean;
+        st[2 * step] = mean * kLn2;
     }
 }
 
