@@ -31,7 +31,7 @@ GluPlan glu_plan(int64_t M, int64_t N, int64_t K, bool b_oc, bool aligned, bool 
     const int64_t limit = (int64_t)1 << 31;
     // (the two halves of W are read through one descriptor; Z's rows are 2 N wide)
     const bool near = grad || 2 * (b_oc ? K : cols) * ldb < limit;
-    p.sh = small_shape(M, cols, K, false, !fits(K, aligned) || !fits(bcols, aligned) || (b_oc && !grad && N % 8 != 0), true);
+    p.sh = low_shape(M, cols, K, !fits(K, aligned) || !fits(bcols, aligned) || (b_oc && !grad && N % 8 != 0), true);
     p.fused = near && p.sh.splits == 1;
     if (!near) p.sh.us += planes_us(1, M, cols);
     // the large tiles: fused where rows of N values are whole vectors, else with planes
@@ -92,7 +92,7 @@ LogitsPlan logits_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned,
     const int64_t fit = std::max<int64_t>(256, kLogitBytes / (4 * p.z_ld) / 256 * 256);
     const int64_t bcols = b_oc ? N : K;
     p.rows = read_again ? std::min(M, fit) : M;
-    p.sh = shape_of(p.rows, N, K, false, b_oc, K, bcols, aligned);
+    p.sh = shape_of(p.rows, N, K, false, b_oc, K, bcols, aligned, true);
     if (512 * p.z_ld >= (int64_t)1 << 31 && p.sh.tile == kRingTile)
         p.sh = small_shape(p.rows, N, K, false, !fits(K, aligned) || !fits(bcols, aligned), false);
     const bool ring = p.sh.tile == kRingTile, split = p.sh.splits > 1;

@@ -135,10 +135,9 @@ double planes_us(int64_t slices, int64_t M, int64_t N) {
 double operand_bytes(int64_t M, int64_t N, int64_t K) { return 2.0 * (double)K * (double)(M + N); }
 double copy_us(int64_t bytes) { return 3 + (double)bytes * 2 / 3.5e6; }
 
-// The general kernel's best form. A product with few tiles may split a long
-// reduction, 128 values to a slice at least.
-Shape small_shape(int64_t M, int64_t N, int64_t K, bool a_oc, bool any, bool may_split) {
-    const int tile = a_oc || M > 64 ? 0 : M <= 32 ? 1 : 3;
+// The general kernel's best form with a tile. A product with few tiles may split
+// a long reduction, 128 values to a slice at least.
+Shape tile_shape(int tile, int64_t M, int64_t N, int64_t K, bool any, bool may_split) {
     const int64_t tiles = tiles_of(tile, M, N);
     const double bytes = operand_bytes(M, N, K);
     Shape best{tile, 1, up(K, 64), small_us(tile, tiles, K, any, bytes)};
@@ -152,14 +151,37 @@ Shape small_shape(int64_t M, int64_t N, int64_t K, bool a_oc, bool any, bool may
     }
     return best;
 }
+// ... with the tile that the rows say
+Shape small_shape(int64_t M, int64_t N, int64_t K, bool a_oc, bool any, bool may_split) {
+    return tile_shape(a_oc || M > 64 ? 0 : M <= 32 ? 1 : 3, M, N, K, any, may_split);
+}
+// ... with lower tiles as well where they give no CU a second block: for the
+// gated layers and the logits, whose epilogues weigh more. Measured (us,
+// weights in the caches) with tiles of 128, 64 and 32 rows: gradient of 1500 x
+// 600 -> 1100 31.8, 19.7 (216 tiles); 200 x 2048 -> 5632 25.0, 19.3 (176), 26.7
+// (308); 256 x 2048 -> 2 x 2048 19.3, 16.7, 14.2 (256); 100 x 1024 -> 2 x 4096
+// 17.6, 13.7, 12.4 (256); but 200 x 2048 -> 2 x 5632 21.5, 26.6 (352), and logits
+// of 200 x 1024 -> 16000 24.4, 27.6 (500). With slices: 500 x 4096 -> 2 x 1000
+// 32.6 (3 slices), 30.7 (4), 44.2 (1).
+Shape low_shape(int64_t M, int64_t N, int64_t K, bool any, bool may_split) {
+    Shape best = small_shape(M, N, K, false, any, may_split);
+    for (int tile : {3, 1}) {
+        if (tiles_of(tile, M, N) > 256) continue;
+        const Shape sh = tile_shape(tile, M, N, K, any, may_split);
+        if (sh.us <= best.us) best = sh;
+    }
+    return best;
+}
 // The ring kernel's, if it takes the product, without any copies it needs.
 Shape ring_shape(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t lda, int64_t ldb) {
     const bool takes = ring_takes(GRP_NONE, a_oc, b_oc, N, K, lda, ldb);
     return Shape{kRingTile, 1, up(K, 64), takes ? ring_us(tiles_of(kRingTile, M, N), K, false, operand_bytes(M, N, K)) : 1e30};
 }
 // The better of both for one product, whose operands' rows are acols and bcols values.
-Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t acols, int64_t bcols, bool aligned) {
-    const Shape small = small_shape(M, N, K, a_oc, !fits(acols, aligned) || !fits(bcols, aligned), true);
+Shape shape_of(int64_t M, int64_t N, int64_t K, bool a_oc, bool b_oc, int64_t acols, int64_t bcols, bool aligned,
+               bool low = false) {
+    const bool any = !fits(acols, aligned) || !fits(bcols, aligned);
+    const Shape small = low ? low_shape(M, N, K, any, true) : small_shape(M, N, K, a_oc, any, true);
     Shape ring = ring_shape(M, N, K, a_oc, b_oc, ring_ld(acols, aligned), ring_ld(bcols, aligned));
     const int64_t bytes = (fits(acols, aligned) ? 0 : M * K * 2) + (fits(bcols, aligned) ? 0 : N * K * 2);
     if (bytes) ring.us += copy_us(bytes);
