@@ -99,16 +99,16 @@ __device__ __forceinline__ float wave_min(float v) {
 // the smaller one, but -inf and NaN do not count
 __device__ __forceinline__ float least_number(float low, float v) { return v > -INFINITY && v < low ? v : low; }
 
-constexpr int kFinishThreads = 1024;
+constexpr int kFinishThreads = 1024;  // at most
 
 // The statistics of the ROWS rows from m0 on, by a block: thread (row, slice)
 // joins every so many-th part of its row, so that with 16 rows a wave's reads
 // are whole 64-byte pieces (4096 rows of 250 parts: 30 us with the parts of a
 // row over the lanes of a wave, 7 so), then pairwise in a fixed order. Rows past the last
 // one repeat it. `maxima` (LDS, ROWS x parts, or none) receives the parts' maxima.
-template <int ROWS>
+template <int ROWS, int THREADS>
 __device__ __forceinline__ void block_stats(const RowLogits& r, int64_t m0, Stats (*s)[ROWS + 1], float* maxima) {
-    constexpr int S = kFinishThreads / ROWS;
+    constexpr int S = THREADS / ROWS;
     const int row = threadIdx.x % ROWS, sl = threadIdx.x / ROWS;
     const int64_t m = m0 + row < r.M ? m0 + row : r.M - 1, step = (int64_t)r.parts * r.M;
     Stats a{-INFINITY, 0.0f, 0.0f};
@@ -243,7 +243,7 @@ __device__ __forceinline__ float value_of(uint32_t order) { return key_value((ui
 // low (about the smallest value that is a number) and high (the largest), as
 // floats first, where values lie close together, then as orders.
 // reach(c): the wave's number of values with an order of at least c.
-template <int SUBS, class F>
+template <int SUBS, int ROWS, class F>
 __device__ __forceinline__ uint32_t reached_by(int k, int most, uint32_t least, float low, float high, RowJoin<SUBS>& join,
                                                int& n, F reach) {
     uint32_t lo = least, hi = order_of(high) + 1;  // k values reach lo, fewer reach hi
@@ -261,23 +261,23 @@ __device__ __forceinline__ uint32_t reached_by(int k, int most, uint32_t least, 
             done = (n >= k && n <= most) || hi - lo <= 1;
         }
         // (rows of a block end together)
-        if (SUBS == 1 ? done : SUBS == 16 ? done : __syncthreads_and(done)) break;
+        if (SUBS == 1 || ROWS == 1 ? done : __syncthreads_and(done)) break;
     }
     return lo;
 }
 
-// SUBS waves to a row, 16 / SUBS rows to a block. TOP: the largest as well, in
+// SUBS waves to a row, ROWS rows to a block. TOP: the largest as well, in
 // four steps: a value that k blocks' maxima or a few more reach, by halving;
 // those blocks (of equal maxima the first ones); their columns' values that
 // reach it, into LDS; the place of each by counting those in front of it. Where
 // more than kCandidates reach it, what k of the first kCandidates reach takes
 // its place; if that is no more (equal values), one wave keeps a sorted list
 // instead.
-constexpr int kCandidates = 256, kMostBlocks = kMaxTop * 3 / 2;
+constexpr int kCandidates = 256, kMostBlocks = kMaxTop + kMaxTop / 4 + 4;
 constexpr int64_t kMaximaBytes = 56 << 10;
-template <int SUBS, bool TOP>
-__global__ __launch_bounds__(kFinishThreads) void logprob_finish_kernel(RowLogits in, LogprobOut out, int in_lds) {
-    constexpr int ROWS = 16 / SUBS;
+template <int SUBS, int ROWS, bool TOP>
+__global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLogits in, LogprobOut out, int in_lds) {
+    static_assert(64 * SUBS * ROWS <= kFinishThreads, "a block's waves");
     __shared__ Stats stats[64][ROWS + 1];
     extern __shared__ float maxima[];  // ROWS x parts, where they fit
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(kFinishThreads) void logprob_finish_kernel(RowLogit
     const bool there = m0 + row < in.M;
     const int64_t m = there ? m0 + row : in.M - 1;  // (waves past the last row do its work again and store nothing)
 
-    block_stats<ROWS>(in, m0, stats, TOP && in_lds ? maxima : nullptr);
+    block_stats<ROWS, 64 * SUBS * ROWS>(in, m0, stats, TOP && in_lds ? maxima : nullptr);
     const Stats a = stats[0][row];
     const float ref = finite_ref(a.mx), log_sum = logf(a.sum);
     if (there && sub == 0 && lane == 0) {
@@ -311,14 +311,14 @@ __global__ __launch_bounds__(kFinishThreads) void logprob_finish_kernel(RowLogit
 
         // the blocks: a wave's share of them is consecutive
         const int per = (parts + SUBS - 1) / SUBS, p0 = sub * per, p1 = p0 + per < parts ? p0 + per : parts;
-        const int most = k + k / 2;
+        const int most = k + k / 4 + 4;
         uint32_t least = 0;
         int count = parts;  // blocks to be read
         if (parts > most) {
             float low = INFINITY;
             for (int p = p0 + lane; p < p1; p += 64) low = least_number(low, value_of(maximum(p)));
             low = join.smallest(wave_min(low));
-            least = reached_by<SUBS>(k, most, 0, low, a.mx, join, count, [&](uint32_t c) {
+            least = reached_by<SUBS, ROWS>(k, most, 0, low, a.mx, join, count, [&](uint32_t c) {
                 int n = 0;
                 for (int p = p0; p < p1; p += 64) n += __popcll(__ballot(p + lane < p1 && maximum(p + lane) >= c));
                 return n;
@@ -354,35 +354,36 @@ __global__ __launch_bounds__(kFinishThreads) void logprob_finish_kernel(RowLogit
         if (sub == 0 && lane == 0) found_n[row] = 0;
         __syncthreads();
 
-        // their columns, two to a lane, four loads ahead
+        // their columns, four to a lane, four loads ahead
         const float* z = in.z + m * in.ld;
         const int total = count * in.width, shift = 31 - __builtin_clz(in.width);
         int n;
         bool sorted = false;
         for (;;) {
-            for (int e0 = 2 * (sub * 64); e0 < total; e0 += 4 * 128 * SUBS) {
-                float v[4][2];
+            // (compared as floats, unless -inf and NaN count too)
+            const bool all = least <= order_of(-INFINITY);
+            const float over = value_of(least);
+            for (int e0 = 4 * (sub * 64); e0 < total; e0 += 4 * 256 * SUBS) {
+                f32x4 v[4];
                 int64_t col[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int e = e0 + u * 128 * SUBS + 2 * lane;
+                    const int e = e0 + u * 256 * SUBS + 4 * lane;
                     col[u] = e < total ? ((int64_t)chosen[row][e >> shift] << shift) + (e & (in.width - 1)) : in.N;
                     // (rows are padded to whole vectors)
-                    const float2 w = col[u] < in.N ? *reinterpret_cast<const float2*>(z + col[u]) : float2{0.0f, 0.0f};
-                    v[u][0] = w.x, v[u][1] = w.y;
+                    v[u] = col[u] < in.N ? *reinterpret_cast<const f32x4*>(z + col[u]) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t key = order_key(v[u][h], (uint32_t)(col[u] + h));
-                        const bool take = col[u] + h < in.N && (uint32_t)(key >> 32) >= least;
+                    for (int h = 0; h < 4; ++h) {
+                        const bool take = (all || v[u][h] >= over) && col[u] + h < in.N;
                         const unsigned long long t = __ballot(take);
                         if (t == 0) continue;
                         int base = 0;
                         if (lane == 0) base = atomicAdd(&found_n[row], (int)__popcll(t));
                         base = __builtin_amdgcn_readfirstlane(base) + (int)__popcll(t & ((1ull << lane) - 1));
-                        if (take && base < kCandidates) found[row][base] = key;
+                        if (take && base < kCandidates) found[row][base] = order_key(v[u][h], (uint32_t)(col[u] + h));
                     }
             }
             __syncthreads();
@@ -395,7 +396,7 @@ __global__ __launch_bounds__(kFinishThreads) void logprob_finish_kernel(RowLogit
             for (int i = sub * 64 + lane; i < have; i += 64 * SUBS) low = least_number(low, key_value(found[row][i]));
             low = join.smallest(wave_min(low));
             int reached;
-            const uint32_t v = reached_by<SUBS>(full ? k : 0, most, least, low, a.mx, join, reached, [&](uint32_t c) {
+            const uint32_t v = reached_by<SUBS, ROWS>(full ? k : 0, most, least, low, a.mx, join, reached, [&](uint32_t c) {
                 int r = 0;
                 for (int i = sub * 64; i < have; i += 64 * SUBS)
                     r += __popcll(__ballot(i + lane < have && (uint32_t)(found[row][i + lane] >> 32) >= c));
@@ -483,7 +484,7 @@ __global__ __launch_bounds__(kFinishThreads) void distill_finish_kernel(RowLogit
                                                                         float* __restrict__ loss) {
     __shared__ Stats stats[64][ROWS + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    block_stats<ROWS>(in, (int64_t)blockIdx.x * ROWS, stats, nullptr);
+    block_stats<ROWS, kFinishThreads>(in, (int64_t)blockIdx.x * ROWS, stats, nullptr);
     const int64_t m = (int64_t)blockIdx.x * ROWS + wave;
     if (wave >= ROWS || m >= in.M) return;  // the whole wave
     const Stats a = stats[0][wave];
@@ -598,21 +599,26 @@ hipError_t launch_row_logits(const FusedArgs& g, float* planes, int64_t pld, int
     return hipGetLastError();
 }
 
-template <int SUBS>
+template <int SUBS, int ROWS>
 static hipError_t logprob_finish(const RowLogits& r, const LogprobOut& o, hipStream_t s) {
-    const int rows = 16 / SUBS;
-    // the maxima of the parts in LDS, unless they are more than it holds beside the rest (44 KB with 16 rows ...)
-    const int64_t bytes = (int64_t)rows * r.parts * 4;
+    // the maxima of the parts in LDS, unless they are more than it holds beside the rest
+    const int64_t bytes = (int64_t)ROWS * r.parts * 4;
     const bool in_lds = o.k > 0 && bytes <= kMaximaBytes;
-    const auto fn = o.k > 0 ? logprob_finish_kernel<SUBS, true> : logprob_finish_kernel<SUBS, false>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)((r.M + rows - 1) / rows)), dim3(kFinishThreads), in_lds ? (unsigned)bytes : 0u, s,
-                       r, o, in_lds ? 1 : 0);
+    const auto fn = o.k > 0 ? logprob_finish_kernel<SUBS, ROWS, true> : logprob_finish_kernel<SUBS, ROWS, false>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)((r.M + ROWS - 1) / ROWS)), dim3(64 * SUBS * ROWS), in_lds ? (unsigned)bytes : 0u,
+                       s, r, o, in_lds ? 1 : 0);
     return hipGetLastError();
 }
 
 hipError_t launch_logprob_finish(const RowLogits& r, const LogprobOut& o, hipStream_t s) {
     if (o.k < 0 || o.k > kMaxTop || r.width < 32 || (r.width & (r.width - 1))) return hipErrorInvalidValue;
-    return r.M <= 512 ? logprob_finish<16>(r, o, s) : r.M <= 2048 ? logprob_finish<4>(r, o, s) : logprob_finish<1>(r, o, s);
+    // waves to a row x rows to a block, measured with 32000 columns and k = 20 (us
+    // with the product over 64, which takes 9 with one row and 256 with 8192 of it):
+    // 16 x 1, 8 x 1, 4 x 1, 1 x 16: one row 16.4, 15.3, 18.4, 39.5; 600 rows 66,
+    // 48, 47, 59; 2048 169, 115, 105, 105; 8192 675, 437, 403, 380 (k = 128: 750,
+    // 548, 501, 603)
+    if (r.M < 1024) return logprob_finish<8, 1>(r, o, s);
+    return r.M <= 2048 || o.k > 64 ? logprob_finish<4, 1>(r, o, s) : logprob_finish<1, 16>(r, o, s);
 }
 
 hipError_t launch_distill_finish(const RowLogits& r, const Listed& t, float* lse, float* slogits, float* loss,
