@@ -3,11 +3,11 @@
 //
 // With G the gate and U the up values, Y = act(G) U, and for a gradient d of Y
 //   dG = d U act'(G),  dU = d act(G).
-// Bound by memory: every value is read and written once, 4 columns of G and
-// the same 4 of U to a lane.
+// Bound by memory: every value is read and written once, 4 or 8 columns of G
+// and the same of U to a lane.
 #include <algorithm>
 
-#include "fused_common.h"
+#include "fused_epilogue.h"
 
 namespace fcs {
 namespace {
@@ -127,40 +127,74 @@ __global__ __launch_bounds__(256) void split_glu_kernel(FusedArgs g, const float
     }
 }
 
-// The elementwise gradient: a block takes 256 columns (4 per lane) of a range
+// W consecutive values of a row, of which `left` are there
+template <int W>
+__device__ __forceinline__ void load_w(const uint16_t* p, int left, float (&v)[W]) {
+    if constexpr (W == 8) {
+        const u16x8 b = load8(p, left);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = bf16_f32(b[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < W; ++q) v[q] = q < left ? bf16_f32(p[q]) : 0.0f;
+    }
+}
+template <int W>
+__device__ __forceinline__ void store_w(uint16_t* p, int left, const float (&v)[W]) {
+    if constexpr (W == 8) {
+        store8(p, left, f32x8{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]});
+    } else {
+        __bf16* c = reinterpret_cast<__bf16*>(p);
+#pragma unroll
+        for (int q = 0; q < W; ++q)
+            if (q < left) c[q] = (__bf16)v[q];
+    }
+}
+
+// The elementwise gradient: a block takes 64 W columns (W per lane) of a range
 // of rows (4 at a time, one per wave), and leaves one partial row.
+template <int KIND, int W>
 __global__ __launch_bounds__(256) void glu_bwd_kernel(const uint16_t* __restrict__ dY, const uint16_t* __restrict__ Z,
                                                       int act, uint16_t* __restrict__ dZ, uint16_t* __restrict__ Y,
                                                       float* __restrict__ part, int64_t M, int64_t N, int parts) {
-    __shared__ float cs_all[4][256];
+    __shared__ float sums[4][64][2 * W + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n = (int64_t)blockIdx.x * 256 + lane * 4;
+    const int64_t n = (int64_t)blockIdx.x * 64 * W + lane * W;
+    const int left = n >= N ? 0 : N - n < W ? (int)(N - n) : W;
     const int64_t rows = (M + parts - 1) / parts, m0 = blockIdx.y * rows;
     const int64_t m1 = m0 + rows < M ? m0 + rows : M;
-    float csg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, csu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (n < N)
-        for (int64_t m = m0 + wave; m < m1; m += 4) {
-            float d[4], gate[4], up[4], sl[4], y[4];
-            load4(dY + m * N + n, n, N, d);
-            load4(Z + m * 2 * N + n, n, N, gate);
-            load4(Z + m * 2 * N + N + n, n, N, up);
-            act_and_slope(act, gate, sl);
+    const ActParams a = act_params(act);
+    float csg[W] = {}, csu[W] = {};
+#pragma unroll 2
+    for (int64_t m = m0 + wave; m < m1; m += 4) {
+        float d[W], gate[W], up[W], y[W];
+        load_w(dY + m * N + n, left, d);
+        load_w(Z + m * 2 * N + n, left, gate);
+        load_w(Z + m * 2 * N + N + n, left, up);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                y[q] = gate[q] * up[q];
-                up[q] = d[q] * up[q] * sl[q];
-                gate[q] = d[q] * gate[q];
-                csg[q] += up[q], csu[q] += gate[q];
-            }
-            if (dZ) {
-                store4_bf16(dZ + m * 2 * N + n, n, N, up);
-                store4_bf16(dZ + m * 2 * N + N + n, n, N, gate);
-            }
-            if (Y) store4_bf16(Y + m * N + n, n, N, y);
+        for (int q = 0; q < W; ++q) {
+            float v, s;
+            act_value_slope<KIND>(a, gate[q], v, s);
+            y[q] = v * up[q];
+            up[q] = d[q] * up[q] * s;
+            gate[q] = d[q] * v;
+            csg[q] += up[q], csu[q] += gate[q];
         }
+        if (dZ) {
+            store_w(dZ + m * 2 * N + n, left, up);
+            store_w(dZ + m * 2 * N + N + n, left, gate);
+        }
+        if (Y) store_w(Y + m * N + n, left, y);
+    }
     if (!part) return;
-    block_colsum(cs_all, csg, part + (int64_t)blockIdx.y * 2 * N, n, N);
-    block_colsum(cs_all, csu, part + (int64_t)blockIdx.y * 2 * N + N, n, N);
+#pragma unroll
+    for (int q = 0; q < W; ++q) sums[wave][lane][q] = csg[q], sums[wave][lane][W + q] = csu[q];
+    __syncthreads();
+    // each wave a quarter of the 2 W sums of a lane's columns
+    float* to = part + (int64_t)blockIdx.y * 2 * N;
+    for (int q = wave; q < 2 * W; q += 4)
+        if (q % W < left)
+            to[(q / W) * N + n + q % W] = ((sums[0][lane][q] + sums[1][lane][q]) + sums[2][lane][q]) + sums[3][lane][q];
 }
 
 }  // namespace
@@ -174,11 +208,30 @@ hipError_t launch_split_glu(EpiMode mode, const FusedArgs& g, const float* plane
     return hipGetLastError();
 }
 
+int glu_bwd_parts(int64_t M, int64_t N) {
+    // about 8192 blocks, at least 16 rows to each (8192 x 8192: 151 us, with 2048 blocks 170)
+    const int64_t cols = (N + 511) / 512;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(M + 15) / 16, 8192 / cols, 65535}));
+}
+
+template <int W>
+static void glu_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16_t* dZ, uint16_t* Y, float* part, int64_t M,
+                    int64_t N, int parts, hipStream_t s) {
+    const int kind = act_kind(act);
+    const auto fn = kind == kNormal ? glu_bwd_kernel<kNormal, W> : kind == kSigmoid ? glu_bwd_kernel<kSigmoid, W> : glu_bwd_kernel<kLinear, W>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)((N + 64 * W - 1) / (64 * W)), (unsigned)parts), dim3(256), 0, s, dY, Z, act, dZ, Y,
+                       part, M, N, parts);
+}
+
 hipError_t launch_glu_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16_t* dZ, uint16_t* Y, float* part,
-                          int64_t M, int64_t N, int parts, hipStream_t s) {
-    if (parts < 1 || parts > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(glu_bwd_kernel, dim3((unsigned)((N + 255) / 256), (unsigned)parts), dim3(256), 0, s, dY, Z, act,
-                       dZ, Y, part, M, N, parts);
+                          int64_t M, int64_t N, hipStream_t s) {
+    const int parts = glu_bwd_parts(M, N);
+    const bool vec = N % 8 == 0 && ((uintptr_t)dY | (uintptr_t)Z | (uintptr_t)dZ | (uintptr_t)Y) % 16 == 0;
+    // (8191 columns: 318 us with two to a lane, 379 with eight from anywhere)
+    if (vec)
+        glu_bwd<8>(dY, Z, act, dZ, Y, part, M, N, parts, s);
+    else
+        glu_bwd<2>(dY, Z, act, dZ, Y, part, M, N, parts, s);
     return hipGetLastError();
 }
 

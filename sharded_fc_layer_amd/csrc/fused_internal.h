@@ -161,9 +161,10 @@ hipError_t launch_xent_finish(const float* stat, int parts, const int64_t* targe
 hipError_t launch_split_glu(EpiMode mode, const FusedArgs& g, const float* planes, int64_t pld, int splits,
                             hipStream_t s);
 // dZ = [dY * up * act'(gate) | dY * act(gate)] and Y = act(gate) * up from Z =
-// [gate | up] (dZ and Y may be none), and the column sums of dZ in `parts` rows
+// [gate | up] (dZ and Y may be none), and the column sums of dZ in glu_bwd_parts rows
+int glu_bwd_parts(int64_t M, int64_t N);
 hipError_t launch_glu_bwd(const uint16_t* dY, const uint16_t* Z, int act, uint16_t* dZ, uint16_t* Y, float* part,
-                          int64_t M, int64_t N, int parts, hipStream_t s);
+                          int64_t M, int64_t N, hipStream_t s);
 
 // ---- the vocabulary's logits (fused_vocab.hip)
 

@@ -67,7 +67,7 @@ hipError_t run_glu(EpiMode mode, const GluPlan& pl, bool b_oc, FusedArgs g, int6
     return launch_fused(mode, GRP_NONE, pl.sh.tile, false, b_oc, g, s);
 }
 
-int64_t glu_bwd_bytes(int64_t M, int64_t N) { return up((int64_t)bwd_act_parts(M, N) * 2 * N * 4, 256); }
+int64_t glu_bwd_bytes(int64_t M, int64_t N) { return up((int64_t)glu_bwd_parts(M, N) * 2 * N * 4, 256); }
 
 // ---------------------------------------------------------- vocabulary
 
@@ -89,9 +89,11 @@ LogitsPlan logits_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned,
     LogitsPlan p;
     int64_t ws = 0;
     p.z_ld = plane_ld(N);
-    const int64_t fit = std::max<int64_t>(256, kLogitBytes / (4 * p.z_ld) / 256 * 256);
+    // (three statistics for 32 columns or more, where no logits are kept)
+    const int64_t row_bytes = read_again ? 4 * p.z_ld : 12 * ((N + 31) / 32);
+    const int64_t fit = std::max<int64_t>(256, kLogitBytes / row_bytes / 256 * 256);
     const int64_t bcols = b_oc ? N : K;
-    p.rows = read_again ? std::min(M, fit) : M;
+    p.rows = std::min(M, fit);
     p.sh = shape_of(p.rows, N, K, false, b_oc, K, bcols, aligned, true);
     if (512 * p.z_ld >= (int64_t)1 << 31 && p.sh.tile == kRingTile)
         p.sh = small_shape(p.rows, N, K, false, !fits(K, aligned) || !fits(bcols, aligned), false);
@@ -256,11 +258,10 @@ fc_status fc_bwd_glu(const void* dY, const void* Z, fc_act act, void* dZ, void* 
     if (st != FC_OK) return st;
     (void)hipGetLastError();
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int parts = bwd_act_parts(M, N);
     float* part = db ? static_cast<float*>(ws) : nullptr;
     hipError_t e = launch_glu_bwd(static_cast<const uint16_t*>(dY), static_cast<const uint16_t*>(Z), act,
-                                  static_cast<uint16_t*>(dZ), static_cast<uint16_t*>(Y), part, M, N, parts, s);
-    if (e == hipSuccess && db) e = launch_colsum_parts(part, db, 2 * N, parts, s);
+                                  static_cast<uint16_t*>(dZ), static_cast<uint16_t*>(Y), part, M, N, s);
+    if (e == hipSuccess && db) e = launch_colsum_parts(part, db, 2 * N, glu_bwd_parts(M, N), s);
     return done(e);
 }
 

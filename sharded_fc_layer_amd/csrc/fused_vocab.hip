@@ -549,20 +549,27 @@ __global__ __launch_bounds__(256) void listed_prep_kernel(Listed t, const float*
         ids[wave][64 * r + lane] = id[r];
     }
     __builtin_amdgcn_wave_barrier();
-    // tokens that are listed several times count together, in order, at their first place
-    for (int i = 0; i < t.n; ++i) {
-        const int64_t other = ids[wave][i];
+    // tokens that are listed several times count together, in order, at their
+    // first place; eight at a time are looked at first, few rows have any
+    for (int i0 = 0; i0 < t.n; i0 += 8) {
         bool again = false;
 #pragma unroll
-        for (int r = 0; r < kPer; ++r) again |= other == id[r] && other >= 0 && i != 64 * r + lane;
-        if (!__ballot(again)) continue;
-        const float q = i < 64 ? __shfl(p[0], i) : __shfl(p[kPer - 1], i - 64);
+        for (int e = 0; e < 8; ++e) {
+            const int64_t other = ids[wave][i0 + e];  // (past the last one: -1)
 #pragma unroll
-        for (int r = 0; r < kPer; ++r)
-            if (other == id[r] && i != 64 * r + lane) {
-                total[r] += q;
-                if (i < 64 * r + lane) firsts[r] = false;
-            }
+            for (int r = 0; r < kPer; ++r) again |= other == id[r] && other >= 0 && i0 + e != 64 * r + lane;
+        }
+        if (!__ballot(again)) continue;
+        for (int i = i0; i < i0 + 8; ++i) {
+            const int64_t other = ids[wave][i];
+            const float q = i < 64 ? __shfl(p[0], i) : __shfl(p[kPer - 1], i - 64);
+#pragma unroll
+            for (int r = 0; r < kPer; ++r)
+                if (other == id[r] && other >= 0 && i != 64 * r + lane) {
+                    total[r] += q;
+                    if (i < 64 * r + lane) firsts[r] = false;
+                }
+        }
     }
 #pragma unroll
     for (int r = 0; r < kPer; ++r) {

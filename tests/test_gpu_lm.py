@@ -34,6 +34,13 @@ SHAPES = [(1, 1, 1), (1, 2048, 520), (3, 31, 7), (16, 512, 384), (32, 264, 136),
 WIDE = [(4096, 512, 2048), (4000, 640, 2056), (2600, 100, 1304), (4001, 600, 2051), (4100, 640, 760)]
 
 
+# the 256 x 256 tiles with a partial last stage; the tiles of 64 rows (the lower ones would be too many, the reduction
+# is too short to split)
+LARGE_GLU = [(4096, 600, 2048), (4104, 200, 2056)]
+LARGE_GRAD = [(4096, 512, 4096), (4000, 640, 4104), (4096, 600, 4096)]
+LOW = [(250, 72, 3200), (256, 71, 3201)]
+
+
 # ---- gated layers
 
 def glu64(z, ez, N, act):
@@ -45,7 +52,7 @@ def glu64(z, ez, N, act):
     return y, ea * (Up.abs() + eU) + a.abs() * eU + U * y.abs()
 
 
-@pytest.mark.parametrize("shape", SHAPES + WIDE)
+@pytest.mark.parametrize("shape", SHAPES + WIDE + LARGE_GLU + LOW)
 @pytest.mark.parametrize("wo", [ROW, COL])
 def test_fwd_glu(shape, wo):
     M, K, N = shape
@@ -106,7 +113,8 @@ def check_glu_grad(dZ, Y, db, want, tol, y, ty, M, what):
         within(db, want.sum(0), tol.sum(0) + (M + 16) * U * (want.abs() + tol).sum(0), what + " db")
 
 
-@pytest.mark.parametrize("shape", SHAPES + [(m, n, k) for m, k, n in WIDE] + [(4096, 100, 4096), (4100, 1100, 4104)])
+@pytest.mark.parametrize("shape", SHAPES + [(m, n, k) for m, k, n in WIDE] + [(4096, 100, 4096), (4100, 1100, 4104)] +
+                         LARGE_GRAD + [(m, k, 2 * n) for m, k, n in LOW])
 @pytest.mark.parametrize("wo", [ROW, COL])
 def test_bwd_data_glu(shape, wo):
     M, N, K = shape  # the reduction runs over the layer's outputs N
@@ -205,7 +213,7 @@ def test_glu_bias_gradient_of_infinite_weights(shape, wo):
 # ---- log probabilities
 
 VOCAB = [(1, 8, 1), (1, 64, 1000), (1, 2048, 5000), (5, 33, 130), (32, 128, 129), (33, 100, 999), (64, 264, 4001),
-         (130, 72, 520), (300, 65, 2050), (600, 96, 3000), (40, 4104, 700), (96, 2001, 300)]
+         (130, 72, 520), (300, 65, 2050), (600, 96, 3000), (40, 4104, 700), (96, 2001, 300), (1500, 64, 1000)]
 VOCAB_WIDE = [(4096, 512, 4096), (4000, 640, 4104), (2309, 131, 3001), (4001, 600, 4099), (2600, 100, 2600)]
 
 
@@ -396,6 +404,25 @@ def test_logprob_of_rows_in_several_chunks():
         best = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :40]
         assert torch.equal(ids[r], best)
         assert torch.equal(sl[r].double(), z.gather(1, n_ids[r]))
+
+
+# rows whose parts' maxima fit a block's LDS with 16 rows to it, or do not (896 parts of 128 columns), or with one
+# row (14336 parts of 32); and of more rows than one chunk has
+@pytest.mark.parametrize("shape", [(2100, 24, 100003), (2304, 16, 115008), (3, 24, 530001), (1100, 16, 260000)])
+@pytest.mark.parametrize("k", [5, 128])
+def test_logprob_of_wide_rows(shape, k):
+    M, K, N = shape
+    g = gen(N)
+    X, W = grid(g, M, K), grid(g, K, N, top=7)
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    ws = stored(W, COL)
+    logp, entropy, lse, top, ids = F.fc_logprob(X, ws, t, w_order=COL, top_k=k)
+    for r in torch.split(torch.arange(M, device="cuda"), 200):
+        z, s, want, wl, p, ent = logprob64(X[r], W, t[r], 0, 1.0)
+        tol = 2.0 ** -20 + (N + 16) * U + 4 * U * want.abs()
+        within(lse[r], want, tol, f"{shape} lse")
+        within(logp[r], wl, 2 * tol + 2 * U * wl.abs(), "logp")
+        assert torch.equal(ids[r], torch.sort(z, dim=1, descending=True, stable=True).indices[:, :k])
 
 
 # ---- distillation
