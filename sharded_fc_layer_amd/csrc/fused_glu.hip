@@ -49,6 +49,32 @@ __device__ __forceinline__ void block_colsum(float (*all)[256], const float (&cs
 
 constexpr int kRowsPerWave = 2, kSplitRows = 4 * kRowsPerWave;  // as split_epilogue_parts counts them
 
+// 4 values of each of H halves (N columns apart) of a row in all planes, summed
+// in order. Eight planes' loads are issued before the first is added: a few
+// rows leave a CU with one wave, whose time is the loads' latency. Rows of
+// planes are padded to 64 columns, so the last vector of the second half ends
+// in the padding: it reaches 1, 2 or 3 columns past 2 N where N mod 4 is 3, 2
+// or 1, and 2 N then ends 2, 4 or 6 columns or more before a multiple of 64.
+template <int H>
+__device__ __forceinline__ void sum_planes(const float* p, int64_t step, int splits, int64_t N, f32x4 (&sum)[H]) {
+    constexpr int B = 8;
+#pragma unroll
+    for (int h = 0; h < H; ++h) sum[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = 0; s0 < splits; s0 += B) {
+        f32x4 v[B][H];
+#pragma unroll
+        for (int s = 0; s < B; ++s)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                v[s][h] = s0 + s < splits ? *reinterpret_cast<const f32x4_any*>(p + (s0 + s) * step + h * N)
+                                          : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < B; ++s)
+#pragma unroll
+            for (int h = 0; h < H; ++h) sum[h] += v[s][h];
+    }
+}
+
 // EPI_GLU: planes of 2 N columns, of which a lane takes 4 and the 4 that lie N
 // further. EPI_DGLU: planes of N columns.
 template <EpiMode MODE>
@@ -60,36 +86,35 @@ __global__ __launch_bounds__(256) void split_glu_kernel(FusedArgs g, const float
     [[maybe_unused]] __shared__ float cs_all[4][256];
     [[maybe_unused]] float csg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, csu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (n < N) {
-        [[maybe_unused]] float bg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, bu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        constexpr int H = MODE == EPI_GLU ? 2 : 1;
+        const int64_t m0 = bm * kSplitRows + wave * kRowsPerWave, step = g.M * pld;
+        // EPI_GLU: the biases; EPI_DGLU: the rows' Z, before the planes
+        float bg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, bu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        [[maybe_unused]] float zg[kRowsPerWave][4], zu[kRowsPerWave][4];
         if (MODE == EPI_GLU && g.bias) {
             load4(g.bias + n, n, N, bg);
             load4(g.bias + N + n, n, N, bu);
         }
+        if constexpr (MODE == EPI_DGLU) {
+#pragma unroll
+            for (int r = 0; r < kRowsPerWave; ++r)
+                if (m0 + r < g.M) {
+                    load4(g.Z + (m0 + r) * 2 * N + n, n, N, zg[r]);
+                    load4(g.Z + (m0 + r) * 2 * N + N + n, n, N, zu[r]);
+                }
+        }
+        f32x4 sum[kRowsPerWave][H];
+#pragma unroll
+        for (int r = 0; r < kRowsPerWave; ++r)
+            if (m0 + r < g.M) sum_planes<H>(planes + (m0 + r) * pld + n, step, splits, N, sum[r]);
 #pragma unroll
         for (int r = 0; r < kRowsPerWave; ++r) {
-            const int64_t m = bm * kSplitRows + wave * kRowsPerWave + r;
+            const int64_t m = m0 + r;
             if (m >= g.M) break;
-            const float* p = planes + m * pld + n;
-            // (the up columns start at any address; past the last one lie others, or the plane's padding)
-            f32x4 sg{0.0f, 0.0f, 0.0f, 0.0f};
-            [[maybe_unused]] f32x4 su{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-            for (int s = 0; s < splits; ++s) {
-                sg += *reinterpret_cast<const f32x4_any*>(p + s * g.M * pld);
-                if constexpr (MODE == EPI_GLU) {
-                    if (n + 4 <= N) {
-                        su += *reinterpret_cast<const f32x4_any*>(p + s * g.M * pld + N);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (n + q < N) su[q] += p[s * g.M * pld + N + q];
-                    }
-                }
-            }
             float vg[4], vu[4];
             if constexpr (MODE == EPI_GLU) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) vg[q] = sg[q] + bg[q], vu[q] = su[q] + bu[q];
+                for (int q = 0; q < 4; ++q) vg[q] = sum[r][0][q] + bg[q], vu[q] = sum[r][H - 1][q] + bu[q];
                 if (g.Z) {
                     store4_bf16(g.Z + m * 2 * N + n, n, N, vg);
                     store4_bf16(g.Z + m * 2 * N + N + n, n, N, vu);
@@ -103,14 +128,15 @@ __global__ __launch_bounds__(256) void split_glu_kernel(FusedArgs g, const float
                     store4_bf16(static_cast<uint16_t*>(g.C) + m * g.ldc + n, n, N, vg);
             } else {
                 float sl[4], y[4];
-                load4(g.Z + m * 2 * N + n, n, N, vg);
-                load4(g.Z + m * 2 * N + N + n, n, N, vu);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) vg[q] = zg[r][q];
                 act_and_slope(g.act, vg, sl);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    y[q] = vg[q] * vu[q];
-                    vu[q] = sg[q] * vu[q] * sl[q];  // dG
-                    vg[q] = sg[q] * vg[q];          // dU
+                    const float d = sum[r][0][q];
+                    y[q] = vg[q] * zu[r][q];
+                    vu[q] = d * zu[r][q] * sl[q];  // dG
+                    vg[q] = d * vg[q];             // dU
                     csg[q] += vu[q], csu[q] += vg[q];
                 }
                 uint16_t* d = static_cast<uint16_t*>(g.C) + m * 2 * N + n;

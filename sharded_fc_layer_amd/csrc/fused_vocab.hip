@@ -446,26 +446,28 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
 
 // ------------------------------------------------- a teacher's tokens
 
-constexpr int kPer = kMaxTop / 64;  // listed tokens to a lane: 64 r + lane
-
-// A row's listed tokens: ids (-1 where there is none), probabilities (0 there)
-// and their logarithms. Returns whether the row has any.
-__device__ __forceinline__ bool teacher_row(const Listed& t, float inv_t, int64_t m, int lane, int64_t (&id)[kPer],
-                                            float (&p)[kPer], float (&logp)[kPer]) {
+// A row's listed tokens, PER of them to a lane (64 r + lane): ids (-1 where
+// there is none), probabilities (0 there) and their logarithms. Returns whether
+// the row has any.
+template <int PER>
+__device__ __forceinline__ bool teacher_row(const Listed& t, float inv_t, int64_t m, int lane, int64_t (&id)[PER],
+                                            float (&p)[PER], float (&logp)[PER]) {
     float mx = -INFINITY;
+    bool some = false;
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) {
+    for (int r = 0; r < PER; ++r) {
         const int i = 64 * r + lane;
         id[r] = i < t.n ? t.ids[m * t.n + i] : -1;
-        logp[r] = id[r] >= 0 ? t.tlogits[m * t.n + i] * inv_t : -INFINITY;
+        logp[r] = i < t.n && id[r] >= 0 ? t.tlogits[m * t.n + i] * inv_t : -INFINITY;
         if (logp[r] == -INFINITY) id[r] = -1;
+        some = some || id[r] >= 0;
         mx = fmaxf(mx, logp[r]);
     }
-    const bool any = __ballot(id[0] >= 0 || id[kPer - 1] >= 0) != 0;
+    const bool any = __ballot(some) != 0;
     mx = wave_max(mx);
     float s = 0.0f;
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) {
+    for (int r = 0; r < PER; ++r) {
         logp[r] = id[r] >= 0 ? logp[r] - mx : 0.0f;
         p[r] = id[r] >= 0 ? exp_f32(logp[r]) : 0.0f;
         s += p[r];
@@ -473,12 +475,12 @@ __device__ __forceinline__ bool teacher_row(const Listed& t, float inv_t, int64_
     s = any ? wave_sum(s) : 1.0f;
     const float ls = logf(s);
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) p[r] /= s, logp[r] -= ls;
+    for (int r = 0; r < PER; ++r) p[r] /= s, logp[r] -= ls;
     return any;
 }
 
 // ROWS rows to a block; their teachers' tokens, a wave to a row.
-template <int ROWS>
+template <int ROWS, int PER>
 __global__ __launch_bounds__(kFinishThreads) void distill_finish_kernel(RowLogits in, Listed t, float* __restrict__ lse,
                                                                         float* __restrict__ slogits,
                                                                         float* __restrict__ loss) {
@@ -489,12 +491,12 @@ __global__ __launch_bounds__(kFinishThreads) void distill_finish_kernel(RowLogit
     if (wave >= ROWS || m >= in.M) return;  // the whole wave
     const Stats a = stats[0][wave];
     const float l = finite_ref(a.mx) * in.inv_t + logf(a.sum);
-    int64_t id[kPer];
-    float p[kPer], logp[kPer];
+    int64_t id[PER];
+    float p[PER], logp[PER];
     const bool any = teacher_row(t, in.inv_t, m, lane, id, p, logp);
     float sum = 0.0f;
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) {
+    for (int r = 0; r < PER; ++r) {
         const int i = 64 * r + lane;
         const uint64_t at = (uint64_t)id[r] - (uint64_t)in.v0;
         const float z = id[r] >= 0 && at < (uint64_t)in.N ? in.z[m * in.ld + (int64_t)at] : 0.0f;
@@ -532,39 +534,45 @@ __global__ __launch_bounds__(256) void listed_need_kernel(Listed t, int64_t M, i
     }
 }
 
+// One wave to a row.
+template <int PER>
 __global__ __launch_bounds__(256) void listed_prep_kernel(Listed t, const float* __restrict__ grad, float inv_t,
                                                           int64_t M, float* __restrict__ p_out, float* __restrict__ gw,
                                                           int64_t* __restrict__ targets) {
-    __shared__ int64_t ids[4][kMaxTop];
+    __shared__ __attribute__((aligned(16))) int64_t ids[4][64 * PER];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t m = (int64_t)blockIdx.x * 4 + wave;
     if (m >= M) return;  // the whole wave, which has its own LDS
-    int64_t id[kPer];
-    float p[kPer], logp[kPer], total[kPer];
-    bool firsts[kPer];
+    int64_t id[PER];
+    float p[PER], logp[PER], total[PER];
+    bool firsts[PER];
     const bool any = teacher_row(t, inv_t, m, lane, id, p, logp);
+    if (lane == 0) {
+        gw[m] = grad[m] * inv_t;
+        targets[m] = any ? -1 : INT64_MIN;
+    }
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) {
+    for (int r = 0; r < PER; ++r) {
         total[r] = p[r], firsts[r] = id[r] >= 0;
         ids[wave][64 * r + lane] = id[r];
     }
     __builtin_amdgcn_wave_barrier();
     // tokens that are listed several times count together, in order, at their
-    // first place; eight at a time are looked at first, few rows have any
-    for (int i0 = 0; i0 < t.n; i0 += 8) {
+    // first place; 16 at a time are looked at first, few rows have any
+    for (int i0 = 0; i0 < t.n; i0 += 16) {
         bool again = false;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 16; ++e) {
             const int64_t other = ids[wave][i0 + e];  // (past the last one: -1)
 #pragma unroll
-            for (int r = 0; r < kPer; ++r) again |= other == id[r] && other >= 0 && i0 + e != 64 * r + lane;
+            for (int r = 0; r < PER; ++r) again |= other == id[r] && other >= 0 && i0 + e != 64 * r + lane;
         }
         if (!__ballot(again)) continue;
-        for (int i = i0; i < i0 + 8; ++i) {
+        for (int i = i0; i < i0 + 16; ++i) {
             const int64_t other = ids[wave][i];
-            const float q = i < 64 ? __shfl(p[0], i) : __shfl(p[kPer - 1], i - 64);
+            const float q = i < 64 ? __shfl(p[0], i) : __shfl(p[PER - 1], i - 64);
 #pragma unroll
-            for (int r = 0; r < kPer; ++r)
+            for (int r = 0; r < PER; ++r)
                 if (other == id[r] && other >= 0 && i != 64 * r + lane) {
                     total[r] += q;
                     if (i < 64 * r + lane) firsts[r] = false;
@@ -572,13 +580,9 @@ __global__ __launch_bounds__(256) void listed_prep_kernel(Listed t, const float*
         }
     }
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) {
+    for (int r = 0; r < PER; ++r) {
         const int i = 64 * r + lane;
         if (i < t.n) p_out[m * t.n + i] = firsts[r] ? total[r] : -1.0f;
-    }
-    if (lane == 0) {
-        gw[m] = grad[m] * inv_t;
-        targets[m] = any ? -1 : INT64_MIN;
     }
 }
 
@@ -632,7 +636,9 @@ hipError_t launch_distill_finish(const RowLogits& r, const Listed& t, float* lse
                                  hipStream_t s) {
     if (t.n < 1 || t.n > kMaxTop) return hipErrorInvalidValue;
     const int rows = r.M <= 1024 ? 4 : 16;
-    hipLaunchKernelGGL(rows == 4 ? distill_finish_kernel<4> : distill_finish_kernel<16>,
+    const bool few = t.n <= 64;
+    hipLaunchKernelGGL(rows == 4 ? (few ? distill_finish_kernel<4, 1> : distill_finish_kernel<4, 2>)
+                                 : (few ? distill_finish_kernel<16, 1> : distill_finish_kernel<16, 2>),
                        dim3((unsigned)((r.M + rows - 1) / rows)), dim3(kFinishThreads), 0, s, r, t, lse, slogits, loss);
     return hipGetLastError();
 }
@@ -648,8 +654,8 @@ hipError_t launch_listed_need(const Listed& t, int64_t M, int64_t N, int64_t v0,
 hipError_t launch_listed_prep(const Listed& t, const float* grad, float inv_t, int64_t M, float* p, float* gw,
                               int64_t* targets, hipStream_t s) {
     if (t.n < 1 || t.n > kMaxTop) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(listed_prep_kernel, dim3((unsigned)((M + 3) / 4)), dim3(256), 0, s, t, grad, inv_t, M, p, gw,
-                       targets);
+    hipLaunchKernelGGL(t.n <= 64 ? listed_prep_kernel<1> : listed_prep_kernel<2>, dim3((unsigned)((M + 3) / 4)), dim3(256),
+                       0, s, t, grad, inv_t, M, p, gw, targets);
     return hipGetLastError();
 }
 
