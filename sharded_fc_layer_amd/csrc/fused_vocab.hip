@@ -99,15 +99,32 @@ __device__ __forceinline__ float wave_min(float v) {
 // the smaller one, but -inf and NaN do not count
 __device__ __forceinline__ float least_number(float low, float v) { return v > -INFINITY && v < low ? v : low; }
 
+// A value and its index as one number that orders by value, then by lowest
+// index; never 0, which stands for nothing. NaN counts as -inf, -0 as 0.
+__device__ __forceinline__ uint64_t order_key(float z, uint32_t index) {
+    z = z != z ? -INFINITY : z + 0.0f;
+    const uint32_t b = __builtin_bit_cast(uint32_t, z);
+    return (uint64_t)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (uint32_t)~index;
+}
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t b = (uint32_t)(key >> 32);
+    return __builtin_bit_cast(float, b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
+}
+__device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~(uint32_t)key; }
+
+// The order of values alone: order_key's upper half.
+__device__ __forceinline__ uint32_t order_of(float z) { return (uint32_t)(order_key(z, 0) >> 32); }
+__device__ __forceinline__ float value_of(uint32_t order) { return key_value((uint64_t)order << 32); }
+
 constexpr int kFinishThreads = 1024;  // at most
 
 // The statistics of the ROWS rows from m0 on, by a block: thread (row, slice)
 // joins every so many-th part of its row, so that with 16 rows a wave's reads
 // are whole 64-byte pieces (4096 rows of 250 parts: 30 us with the parts of a
 // row over the lanes of a wave, 7 so), then pairwise in a fixed order. Rows past the last
-// one repeat it. `maxima` (LDS, ROWS x parts, or none) receives the parts' maxima.
+// one repeat it. `maxima` (LDS, rows of `stride`, or none) receives the orders of the parts' maxima.
 template <int ROWS, int THREADS>
-__device__ __forceinline__ void block_stats(const RowLogits& r, int64_t m0, Stats (*s)[ROWS + 1], float* maxima) {
+__device__ __forceinline__ void block_stats(const RowLogits& r, int64_t m0, Stats (*s)[ROWS + 1], uint32_t* maxima, int stride) {
     constexpr int S = THREADS / ROWS;
     const int row = threadIdx.x % ROWS, sl = threadIdx.x / ROWS;
     const int64_t m = m0 + row < r.M ? m0 + row : r.M - 1, step = (int64_t)r.parts * r.M;
@@ -116,7 +133,7 @@ __device__ __forceinline__ void block_stats(const RowLogits& r, int64_t m0, Stat
     for (int p = sl; p < r.parts; p += S) {
         const float* st = r.stat + (int64_t)p * r.M + m;
         const Stats b{st[0], st[step], st[2 * step]};
-        if (maxima) maxima[row * r.parts + p] = b.mx;
+        if (maxima) maxima[row * stride + p] = order_of(b.mx);
         join_stats(a, b, r.inv_t);
     }
     // 64 slices to LDS at most, the others' through the lanes of a wave first
@@ -143,19 +160,6 @@ __device__ __forceinline__ void block_stats(const RowLogits& r, int64_t m0, Stat
 }
 
 // ------------------------------------------------- the largest of a row
-
-// A value and its index as one number that orders by value, then by lowest
-// index; never 0, which stands for nothing. NaN counts as -inf, -0 as 0.
-__device__ __forceinline__ uint64_t order_key(float z, uint32_t index) {
-    z = z != z ? -INFINITY : z + 0.0f;
-    const uint32_t b = __builtin_bit_cast(uint32_t, z);
-    return (uint64_t)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (uint32_t)~index;
-}
-__device__ __forceinline__ float key_value(uint64_t key) {
-    const uint32_t b = (uint32_t)(key >> 32);
-    return __builtin_bit_cast(float, b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
-}
-__device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~(uint32_t)key; }
 
 __device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
     return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
@@ -198,9 +202,6 @@ struct TopList {
     }
 };
 
-// Whole 32-bit order of values: that of order_key's upper half.
-__device__ __forceinline__ uint32_t order_of(float z) { return (uint32_t)(order_key(z, 0) >> 32); }
-
 // What a row's SUBS waves have, joined by all of them: a sum, or the smallest,
 // of a value that is the same in a wave's lanes. `slot` is LDS for 2 x 16
 // values, used in turn, so that one barrier lies between a value's writes and
@@ -234,8 +235,6 @@ struct RowJoin {
         return s;
     }
 };
-
-__device__ __forceinline__ float value_of(uint32_t order) { return key_value((uint64_t)order << 32); }
 
 // An order v >= least (which at least k of a row's values reach) that at least
 // k, and at most `most`, of its values reach; or, where equal values leave no
@@ -275,18 +274,26 @@ __device__ __forceinline__ uint32_t reached_by(int k, int most, uint32_t least, 
 // instead.
 constexpr int kCandidates = 256, kMostBlocks = kMaxTop + kMaxTop / 4 + 4;
 constexpr int64_t kMaximaBytes = 56 << 10;
+// a row's words of LDS: its parts' maxima, if they are there, or the candidates
+__host__ __device__ inline int row_words(int parts, int in_lds) {
+    const int words = (in_lds ? parts : 0) + (in_lds ? parts & 1 : 0);
+    return words > 2 * kCandidates ? words : 2 * kCandidates;
+}
 template <int SUBS, int ROWS, bool TOP>
 __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLogits in, LogprobOut out, int in_lds) {
     static_assert(64 * SUBS * ROWS <= kFinishThreads, "a block's waves");
     __shared__ Stats stats[64][ROWS + 1];
-    extern __shared__ float maxima[];  // ROWS x parts, where they fit
+    // a row's maxima, where they fit, and then, in their place, the values found; of this row's waves alone
+    extern __shared__ uint64_t row_space[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sub = wave % SUBS, first = wave - sub, row = wave / SUBS;
     const int64_t m0 = (int64_t)blockIdx.x * ROWS;
     const bool there = m0 + row < in.M;
     const int64_t m = there ? m0 + row : in.M - 1;  // (waves past the last row do its work again and store nothing)
 
-    block_stats<ROWS, 64 * SUBS * ROWS>(in, m0, stats, TOP && in_lds ? maxima : nullptr);
+    const int stride = row_words(in.parts, in_lds);
+    uint32_t* maxima = reinterpret_cast<uint32_t*>(row_space);
+    block_stats<ROWS, 64 * SUBS * ROWS>(in, m0, stats, TOP && in_lds ? maxima : nullptr, stride);
     const Stats a = stats[0][row];
     const float ref = finite_ref(a.mx), log_sum = logf(a.sum);
     if (there && sub == 0 && lane == 0) {
@@ -303,11 +310,18 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
         __shared__ int slots[2][16];
         __shared__ int taken[16][2];
         __shared__ uint32_t chosen[ROWS][kMostBlocks];
-        __shared__ uint64_t found[ROWS][kCandidates];
         __shared__ int found_n[ROWS];
+        maxima += row * stride;
+        uint64_t* found = reinterpret_cast<uint64_t*>(maxima);
+        auto sync = [] {
+            if constexpr (SUBS > 1)
+                __syncthreads();
+            else
+                __builtin_amdgcn_wave_barrier();  // one wave's LDS accesses are in order
+        };
         RowJoin<SUBS> join{slots, wave, first, 0};
         const int k = out.k, parts = in.parts;
-        auto maximum = [&](int p) { return order_of(in_lds ? maxima[row * parts + p] : in.stat[(int64_t)p * in.M + m]); };
+        auto maximum = [&](int p) { return in_lds ? maxima[p] : order_of(in.stat[(int64_t)p * in.M + m]); };
 
         // the blocks: a wave's share of them is consecutive
         const int per = (parts + SUBS - 1) / SUBS, p0 = sub * per, p1 = p0 + per < parts ? p0 + per : parts;
@@ -333,7 +347,7 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
             equal += __popcll(__ballot(p + lane < p1 && o == least));
         }
         if (lane == 0) taken[wave][0] = above, taken[wave][1] = equal;
-        __syncthreads();
+        sync();
         int at = 0, equal_at = 0, all_above = 0;
 #pragma unroll
         for (int w = 0; w < SUBS; ++w) {
@@ -352,7 +366,7 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
             equal_at += __popcll(eq);
         }
         if (sub == 0 && lane == 0) found_n[row] = 0;
-        __syncthreads();
+        sync();
 
         // their columns, four to a lane, four loads ahead
         const float* z = in.z + m * in.ld;
@@ -363,6 +377,7 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
             // (compared as floats, unless -inf and NaN count too)
             const bool all = least <= order_of(-INFINITY);
             const float over = value_of(least);
+            n = 0;
             for (int e0 = 4 * (sub * 64); e0 < total; e0 += 4 * 256 * SUBS) {
                 f32x4 v[4];
                 int64_t col[4];
@@ -380,34 +395,38 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
                         const bool take = (all || v[u][h] >= over) && col[u] + h < in.N;
                         const unsigned long long t = __ballot(take);
                         if (t == 0) continue;
-                        int base = 0;
-                        if (lane == 0) base = atomicAdd(&found_n[row], (int)__popcll(t));
-                        base = __builtin_amdgcn_readfirstlane(base) + (int)__popcll(t & ((1ull << lane) - 1));
-                        if (take && base < kCandidates) found[row][base] = order_key(v[u][h], (uint32_t)(col[u] + h));
+                        int base = n;
+                        if constexpr (SUBS > 1) {
+                            if (lane == 0) base = atomicAdd(&found_n[row], (int)__popcll(t));
+                            base = __builtin_amdgcn_readfirstlane(base);
+                        }
+                        n += (int)__popcll(t);
+                        base += (int)__popcll(t & ((1ull << lane) - 1));
+                        if (take && base < kCandidates) found[base] = order_key(v[u][h], (uint32_t)(col[u] + h));
                     }
             }
-            __syncthreads();
-            n = found_n[row];
-            // (all rows of the block go round while one has too many)
+            sync();
+            if constexpr (SUBS > 1) n = found_n[row];
+            // (where rows share barriers, all go round while one has too many)
             const bool full = n > kCandidates && !sorted;
-            if (!__syncthreads_or(full)) break;
+            if (SUBS == 1 ? !full : !__syncthreads_or(full)) break;
             const int have = n < kCandidates ? n : kCandidates;
             float low = INFINITY;
-            for (int i = sub * 64 + lane; i < have; i += 64 * SUBS) low = least_number(low, key_value(found[row][i]));
+            for (int i = sub * 64 + lane; i < have; i += 64 * SUBS) low = least_number(low, key_value(found[i]));
             low = join.smallest(wave_min(low));
             int reached;
             const uint32_t v = reached_by<SUBS, ROWS>(full ? k : 0, most, least, low, a.mx, join, reached, [&](uint32_t c) {
                 int r = 0;
                 for (int i = sub * 64; i < have; i += 64 * SUBS)
-                    r += __popcll(__ballot(i + lane < have && (uint32_t)(found[row][i + lane] >> 32) >= c));
+                    r += __popcll(__ballot(i + lane < have && (uint32_t)(found[i + lane] >> 32) >= c));
                 return r;
             });
             const uint32_t more = full ? v : least;
             if (full && more == least) sorted = true;  // equal values
             least = more;
-            __syncthreads();
+            sync();
             if (sub == 0 && lane == 0) found_n[row] = 0;
-            __syncthreads();
+            sync();
         }
         if (n > kCandidates) {
             if (sub != 0) return;  // (no barrier follows)
@@ -432,10 +451,10 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
             return;
         }
         for (int i = sub * 64 + lane; i < n; i += 64 * SUBS) {
-            const uint64_t key = found[row][i];
+            const uint64_t key = found[i];
             int rank = 0;
 #pragma unroll 4
-            for (int j = 0; j < n; ++j) rank += found[row][j] > key;
+            for (int j = 0; j < n; ++j) rank += found[j] > key;
             if (there && rank < k) {
                 out.top_ids[m * k + rank] = (int64_t)key_index(key) + in.v0;
                 out.top_logp[m * k + rank] = a.sum == 0.0f ? -INFINITY : (key_value(key) - ref) * in.inv_t - log_sum;
@@ -486,7 +505,7 @@ __global__ __launch_bounds__(kFinishThreads) void distill_finish_kernel(RowLogit
                                                                         float* __restrict__ loss) {
     __shared__ Stats stats[64][ROWS + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    block_stats<ROWS, kFinishThreads>(in, (int64_t)blockIdx.x * ROWS, stats, nullptr);
+    block_stats<ROWS, kFinishThreads>(in, (int64_t)blockIdx.x * ROWS, stats, nullptr, 0);
     const int64_t m = (int64_t)blockIdx.x * ROWS + wave;
     if (wave >= ROWS || m >= in.M) return;  // the whole wave
     const Stats a = stats[0][wave];
@@ -615,21 +634,20 @@ static hipError_t logprob_finish(const RowLogits& r, const LogprobOut& o, hipStr
     // the maxima of the parts in LDS, unless they are more than it holds beside the rest
     const int64_t bytes = (int64_t)ROWS * r.parts * 4;
     const bool in_lds = o.k > 0 && bytes <= kMaximaBytes;
+    const unsigned lds = o.k > 0 ? (unsigned)(ROWS * row_words(r.parts, in_lds) * 4) : 0u;
     const auto fn = o.k > 0 ? logprob_finish_kernel<SUBS, ROWS, true> : logprob_finish_kernel<SUBS, ROWS, false>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)((r.M + ROWS - 1) / ROWS)), dim3(64 * SUBS * ROWS), in_lds ? (unsigned)bytes : 0u,
-                       s, r, o, in_lds ? 1 : 0);
+    hipLaunchKernelGGL(fn, dim3((unsigned)((r.M + ROWS - 1) / ROWS)), dim3(64 * SUBS * ROWS), lds, s, r, o, in_lds ? 1 : 0);
     return hipGetLastError();
 }
 
 hipError_t launch_logprob_finish(const RowLogits& r, const LogprobOut& o, hipStream_t s) {
     if (o.k < 0 || o.k > kMaxTop || r.width < 32 || (r.width & (r.width - 1))) return hipErrorInvalidValue;
-    // waves to a row x rows to a block, measured with 32000 columns and k = 20 (us
-    // with the product over 64, which takes 9 with one row and 256 with 8192 of it):
-    // 16 x 1, 8 x 1, 4 x 1, 1 x 16: one row 16.4, 15.3, 18.4, 39.5; 600 rows 66,
-    // 48, 47, 59; 2048 169, 115, 105, 105; 8192 675, 437, 403, 380 (k = 128: 750,
-    // 548, 501, 603)
+    // waves to a row x rows to a block, measured with 32000 columns (us, with the
+    // product over 64): 8 x 1, 4 x 1, 1 x 16 for k = 20: 300 rows 37, 36, 45, 1200
+    // rows 76, 71, 73, 2048 114, 105, 99, 8192 441, 389, 353; for k = 128: 300 rows
+    // 43, 45, 86, 2048 135, 126, 141, 8192 528, 478, 467
     if (r.M < 1024) return logprob_finish<8, 1>(r, o, s);
-    return r.M <= 2048 || o.k > 64 ? logprob_finish<4, 1>(r, o, s) : logprob_finish<1, 16>(r, o, s);
+    return r.M < (o.k > 64 ? 4096 : 2048) ? logprob_finish<4, 1>(r, o, s) : logprob_finish<1, 16>(r, o, s);
 }
 
 hipError_t launch_distill_finish(const RowLogits& r, const Listed& t, float* lse, float* slogits, float* loss,
