@@ -70,9 +70,9 @@ hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b
                  : kind == kSigmoid ? fused_ring<EPI_DACT, kSigmoid>(head, vec, a_oc, b_oc)
                                     : fused_ring<EPI_DACT, kLinear>(head, vec, a_oc, b_oc);
         else if (mode == EPI_GLU)
-            fn = kind == kNormal    ? fused_ring<EPI_GLU, kNormal>(head, true, a_oc, b_oc)
-                 : kind == kSigmoid ? fused_ring<EPI_GLU, kSigmoid>(head, true, a_oc, b_oc)
-                                    : fused_ring<EPI_GLU, kLinear>(head, true, a_oc, b_oc);
+            fn = kind == kNormal    ? fused_ring<EPI_GLU, kNormal>(head, !f32, a_oc, b_oc)
+                 : kind == kSigmoid ? fused_ring<EPI_GLU, kSigmoid>(head, !f32, a_oc, b_oc)
+                                    : fused_ring<EPI_GLU, kLinear>(head, !f32, a_oc, b_oc);
         else if (mode == EPI_DGLU)
             fn = kind == kNormal    ? fused_ring<EPI_DGLU, kNormal>(head, true, a_oc, b_oc)
                  : kind == kSigmoid ? fused_ring<EPI_DGLU, kSigmoid>(head, true, a_oc, b_oc)

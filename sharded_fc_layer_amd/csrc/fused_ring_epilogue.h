@@ -430,20 +430,23 @@ __device__ __forceinline__ void ring_logits(const FusedArgs& g, const TilePos& t
 // the up projection of outputs 16 p .. 16 p + 15 of its 64. Z's values (64 of
 // either half) and Y's are made where the accumulators lie and go through LDS,
 // 16 rows at a time in two buffers of 8 KB, so that stores are whole lines of
-// each half. Rows on 16-byte boundaries, N a multiple of 8; outputs that are
-// not wanted are descriptors of no size.
-template <int KIND>
+// each half. Rows on 16-byte boundaries, N a multiple of 8; a Z that is not
+// wanted is a descriptor of no size. F32: an fp32 output.
+//
+// Bound by the matrix units and, where they end, by the stores of Z: 8192 x
+// 2048 -> 2 x 8192, silu, takes 436 us with Z kept (1260 TFLOP/s) and 415
+// without, where a plain product of these 16384 columns with its bias takes
+// 417. (The function of a value is 10 of them: 418 and 406 without one.)
+template <int KIND, bool F32>
 __device__ __forceinline__ void ring_glu(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
                                          const f32x4 (&acc)[8][8], char* stage) {
     const int lr = lane & 15, lk = lane >> 4;
     const int64_t n0 = t.n0 + wave_n * 64, m0 = t.m0 + wave_m * 128;
     const int rows = t.M - m0 > 128 ? 128 : t.M > m0 ? (int)(t.M - m0) : 0;
     const int cols = g.N - n0 > 64 ? 64 : g.N > n0 ? (int)(g.N - n0) : 0;
-    const bool f32 = g.out_f32 != 0;
     const uint32_t ldc = (uint32_t)g.ldc, ldz = 2 * (uint32_t)g.N;
     const __amdgpu_buffer_rsrc_t rz = buffer_at(g.Z ? g.Z + m0 * 2 * g.N + n0 : nullptr);
-    const __amdgpu_buffer_rsrc_t rzu = buffer_at(g.Z ? g.Z + m0 * 2 * g.N + g.N + n0 : nullptr);
-    const __amdgpu_buffer_rsrc_t ry = buffer_at(static_cast<char*>(g.C) + (m0 * g.ldc + n0) * (f32 ? 4 : 2));
+    const __amdgpu_buffer_rsrc_t ry = buffer_at(static_cast<char*>(g.C) + (m0 * g.ldc + n0) * (F32 ? 4 : 2));
     const ActParams a = act_params(g.act);
     f32x4 bg[4], bu[4];
     const __amdgpu_buffer_rsrc_t rb = buffer_at(g.bias ? g.bias + n0 : nullptr);
@@ -456,10 +459,12 @@ __device__ __forceinline__ void ring_glu(const FusedArgs& g, const TilePos& t, i
 #pragma unroll
         for (int q = 0; q < 4; ++q) bg[p][q] = bf16_f32(x[q]), bu[p][q] = bf16_f32(y[q]);
     }
-    // reading back: Z's 16-byte chunk ch of rows 4 u + rq; Y's (bf16: 8 chunks to a row, fp32: 16)
+    // reading back: Z's 16-byte chunk ch (0 .. 7 the gate's) of rows 4 u + rq;
+    // Y's 8 chunks of rows 8 u + yrq (fp32: 16 of rows 4 u + yrq)
     const int rq = lane >> 4, ch = lane & 15;
-    const int yrq = f32 ? lane >> 4 : lane >> 3, ych = f32 ? lane & 15 : lane & 7, ystep = f32 ? 4 : 8;
-    const bool z_in = 8 * (ch & 7) < cols, y_in = (f32 ? 4 : 8) * ych < cols;
+    const int yrq = F32 ? lane >> 4 : lane >> 3, ych = F32 ? lane & 15 : lane & 7;
+    const bool z_in = 8 * (ch & 7) < cols, y_in = (F32 ? 4 : 8) * ych < cols;
+    const uint32_t z_col = 8 * (ch & 7) + (ch < 8 ? 0u : (uint32_t)g.N);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         char* zs = stage + (i & 1) * 8192;
@@ -471,10 +476,10 @@ __device__ __forceinline__ void ring_glu(const FusedArgs& g, const TilePos& t, i
 #pragma unroll
             for (int q = 0; q < 4; ++q) y[q] = act_value<KIND>(a, gate[q]) * up[q];
             const int c = 2 * (16 * p + 4 * lk);  // byte in a half's 128
-            *reinterpret_cast<u32x2*>(zs + lr * 256 + ((((c >> 4)) ^ lr) << 4) + (c & 15)) = pack_bf16(gate);
+            *reinterpret_cast<u32x2*>(zs + lr * 256 + (((c >> 4) ^ lr) << 4) + (c & 15)) = pack_bf16(gate);
             *reinterpret_cast<u32x2*>(zs + lr * 256 + ((((c >> 4) + 8) ^ lr) << 4) + (c & 15)) = pack_bf16(up);
-            // rows of 256 bytes; of a bf16 output's chunks the first 8 are used
-            if (f32)
+            // (rows of 256 bytes; of a bf16 output's chunks the first 8 are used)
+            if constexpr (F32)
                 *reinterpret_cast<f32x4*>(ys + lr * 256 + (((4 * p + lk) ^ lr) << 4)) = y;
             else
                 *reinterpret_cast<u32x2*>(ys + lr * 256 + (((c >> 4) ^ (lr & 7)) << 4) + (c & 15)) = pack_bf16(y);
@@ -483,16 +488,14 @@ __device__ __forceinline__ void ring_glu(const FusedArgs& g, const TilePos& t, i
         for (int u = 0; u < 4; ++u) {
             const int r = 4 * u + rq, row = 16 * i + r;
             const u32x4 v = *reinterpret_cast<const u32x4*>(zs + r * 256 + ((ch ^ r) << 4));
-            const uint32_t o = row < rows && z_in ? 2 * ((uint32_t)row * ldz + 8 * (ch & 7)) : kOOB;
-            __builtin_amdgcn_raw_buffer_store_b128(v, rz, ch < 8 ? o : kOOB, 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b128(v, rzu, ch < 8 ? kOOB : o, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(v, rz, row < rows && z_in ? 2 * ((uint32_t)row * ldz + z_col) : kOOB, 0, 0);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int r = ystep * u + yrq, row = 16 * i + r;  // (bf16: two accesses, the others past the group)
-            const u32x4 v = *reinterpret_cast<const u32x4*>(ys + (r & 15) * 256 + ((f32 ? ych ^ (r & 15) : ych ^ (r & 7)) << 4));
-            const uint32_t o = f32 ? 4 * ((uint32_t)row * ldc + 4 * ych) : 2 * ((uint32_t)row * ldc + 8 * ych);
-            __builtin_amdgcn_raw_buffer_store_b128(v, ry, r < 16 && row < rows && y_in ? o : kOOB, 0, 0);
+        for (int u = 0; u < (F32 ? 4 : 2); ++u) {
+            const int r = (F32 ? 4 : 8) * u + yrq, row = 16 * i + r;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(ys + r * 256 + ((ych ^ (F32 ? r : r & 7)) << 4));
+            const uint32_t o = F32 ? 4 * ((uint32_t)row * ldc + 4 * ych) : 2 * ((uint32_t)row * ldc + 8 * ych);
+            __builtin_amdgcn_raw_buffer_store_b128(v, ry, row < rows && y_in ? o : kOOB, 0, 0);
         }
         asm volatile("" ::: "memory");  // keeps the groups in this order
     }
@@ -588,7 +591,7 @@ __device__ __forceinline__ void ring_epilogue(const FusedArgs& g, const TilePos&
     if constexpr (MODE == EPI_STATS) {
         ring_stats<TN>(g, t, wave_m, wave_n, lane, acc);
     } else if constexpr (MODE == EPI_GLU) {
-        ring_glu<KIND>(g, t, wave_m, wave_n, lane, acc, stage);
+        ring_glu<KIND, !VEC>(g, t, wave_m, wave_n, lane, acc, stage);
     } else if constexpr (MODE == EPI_DGLU) {
         ring_dglu<KIND>(g, t, wave_m, wave_n, lane, acc, stage);
     } else if constexpr (MODE == EPI_LOGITS) {

@@ -2,6 +2,6 @@
 #define FCU_MODE EPI_GLU
 #define FCU_KIND 2
 #define FCU_GROUPED 0
-#define FCU_ANY_ROWS 0
+#define FCU_ANY_ROWS 1
 #define FCU_COLUMN_MAJOR_A 0
 #include "fused_ring_table.inc"
