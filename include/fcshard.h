@@ -295,8 +295,9 @@ fc_status fc_stamped_call(fc_op op, const void* P, fc_order p_order, const void*
  *
  * The FC layer's products with what a language model does around them:
  * activations in the epilogue, the loss over a vocabulary projection, expert
- * layers, gated layers, log probabilities and distillation. Matrices are laid out as above (tightly packed, bf16 unless
- * stated), sums are held in fp32 and rounded once on output unless stated.
+ * layers, gated layers, log probabilities and distillation. Matrices are laid
+ * out as above (tightly packed, bf16 unless stated), sums are held in fp32 and
+ * rounded once on output unless stated.
  * Calls enqueue kernels on `stream` and return: they neither allocate nor
  * synchronize, keep nothing between calls and may be captured into graphs.
  * Their plans depend on the arguments alone (fc_tune does not apply), and the

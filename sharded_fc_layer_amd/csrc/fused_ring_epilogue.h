@@ -342,7 +342,11 @@ __device__ __forceinline__ void ring_stats(const FusedArgs& g, const TilePos& t,
 // EPI_LOGITS where the accumulators lie: ring_stats with the mean distance from
 // the maximum; KEEP: the logits are stored too, 16 rows x 64 bytes to an
 // access, into rows that are padded to 64 columns; where g.need says so only.
-// (8192 x 2048 x 32000: 774 us without them, 950 with all)
+// Bound by the matrix units without them, and by the stores that come at each
+// tile's end with them: 8192 x 2048 x 32000 takes 783 us (1370 TFLOP/s), 849
+// with all (1.05 GB), 834 with the parts of 128 columns that hold one of a
+// row's 64 listed tokens (a fifth of them). Stores that pass the caches gain
+// nothing, stores of whole lines through LDS lose (a call 980 us against 948).
 template <int TN, bool KEEP>
 __device__ __forceinline__ void ring_logits(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
                                             const f32x4 (&acc)[8][TN]) {
@@ -505,6 +509,11 @@ __device__ __forceinline__ void ring_glu(const FusedArgs& g, const TilePos& t, i
 // fourth row; Z's two halves are loaded DEPTH groups of 16 rows ahead. Rows on
 // 16-byte boundaries, N a multiple of 8. Column sums as there: rows outside
 // are read from a row of zeros, since they may be products with infinities.
+//
+// Bound by the matrix units and memory, one after the other: 8192 x 2048 ->
+// 8192 takes 328 us, of which the product alone is 199 and the 671 MB of Z, dZ
+// and Y are 130 at a copy's rate; 303 without Y. One block owns a CU, so a
+// tile's epilogue runs beside other CUs' products only (FusedArgs::stagger).
 template <int KIND>
 __device__ __forceinline__ void ring_dglu(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
                                           const f32x4 (&acc)[8][8], char* stage) {

@@ -2,7 +2,8 @@
 // reduction index contiguous (nn.Linear's layout). One pass over W, one launch.
 //
 // Bound by reading W (one row, 2048 x 8192: 7.0 us replayed in a graph, 4.8
-// TB/s; the general kernel 12.3). A block takes 16 output columns, i.e. 16 rows of W's
+// TB/s; the general kernel 12.3; gated, 2048 -> 2 x 8192: 12.5, 5.4 TB/s, and
+// 16.2). A block takes 16 output columns, i.e. 16 rows of W's
 // storage, and its waves interleave 64-value pieces of the reduction, so that
 // a block reads whole 128-byte lines, 512 or 1024 bytes in a row of each. W
 // goes straight from memory into MFMA operands (16 x 16 x 32, W as source A):
