@@ -121,9 +121,10 @@ bool ring_takes(GroupMode grp, bool a_oc, bool b_oc, int64_t N, int64_t K, int64
 hipError_t launch_fused(EpiMode mode, GroupMode grp, int tile, bool a_oc, bool b_oc, const FusedArgs& g,
                         hipStream_t s);
 
-// EPI_ACT and EPI_GLU for at most 32 rows, both operands reduction-contiguous (fused_skinny.hip)
+// EPI_ACT, EPI_GLU (at most 32 rows) and EPI_LOGITS (16; parts of 32 columns), both operands reduction-contiguous (fused_skinny.hip)
 hipError_t launch_fused_skinny(const FusedArgs& g, hipStream_t s);
 hipError_t launch_fused_skinny_glu(const FusedArgs& g, hipStream_t s);
+hipError_t launch_fused_skinny_logits(const FusedArgs& g, hipStream_t s);
 
 // dst (rows x ld) = src (rows x cols) with zeros in columns cols .. ld - 1;
 // any cols and src alignment; ld a multiple of 8, dst 16-byte aligned.

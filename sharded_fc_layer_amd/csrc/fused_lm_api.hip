@@ -10,9 +10,13 @@ namespace {
 // The few-row kernel against the general one (us, W from memory; from the
 // caches): 2048 -> 8192 one row 16.0 and 19.8 (12.4; 16.2), 16 rows 19.4 and
 // 22.5 (14.9; 17.4), 32 rows 23.1 and 23.0; 4096 -> 14336 one row 49.6 and 55.8
-// (39.3; 35.1), 4 rows 51.9 and 60.6 (40.2; 34.8), 16 rows 60.5 and 57.2.
-bool few_rows_pay(int64_t M, int64_t N, int64_t K) {
-    return N <= (M <= 8 ? 16384 : M <= 16 ? 8192 : 4096) && K >= 256;
+// (39.3; 35.1), 4 rows 51.9 and 60.6 (40.2; 34.8), 16 rows 60.5 and 57.2. Rows
+// on odd elements are slower to read: 1001 -> 1531 one row 8.0 and 11.3, 32 rows
+// 11.7 and 14.5, 511 -> 4000 8.5 and 12.5, 12.1 and 14.8, but 2047 -> 4000 18.9
+// and 18.8, 30.8 and 21.6, 4095 -> 14336 114 and 78.
+bool few_rows_pay(int64_t M, int64_t N, int64_t K, bool aligned) {
+    const bool odd = K % 2 != 0 || !aligned;
+    return N <= (M <= 8 ? 16384 : M <= 16 ? 8192 : 4096) && K >= 256 && (!odd || N * K <= 1 << 22);
 }
 
 // A gated product: the plain one of 2 N columns (forward) or of N (its data
@@ -41,7 +45,7 @@ GluPlan glu_plan(int64_t M, int64_t N, int64_t K, bool b_oc, bool aligned, bool 
     if (copies) ring.us += copy_us(copies);
     if (!ring_fused) ring.us += planes_us(1, M, cols);
     if (512 * plane_ld(cols) < limit && ring.us < p.sh.us) p.sh = ring, p.fused = ring_fused;
-    if (!grad && M <= 32 && !b_oc && few_rows_pay(M, N, K)) p.sh = Shape{kSkinny, 1, K, 0}, p.fused = true;
+    if (!grad && M <= 32 && !b_oc && few_rows_pay(M, N, K, aligned)) p.sh = Shape{kSkinny, 1, K, 0}, p.fused = true;
     const bool large = p.sh.tile == kRingTile;
     p.A = operand(M, K, aligned, large, &ws);
     p.B = operand(b_oc ? K : cols, bcols, aligned, large, &ws);
@@ -76,6 +80,16 @@ bool bad_temperature(float t) { return !(t >= 0x1p-10f && t <= 0x1p10f); }
 // A row's logits and their statistics, a chunk of rows at a time: the workspace
 // holds the chunk's logits.
 constexpr int64_t kLogitBytes = (int64_t)1024 << 20;
+// The few-row kernel against the general one (us, W from memory, k = 0): one
+// row, 2048 -> 8000: 13.8 and 17.0, 32000: 32.7 and 38.9, 128000: 102 and 134,
+// 4096 -> 128256: 205 and 232; 8 rows 14.7 and 17.7, 34.5 and 37.8, 110 and 121,
+// 211 and 229; 16 rows 15.1 and 17.7, 36.9 and 38.0, 120 and 123, and over 4096
+// (32000) 64.4 and 62.5; 32 rows of 32000 45.5 and 39.0. Where W stays in the
+// caches it loses up to an eighth (32000: 28.5 and 25.5). Rows on odd elements are
+// read one by one (2047 -> 32000: 78 and 49).
+bool few_logit_rows_pay(int64_t M, int64_t K, bool aligned) {
+    return M <= (K <= 2048 ? 16 : 8) && K >= 256 && K % 2 == 0 && aligned;
+}
 struct LogitsPlan {
     Operand A, B;
     Shape sh;
@@ -97,13 +111,14 @@ LogitsPlan logits_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned,
     p.sh = shape_of(p.rows, N, K, false, b_oc, K, bcols, aligned, true);
     if (512 * p.z_ld >= (int64_t)1 << 31 && p.sh.tile == kRingTile)
         p.sh = small_shape(p.rows, N, K, false, !fits(K, aligned) || !fits(bcols, aligned), false);
-    const bool ring = p.sh.tile == kRingTile, split = p.sh.splits > 1;
+    if (!b_oc && few_logit_rows_pay(M, K, aligned)) p.sh = Shape{kSkinny, 1, K, 0};
+    const bool ring = p.sh.tile == kRingTile, split = p.sh.splits > 1, few = p.sh.tile == kSkinny;
     p.keep = read_again || split;
     p.A = operand(M, K, aligned, ring, &ws);
     p.B = operand(b_oc ? K : N, bcols, aligned, ring, &ws);
-    const FusedTile& t = kFusedTiles[p.sh.tile];
-    p.width = split ? kLogitCols : t.bn / t.wave_cols;
-    p.parts = split ? (int)((N + p.width - 1) / p.width) : (int)((N + t.bn - 1) / t.bn) * t.wave_cols;
+    const FusedTile& t = kFusedTiles[few ? 0 : p.sh.tile];
+    p.width = split ? kLogitCols : few ? 32 : t.bn / t.wave_cols;
+    p.parts = split || few ? (int)((N + p.width - 1) / p.width) : (int)((N + t.bn - 1) / t.bn) * t.wave_cols;
     p.z_off = ws;
     if (p.keep) ws += p.sh.splits * p.rows * p.z_ld * 4;
     p.stat_off = ws;
@@ -150,6 +165,7 @@ hipError_t run_logits(const LogitsPlan& pl, const LogitsCall& c, const uint16_t*
     }
     g.C = pl.keep ? z : nullptr;
     g.ldc = pl.z_ld;
+    if (pl.sh.tile == kSkinny) return launch_fused_skinny_logits(g, s);
     g.k_split = pl.sh.k_split, g.splits = 1, g.c_split_stride = 0;
     return launch_fused(EPI_LOGITS, GRP_NONE, pl.sh.tile, false, b_oc, g, s);
 }

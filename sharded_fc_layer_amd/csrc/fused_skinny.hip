@@ -1,4 +1,4 @@
-// fc_fwd_act and fc_fwd_glu for a few rows (decoding): M <= 32, W with its
+// fc_fwd_act, fc_fwd_glu and logits for a few rows (decoding): M <= 32, W with its
 // reduction index contiguous (nn.Linear's layout). One pass over W, one launch.
 //
 // Bound by reading W (one row, 2048 x 8192: 7.0 us replayed in a graph, 4.8
@@ -18,31 +18,40 @@
 namespace fcs {
 namespace {
 
-template <int TM, int WAVES, int HALVES>
+// What a block's columns are: 16 of a layer's, 16 of the gate's and of the up
+// projection's, or 16 SETS logits. U: pieces in flight to a wave. A gated layer
+// of one row, 2048 -> 2 x 8192: 12.5 us with two, 13.8 with four. Logits of one
+// row, 2048 -> 32000: 32.7 with one of two sets, 33.1 with two, 34.1 with four,
+// 34.9 with one of four sets (57.5 against 49.2 at 50001 columns).
+enum SkinnyForm { SKINNY_ACT, SKINNY_GLU, SKINNY_LOGITS };
+
+template <int TM, int WAVES, SkinnyForm FORM, int SETS, int U>
 __global__ __launch_bounds__(64 * WAVES) void fused_skinny_kernel(FusedArgs g) {
-    constexpr int U = 4 / HALVES;  // pieces in flight (a gated layer: 4 measured slower, 13.8 us against 12.5)
-    __shared__ f32x4 part[WAVES][TM * HALVES][64];
+    __shared__ f32x4 part[WAVES][TM * SETS][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lk = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n0 = (int64_t)blockIdx.x * (FORM == SKINNY_LOGITS ? 16 * SETS : 16);
     const int K = (int)g.K;
     const uint16_t* w_row = g.B + (n0 + lr) * g.ldb;
-    const bool row_in = n0 + lr < g.N;
+    const int64_t apart = FORM == SKINNY_LOGITS ? 16 : g.N;  // between sets of 16 columns
+    bool row_in[SETS];
+#pragma unroll
+    for (int e = 0; e < SETS; ++e) row_in[e] = n0 + lr + (FORM == SKINNY_LOGITS ? 16 * e : 0) < g.N;
 
-    f32x4 acc[TM][HALVES][2];
+    f32x4 acc[TM][SETS][2];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int e = 0; e < HALVES; ++e) acc[i][e][0] = acc[i][e][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int e = 0; e < SETS; ++e) acc[i][e][0] = acc[i][e][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int p0 = wave * 64; p0 < K; p0 += U * WAVES * 64) {
-        u16x8 w[U][HALVES][2], x[U][TM][2];
+        u16x8 w[U][SETS][2], x[U][TM][2];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = p0 + u * WAVES * 64 + 16 * lk + 8 * h;
 #pragma unroll
-                for (int e = 0; e < HALVES; ++e) w[u][e][h] = load8(w_row + e * g.N * g.ldb + k, row_in ? K - k : 0);
+                for (int e = 0; e < SETS; ++e) w[u][e][h] = load8(w_row + e * apart * g.ldb + k, row_in[e] ? K - k : 0);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -60,7 +69,7 @@ __global__ __launch_bounds__(64 * WAVES) void fused_skinny_kernel(FusedArgs g) {
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int e = 0; e < HALVES; ++e)
+                    for (int e = 0; e < SETS; ++e)
                         acc[i][e][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                             __builtin_bit_cast(bf16x8, w[u][e][h]), __builtin_bit_cast(bf16x8, x[u][i][h]),
                             acc[i][e][h], 0, 0, 0);
@@ -68,29 +77,69 @@ __global__ __launch_bounds__(64 * WAVES) void fused_skinny_kernel(FusedArgs g) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int e = 0; e < HALVES; ++e) part[wave][i * HALVES + e][lane] = acc[i][e][0] + acc[i][e][1];
+        for (int e = 0; e < SETS; ++e) part[wave][i * SETS + e][lane] = acc[i][e][0] + acc[i][e][1];
     __syncthreads();
     if (wave >= TM) return;
     // wave i: rows 16 i .. 16 i + 15, this lane's row and 4 columns
-    f32x4 s = part[0][wave * HALVES][lane];
-    [[maybe_unused]] f32x4 su = part[0][wave * HALVES + HALVES - 1][lane];
+    f32x4 s[SETS];
 #pragma unroll
-    for (int q = 1; q < WAVES; ++q) {
-        s += part[q][wave * HALVES][lane];
-        if constexpr (HALVES == 2) su += part[q][wave * HALVES + 1][lane];
-    }
+    for (int e = 0; e < SETS; ++e) s[e] = part[0][wave * SETS + e][lane];
+#pragma unroll
+    for (int q = 1; q < WAVES; ++q)
+#pragma unroll
+        for (int e = 0; e < SETS; ++e) s[e] += part[q][wave * SETS + e][lane];
     const int64_t m = 16 * wave + lr, n = n0 + 4 * lk;
+    if constexpr (FORM == SKINNY_LOGITS) {
+        // the row's statistics over these columns (C's rows are padded to 64)
+        float z[4 * SETS];
+        int hit = -1;
+        const uint64_t at = g.targets ? (uint64_t)g.targets[m < g.M ? m : 0] - (uint64_t)g.v0 : ~(uint64_t)0;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4 * SETS; ++q) {
+            const int64_t c = n + 16 * (q / 4) + q % 4;
+            z[q] = c < g.N ? s[q / 4][q % 4] : -INFINITY;
+            if (at == (uint64_t)c && c < g.N) hit = q;
+            mx = fmaxf(mx, z[q]);
+        }
+        if (g.C && m < g.M) {
+            float* row = static_cast<float*>(g.C) + m * g.ldc + n;
+#pragma unroll
+            for (int e = 0; e < SETS; ++e) *reinterpret_cast<f32x4*>(row + 16 * e) = s[e];
+        }
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        const float ref = __builtin_isinf(mx) ? 0.0f : mx, c = g.inv_t * kLog2e;
+        float sum = 0.0f, mean = 0.0f, target = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4 * SETS; ++q) {
+            add_exp(z[q], ref, c, sum, mean);
+            target = hit == q ? z[q] : target;
+        }
+        sum += __shfl_xor(sum, 16), mean += __shfl_xor(mean, 16);
+        sum += __shfl_xor(sum, 32), mean += __shfl_xor(mean, 32);
+        if (m >= g.M) return;
+        if (hit >= 0) g.tlogit[m] = target;
+        if (lk == 0) {
+            float* st = g.stat + (int64_t)blockIdx.x * g.M + m;
+            const int64_t step = (int64_t)gridDim.x * g.M;
+            st[0] = mx;
+            st[step] = sum;
+            st[2 * step] = mean * kLn2;
+        }
+        return;
+    }
     if (m >= g.M || n >= g.N) return;
     const int64_t at = m * g.ldc + n;
-    float v[4] = {s[0], s[1], s[2], s[3]};
+    float v[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
     if (g.bias) {
         float b[4];
         load4(g.bias + n, n, g.N, b);
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] += b[q];
     }
-    if constexpr (HALVES == 2) {
-        float up[4] = {su[0], su[1], su[2], su[3]};
+    if constexpr (FORM == SKINNY_GLU) {
+        float up[4] = {s[SETS - 1][0], s[SETS - 1][1], s[SETS - 1][2], s[SETS - 1][3]};
         if (g.bias) {
             float b[4];
             load4(g.bias + g.N + n, n, g.N, b);
@@ -108,7 +157,7 @@ __global__ __launch_bounds__(64 * WAVES) void fused_skinny_kernel(FusedArgs g) {
         if (g.Z) store4_bf16(g.Z + at, n, g.N, v);
         act_values(g.act, v);
     }
-    if (HALVES == 1 && g.R) {
+    if (FORM == SKINNY_ACT && g.R) {
         float r[4];
         load4(g.R + at, n, g.N, r);
 #pragma unroll
@@ -122,19 +171,22 @@ __global__ __launch_bounds__(64 * WAVES) void fused_skinny_kernel(FusedArgs g) {
 
 }  // namespace
 
-template <int HALVES>
+template <SkinnyForm FORM, int SETS, int U, int MOST = 2>
 static hipError_t launch_skinny(const FusedArgs& g, hipStream_t s) {
-    if (g.M > 32) return hipErrorInvalidValue;
-    const unsigned blocks = (unsigned)((g.N + 15) / 16);
+    if (g.M > 16 * MOST) return hipErrorInvalidValue;
+    constexpr int cols = FORM == SKINNY_LOGITS ? 16 * SETS : 16;
+    const unsigned blocks = (unsigned)((g.N + cols - 1) / cols);
     // fewer blocks than CUs: twice the waves to each
     const bool wide = blocks < 256;
-    const auto fn = g.M <= 16 ? (wide ? fused_skinny_kernel<1, 16, HALVES> : fused_skinny_kernel<1, 8, HALVES>)
-                              : (wide ? fused_skinny_kernel<2, 16, HALVES> : fused_skinny_kernel<2, 8, HALVES>);
+    const auto fn = g.M <= 16
+        ? (wide ? fused_skinny_kernel<1, 16, FORM, SETS, U> : fused_skinny_kernel<1, 8, FORM, SETS, U>)
+        : (wide ? fused_skinny_kernel<MOST, 16, FORM, SETS, U> : fused_skinny_kernel<MOST, 8, FORM, SETS, U>);
     hipLaunchKernelGGL(fn, dim3(blocks), dim3(wide ? 1024 : 512), 0, s, g);
     return hipGetLastError();
 }
 
-hipError_t launch_fused_skinny(const FusedArgs& g, hipStream_t s) { return launch_skinny<1>(g, s); }
-hipError_t launch_fused_skinny_glu(const FusedArgs& g, hipStream_t s) { return launch_skinny<2>(g, s); }
+hipError_t launch_fused_skinny(const FusedArgs& g, hipStream_t s) { return launch_skinny<SKINNY_ACT, 1, 4>(g, s); }
+hipError_t launch_fused_skinny_glu(const FusedArgs& g, hipStream_t s) { return launch_skinny<SKINNY_GLU, 2, 2>(g, s); }
+hipError_t launch_fused_skinny_logits(const FusedArgs& g, hipStream_t s) { return launch_skinny<SKINNY_LOGITS, 2, 1, 1>(g, s); }
 
 }  // namespace fcs

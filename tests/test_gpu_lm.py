@@ -623,6 +623,79 @@ def test_distill_gradient_by_differences():
     assert abs((a - b).sum().item() - (step * dX.double()).sum().item()) <= bound
 
 
+# ---- few rows, W with its reduction contiguous: parts of 32 columns, many and few blocks, K at its least, partial pieces
+
+FEW = [(1, 256, 1), (1, 2048, 8200), (3, 264, 31), (5, 2048, 33), (8, 2056, 1000), (9, 258, 9000), (16, 320, 20001),
+       (16, 2048, 65), (8, 4090, 300)]
+
+
+@pytest.mark.parametrize("shape", FEW)
+def test_few_rows_of_logits(shape):
+    test_logprob(shape, COL)
+    test_logprob_normal_inputs(shape)
+    test_distill_fwd(shape, COL)
+
+
+@pytest.mark.parametrize("shape", [(3, 512, 4100), (20, 512, 4096)])
+def test_few_rows_of_a_wide_gated_layer(shape):
+    """Blocks of eight waves, for up to 16 and up to 32 rows."""
+    test_fwd_glu(shape, COL)
+    test_fwd_glu_integers_are_exact(shape, COL)
+
+
+@pytest.mark.parametrize("k", [1, 64, 128])
+def test_few_equal_rows(k):
+    """All logits equal, and blocks of equal ones: the lowest indices."""
+    M, K, N = 3, 256, 10000
+    X, W = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda"), torch.zeros((K, N), dtype=torch.bfloat16, device="cuda")
+    X[1:, 0] = 1.0
+    W[0] = (torch.arange(N, device="cuda") // 50 % 7).to(torch.bfloat16)
+    want = torch.sort(X.float() @ W.float(), dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(F.fc_logprob(X, stored(W, COL), w_order=COL, top_k=k)[4], want)
+
+
+def test_few_rows_that_are_not_finite():
+    M, K, N = 6, 256, 3000
+    X, W = normal(gen(4), M, K), normal(gen(5), K, N, scale=0.1)
+    X[0], X[3], X[5] = float("nan"), INF, -INF
+    W[:, 5] = 0.0
+    good = torch.tensor([1, 2, 4], device="cuda")
+    ez = (K + 16) * U * (X[good].double().abs() @ W.double().abs()).max(1).values
+    z, s, lse, logp, p, entropy = logprob64(X[good], W, good, 0, 1.0)
+    got = F.fc_logprob(X, stored(W, COL), torch.arange(M, device="cuda"), w_order=COL, top_k=100)
+    assert bool(((got[4] >= 0) & (got[4] < N)).all())
+    assert bool((torch.sort(got[4], 1).values.diff(dim=1) > 0).all())  # each once
+    assert bool(torch.isnan(got[2][0]))
+    within(got[2][good], lse, ez + 2.0 ** -20 + (N + 16) * U + 4 * U * lse.abs(), "lse")
+    want = torch.sort(z, 1, descending=True).values[:, :100] - lse[:, None]
+    within(got[3][good], want, (2 * ez + 2.0 ** -18)[:, None] + 4 * U * want.abs(), "top")
+    # one infinite logit, one of -inf, the others finite
+    X, W = torch.zeros((2, K), dtype=torch.bfloat16, device="cuda"), torch.zeros((K, N), dtype=torch.bfloat16, device="cuda")
+    X[:, 0] = 1.0
+    W[0, 40], W[0, 41] = -INF, 1.0
+    logp, entropy, lse, top, ids = F.fc_logprob(X, stored(W, COL), torch.tensor([40, 41], device="cuda"), w_order=COL,
+                                                top_k=2)
+    full = torch.log(torch.tensor(N - 2 + 2.718281828459045, dtype=torch.float64)).item()
+    within(lse, torch.full((2,), full, device="cuda").double(), (N + 16) * U + 2.0 ** -20 + 4 * U * full, "lse")
+    assert logp[0].item() == -INF and ids.tolist() == [[41, 0]] * 2
+
+
+@pytest.mark.parametrize("shape", [(4096, 512, 2048), (3, 512, 2048), (300, 520, 264)])
+def test_glu_bias_at_any_element(shape):
+    """Operands on 16-byte boundaries, the bias alone at odd elements."""
+    M, K, N = shape
+    g = gen(6)
+    X, W, b = integers(g, M, K), integers(g, K, 2 * N), integers(g, 2 * N)
+    z = (X.double() @ W.double() + b.double()).float()
+    y = act64(z[:, :N], F.ACT_RELU) * z[:, N:]
+    for wo in (ROW, COL):
+        for bias in (b, shifted(b)):
+            Y, Z = F.fc_fwd_glu(X, stored(W, wo), bias=bias, act=F.ACT_RELU, w_order=wo, out_dtype=F.OUT_F32, keep_z=True)
+            assert torch.equal(Y, y) and torch.equal(Z, z.to(torch.bfloat16))
+            Y = F.fc_fwd_glu(X, stored(W, wo), bias=bias, act=F.ACT_RELU, w_order=wo)
+            assert torch.equal(Y, y.to(torch.bfloat16))
+
+
 # ---- memory, streams, graphs
 
 @pytest.mark.parametrize("shape", [(1, 1, 1), (2, 9, 2), (65, 7, 3), (129, 33, 1), (70, 39, 5), (16, 264, 24),
