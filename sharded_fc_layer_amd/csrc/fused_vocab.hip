@@ -271,7 +271,8 @@ __device__ __forceinline__ uint32_t reached_by(int k, int most, uint32_t least, 
 }
 
 // SUBS waves to a row, ROWS rows to a block. TOP: the largest as well, in
-// four steps: a value that k blocks' maxima or a few more reach, by halving;
+// four steps: a value that k blocks' maxima or a few more reach, by halving
+// (k = 100 of 126 blocks: 614 us, and 1146 without one where all were read);
 // those blocks (of equal maxima the first ones); their columns' values that
 // reach it, into LDS; the place of each by counting those in front of it. Where
 // more than kCandidates reach it, what k of the first kCandidates reach takes
@@ -335,11 +336,11 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
         const int most = k + k / 4 + 4;
         uint32_t least = 0;
         int count = parts;  // blocks to be read
-        if (parts > most) {
+        if (4 * parts >= 5 * k && parts * in.width > kCandidates) {
             float low = INFINITY;
             for (int p = p0 + lane; p < p1; p += 64) low = least_number(low, value_of(maximum(p)));
             low = join.smallest(wave_min(low));
-            least = reached_by<SUBS, ROWS>(k, most, 0, low, a.mx, join, count, [&](uint32_t c) {
+            least = reached_by<SUBS, ROWS>(k, parts > most ? most : k + k / 16 + 2, 0, low, a.mx, join, count, [&](uint32_t c) {
                 int n = 0;
                 for (int p = p0; p < p1; p += 64) n += __popcll(__ballot(p + lane < p1 && maximum(p + lane) >= c));
                 return n;
@@ -378,6 +379,43 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
         // their columns, four to a lane, four loads ahead
         const float* z = in.z + m * in.ld;
         const int total = count * in.width, shift = 31 - __builtin_clz(in.width);
+        if (least == 0 && total > kCandidates) {
+            // (fewer than 1.25 k parts: a value that k of the maxima of 512 groups of columns reach takes their
+            // place. 8192 rows of 16032 columns, k = 128, with the product over 2048: 691 us, and 1359 where the
+            // candidates alone tell, in five rounds)
+            constexpr int R = 8 / SUBS;  // groups to a lane
+            float mx[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) mx[r] = -INFINITY;
+            for (int e0 = 4 * (sub * 64); e0 < total; e0 += 4 * 256 * SUBS) {
+                f32x4 v[4];
+                int64_t col[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int e = e0 + u * 256 * SUBS + 4 * lane;
+                    col[u] = e < total ? ((int64_t)chosen[row][e >> shift] << shift) + (e & (in.width - 1)) : in.N;
+                    v[u] = col[u] < in.N ? *reinterpret_cast<const f32x4*>(z + col[u]) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        if (col[u] + h < in.N) mx[(4 * u + h) % R] = fmaxf(mx[(4 * u + h) % R], v[u][h]);
+            }
+            // (a group without a number counts as -inf, which all columns reach)
+            float low = INFINITY;
+            uint32_t o[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) o[r] = order_of(mx[r]), low = least_number(low, mx[r]);
+            low = join.smallest(wave_min(low));
+            int reached;
+            least = reached_by<SUBS, ROWS>(k, k + k / 8 + 2, 0, low, a.mx, join, reached, [&](uint32_t c) {
+                int r = 0;
+#pragma unroll
+                for (int i = 0; i < R; ++i) r += __popcll(__ballot(o[i] >= c));
+                return r;
+            });
+        }
         int n;
         bool sorted = false;
         for (;;) {

@@ -623,6 +623,21 @@ def test_distill_gradient_by_differences():
     assert abs((a - b).sum().item() - (step * dX.double()).sum().item()) <= bound
 
 
+@pytest.mark.parametrize("shape", [(3, 256, 4000), (300, 64, 4100), (1200, 64, 2900), (2304, 64, 16032), (4096, 64, 1000)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_alternatives_of_about_as_many_parts(shape, wo):
+    """Alternatives for fewer, as many and more than the parts of a row; values that repeat, and that do not."""
+    M, K, N = shape
+    g = gen(M + N)
+    X, W = grid(g, M, K), grid(g, K, N)
+    Xn, Wn = normal(g, M, K), normal(g, K, N, scale=0.3)
+    ez = (K + 16) * U * (Xn.double().abs() @ Wn.double().abs()).max(1).values
+    t = torch.randint(0, N, (M,), device="cuda", generator=g)
+    for k in (7, 8, 23, 32, 72, 100, 101, 125, 128):
+        check_logprob(X, stored(W, wo), W, wo, t, 0, 1.0, k, what=f"{shape} {wo} {k}")
+        check_logprob(Xn, stored(Wn, wo), Wn, wo, t, 0, 1.0, k, ez=ez, ids=False, what=f"{shape} {wo} {k} normal")
+
+
 # ---- few rows, W with its reduction contiguous: parts of 32 columns, many and few blocks, K at its least, partial pieces
 
 FEW = [(1, 256, 1), (1, 2048, 8200), (3, 264, 31), (5, 2048, 33), (8, 2056, 1000), (9, 258, 9000), (16, 320, 20001),
