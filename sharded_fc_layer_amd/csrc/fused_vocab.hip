@@ -512,7 +512,9 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
 
 // A row's listed tokens, PER of them to a lane (64 r + lane): ids (-1 where
 // there is none), probabilities (0 there) and their logarithms. Returns whether
-// the row has any.
+// the row has any. 1 / T scales the distances from the largest logit, not the
+// logits: a finite one times 1 / T may be infinite, which would read as absent;
+// a distance that becomes infinite has the probability 0 anyway.
 template <int PER>
 __device__ __forceinline__ bool teacher_row(const Listed& t, float inv_t, int64_t m, int lane, int64_t (&id)[PER],
                                             float (&p)[PER], float (&logp)[PER]) {
@@ -522,7 +524,7 @@ __device__ __forceinline__ bool teacher_row(const Listed& t, float inv_t, int64_
     for (int r = 0; r < PER; ++r) {
         const int i = 64 * r + lane;
         id[r] = i < t.n ? t.ids[m * t.n + i] : -1;
-        logp[r] = i < t.n && id[r] >= 0 ? t.tlogits[m * t.n + i] * inv_t : -INFINITY;
+        logp[r] = i < t.n && id[r] >= 0 ? t.tlogits[m * t.n + i] : -INFINITY;
         if (logp[r] == -INFINITY) id[r] = -1;
         some = some || id[r] >= 0;
         mx = fmaxf(mx, logp[r]);
@@ -532,7 +534,7 @@ __device__ __forceinline__ bool teacher_row(const Listed& t, float inv_t, int64_
     float s = 0.0f;
 #pragma unroll
     for (int r = 0; r < PER; ++r) {
-        logp[r] = id[r] >= 0 ? logp[r] - mx : 0.0f;
+        logp[r] = id[r] >= 0 ? (logp[r] - mx) * inv_t : 0.0f;
         p[r] = id[r] >= 0 ? exp_f32(logp[r]) : 0.0f;
         s += p[r];
     }

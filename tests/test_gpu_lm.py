@@ -967,3 +967,56 @@ def test_a_decoding_step():
         off = H * 2 * ((torch.nn.functional.silu(G) * Up).abs() @ W2.double().abs().t() + y.abs()) @ E.double().abs().t()
         assert abs(out[0].item() - want[0, r].item()) <= 2 * off.max().item()
         assert bool((want[0, out[4][0]] >= want.max() - 4 * off.max() - (out[3].max() - out[3].min()).double()).all())
+
+
+# ---- a teacher's logits and temperatures at their ends
+
+@pytest.mark.parametrize("T", [0.7, 2.0 ** -10, 0.5, 1.0, 2.0 ** 10])
+@pytest.mark.parametrize("n", [5, 64, 100])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_distill_of_teacher_logits_at_the_ends(n, T, wo):
+    """A finite teacher's logit is there, however it scales: the type's lowest value as a mask, and large ones whose
+    quotient by T leaves the type. All differences are zero or more than T x 10^30, so the largest ones of a row share
+    its probability. Only -inf and negative ids are absent."""
+    M, K, N = 70, 24, 1000
+    low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    g = gen(n)
+    X, W = grid(g, M, K), grid(g, K, N)  # exact logits
+    ids = torch.rand((M, N), device="cuda", generator=g).argsort(1)[:, :n].contiguous()
+    tl = torch.full((M, n), low, device="cuda")  # rows 0, 6, ..: masked tokens alone
+    tl[1::6, 0] = 0.0                            # one token that is not masked
+    tl[2::6, 1:3] = high
+    tl[3::6] = torch.where(torch.arange(n, device="cuda") % 3 == 0, 1e38, 5e37)
+    tl[4::6] = torch.where(torch.arange(n, device="cuda") % 2 == 0, -1e36, -2e36)
+    tl[::2, n - 1] = -INF
+    ids[1::5, n - 2] = -1
+    there = (ids >= 0) & (tl != -INF)
+    best = there & (tl == torch.where(there, tl, -INF).max(1, keepdim=True).values)
+    p = best.double() / best.sum(1, keepdim=True)
+    z = X.double() @ W.double()
+    sl = torch.where(there, z.gather(1, torch.where(there, ids, 0)), 0.0)
+    lse = torch.logsumexp(z / T, 1)
+    loss, got_lse, slogits = F.fc_distill_fwd(X, stored(W, wo), ids, tl, w_order=wo, temperature=T)
+    e_lse = 3 * U * z.abs().max(1).values / T + 2.0 ** -20 + (N + 16) * U + 4 * U * lse.abs()
+    within(got_lse, lse, e_lse, f"{T} lse")
+    assert torch.equal(slogits.double(), sl), f"{T} slogits"
+    logp = torch.where(best, torch.log(p), 0.0)
+    term, size = logp - sl / T + lse[:, None], logp.abs() + sl.abs() / T + lse.abs()[:, None]
+    ep = 2.0 ** -20 * (1 + logp.abs())
+    tol = (p * (ep * term.abs() + e_lse[:, None] + 4 * U * size + ep)).sum(1) + (n + 16) * U * (p * term.abs()).sum(1)
+    within(loss, (p * term).sum(1), tol, f"{T} loss")
+
+    w = torch.rand(M, device="cuda", generator=g) - 0.3
+    lse32 = lse.float()
+    dX, _ = F.fc_distill_bwd(X, stored(W, wo), ids, tl, sl.float(), lse32, w, w_order=wo, temperature=T,
+                             dx_dtype=F.OUT_F32)
+    s = z / T
+    q = torch.exp(s - lse32.double()[:, None])
+    hot = torch.zeros_like(q).scatter_add_(1, torch.where(there, ids, 0), p)
+    wc = (w.double() / T)[:, None]
+    D = wc * (q - hot)
+    eq = q * torch.expm1(2.0 ** -22 * (1 + s.abs() + lse.abs()[:, None]))
+    eD = wc.abs() * (eq + hot * (ep.amax(1, keepdim=True) + n * U) + 4 * U * (q + hot))
+    eD = eD + H * (D.abs() + eD) + (wc.abs() + 2) * 2.0 ** -126  # numbers under 2^-126 may be flushed to zero
+    aW = W.double().abs().t()
+    within(dX, D @ W.double().t(), eD @ aW + (N + 16) * U * ((D.abs() + eD) @ aW) + (N + 16) * 2.0 ** -126, f"{T} dX")
