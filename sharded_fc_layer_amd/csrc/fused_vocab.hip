@@ -5,8 +5,11 @@
 //
 // With m a row's largest logit, T the temperature, e_j = exp((z_j - m) / T),
 // s = sum_j e_j and w = sum_j e_j (z_j - m) / T:
-//   lse = m / T + log s,  log p_j = (z_j - m) / T - log s,  entropy = log s - w / s.
-// None of these subtracts large numbers that are nearly equal. Sets of columns
+//   lse = m / T + log s,  log p_j = (z_j - m) / T - log s,  entropy = log s - w / s,
+// and a distillation's loss = sum_k p_k (log p_k - log q_k) over the listed
+// tokens, q_k as p_j. None of these subtracts large numbers that are nearly
+// equal (lse alone has the size of z / T, which is 1e4 and more where T is
+// small, and is rounded so). Sets of columns
 // (m, s, w) are joined by scaling both to the larger maximum.
 //
 // The k largest logits without reading all of them again: ordered by value,
@@ -557,7 +560,7 @@ __global__ __launch_bounds__(kFinishThreads) void distill_finish_kernel(RowLogit
     const int64_t m = (int64_t)blockIdx.x * ROWS + wave;
     if (wave >= ROWS || m >= in.M) return;  // the whole wave
     const Stats a = stats[0][wave];
-    const float l = finite_ref(a.mx) * in.inv_t + logf(a.sum);
+    const float ref = finite_ref(a.mx), log_sum = logf(a.sum);
     int64_t id[PER];
     float p[PER], logp[PER];
     const bool any = teacher_row(t, in.inv_t, m, lane, id, p, logp);
@@ -568,11 +571,12 @@ __global__ __launch_bounds__(kFinishThreads) void distill_finish_kernel(RowLogit
         const uint64_t at = (uint64_t)id[r] - (uint64_t)in.v0;
         const float z = id[r] >= 0 && at < (uint64_t)in.N ? in.z[m * in.ld + (int64_t)at] : 0.0f;
         if (i < t.n) slogits[m * t.n + i] = z;
-        if (p[r] != 0.0f) sum += p[r] * (logp[r] + (l - z * in.inv_t));
+        // (halves: the distance of two finite logits may be more than the type holds, its quotient by T not)
+        if (p[r] != 0.0f) sum += p[r] * (logp[r] + ((0.5f * ref - 0.5f * z) * (2.0f * in.inv_t) + log_sum));
     }
     sum = wave_sum(sum);
     if (lane == 0) {
-        lse[m] = l;
+        lse[m] = ref * in.inv_t + log_sum;
         loss[m] = any ? sum : 0.0f;
     }
 }

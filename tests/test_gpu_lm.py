@@ -1020,3 +1020,51 @@ def test_distill_of_teacher_logits_at_the_ends(n, T, wo):
     eD = eD + H * (D.abs() + eD) + (wc.abs() + 2) * 2.0 ** -126  # numbers under 2^-126 may be flushed to zero
     aW = W.double().abs().t()
     within(dX, D @ W.double().t(), eD @ aW + (N + 16) * U * ((D.abs() + eD) @ aW) + (N + 16) * 2.0 ** -126, f"{T} dX")
+
+
+@pytest.mark.parametrize("T", [2.0 ** -10, 2.0 ** -9, 0.0013])
+@pytest.mark.parametrize("shape", [(40, 500), (3, 900), (2304, 1400)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_distill_loss_at_low_temperatures(shape, T, wo):
+    """z / T is of the order of 1e4 here and the loss of tokens near the maximum of the order of one: its error goes by
+    the distances from the maximum, not by z / T and the logarithm of the normaliser, which differ by as little."""
+    (M, N), K, n = shape, 256, 8
+    g = gen(N)
+    X = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros((K, N), dtype=torch.bfloat16, device="cuda")
+    X[:, 0] = (1 + (torch.arange(M, device="cuda") % 100) / 128).to(torch.bfloat16)  # logits 16 .. 29, and up to
+    X[:, 1] = 1.0                                                                   # 255 / 1024 more: exact
+    W[0] = 16.0
+    W[1] = (torch.randint(0, 256, (N,), device="cuda", generator=g) / 1024).to(torch.bfloat16)
+    z = X.double() @ W.double()
+    assert torch.equal(z, (X.float() @ W.float()).double()) and z.min() >= 16
+    ids = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :n].contiguous()
+    tl = torch.randn((M, n), device="cuda", generator=g) * T
+    loss, lse, slogits = F.fc_distill_fwd(X, stored(W, wo), ids, tl, w_order=wo, temperature=T)
+    sl, top = z.gather(1, ids), z.max(1).values[:, None]
+    assert torch.equal(slogits.double(), sl)
+    want = torch.logsumexp(z / T, 1)
+    e_log = 2.0 ** -20 + (N + 16) * U  # of the logarithm of the sum, relative to the maximum
+    within(lse, want, 3 * U * z.max(1).values / T + e_log + 4 * U * want.abs(), "lse")
+    logp = torch.log_softmax(tl.double() / T, 1)
+    p, far, ls = logp.exp(), (top - sl) / T, torch.log(torch.exp((z - top) / T).sum(1))[:, None]
+    term, size = logp + far + ls, logp.abs() + far + ls.abs()
+    ep = 2.0 ** -20 * (1 + logp.abs()) + 4 * U * (tl.double() / T).abs().amax(1, keepdim=True)
+    tol = (p * (ep * term.abs() + ep + e_log + 7 * U * size)).sum(1) + (n + 16) * U * (p * term.abs()).sum(1)
+    within(loss, (p * term).sum(1), tol, f"{shape} {T} loss")
+
+
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_distill_loss_of_logits_at_the_ends(wo):
+    """Logits whose distance is more than fp32 holds, its quotient by T not."""
+    N, T = 400, 2.0 ** 10
+    W = torch.full((1, N), 1.0, device="cuda").to(torch.bfloat16)
+    W[0, 7], W[0, 50] = 3e38, -3e38
+    ids, tl = torch.tensor([[50, 7]], device="cuda"), torch.zeros((1, 2), device="cuda")
+    loss, lse, slogits = F.fc_distill_fwd(torch.ones((1, 1), dtype=torch.bfloat16, device="cuda"), stored(W, wo), ids, tl,
+                                          w_order=wo, temperature=T)
+    z = W.double()[0]
+    assert torch.equal(slogits.double(), z[ids])
+    within(lse, z[7:8] / T, 4 * U * z[7:8] / T, "lse")
+    want = (z[7:8] - z[50:51]) / T / 2
+    within(loss, want, 2.0 ** -20 * want, "loss")
