@@ -1068,3 +1068,77 @@ def test_distill_loss_of_logits_at_the_ends(wo):
     within(lse, z[7:8] / T, 4 * U * z[7:8] / T, "lse")
     want = (z[7:8] - z[50:51]) / T / 2
     within(loss, want, 2.0 ** -20 * want, "loss")
+
+
+# ---- gradients against differences, row by row
+
+def glu_line(act):
+    """Rows of the gated layer with their gradients in 64 bits, and steps of 2^-7 along the signs of these gradients:
+    (X, W, R, step, differences of sum_j R_ij Y_ij over the step, gradient of Z, change of Z). X, X + step and X - step
+    are bf16 numbers and their products with W are exact in fp32. No gate lies near relu's kink where R is not zero."""
+    M, K, N = 24, 256, 40
+    g = torch.Generator().manual_seed(3)
+    X = torch.clamp(torch.round(torch.randn((M, K), generator=g) * 8), -28, 28).double() / 16  # within 1.75
+    W = torch.clamp(torch.round(torch.randn((K, 2 * N), generator=g) * 4), -16, 16).double() / 32
+    R = torch.randint(0, 2, (M, N), generator=g).double() * 2 - 1
+    z = X @ W
+    R = torch.where(z[:, :N].abs() > 0.5, R, 0.0)
+
+    def loss(x):
+        q = x @ W
+        return (R * act64(q[:, :N], act) * q[:, N:]).sum(1)
+
+    G, Up = z[:, :N], z[:, N:]
+    dZ = torch.cat([R * Up * slope64(G, act), R * act64(G, act)], 1)
+    step = torch.where(dZ @ W.t() >= 0, 1.0, -1.0).double() * 2.0 ** -7
+    return X, W, R, step, loss(X + step) - loss(X - step), dZ, step @ W
+
+
+def glu_line_bound(X, W, R, act, dZ, d):
+    """How far the difference of the library's losses and its gradient's product with twice the step may lie apart, for
+    each row."""
+    N = R.shape[1]
+    G, Up = (X @ W).split(N, 1)
+    dg, du = d.abs().split(N, 1)
+    a = act64(G, act)
+    # the differences: third derivatives (|act''| <= 2, |act'''| <= 2), and two fp32 outputs of exact Z
+    third = (2 * dg ** 3 * (Up.abs() + du) + 6 * dg ** 2 * du) / 3
+    big = (G.abs() + dg, Up.abs() + du)
+    e_y = 2 * (2.0 ** -20 * (1 + big[0] ** 2) * big[1] + U * (a.abs() + 1.13 * dg) * big[1])
+    # the gradient: Z rounded to bf16 (the slope of a slope is 2 at most), the functions' own errors, dZ rounded
+    e_dg = R.abs() * Up.abs() * (1.13 * H + 2 * H * G.abs()) * (1 + H) + R.abs() * Up.abs() * 2.0 ** -20 * (1 + G * G)
+    e_du = R.abs() * (1.13 * H * G.abs() + 2.0 ** -20 * (1 + G * G))
+    e = torch.cat([e_dg, e_du], 1)
+    e = e + H * (dZ.abs() + e)
+    # ... and the fp32 product over 2 N columns
+    e = e + (2 * N + 16) * U * (dZ.abs() + e)
+    return (R.abs() * (third + e_y)).sum(1) + 2 * (d.abs() * e).sum(1)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_glu_gradient_against_differences_of_each_row(act):
+    """The difference of each row's loss along its gradient is the gradient's size, which the errors are a small part
+    of: a gradient without one of its halves, or with another sign, is told from the right one in every row."""
+    X, W, R, step, want, dZ64, d = glu_line(act)
+    N = R.shape[1]
+    bound = glu_line_bound(X, W, R, act, dZ64, d)
+    cut = bound / want.abs()
+    assert bool((cut < 0.05).all())
+    halves = [torch.cat([dZ64[:, :N] * i, dZ64[:, N:] * j], 1) for i, j in ((0, 1), (1, 0), (0, 0), (-1, 1), (1, -1), (-1, -1))]
+    for wrong in halves:
+        assert bool((((2 * d * wrong).sum(1) - want).abs() > 2 * bound).all())
+
+    dev = [t.cuda() for t in (X, X + step, X - step, W, R)]
+    x, xa, xb, w, r = (t.to(torch.bfloat16) for t in dev)
+    assert all(torch.equal(t.double(), s) for t, s in zip((x, xa, xb, w, r), dev))  # all are bf16 numbers
+    for wo in (ROW, COL):
+        ws = stored(w, wo)
+        ya, yb = (F.fc_fwd_glu(t, ws, act=act, w_order=wo, out_dtype=F.OUT_F32).double() for t in (xa, xb))
+        diff = (dev[4] * (ya - yb)).sum(1).cpu()
+        _, Z = F.fc_fwd_glu(x, ws, act=act, w_order=wo, keep_z=True)
+        dZ, _, _ = F.fc_bwd_glu(r, Z, act)
+        dX = F.fc_bwd_data(dZ, ws, w_order=wo, out_dtype=F.OUT_F32)
+        ours = (2 * step * dX.double().cpu()).sum(1)
+        log(f"  {ACT_NAMES[act]}: bound / difference up to {cut.max().item():.3g}, "
+            f"error / bound {((diff - ours).abs() / bound).max().item():.3g}")
+        assert bool(((diff - ours).abs() <= bound).all()), ACT_NAMES[act]
