@@ -1142,3 +1142,86 @@ def test_glu_gradient_against_differences_of_each_row(act):
         log(f"  {ACT_NAMES[act]}: bound / difference up to {cut.max().item():.3g}, "
             f"error / bound {((diff - ours).abs() / bound).max().item():.3g}")
         assert bool(((diff - ours).abs() <= bound).all()), ACT_NAMES[act]
+
+
+def distill_line(T):
+    """Rows with a teacher's tokens, their losses' gradients in 64 bits, and steps of 2^-7 along the signs of these
+    gradients: X, X + step and X - step are bf16 numbers and their products with W are exact in fp32."""
+    M, K, N, n = 40, 256, 500, 9
+    g = torch.Generator().manual_seed(31)
+    X = torch.clamp(torch.round(torch.randn((M, K), generator=g) * 8), -28, 28).double() / 16  # within 1.75
+    W = torch.clamp(torch.round(torch.randn((K, N), generator=g) * 4), -16, 16).double() / 8 * min(T, 1.0)
+    ids = torch.rand((M, N), generator=g).argsort(1)[:, :n].contiguous()
+    ids[torch.rand((M, n), generator=g) < 0.3] = -1
+    ids[:, 0], ids[:, 1] = ids[:, 0].abs(), ids[:, 0].abs()  # the first token twice
+    ids[1::7] = -1
+    tl = torch.randn((M, n), generator=g)
+    there = ids >= 0
+    any_ = there.any(1)
+    t = torch.where(there, tl.double() / T, -INF)
+    p = torch.where(there, torch.softmax(torch.where(any_[:, None], t, 0.0), 1), 0.0)
+    hot = torch.zeros((M, N), dtype=torch.float64).scatter_add_(1, torch.where(there, ids, 0), p)
+
+    def loss(x):
+        logq = torch.log_softmax((x @ W) / T, 1)
+        return -(hot * logq).sum(1) + torch.special.xlogy(p, p).sum(1)
+
+    q = torch.softmax((X @ W) / T, 1)
+    D = torch.where(any_[:, None], (q - hot) / T, 0.0)
+    step = torch.where(D @ W.t() >= 0, 1.0, -1.0).double() * 2.0 ** -7
+    want = torch.where(any_, loss(X + step) - loss(X - step), 0.0)
+    return X, W, ids, tl, any_, p, hot, q, D, step, want
+
+
+def distill_line_bound(X, W, T, tl, p, hot, q, D, step):
+    """As glu_line_bound, of the loss and dX = D . W^T."""
+    N, n = W.shape[1], p.shape[1]
+    z, d = X @ W, step @ W
+    # the third cumulant of a variable within a range r is at most r^3 / (6 sqrt 3)
+    third = ((d.max(1).values - d.min(1).values) / T) ** 3 / (18 * 3 ** 0.5)
+    # a loss: the normaliser's error and its rounding, each term's, p's relative error (as in test_distill_fwd; the
+    # logits are exact)
+    lse = torch.logsumexp(z / T, 1).abs() + (d / T).abs().max(1).values
+    far = (z.abs() + d.abs()).max(1).values / T
+    logp = torch.where(p > 0, torch.log(p), 0.0)
+    e_lse = 3 * U * far + 2.0 ** -20 + (N + 16) * U + 4 * U * lse
+    size = logp.abs() + (far + lse)[:, None]
+    ep = 2.0 ** -20 * (1 + logp.abs()) + 4 * U * (tl.double() / T).abs().amax(1, keepdim=True)
+    e_loss = (p * (ep * size + e_lse[:, None] + 4 * U * size + ep)).sum(1) + (n + 16) * U * (p * size).sum(1)
+    # the gradient: probabilities on either side, D rounded to bf16, the fp32 product
+    eq = q * 2.0 ** -21 * (1 + far + lse)[:, None]
+    eh = hot * (ep + n * U).amax(1, keepdim=True)
+    e_d = (eq + eh + 4 * U * (q + hot)) / T
+    e_d = e_d + H * (D.abs() + e_d)
+    e_d = e_d + (N + 16) * U * (D.abs() + e_d)
+    return third + 2 * e_loss + 2 * (e_d * (step.abs() @ W.abs())).sum(1)
+
+
+@pytest.mark.parametrize("T", [1.0, 2.0, 0.5])
+def test_distill_gradient_against_differences_of_each_row(T):
+    """As for the gated layer: without the teacher's share, without the student's, at another temperature or with the
+    other sign the gradient lies outside the bound in every row."""
+    X, W, ids, tl, any_, p, hot, q, D, step, want = distill_line(T)
+    bound = distill_line_bound(X, W, T, tl, p, hot, q, D, step)
+    d = step @ W
+    cut = (bound / want.abs())[any_]
+    assert bool((cut < 0.05).all())
+    for wrong in (q / T, -hot / T, -D, 0 * D, 2 * D, D / 2):
+        assert bool((((2 * d * wrong).sum(1) - want).abs() > 2 * bound)[any_].all())
+
+    dev = [t.cuda() for t in (X, X + step, X - step, W)]
+    x, xa, xb, w = (t.to(torch.bfloat16) for t in dev)
+    assert all(torch.equal(t.double(), s) for t, s in zip((x, xa, xb, w), dev))  # all are bf16 numbers
+    ids, tl = ids.cuda(), tl.cuda()
+    for wo in (ROW, COL):
+        ws = stored(w, wo)
+        a, b = (F.fc_distill_fwd(t, ws, ids, tl, w_order=wo, temperature=T)[0].double() for t in (xa, xb))
+        diff = (a - b).cpu()
+        _, lse, sl = F.fc_distill_fwd(x, ws, ids, tl, w_order=wo, temperature=T)
+        dX, _ = F.fc_distill_bwd(x, ws, ids, tl, sl, lse, torch.ones(len(X), device="cuda"), w_order=wo, temperature=T,
+                                 dx_dtype=F.OUT_F32)
+        ours = (2 * step * dX.double().cpu()).sum(1)
+        log(f"  T {T}: bound / difference up to {cut.max().item():.3g}, "
+            f"error / bound {((diff - ours).abs() / bound).max().item():.3g}")
+        assert bool(((diff - ours).abs() <= bound).all())
+        assert bool((diff[~any_] == 0).all()) and bool((ours[~any_] == 0).all())
