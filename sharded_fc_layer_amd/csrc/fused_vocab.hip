@@ -88,6 +88,14 @@ __global__ __launch_bounds__(256) void row_logits_kernel(FusedArgs g, float* __r
     }
 }
 
+// Between a wave's writes to LDS and its other lanes' reads (or writes of
+// another type) there. The LDS takes one wave's accesses in order, so this
+// costs no instruction: it keeps the compiler from moving them past each other.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
@@ -328,7 +336,7 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
             if constexpr (SUBS > 1)
                 __syncthreads();
             else
-                __builtin_amdgcn_wave_barrier();  // one wave's LDS accesses are in order
+                wave_sync();
         };
         RowJoin<SUBS> join{slots, wave, first, 0};
         const int k = out.k, parts = in.parts;
@@ -595,7 +603,7 @@ __global__ __launch_bounds__(256) void listed_need_kernel(Listed t, int64_t M, i
     for (int w0 = 0; w0 < words; w0 += kNeedWords) {
         const int here = words - w0 < kNeedWords ? words - w0 : kNeedWords;
         for (int w = lane; w < here; w += 64) bits[wave][w] = 0;
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         for (int i = lane; i < t.n; i += 64) {
             const int64_t id = t.ids[m * t.n + i];
             const uint64_t at = (uint64_t)id - (uint64_t)v0;
@@ -603,7 +611,7 @@ __global__ __launch_bounds__(256) void listed_need_kernel(Listed t, int64_t M, i
             const int part = (int)(at >> shift), w = (part >> 5) - w0;
             if (w >= 0 && w < here) atomicOr(&bits[wave][w], 1u << (part & 31));
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         for (int w = lane; w < here; w += 64) need[(int64_t)(w0 + w) * M + m] = bits[wave][w];
     }
 }
@@ -631,7 +639,7 @@ __global__ __launch_bounds__(256) void listed_prep_kernel(Listed t, const float*
         total[r] = p[r], firsts[r] = id[r] >= 0;
         ids[wave][64 * r + lane] = id[r];
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     // tokens that are listed several times count together, in order, at their
     // first place; 16 at a time are looked at first, few rows have any
     for (int i0 = 0; i0 < t.n; i0 += 16) {
