@@ -344,8 +344,7 @@ struct GluEpilogue {
         bg = load8(g.bias + n, g.bias ? left : 0);
         bu = load8(g.bias + g.N + n, g.bias ? left : 0);
     }
-    template <int UN>
-    __device__ __forceinline__ void walk(const char* stage, int64_t m0, int rows, int64_t, int, int) const {
+    __device__ __forceinline__ void walk(const char* stage, int64_t m0, int rows) const {
 #pragma unroll 1
         for (int r0 = 0; r0 < rows; r0 += kRows) {
             const int r = r0 + rq;
@@ -372,7 +371,6 @@ struct GluEpilogue {
                 store8(static_cast<uint16_t*>(g.C) + m * g.ldc + n, cols, gate);
         }
     }
-    __device__ __forceinline__ void finish(int64_t) const {}
 };
 
 template <GroupMode GRP>

@@ -330,12 +330,15 @@ __global__ __launch_bounds__(kThreads) void fused_gemm_kernel(FusedArgs g) {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) stage_block<32, WTN>(stage, 32 * i, 32 * j, lane, acc[i][j]);
-    typedef std::conditional_t<kPairs, GluEpilogue<WTN>, Epilogue<MODE, WTN>> E;
-    E e(g, t, t.n0 + (kPairs ? wn0 / 2 : wn0), lane);
-    constexpr int kStep = E::kRows;  // rows per access
-    e.template walk<WTM / kStep >= 4 ? 4 : WTM / kStep>(stage, t.m0 + wm0, WTM, output_base<GRP>(g, t), t.tn * WC + wave_n,
-                                                        (int)((g.N + BN - 1) / BN) * WC);
-    e.finish((int64_t)t.tm * WR + wave_m);
+    if constexpr (kPairs) {
+        GluEpilogue<WTN>(g, t, t.n0 + wn0 / 2, lane).walk(stage, t.m0 + wm0, WTM);
+    } else {
+        Epilogue<MODE, WTN> e(g, t, t.n0 + wn0, lane);
+        constexpr int kStep = 64 / (WTN / 8);  // rows per access
+        e.template walk<WTM / kStep >= 4 ? 4 : WTM / kStep>(stage, t.m0 + wm0, WTM, output_base<GRP>(g, t),
+                                                            t.tn * WC + wave_n, (int)((g.N + BN - 1) / BN) * WC);
+        e.finish((int64_t)t.tm * WR + wave_m);
+    }
 }
 
 

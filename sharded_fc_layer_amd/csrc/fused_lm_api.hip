@@ -134,12 +134,11 @@ LogitsPlan logits_plan(int64_t M, int64_t K, int64_t N, bool b_oc, bool aligned,
 
 // Rows m0 .. m0 + rows - 1: their logits' statistics (and the logits), for the kernels that follow.
 struct LogitsCall {
-    const void *X, *W;
     int w_order;
     const int64_t* targets;  // or none
     int64_t v0;
     float inv_t;
-    int64_t M, K, N;
+    int64_t K, N;
     const Listed* listed;    // of these rows, or none
 };
 hipError_t run_logits(const LogitsPlan& pl, const LogitsCall& c, const uint16_t* x, const uint16_t* w, int64_t m0,
@@ -311,7 +310,7 @@ fc_status fc_logprob(const void* X, const void* W, fc_order w_order, const int64
     const uint16_t *x, *w;
     hipError_t e;
     if ((e = place(pl.A, X, &x, pl.B, W, &w, base, s)) != hipSuccess) return done(e);
-    const LogitsCall call{X, W, w_order, targets, vocab_start, 1.0f / temperature, M, K, N, nullptr};
+    const LogitsCall call{w_order, targets, vocab_start, 1.0f / temperature, K, N, nullptr};
     for (int64_t m0 = 0; m0 < M; m0 += pl.rows) {
         RowLogits r;
         if ((e = run_logits(pl, call, x, w, m0, std::min(pl.rows, M - m0), base, &r, s)) != hipSuccess) return done(e);
@@ -352,7 +351,7 @@ fc_status fc_distill_fwd(const void* X, const void* W, fc_order w_order, const i
     if ((e = place(pl.A, X, &x, pl.B, W, &w, base, s)) != hipSuccess) return done(e);
     for (int64_t m0 = 0; m0 < M; m0 += pl.rows) {
         const Listed t{ids + m0 * top_n, tlogits + m0 * top_n, top_n, nullptr, nullptr};
-        const LogitsCall call{X, W, w_order, nullptr, vocab_start, 1.0f / temperature, M, K, N, &t};
+        const LogitsCall call{w_order, nullptr, vocab_start, 1.0f / temperature, K, N, &t};
         RowLogits r;
         if ((e = run_logits(pl, call, x, w, m0, std::min(pl.rows, M - m0), base, &r, s)) != hipSuccess) return done(e);
         if ((e = launch_distill_finish(r, t, lse + m0, slogits + m0 * top_n, loss + m0, s)) != hipSuccess) return done(e);

@@ -47,7 +47,7 @@ __device__ __forceinline__ void join_stats(Stats& a, const Stats& b, float inv_t
     a.sum = a.sum * fa + b.sum * fb;
     a.mx = top;
 }
-// The planes of a product, 256 columns of one row to a wave, 4 to a lane: their
+// The planes of a split product, 256 columns of one row to a wave, 4 to a lane: their
 // sum, which is left in plane 0, and its statistics.
 __global__ __launch_bounds__(256) void row_logits_kernel(FusedArgs g, float* __restrict__ planes, int64_t pld,
                                                          int splits) {
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void row_logits_kernel(FusedArgs g, float* __r
         z = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll 4
         for (int s = 1; s < splits; ++s) z += *reinterpret_cast<const f32x4*>(p + s * g.M * pld);
-        if (splits > 1) *reinterpret_cast<f32x4*>(p) = z;
+        *reinterpret_cast<f32x4*>(p) = z;
         const uint64_t hit = g.targets ? (uint64_t)g.targets[m] - (uint64_t)g.v0 - (uint64_t)n : ~(uint64_t)0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -258,25 +258,19 @@ struct RowJoin {
 // low (about the smallest value that is a number) and high (the largest), as
 // floats first, where values lie close together, then as orders.
 // reach(c): the wave's number of values with an order of at least c.
-template <int SUBS, int ROWS, class F>
+template <int SUBS, class F>
 __device__ __forceinline__ uint32_t reached_by(int k, int most, uint32_t least, float low, float high, RowJoin<SUBS>& join,
                                                int& n, F reach) {
     uint32_t lo = least, hi = order_of(high) + 1;  // k values reach lo, fewer reach hi
     n = 0;
-    bool done = false;
-    for (int round = 0;; ++round) {
+    for (int round = 0; !(n >= k && n <= most) && hi - lo > 1; ++round) {
         uint32_t c = order_of(0.5f * low + 0.5f * high);
         if (round >= 8 || c <= lo || c >= hi) c = lo + (hi - lo) / 2;
-        const int here = join.sum(done ? 0 : reach(c));
-        if (!done) {
-            if (here >= k)
-                lo = c, n = here, low = value_of(c);
-            else
-                hi = c, high = value_of(c);
-            done = (n >= k && n <= most) || hi - lo <= 1;
-        }
-        // (rows of a block end together)
-        if (SUBS == 1 || ROWS == 1 ? done : __syncthreads_and(done)) break;
+        const int here = join.sum(reach(c));
+        if (here >= k)
+            lo = c, n = here, low = value_of(c);
+        else
+            hi = c, high = value_of(c);
     }
     return lo;
 }
@@ -301,6 +295,7 @@ __host__ __device__ inline int row_words(int parts, int in_lds) {
 template <int SUBS, int ROWS, bool TOP>
 __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLogits in, LogprobOut out, int in_lds) {
     static_assert(64 * SUBS * ROWS <= kFinishThreads, "a block's waves");
+    static_assert(SUBS == 1 || ROWS == 1, "rows of several waves each do not share their barriers");
     __shared__ Stats stats[64][ROWS + 1];
     // a row's maxima, where they fit, and then, in their place, the values found; of this row's waves alone
     extern __shared__ uint64_t row_space[];
@@ -351,7 +346,7 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
             float low = INFINITY;
             for (int p = p0 + lane; p < p1; p += 64) low = least_number(low, value_of(maximum(p)));
             low = join.smallest(wave_min(low));
-            least = reached_by<SUBS, ROWS>(k, parts > most ? most : k + k / 16 + 2, 0, low, a.mx, join, count, [&](uint32_t c) {
+            least = reached_by<SUBS>(k, parts > most ? most : k + k / 16 + 2, 0, low, a.mx, join, count, [&](uint32_t c) {
                 int n = 0;
                 for (int p = p0; p < p1; p += 64) n += __popcll(__ballot(p + lane < p1 && maximum(p + lane) >= c));
                 return n;
@@ -420,7 +415,7 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
             for (int r = 0; r < R; ++r) o[r] = order_of(mx[r]), low = least_number(low, mx[r]);
             low = join.smallest(wave_min(low));
             int reached;
-            least = reached_by<SUBS, ROWS>(k, k + k / 8 + 2, 0, low, a.mx, join, reached, [&](uint32_t c) {
+            least = reached_by<SUBS>(k, k + k / 8 + 2, 0, low, a.mx, join, reached, [&](uint32_t c) {
                 int r = 0;
 #pragma unroll
                 for (int i = 0; i < R; ++i) r += __popcll(__ballot(o[i] >= c));
@@ -463,22 +458,18 @@ __global__ __launch_bounds__(64 * SUBS * ROWS) void logprob_finish_kernel(RowLog
             }
             sync();
             if constexpr (SUBS > 1) n = found_n[row];
-            // (where rows share barriers, all go round while one has too many)
-            const bool full = n > kCandidates && !sorted;
-            if (SUBS == 1 ? !full : !__syncthreads_or(full)) break;
-            const int have = n < kCandidates ? n : kCandidates;
+            if (n <= kCandidates || sorted) break;
             float low = INFINITY;
-            for (int i = sub * 64 + lane; i < have; i += 64 * SUBS) low = least_number(low, key_value(found[i]));
+            for (int i = sub * 64 + lane; i < kCandidates; i += 64 * SUBS) low = least_number(low, key_value(found[i]));
             low = join.smallest(wave_min(low));
             int reached;
-            const uint32_t v = reached_by<SUBS, ROWS>(full ? k : 0, most, least, low, a.mx, join, reached, [&](uint32_t c) {
+            const uint32_t more = reached_by<SUBS>(k, most, least, low, a.mx, join, reached, [&](uint32_t c) {
                 int r = 0;
-                for (int i = sub * 64; i < have; i += 64 * SUBS)
-                    r += __popcll(__ballot(i + lane < have && (uint32_t)(found[i + lane] >> 32) >= c));
+                for (int i = sub * 64; i < kCandidates; i += 64 * SUBS)
+                    r += __popcll(__ballot((uint32_t)(found[i + lane] >> 32) >= c));
                 return r;
             });
-            const uint32_t more = full ? v : least;
-            if (full && more == least) sorted = true;  // equal values
+            sorted = more == least;  // equal values
             least = more;
             sync();
             if (sub == 0 && lane == 0) found_n[row] = 0;
