@@ -290,6 +290,12 @@ def report(out_dir: str, workload: str, number: int, prof: str, source_hash: str
         ran = ((rec or {}).get("config") or {}).get("workload")
         if ran is not None and ran != w:
             raise ValueError(f"the {run} run of --workload {number} timed workload {ran!r}, not {w!r}")
+    # the figures belong to the sources that ran: every run's bench line says which
+    for run in [f"{r}_{tag}" for r in ("trace", "mfma", "fetch", "write")] + \
+               [f"{r}_{tag}_p{i}" for i in alt_plans for r in ("fetch", "write")]:
+        ran = (_bench_line(os.path.join(prof, f"{run}.log")) or {}).get("kernel_source_hash")
+        if ran is not None and ran != source_hash:
+            raise ValueError(f"the {run} run was of kernel sources {ran}, not {source_hash}")
     plan_lines = []
     try:
         with open(plans) as f:

@@ -173,3 +173,18 @@ def test_forced_plan_runs_add_only_what_the_tuned_runs_lack():
     assert k1["by_grid"]["128"] == {"launches": 2, "hbm_bytes_per_launch": 30.0, "run": "p576"}
     assert "run" not in k1 and "run" not in k1["by_grid"]["64"]
     assert k2["run"] == "p576" and k2["hbm_bytes_per_launch"] == 7.0
+
+
+@pytest.mark.parametrize("run", ["trace_w2", "mfma_w2", "fetch_w2", "write_w2", "fetch_w2_p512", "write_w2_p512"])
+def test_report_refuses_runs_of_other_kernel_sources(run):
+    """A report states the sources its figures were taken on: a run whose bench
+    line names others is refused before anything is written."""
+    import json
+    with tempfile.TemporaryDirectory() as d:
+        line = {"metric": "m", "value": 1.0, "kernel_source_hash": "a" * 16,
+                "config": {"workload": "gpt_block_h2048_t8192"}}
+        with open(os.path.join(d, f"{run}.log"), "w") as f:
+            f.write(json.dumps(line) + "\n")
+        with pytest.raises(ValueError, match="kernel sources aaaaaaaaaaaaaaaa, not 0000000000000000"):
+            R.report(d, "gpt_block_h2048_t8192", 2, d, "0" * 16, alt_plans=(512,))
+        assert os.listdir(d) == [f"{run}.log"]
