@@ -449,7 +449,9 @@ int64_t fc_fwd_glu_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_order, i
  *   db = the sums of dZ's columns before rounding    2K fp32 values, or NULL
  * fc_bwd_data and fc_bwd_weight of dZ (as the gradient of a layer of 2K
  * outputs) are the gated layer's own gradients, fc_bwd_weight of H and dY that
- * of W; so the layer's output need not be kept.
+ * of W; so the layer's output need not be kept. H comes from the rounded Z: it
+ * differs from fc_fwd_glu's Y, made from the fp32 Z, by what Z's rounding to
+ * bf16 passes on, and W's gradient then is that of H, not of Y.
  */
 fc_status fc_bwd_data_glu(const void* dY, const void* W, fc_order w_order, const void* Z, fc_act act, void* dZ, void* H,
                           float* db, int64_t M, int64_t K, int64_t N, void* ws, int64_t ws_bytes, void* stream);
@@ -458,8 +460,8 @@ int64_t fc_bwd_data_glu_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_ord
 /*
  * The same from the gradient dY (bf16, M x N) of fc_fwd_glu's output itself:
  *   dZ = [dY * U * act'(G) | dY * act(G)], Y = act(G) * U, db = dZ's column sums
- * of which dZ, Y (bf16) and db (fp32, 2N) may be NULL, not all. No workspace is
- * needed without db.
+ * (Y from the rounded Z, as H above), of which dZ, Y (bf16) and db (fp32, 2N)
+ * may be NULL, not all. No workspace is needed without db.
  */
 fc_status fc_bwd_glu(const void* dY, const void* Z, fc_act act, void* dZ, void* Y, float* db, int64_t M, int64_t N,
                      void* ws, int64_t ws_bytes, void* stream);
@@ -524,7 +526,9 @@ int64_t fc_distill_fwd_ws_bytes(int64_t M, int64_t K, int64_t N, fc_order w_orde
  * rows of zeros where a row has no tokens;
  *   dX = D . W^T (M x K, bf16 or fp32; a shard's share of the sum)
  *   dW = X^T . D (K x N row-major, any output type)
- * The logits are computed again and D is rounded to bf16 as in fc_xent_bwd.
+ * The logits are computed again and D is rounded to bf16 as in fc_xent_bwd: fp32
+ * gradients carry this rounding too. lse is an fp32 number of the size of z / T:
+ * at 1e4 its own rounding is up to 5e-4 of every probability.
  */
 fc_status fc_distill_bwd(const void* X, const void* W, fc_order w_order, const int64_t* ids, const float* tlogits,
                          int top_n, int64_t vocab_start, float temperature, const float* slogits, const float* lse,

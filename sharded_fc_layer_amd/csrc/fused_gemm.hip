@@ -27,8 +27,11 @@ static int head_of(GroupMode grp, int64_t K) {
 // round's epilogues (at 5 TB/s), for the one that moves most, EPI_DGLU with 10
 // bytes a value. Outputs 8192 wide over 2048: 4096 rows (two rounds of tiles)
 // 190 us without, 170 with it, 8192 rows 335 and 322, 16384 rows 669 and 654;
-// over 6144 no difference. All of that time or more of it gains less, and none
-// of the others gains (EPI_LOGITS that stores 8192 x 32000: 948 and 949).
+// over 6144 no difference. 8192 rows over shorter reductions, without and with
+// it: 1024 257 and 244, 512 215 and 210, 256 and 128 the same, 64 153 and 159
+// (the call is its epilogue's traffic there). All of that time or more of it
+// gains less, and none of the others gains (EPI_LOGITS that stores 8192 x 32000:
+// 948 and 949).
 static int ring_stagger_ticks(EpiMode mode, const FusedArgs& g, int64_t blocks) {
     if (mode != EPI_DGLU || blocks < 512) return 0;
     const double bytes = 65536 * (8.0 + (g.Y ? 2.0 : 0.0));  // of a tile's epilogue

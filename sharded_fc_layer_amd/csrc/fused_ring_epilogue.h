@@ -438,9 +438,10 @@ __device__ __forceinline__ void ring_logits(const FusedArgs& g, const TilePos& t
 // wanted is a descriptor of no size. F32: an fp32 output.
 //
 // Bound by the matrix units and, where they end, by the stores of Z: 8192 x
-// 2048 -> 2 x 8192, silu, takes 436 us with Z kept (1260 TFLOP/s) and 415
-// without, where a plain product of these 16384 columns with its bias takes
-// 417. (The function of a value is 10 of them: 418 and 406 without one.)
+// 2048 -> 2 x 8192, silu, takes 427 to 442 us with Z kept (1290 to 1245
+// TFLOP/s) and 415 without, where a plain product of these 16384 columns with
+// its bias takes 417. (The function of a value is 10 of them: 418 and 406
+// without one.)
 template <int KIND, bool F32>
 __device__ __forceinline__ void ring_glu(const FusedArgs& g, const TilePos& t, int wave_m, int wave_n, int lane,
                                          const f32x4 (&acc)[8][8], char* stage) {

@@ -10,9 +10,9 @@
 // a lane takes 32 consecutive bytes of its row, which are the reduction
 // values 16 (lane / 16) .. +15 of the piece and serve two MFMAs; the order of
 // the reduction within a piece is the same permutation for X, whose rows past
-// M count as zeros. Rows of either start at any element. Eight W loads per wave
-// are in flight. The waves' sums meet in LDS, and one wave for each 16 rows adds
-// them in order and runs the epilogue.
+// M count as zeros. Rows of either start at any element. A wave has eight loads of
+// W in flight (2 U SETS; logits four). The waves' sums meet in LDS, and one wave
+// for each 16 rows adds them in order and runs the epilogue.
 #include "fused_epilogue.h"
 
 namespace fcs {

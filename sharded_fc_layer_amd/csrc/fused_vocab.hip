@@ -19,9 +19,14 @@
 // block maxima are searched first, then the k blocks' columns.
 //
 // Bound by the latency of a row's few dependent reads, which its neighbours
-// hide where there are many, and by the loads of the chosen columns. 32000
-// columns (us): 8192 rows, k = 20: 49 and k = 64: 128, beside their product's
-// 849; one row, k = 20: 11. Reading all logits again would be 210 for 8192 rows.
+// hide where there are many (one row: its waves wait in 64 % of their cycles),
+// and by the loads of the chosen columns (8192 rows, k = 64: 358 MB at 2.8
+// TB/s). 32000 columns (us): 8192 rows, k = 20: 49 and k = 64: 128, beside their
+// product's 849; one row, k = 20: 11. Reading all logits again would be 210 for
+// 8192 rows. Where a row's block maxima do not fit LDS (16 rows to a block, from
+// 114689 columns on) every step of the search reads them from the caches: calls
+// of 8192 rows over 2048, without alternatives, with k = 20, with 64: 112000
+// columns 2744, 3390, 3417, 128256 columns 3194, 3928, 4086.
 #include <algorithm>
 
 #include "fused_common.h"
@@ -547,8 +552,10 @@ __device__ __forceinline__ bool teacher_row(const Listed& t, float inv_t, int64_
     return any;
 }
 
-// ROWS rows to a block; their teachers' tokens, a wave to a row: 24 us for 8192
-// rows of 64 tokens, most of them the statistics of 250 parts a row (25 MB).
+// ROWS rows to a block; their teachers' tokens, a wave to a row. Bound by
+// memory: 24 us for 8192 rows of 64 tokens, 119 MB at 4.9 TB/s, of which a
+// 128-byte line for each token's logit is 67, the statistics of 250 parts a row
+// 25, the tokens 6.
 template <int ROWS, int PER>
 __global__ __launch_bounds__(kFinishThreads) void distill_finish_kernel(RowLogits in, Listed t, float* __restrict__ lse,
                                                                         float* __restrict__ slogits,
@@ -607,8 +614,8 @@ __global__ __launch_bounds__(256) void listed_need_kernel(Listed t, int64_t M, i
     }
 }
 
-// One wave to a row (8192 rows of 64 tokens: 14 us, 4 MB in, 4 MB out; most rows
-// list no token twice).
+// One wave to a row (8192 rows of 64 tokens: 14 us, 6.3 MB in, 2.1 MB out, the
+// waves wait in 58 % of their cycles; most rows list no token twice).
 template <int PER>
 __global__ __launch_bounds__(256) void listed_prep_kernel(Listed t, const float* __restrict__ grad, float inv_t,
                                                           int64_t M, float* __restrict__ p_out, float* __restrict__ gw,
@@ -662,7 +669,8 @@ __global__ __launch_bounds__(256) void listed_prep_kernel(Listed t, const float*
 
 // One thread to a listed token, whose entry of D the product's epilogue has
 // written as if nothing were listed: it is made again from the kept logit, so D
-// is rounded once. 2-byte writes anywhere: 10 us for 8192 rows of 64 tokens.
+// is rounded once. 2-byte writes anywhere: 10 us for 8192 rows of 64 tokens, 9
+// MB in and 8 MB out, the waves wait in 90 % of their cycles.
 __global__ __launch_bounds__(256) void listed_grad_kernel(Listed t, const float* __restrict__ lse,
                                                           const float* __restrict__ gw, float inv_t,
                                                           const float* __restrict__ scale, uint16_t* __restrict__ D,

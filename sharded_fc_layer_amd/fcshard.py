@@ -569,7 +569,8 @@ def fc_bwd_data_glu(dY, W, Z, act: int = ACT_SILU, w_order: int = ROW, keep_y: b
     """The gradient through a product and the gated layer below it: dH = dY . W^T,
     dZ = [dH * U * act'(G) | dH * act(G)], where Z = [G | U] (M x 2K) is what the
     layer's fc_fwd_glu left and W (K x N) is the product's. Returns dZ (M x 2K);
-    with keep_y also the layer's output act(G) * U (M x K), with bias_grad also
+    with keep_y also the layer's output act(G) * U (M x K; from the bf16 Z, where
+    fc_fwd_glu's is from the fp32 one), with bias_grad also
     dZ's column sums (fp32, 2K), as a tuple in this order."""
     import torch
     _bf16_2d(dY, "dY"), _bf16_2d(W, "W"), _order(w_order, "w_order")
