@@ -1225,3 +1225,26 @@ def test_distill_gradient_against_differences_of_each_row(T):
             f"error / bound {((diff - ours).abs() / bound).max().item():.3g}")
         assert bool(((diff - ours).abs() <= bound).all())
         assert bool((diff[~any_] == 0).all()) and bool((ours[~any_] == 0).all())
+
+
+# ---- the largest sizes: outputs whose columns or rows run into the millions
+
+@pytest.mark.parametrize("shape", [(2, 8, 1 << 22), (3, 256, 1 << 21), (1 << 20, 16, 48)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_largest_vocabularies_and_rows(shape, wo):
+    test_logprob(shape, wo)
+    test_distill_fwd(shape, wo)
+    check_distill_bwd(shape, wo, 0, shape[2], 1.0, 21, 3)
+
+
+@pytest.mark.parametrize("shape", [(2, 64, 1 << 21), (2, 260, 1 << 21), (1 << 20, 32, 24)])
+@pytest.mark.parametrize("wo", [ROW, COL])
+def test_largest_gated_layers(shape, wo):
+    M, K, N = shape
+    test_fwd_glu_integers_are_exact(shape, wo)
+    test_bwd_data_glu((M, K, N), wo)
+
+
+@pytest.mark.parametrize("shape", [(1 << 20, 40), (1 << 22, 3), (3, 1 << 21), (3, (1 << 21) - 1)])
+def test_largest_elementwise_gradients(shape):
+    test_bwd_glu(shape)
